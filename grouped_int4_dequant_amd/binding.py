@@ -108,6 +108,21 @@ def load() -> ctypes.CDLL:
         lib.moe_prepared_bytes.restype = ctypes.c_size_t
         lib.moe_prepare_weights.argtypes = [ctypes.POINTER(MoeLayerT), _P, ctypes.c_size_t, _P]
         lib.moe_prepare_weights.restype = ctypes.c_int
+        I, L = _I32, ctypes.c_int64
+        lib.moe_grouped_gemm.argtypes = [I, _P, L, I, _P, _P, I, I, I, I, _P, _P, I, L, _P]
+        lib.moe_grouped_gemm_dgrad.argtypes = [I, _P, L, _P, I, I, I, I, _P, _P, I, L, _P]
+        lib.moe_grouped_gemm_wgrad.argtypes = [I, _P, L, _P, L, I, _P, _P, I, I, I, I, _P, I, I, _P]
+        lib.moe_combine.argtypes = [I, _P, L, I, _P, _P, I, I, I, _P, I, L, _P, I, L, _P]
+        lib.moe_combine_backward.argtypes = [I, _P, L, _P, L, I, _P, _P, I, I, I, _P, L, _P, _P]
+        lib.moe_adapter_plan.argtypes = [_P, I, I, _P, _P, _P]
+        lib.moe_adapter_forward.argtypes = [I, _P, L, I, I, I, I, I, _P, _P, _P, _P, _P, _P, L, _P, I, L, _P]
+        lib.moe_adapter_backward.argtypes = [I, _P, L, _P, L, I, I, I, I, I, _P, _P, _P, _P, _P, _P, L, _P, I, L,
+                                             _P, _P, I, I, _P, ctypes.c_size_t, _P]
+        for name in ("moe_grouped_gemm", "moe_grouped_gemm_dgrad", "moe_grouped_gemm_wgrad", "moe_combine",
+                     "moe_combine_backward", "moe_adapter_plan", "moe_adapter_forward", "moe_adapter_backward"):
+            getattr(lib, name).restype = ctypes.c_int
+        lib.moe_adapter_backward_workspace_bytes.argtypes = [I, I]
+        lib.moe_adapter_backward_workspace_bytes.restype = ctypes.c_size_t
         lib.moe_status_string.argtypes = [ctypes.c_int]
         lib.moe_status_string.restype = ctypes.c_char_p
         _lib = lib
@@ -484,3 +499,291 @@ def prefill_chunked(layer: Layer, x: torch.Tensor, logits: torch.Tensor, chunk: 
                                       chunk, y.data_ptr(), ws.data_ptr(), ws.numel(),
                                       _stream(stream)), "moe_prefill_chunked")
     return y
+
+
+# ---------------------------------------------------------- 16-bit operators
+# Tensors are bf16 or fp16 (one type per call), results of that type or fp32.
+# Activations and results may be row-strided views (their columns contiguous);
+# a call runs on the tensors' device, on `stream` or that device's current
+# stream, and what it allocates belongs to that stream.
+_CODES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+class _Call:
+    """One call: its device and stream, and the checks of its tensors."""
+
+    def __init__(self, lead: torch.Tensor, name: str, stream):
+        if not isinstance(lead, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if lead.dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError(f"{name} must be bfloat16 or float16, got {lead.dtype}")
+        if not lead.is_cuda:
+            raise ValueError(f"{name} must be on the GPU")
+        self.dtype, self.device = lead.dtype, lead.device
+        self.code = _CODES[lead.dtype]
+        self.stream = torch.cuda.current_stream(lead.device) if stream is None else stream
+        if self.stream.device != lead.device:
+            raise ValueError(f"stream must be of {lead.device}, got {self.stream.device}")
+
+    def need(self, t, name, dtype, shape):
+        """A contiguous tensor of the call's device."""
+        _need(t, name, dtype, shape)
+        self._here(t, name)
+        return t
+
+    def rows(self, t, name, shape, dtypes=None):
+        """A matrix with contiguous columns and a row stride of at least its width."""
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype not in (dtypes or (self.dtype,)):
+            raise TypeError(f"{name} must be {' or '.join(map(str, dtypes or (self.dtype,)))}, got {t.dtype}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+            raise ValueError(f"{name} must have contiguous columns and rows that do not overlap")
+        self._here(t, name)
+        return t
+
+    def result(self, t, name, shape, dtype):
+        """The given result matrix, or a new one of `dtype` (None: the call's type)."""
+        if t is not None:
+            if dtype is not None and t.dtype != dtype:
+                raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+            return self.rows(t, name, shape, (self.dtype, torch.float32))
+        return self.new(shape, self._type(dtype, name))
+
+    def whole(self, t, name, shape, dtype):
+        """The given contiguous result, or a new one of `dtype` (None: the call's type)."""
+        if t is None:
+            return self.new(shape, self._type(dtype, name))
+        if t.dtype not in (self.dtype, torch.float32) or (dtype is not None and t.dtype != dtype):
+            raise TypeError(f"{name} must be {dtype or self.dtype}, got {t.dtype}")
+        return self.need(t, name, t.dtype, shape)
+
+    def _type(self, dtype, name):
+        dtype = self.dtype if dtype is None else dtype
+        if dtype not in (self.dtype, torch.float32):
+            raise TypeError(f"{name} must be {self.dtype} or float32, not {dtype}")
+        return dtype
+
+    def new(self, shape, dtype):
+        with torch.cuda.stream(self.stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def _here(self, t, name):
+        if t.device != self.device:
+            raise ValueError(f"{name} must be on {self.device}, got {t.device}")
+
+    def __call__(self, what, *args):
+        with torch.cuda.device(self.device):
+            _check(getattr(load(), what)(*args, self.stream.cuda_stream), what)
+
+
+def _ld(t: Optional[torch.Tensor]) -> int:
+    """Row stride of a matrix; its width where it has at most one row."""
+    return 0 if t is None else t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _groups(c: _Call, offsets: torch.Tensor, G: int) -> torch.Tensor:
+    return c.need(offsets, "offsets", torch.int32, (G + 1,))
+
+
+def grouped_gemm(A: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, a_row: Optional[torch.Tensor] = None,
+                 out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
+    """moe_grouped_gemm: C[p] = A[row(p)] @ W[e]^T for the sorted rows p of
+    each group e (offsets[e] .. offsets[e+1]). A [rows][K], W [G][N][K], a_row
+    int32 [P] (None: row(p) = p). Returns C [P][N]; rows behind the last group
+    are not written."""
+    c = _Call(A, "A", stream)
+    if A.dim() != 2 or not isinstance(W, torch.Tensor) or W.dim() != 3:
+        raise ValueError("A must be [rows][K] and W [G][N][K]")
+    G, N, K = W.shape
+    c.rows(A, "A", (A.shape[0], K))
+    c.need(W, "W", c.dtype, (G, N, K))
+    P = A.shape[0] if a_row is None else a_row.numel()
+    if a_row is not None:
+        c.need(a_row, "a_row", torch.int32, (P,))
+    _groups(c, offsets, G)
+    C = c.result(out, "out", (P, N), out_dtype)
+    c("moe_grouped_gemm", c.code, A.data_ptr(), _ld(A), A.shape[0], _ptr(a_row), offsets.data_ptr(), G, P, N, K,
+      W.data_ptr(), C.data_ptr(), _CODES[C.dtype], _ld(C))
+    return C
+
+
+def grouped_gemm_dgrad(dC: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, out: Optional[torch.Tensor] = None,
+                       out_dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
+    """moe_grouped_gemm_dgrad: dA[p] = dC[p] @ W[e] for the sorted rows p of
+    each group e. Returns dA [P][K], by sorted row."""
+    c = _Call(dC, "dC", stream)
+    if dC.dim() != 2 or not isinstance(W, torch.Tensor) or W.dim() != 3:
+        raise ValueError("dC must be [P][N] and W [G][N][K]")
+    G, N, K = W.shape
+    P = dC.shape[0]
+    c.rows(dC, "dC", (P, N))
+    c.need(W, "W", c.dtype, (G, N, K))
+    _groups(c, offsets, G)
+    dA = c.result(out, "out", (P, K), out_dtype)
+    c("moe_grouped_gemm_dgrad", c.code, dC.data_ptr(), _ld(dC), offsets.data_ptr(), G, P, N, K, W.data_ptr(),
+      dA.data_ptr(), _CODES[dA.dtype], _ld(dA))
+    return dA
+
+
+def grouped_gemm_wgrad(dC: torch.Tensor, A: torch.Tensor, offsets: torch.Tensor, a_row: Optional[torch.Tensor] = None,
+                       out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                       accumulate: bool = False, stream=None) -> torch.Tensor:
+    """moe_grouped_gemm_wgrad: dW[e] = dC[rows of e]^T @ A[row(rows of e)].
+    Returns dW [G][N][K]; with accumulate it is added to `out` (fp32)."""
+    c = _Call(dC, "dC", stream)
+    if dC.dim() != 2 or not isinstance(A, torch.Tensor) or A.dim() != 2:
+        raise ValueError("dC must be [P][N] and A [rows][K]")
+    if not isinstance(offsets, torch.Tensor) or offsets.numel() < 2:
+        raise ValueError("offsets must hold the G + 1 group bounds")
+    P, N = dC.shape
+    K, G = A.shape[1], offsets.numel() - 1
+    c.rows(dC, "dC", (P, N))
+    c.rows(A, "A", (A.shape[0], K))
+    if a_row is not None:
+        c.need(a_row, "a_row", torch.int32, (P,))
+    elif A.shape[0] != P:
+        raise ValueError(f"A must have the {P} rows of dC when a_row is not given, got {A.shape[0]}")
+    _groups(c, offsets, G)
+    if accumulate and out is None:
+        raise ValueError("accumulate needs the tensor to add to in `out`")
+    dW = c.whole(out, "out", (G, N, K), out_dtype)
+    c("moe_grouped_gemm_wgrad", c.code, dC.data_ptr(), _ld(dC), A.data_ptr(), _ld(A), A.shape[0], _ptr(a_row),
+      offsets.data_ptr(), G, P, N, K, dW.data_ptr(), _CODES[dW.dtype], int(accumulate))
+    return dW
+
+
+def combine(o: torch.Tensor, pair_pos: torch.Tensor, weights: Optional[torch.Tensor] = None,
+            add: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+            out_dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
+    """moe_combine: y[t] = sum_j weights[t][j] * o[pair_pos[t][j]] + add[t].
+    o [P][d], pair_pos int32 [T][k], weights fp32 [T][k] (None: ones), add
+    [T][d] (None: none). Returns y [T][d]."""
+    c = _Call(o, "o", stream)
+    if o.dim() != 2 or not isinstance(pair_pos, torch.Tensor) or pair_pos.dim() != 2:
+        raise ValueError("o must be [P][d] and pair_pos [T][k]")
+    (P, d), (T, k) = o.shape, pair_pos.shape
+    c.rows(o, "o", (P, d))
+    c.need(pair_pos, "pair_pos", torch.int32, (T, k))
+    if weights is not None:
+        c.need(weights, "weights", torch.float32, (T, k))
+    if add is not None:
+        c.rows(add, "add", (T, d), (c.dtype, torch.float32))
+    y = c.result(out, "out", (T, d), out_dtype)
+    c("moe_combine", c.code, o.data_ptr(), _ld(o), P, pair_pos.data_ptr(), _ptr(weights), T, k, d, _ptr(add),
+      c.code if add is None else _CODES[add.dtype], _ld(add), y.data_ptr(), _CODES[y.dtype], _ld(y))
+    return y
+
+
+def combine_backward(dy: torch.Tensor, o: torch.Tensor, pair_pos: torch.Tensor, weights: Optional[torch.Tensor] = None,
+                     d_o: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None, stream=None):
+    """moe_combine_backward: (d_o [P][d], dw fp32 [T][k]) with d_o[pair_pos[t][j]]
+    = weights[t][j] * dy[t] and dw[t][j] = <dy[t], o[pair_pos[t][j]]>. Rows of
+    d_o that no pair names are not written."""
+    c = _Call(dy, "dy", stream)
+    if dy.dim() != 2 or not isinstance(o, torch.Tensor) or o.dim() != 2 or not isinstance(pair_pos, torch.Tensor) or pair_pos.dim() != 2:
+        raise ValueError("dy must be [T][d], o [P][d] and pair_pos [T][k]")
+    (P, d), (T, k) = o.shape, pair_pos.shape
+    c.rows(dy, "dy", (T, d))
+    c.rows(o, "o", (P, d))
+    c.need(pair_pos, "pair_pos", torch.int32, (T, k))
+    if weights is not None:
+        c.need(weights, "weights", torch.float32, (T, k))
+    d_o = c.new((P, d), c.dtype) if d_o is None else c.rows(d_o, "d_o", (P, d))
+    dw = c.new((T, k), torch.float32) if dw is None else c.need(dw, "dw", torch.float32, (T, k))
+    c("moe_combine_backward", c.code, dy.data_ptr(), _ld(dy), o.data_ptr(), _ld(o), P, pair_pos.data_ptr(), _ptr(weights),
+      T, k, d, d_o.data_ptr(), _ld(d_o), dw.data_ptr())
+    return d_o, dw
+
+
+def adapter_plan(row_adapter: torch.Tensor, n: int, stream=None):
+    """moe_adapter_plan: (rows int32 [T], offsets int32 [n+1]), the batch's rows
+    sorted by adapter (row_adapter int32 [T]; outside [0, n): no adapter, sorted
+    behind the others). One plan serves every projection of the batch."""
+    _need(row_adapter, "row_adapter", torch.int32, (row_adapter.numel(),))
+    dev = row_adapter.device
+    s = torch.cuda.current_stream(dev) if stream is None else stream
+    if s.device != dev:
+        raise ValueError(f"stream must be of {dev}, got {s.device}")
+    if n < 1:
+        raise ValueError("n must be at least 1")
+    T = row_adapter.numel()
+    with torch.cuda.stream(s):
+        rows = torch.empty(T, dtype=torch.int32, device=dev)
+        offsets = torch.empty(n + 1, dtype=torch.int32, device=dev)
+        _check(load().moe_adapter_plan(row_adapter.data_ptr(), T, n, rows.data_ptr(), offsets.data_ptr(), s.cuda_stream),
+               "moe_adapter_plan")
+    return rows, offsets
+
+
+def _adapter_args(c: _Call, x, A, B, scale, plan):
+    if x.dim() != 2 or not isinstance(A, torch.Tensor) or A.dim() != 3 or not isinstance(B, torch.Tensor) or B.dim() != 3:
+        raise ValueError("x must be [T][K], A [n][r][K] and B [n][N][r]")
+    (T, K), (n, r, _), N = x.shape, A.shape, B.shape[1]
+    c.rows(x, "x", (T, K))
+    c.need(A, "A", c.dtype, (n, r, K))
+    c.need(B, "B", c.dtype, (n, N, r))
+    if scale is not None:
+        c.need(scale, "scale", torch.float32, (n,))
+    rows, offsets = plan
+    c.need(rows, "rows", torch.int32, (T,))
+    c.need(offsets, "offsets", torch.int32, (n + 1,))
+    return T, K, N, r, n, rows, offsets
+
+
+def adapter_forward(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scale: Optional[torch.Tensor], plan,
+                    base: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                    out_dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
+    """moe_adapter_forward: y[t] = base[t] + scale[a] * (x[t] @ A[a]^T) @ B[a]^T
+    with a the adapter of row t; y[t] = base[t] for rows without one. x [T][K],
+    A [n][r][K], B [n][N][r], scale fp32 [n] (None: ones), plan =
+    adapter_plan(...), base [T][N] of y's type (None: zeros). out may be base
+    itself (in place). Returns y [T][N]."""
+    c = _Call(x, "x", stream)
+    T, K, N, r, n, rows, offsets = _adapter_args(c, x, A, B, scale, plan)
+    if base is not None:
+        c.rows(base, "base", (T, N), (c.dtype, torch.float32))
+        out_dtype = base.dtype if out_dtype is None and out is None else out_dtype
+    y = c.result(out, "out", (T, N), out_dtype)
+    if base is not None and base.dtype != y.dtype:
+        raise TypeError(f"base must be {y.dtype} like the result, got {base.dtype}")
+    c("moe_adapter_forward", c.code, x.data_ptr(), _ld(x), T, K, N, r, n, A.data_ptr(), B.data_ptr(), _ptr(scale),
+      rows.data_ptr(), offsets.data_ptr(), _ptr(base), _ld(base), y.data_ptr(), _CODES[y.dtype], _ld(y))
+    return y
+
+
+def adapter_backward_workspace_bytes(T: int, r: int) -> int:
+    return int(load().moe_adapter_backward_workspace_bytes(T, r))
+
+
+def adapter_backward(dy: torch.Tensor, x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scale: Optional[torch.Tensor],
+                     plan, dx_base: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                     dA: Optional[torch.Tensor] = None, dB: Optional[torch.Tensor] = None,
+                     grad_dtype: Optional[torch.dtype] = None, accumulate: bool = False,
+                     ws: Optional[torch.Tensor] = None, stream=None):
+    """moe_adapter_backward: (dx [T][K], dA [n][r][K], dB [n][N][r]) from dy
+    [T][N]. dx_base [T][K] (None: zeros) is added to dx, which is of its type
+    (else x's) and may be dx_base itself; dA and dB are of grad_dtype (None:
+    x's type), and with accumulate are added to the given dA and dB (fp32)."""
+    c = _Call(x, "x", stream)
+    T, K, N, r, n, rows, offsets = _adapter_args(c, x, A, B, scale, plan)
+    c.rows(dy, "dy", (T, N))
+    if dx_base is not None:
+        c.rows(dx_base, "dx_base", (T, K), (c.dtype, torch.float32))
+    dx = c.result(dx, "dx", (T, K), None if dx_base is None else dx_base.dtype)
+    if accumulate and (dA is None or dB is None):
+        raise ValueError("accumulate needs the tensors to add to in dA and dB")
+    dA = c.whole(dA, "dA", (n, r, K), grad_dtype)
+    dB = c.whole(dB, "dB", (n, N, r), dA.dtype)
+    need = adapter_backward_workspace_bytes(T, r)
+    if ws is None:
+        ws = c.new(max(need, 1), torch.uint8)
+    else:
+        c._here(ws, "ws")
+    c("moe_adapter_backward", c.code, dy.data_ptr(), _ld(dy), x.data_ptr(), _ld(x), T, K, N, r, n, A.data_ptr(),
+      B.data_ptr(), _ptr(scale), rows.data_ptr(), offsets.data_ptr(), _ptr(dx_base), _ld(dx_base), dx.data_ptr(),
+      _CODES[dx.dtype], _ld(dx), dA.data_ptr(), dB.data_ptr(), _CODES[dA.dtype], int(accumulate), ws.data_ptr(),
+      ws.numel() * ws.element_size())
+    return dx, dA, dB

@@ -1,0 +1,112 @@
+// Device pieces shared by the 16-bit operators: element types with their
+// matrix instruction, direct loads into LDS, and the search that maps a tile
+// number to rows of a group.
+#pragma once
+
+#include "grouped_internal.h"
+
+namespace moe {
+
+typedef float f4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+typedef short s4 __attribute__((ext_vector_type(4)));
+typedef short s8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+
+struct Bf16 {
+  static __device__ __forceinline__ f4 mfma(s8 a, s8 b, f4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, a), __builtin_bit_cast(bf8, b), c, 0, 0, 0);
+  }
+  // nearest, ties to even; NaN stays NaN
+  static __device__ __forceinline__ uint16_t from(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
+  static __device__ __forceinline__ float to(uint16_t b) { return __builtin_bit_cast(float, (uint32_t)b << 16); }
+};
+struct Fp16 {
+  static __device__ __forceinline__ f4 mfma(s8 a, s8 b, f4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, a), __builtin_bit_cast(h8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ uint16_t from(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
+  static __device__ __forceinline__ float to(uint16_t b) { return (float)__builtin_bit_cast(_Float16, b); }
+};
+
+// 16 bytes from each lane's own address to LDS: lane l's land at dst + 16 l.
+// dst is the same for the whole wave.
+__device__ __forceinline__ void load_lds16(const void *src, void *dst) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
+                                   (__attribute__((address_space(3))) void *)dst, 16, 0, 0);
+}
+
+// Lane p of each 16-lane group names four 16-bit elements of row p / 4 of a
+// 4 x 16 block (columns 4 (p % 4) ..); it receives column p, rows 0..3.
+__device__ __forceinline__ s4 read_lds_tr(const void *p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4 *)p);
+}
+
+struct GroupTile {
+  int e;       // group, or -1: no such tile
+  int first;   // first sorted row of the group
+  int count;   // rows of the group
+  int before;  // row tiles of the groups before it
+  int total;   // row tiles of all groups
+};
+
+// Group that holds row tile m, when every group's rows are cut into tiles of
+// `rows`. Every wave searches by itself: lane l adds up the tiles of its run
+// of ceil(G / 64) groups, a prefix sum over the lanes finds the lane that
+// holds tile m, and its run is walked again. Offsets outside [0, P] are
+// taken as the nearest of the two and a group that ends before it begins as empty, so that no
+// address formed from them leaves the caller's arrays. m must be the same
+// for the whole wave; with m < 0 only `total` is found.
+__device__ __forceinline__ GroupTile find_group(const int32_t *offsets, int G, int P, int rows, int m) {
+  const int lane = threadIdx.x & 63;
+  const int run = (G + 63) >> 6;
+  const int g0 = min(lane * run, G), g1 = min(g0 + run, G);
+  auto at = [&](int g) { return min(max(offsets[g], 0), P); };
+  int mine = 0;
+  int prev = at(g0);
+  for (int g = g0; g < g1; ++g) {
+    const int next = at(g + 1);
+    mine += (max(next - prev, 0) + rows - 1) / rows;
+    prev = next;
+  }
+  int sum = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int v = __shfl_up(sum, d);
+    if (lane >= d) sum += v;
+  }
+  GroupTile t;
+  t.total = __shfl(sum, 63);
+  t.e = -1;
+  t.first = t.count = t.before = 0;
+  const uint64_t past = __ballot(sum > m);
+  if (m < 0 || past == 0) return t;
+  const int owner = __builtin_ctzll(past);
+  int before = __shfl(sum - mine, owner);
+  int g = __shfl(g0, owner);
+  const int end = __shfl(g1, owner);
+  int a = at(g);
+  for (; g < end; ++g) {
+    const int b = at(g + 1);
+    const int n = (max(b - a, 0) + rows - 1) / rows;
+    if (m < before + n) {
+      t.e = g;
+      t.first = a;
+      t.count = b - a;
+      t.before = before;
+      break;
+    }
+    before += n;
+    a = b;
+  }
+  t.e = __builtin_amdgcn_readfirstlane(t.e);
+  t.first = __builtin_amdgcn_readfirstlane(t.first);
+  t.count = __builtin_amdgcn_readfirstlane(t.count);
+  t.before = __builtin_amdgcn_readfirstlane(t.before);
+  t.total = __builtin_amdgcn_readfirstlane(t.total);
+  return t;
+}
+
+}  // namespace moe

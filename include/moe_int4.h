@@ -468,6 +468,164 @@ int moe_layer_graph_launch(moe_layer_graph_t *graph, hipStream_t stream);
 /* Release the graph and what it holds (after its launches have completed). */
 int moe_layer_graph_destroy(moe_layer_graph_t *graph);
 
+/* ------------------------------------------------------------------------
+ * 16-bit operators beside the int4 layer: products grouped by expert with
+ * unquantised weights and their gradients, the weighted combine of expert
+ * rows and its gradient, and low-rank adapters of many requests beside a
+ * shared projection and their gradients.
+ *
+ * Conventions shared by them, beyond those at the top:
+ *   - dtype is the type of the operands: MOE_BF16 or MOE_FP16. Results are
+ *     of that type or MOE_FP32; any other code is MOE_EINVAL. Products are exact
+ *     in fp32, sums are held in fp32 in a fixed order (repeated calls agree
+ *     bit for bit) and rounded once, to nearest even, where they are stored.
+ *   - A matrix of activations or results is given by its first element and
+ *     its row stride in elements (lda, ldc, ...), at least its width; its columns
+ *     are contiguous. Weights, adapters and their gradients are contiguous.
+ *   - Pointers need the alignment of their element type only (else
+ *     MOE_EINVAL). Operands whose rows are whole 16-byte units at 16-byte
+ *     alignment take wide loads; others are read element by element, which
+ *     is several times slower.
+ *   - The rows of a group are offsets[e] .. offsets[e+1] of the sorted order
+ *     (int32 [G+1], device, non-decreasing from 0, as moe_route writes). Groups
+ *     may be empty. offsets[G] may be below P: rows from offsets[G] on belong to no
+ *     group and outputs keep what they held there. Values outside [0, P] are
+ *     taken as the nearest of the two.
+ *   - Outputs must not overlap inputs unless stated, and no output row may be
+ *     reached twice (row stride at least the width; a permutation of rows).
+ *   - stream must belong to the current device.
+ */
+#define MOE_BF16 0
+#define MOE_FP16 1
+#define MOE_FP32 2
+#define MOE_MAX_ADAPTERS 1024
+#define MOE_MAX_ADAPTER_RANK 128
+
+/*
+ * Product grouped by expert with 16-bit weights:
+ *     C[p][n] = sum_k A[row(p)][k] * W_e[n][k],  p in group e, n < N, k < K
+ *   A     dtype [a_rows][lda]; row(p) = a_row[p] when a_row (int32 [P]) is
+ *         non-null, else p. A row index outside [0, a_rows) reads as zeros (a masked row:
+ *         its C row is zeros), so no index leaves A. Indices may repeat.
+ *   W     dtype [G][N][K]
+ *   C     dtype or fp32 [P][ldc]
+ * With moe_route's sorted_token and offsets as a_row and offsets this is the
+ * expert projection of the routed tokens. An infinity or NaN reaches only the
+ * results whose sum it enters. Errors: MOE_EINVAL (null or misaligned
+ * pointer, unknown type, G, N or K < 1, P or a_rows < 0, a stride below the
+ * width), MOE_EUNSUPPORTED (G > MOE_MAX_EXPERTS, or 2^32 or more
+ * threads), MOE_EHIP. P == 0 enqueues nothing. One kernel; no workspace.
+ */
+int moe_grouped_gemm(int32_t dtype, const void *A, int64_t lda, int32_t a_rows, const int32_t *a_row,
+                     const int32_t *offsets, int32_t G, int32_t P, int32_t N, int32_t K, const void *W, void *C,
+                     int32_t c_dtype, int64_t ldc, hipStream_t stream);
+
+/*
+ * Gradient of moe_grouped_gemm's input rows:
+ *     dA[p][k] = sum_n dC[p][n] * W_e[n][k],  p in group e
+ * dC dtype [P][lddc], W as above, dA dtype or fp32 [P][ldda], by sorted row
+ * (moe_combine with w = NULL adds up the rows of each token when the forward
+ * call gathered them through a_row). Errors as moe_grouped_gemm.
+ */
+int moe_grouped_gemm_dgrad(int32_t dtype, const void *dC, int64_t lddc, const int32_t *offsets, int32_t G, int32_t P,
+                           int32_t N, int32_t K, const void *W, void *dA, int32_t da_dtype, int64_t ldda,
+                           hipStream_t stream);
+
+/*
+ * Gradient of moe_grouped_gemm's weights:
+ *     dW_e[n][k] = sum_{p in group e} dC[p][n] * A[row(p)][k]
+ * for every group; an empty group's dW is zeros. accumulate != 0 (fp32 dW
+ * only, else MOE_EUNSUPPORTED) adds to what dW holds. A, a_row, a_rows and dC
+ * as above; dW dtype or fp32 [G][N][K]. P == 0 still writes the zeros. Errors
+ * as moe_grouped_gemm.
+ */
+int moe_grouped_gemm_wgrad(int32_t dtype, const void *dC, int64_t lddc, const void *A, int64_t lda, int32_t a_rows,
+                           const int32_t *a_row, const int32_t *offsets, int32_t G, int32_t P, int32_t N, int32_t K,
+                           void *dW, int32_t dw_dtype, int32_t accumulate, hipStream_t stream);
+
+/*
+ * Weighted combine of expert rows:
+ *     y[t] = sum_j w[t][j] * o[pair_pos[t][j]] + add[t],  j < k
+ *   o         dtype [P][ldo]; pair_pos int32 [T][k] (as moe_route writes);
+ *             an entry outside [0, P) is a dropped pair and adds nothing
+ *   w         fp32 [T][k], or NULL for ones
+ *   add       dtype or fp32 (add_dtype) [T][ldadd], or NULL; may be y itself
+ *             when type and stride are equal
+ *   y         dtype or fp32 [T][ldy], d columns
+ * Slots are added in ascending order, `add` last. Errors: MOE_EINVAL,
+ * MOE_EUNSUPPORTED (T > MOE_MAX_TOKENS, k > MOE_MAX_EXPERTS), MOE_EHIP.
+ * T == 0 enqueues nothing.
+ */
+int moe_combine(int32_t dtype, const void *o, int64_t ldo, int32_t P, const int32_t *pair_pos, const float *w, int32_t T,
+                int32_t k, int32_t d, const void *add, int32_t add_dtype, int64_t ldadd, void *y, int32_t y_dtype,
+                int64_t ldy, hipStream_t stream);
+
+/*
+ * Gradient of moe_combine (that of `add` is dy itself):
+ *     d_o[pair_pos[t][j]] = w[t][j] * dy[t],  dw[t][j] = <dy[t], o[pair_pos[t][j]]>
+ * dy dtype [T][lddy]; d_o dtype [P][lddo], or NULL (not wanted); dw fp32
+ * [T][k], or NULL (then o is not read and may be NULL). Dropped pairs write
+ * no row of d_o and a dw of 0; rows of d_o that no pair names keep what they
+ * held. No two pairs may name the same row. Errors as moe_combine.
+ */
+int moe_combine_backward(int32_t dtype, const void *dy, int64_t lddy, const void *o, int64_t ldo, int32_t P,
+                         const int32_t *pair_pos, const float *w, int32_t T, int32_t k, int32_t d, void *d_o,
+                         int64_t lddo, float *dw, hipStream_t stream);
+
+/*
+ * Sort a batch's rows by adapter: rows[0 .. offsets[n]) are the rows with an
+ * adapter, grouped by it and ascending inside each group, then come the rows
+ * without one (row_adapter outside [0, n)). row_adapter int32 [T]; rows int32 [T];
+ * offsets int32 [n+1]. The result serves every projection of the batch. One
+ * kernel of one workgroup; T == 0 writes offsets alone. Errors: MOE_EINVAL,
+ * MOE_EUNSUPPORTED (n > MOE_MAX_ADAPTERS, T > MOE_MAX_TOKENS), MOE_EHIP.
+ */
+int moe_adapter_plan(const int32_t *row_adapter, int32_t T, int32_t n, int32_t *rows, int32_t *offsets, hipStream_t stream);
+
+/*
+ * Low-rank adapters of many requests at once, beside a shared projection:
+ *     y[t] = base[t] + scale[a] * B_a (A_a x[t]),  a = adapter of row t
+ * and y[t] = base[t] for rows without one.
+ *   x      dtype [T][ldx], K columns
+ *   A, B   dtype [n][r][K] and [n][N][r] (an adapter of lower rank: zeros in
+ *          its last rows of A or columns of B)
+ *   scale  fp32 [n], or NULL for ones
+ *   rows, offsets   as moe_adapter_plan writes (entries of rows outside
+ *          [0, T) are skipped)
+ *   base   the shared projection's output, of y's type [T][ldbase], or NULL
+ *          for zeros; may be y itself with the same stride
+ *   y      dtype or fp32 [T][ldy], N columns
+ * A_a x[t] is held in fp32. One kernel; no workspace. Errors: MOE_EINVAL,
+ * MOE_EUNSUPPORTED (r > MOE_MAX_ADAPTER_RANK, n > MOE_MAX_ADAPTERS,
+ * T > MOE_MAX_TOKENS), MOE_EHIP. T == 0 enqueues nothing.
+ */
+int moe_adapter_forward(int32_t dtype, const void *x, int64_t ldx, int32_t T, int32_t K, int32_t N, int32_t r, int32_t n,
+                        const void *A, const void *B, const float *scale, const int32_t *rows, const int32_t *offsets,
+                        const void *base, int64_t ldbase, void *y, int32_t y_dtype, int64_t ldy, hipStream_t stream);
+
+/*
+ * Gradients of moe_adapter_forward (that of base is dy itself):
+ *     g[t] = scale[a] * B_a^T dy[t]       dx[t] = dx_base[t] + A_a^T g[t]
+ *     dA_a = sum_t g[t] x[t]^T            dB_a  = scale[a] * sum_t dy[t] (A_a x[t])^T
+ *   dy     dtype [T][lddy], N columns; x, A, B, scale, rows, offsets as above
+ *   dx     dtype or fp32 [T][lddx], or NULL (not wanted). dx_base, of dx's
+ *          type: the shared projection's input gradient, or NULL for zeros;
+ *          may be dx itself with the same stride. Rows without an adapter get dx_base.
+ *   dA, dB dtype or fp32 (g_dtype) [n][r][K] and [n][N][r], each or NULL; an
+ *          adapter without rows gets zeros. accumulate != 0 (fp32 only, else
+ *          MOE_EUNSUPPORTED) adds to what they hold.
+ *   ws     moe_adapter_backward_workspace_bytes(T, r) bytes, 256-byte
+ *          aligned (needed with dA or dB)
+ * g and A_a x[t] are held in fp32. Errors as moe_adapter_forward, and
+ * MOE_EWORKSPACE.
+ */
+size_t moe_adapter_backward_workspace_bytes(int32_t T, int32_t r);
+int moe_adapter_backward(int32_t dtype, const void *dy, int64_t lddy, const void *x, int64_t ldx, int32_t T, int32_t K,
+                         int32_t N, int32_t r, int32_t n, const void *A, const void *B, const float *scale,
+                         const int32_t *rows, const int32_t *offsets, const void *dx_base, int64_t lddx_base, void *dx,
+                         int32_t dx_dtype, int64_t lddx, void *dA, void *dB, int32_t g_dtype, int32_t accumulate, void *ws,
+                         size_t ws_bytes, hipStream_t stream);
+
 /* Static description of a status code. Never NULL. */
 const char *moe_status_string(int status);
 
