@@ -37,7 +37,7 @@ __device__ __forceinline__ s8 load8(const uint16_t *p, int left, bool vec) {
 // (-1: rows without one), or n == 0.
 struct RowBlock { int e, at, n; };
 __device__ __forceinline__ RowBlock find_rows(const int32_t *offsets, int adapters, int T, int m) {
-  const GroupTile g = find_group(offsets, adapters, T, kAdRows, m);
+  const GroupTile g = find_group(offsets, adapters, T, kAdRows, [&](int) { return m; });
   RowBlock b;
   if (g.e >= 0) {
     b.e = g.e;

@@ -18,8 +18,19 @@ size_t size_of(int32_t t) { return t == MOE_FP32 ? 4 : 2; }
 bool typed(const void *p, int32_t t) { return aligned(p, size_of(t)); }
 // 16-byte units of rows of `width` 16-bit elements are aligned and whole
 bool units(const void *p, int64_t ld, int64_t width) { return aligned(p, 16) && ld % 8 == 0 && width % 8 == 0; }
-// runs of n elements of type t start at multiples of their own size
-bool runs(const void *p, int32_t t, int64_t ld, int n) { return aligned(p, n * size_of(t)) && ld % n == 0; }
+// 16-byte runs of rows of elements of type t are aligned
+bool runs(const void *p, int32_t t, int64_t ld) { return aligned(p, 16) && ld * size_of(t) % 16 == 0; }
+
+// The wide-tile kernel reads its operands through 31-bit byte offsets: from
+// the start of A where rows are gathered, of the tile's rows where they are
+// consecutive, of a group's rows for the weight gradient, and of a group's weights.
+bool wide_tiles(const GroupedArgs &a, GroupedMode mode) {
+  const int64_t limit = (int64_t)1 << 30;  // elements
+  if (!a.vec || a.a_rows < 1) return false;
+  if ((int64_t)a.N * a.K >= limit || 256 * a.ld_rows >= limit) return false;
+  if (mode == kWgrad) return a.P * a.ld_w < limit && a.a_rows * a.ld_rows < limit;
+  return !a.a_row || a.a_rows * a.ld_rows < limit;
+}
 
 int status(hipError_t e) {
   return e == hipSuccess ? MOE_OK : e == hipErrorInvalidConfiguration ? MOE_EUNSUPPORTED : MOE_EHIP;
@@ -66,7 +77,8 @@ int moe_grouped_gemm(int32_t dtype, const void *A, int64_t lda, int32_t a_rows, 
   a.ld_out = ldc;
   a.out_f32 = c_dtype == MOE_FP32;
   a.vec = units(A, lda, K) && units(W, K, K);
-  a.vec_out = runs(C, c_dtype, ldc, 4) && N % 4 == 0;
+  a.wide = wide_tiles(a, kFwd);
+  a.vec_out = runs(C, c_dtype, ldc) && N % 4 == 0;
   return status(launch_grouped(a, kFwd, dtype == MOE_FP16, stream));
 }
 
@@ -90,7 +102,8 @@ int moe_grouped_gemm_dgrad(int32_t dtype, const void *dC, int64_t lddc, const in
   a.ld_out = ldda;
   a.out_f32 = da_dtype == MOE_FP32;
   a.vec = units(dC, lddc, N) && units(W, K, K);
-  a.vec_out = runs(dA, da_dtype, ldda, 4) && K % 4 == 0;
+  a.wide = wide_tiles(a, kDgrad);
+  a.vec_out = runs(dA, da_dtype, ldda) && K % 4 == 0;
   return status(launch_grouped(a, kDgrad, dtype == MOE_FP16, stream));
 }
 
@@ -118,7 +131,8 @@ int moe_grouped_gemm_wgrad(int32_t dtype, const void *dC, int64_t lddc, const vo
   a.out_f32 = dw_dtype == MOE_FP32;
   a.accumulate = accumulate != 0;
   a.vec = units(dC, lddc, N) && units(A, lda, K);
-  a.vec_out = runs(dW, dw_dtype, K, 4);
+  a.wide = wide_tiles(a, kWgrad);
+  a.vec_out = runs(dW, dw_dtype, K) && K % 4 == 0;
   return status(launch_grouped(a, kWgrad, dtype == MOE_FP16, stream));
 }
 

@@ -44,6 +44,17 @@ __device__ __forceinline__ s4 read_lds_tr(const void *p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s4 *)p);
 }
 
+// Workgroups go to the eight XCDs in turn, each with an L2 of its own. Of
+// `total` work items, workgroup b takes the one that gives every XCD a run of
+// consecutive items (so those that share operands share an L2), or -1 when it has none.
+__device__ __forceinline__ int xcd_item(int b, int total) {
+  const int run = (total + 7) >> 3;
+  const int item = (b & 7) * run + (b >> 3);
+  return (b >> 3) < run && item < total ? item : -1;
+}
+// Workgroups to launch for at most `most` items.
+inline int64_t xcd_grid(int64_t most) { return (most + 7) / 8 * 8; }
+
 struct GroupTile {
   int e;       // group, or -1: no such tile
   int first;   // first sorted row of the group
@@ -57,9 +68,10 @@ struct GroupTile {
 // of ceil(G / 64) groups, a prefix sum over the lanes finds the lane that
 // holds tile m, and its run is walked again. Offsets outside [0, P] are
 // taken as the nearest of the two and a group that ends before it begins as empty, so that no
-// address formed from them leaves the caller's arrays. m must be the same
-// for the whole wave; with m < 0 only `total` is found.
-__device__ __forceinline__ GroupTile find_group(const int32_t *offsets, int G, int P, int rows, int m) {
+// address formed from them leaves the caller's arrays. m is pick(total tiles),
+// the same for the whole wave; with m < 0 only `total` is found.
+template <typename Pick>
+__device__ __forceinline__ GroupTile find_group(const int32_t *offsets, int G, int P, int rows, Pick pick) {
   const int lane = threadIdx.x & 63;
   const int run = (G + 63) >> 6;
   const int g0 = min(lane * run, G), g1 = min(g0 + run, G);
@@ -78,7 +90,8 @@ __device__ __forceinline__ GroupTile find_group(const int32_t *offsets, int G, i
     if (lane >= d) sum += v;
   }
   GroupTile t;
-  t.total = __shfl(sum, 63);
+  t.total = __builtin_amdgcn_readfirstlane(__shfl(sum, 63));
+  const int m = pick(t.total);
   t.e = -1;
   t.first = t.count = t.before = 0;
   const uint64_t past = __ballot(sum > m);
@@ -105,7 +118,6 @@ __device__ __forceinline__ GroupTile find_group(const int32_t *offsets, int G, i
   t.first = __builtin_amdgcn_readfirstlane(t.first);
   t.count = __builtin_amdgcn_readfirstlane(t.count);
   t.before = __builtin_amdgcn_readfirstlane(t.before);
-  t.total = __builtin_amdgcn_readfirstlane(t.total);
   return t;
 }
 

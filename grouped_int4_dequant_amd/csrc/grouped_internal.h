@@ -40,6 +40,7 @@ struct GroupedArgs {
   int32_t out_f32;          // out is fp32, else the operands' type
   int32_t accumulate;       // fp32 out only: out += result
   int32_t vec;              // every 16-byte unit of the operands is aligned and whole
+  int32_t wide;             // operand rows are at least eight elements wide where they lie across
   int32_t vec_out;          // four consecutive outputs may be stored at once
 };
 

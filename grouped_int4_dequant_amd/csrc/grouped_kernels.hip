@@ -12,6 +12,8 @@
 
 #include "grouped_device.h"
 
+#include <type_traits>
+
 namespace moe {
 namespace {
 
@@ -76,7 +78,7 @@ __global__ __launch_bounds__(64 * WI * WJ) void grouped_kernel(GroupedArgs a) {
     const int J = Mode == kFwd ? a.N : a.K;
     const int tj = (J + BJ - 1) / BJ;
     const int m = blockIdx.x / tj;
-    const GroupTile g = find_group(a.offsets, a.G, a.P, BI, m);
+    const GroupTile g = find_group(a.offsets, a.G, a.P, BI, [&](int) { return m; });
     if (g.e < 0) return;
     e = g.e;
     const int t = blockIdx.x - g.before * tj, mt = (g.count + BI - 1) / BI;
@@ -278,8 +280,372 @@ __global__ __launch_bounds__(64 * WI * WJ) void grouped_kernel(GroupedArgs a) {
   }
 }
 
+// ---------------------------------------------------------------- wide tiles
+// 256 x 256 outputs a workgroup of eight waves (each 128 x 64: 128 accumulator
+// registers a lane, two waves a SIMD), 64 r a step, two LDS buffers of a step's
+// operands. Both halves (32 r) of a step pass through registers one half ahead
+// of their use:
+//   half 0: its matrix instructions, and the LDS reads of half 1;
+//   meeting: the step's buffer is read out, the next step's has landed;
+//   half 1: its matrix instructions, the LDS reads of the next step's half 0, and
+//           the requests of the step after next into the buffer that is free.
+// So a request has one whole step (2048 cycles of matrix instructions a SIMD) to land,
+// and one meeting a step suffices.
+//
+// Output rows belong to the two row waves by alternating 16-row blocks, so
+// that a tile of fewer rows (TI < 8) has work for both. Output columns are
+// numbered so that a lane ends with 16 consecutive columns of a row in its four
+// blocks: block j, operand row m holds column 16 (m / 4) + 4 j + m % 4 of the wave's 64.
+constexpr int kTJ = 4;                  // 16 x 16 blocks of a wave along the columns
+constexpr int kWide = 256;              // rows and columns of a tile
+constexpr int kWideThreads = 512;
+constexpr int kUnits = 4;               // requests of a thread for each operand of a step, 16 bytes each
+constexpr int kWideBytes = 35 * 1024;   // an operand of a step with its gaps
+
+// Where 1 KiB piece c (what one wave requests at once) of an operand lies in LDS.
+// A straight operand's piece is eight rows of 128 bytes, whose 16-byte units are swapped
+// by row so that the 16 rows of a fetch fall on distinct banks. An across
+// operand's piece is two r of 512 bytes, in order; gaps between the pieces keep the
+// fetches, which take 32 or 4 x 8 bytes of 16 r at once, off each other's banks:
+// the row operand's (in the weight gradient, whose fetch h takes r = 16 h + 4 q4 + x) by 32 bytes a
+// piece, the column operand's by 16 and 128 bytes by the bits of c that vary in a fetch.
+template <int Mode>
+__device__ __forceinline__ constexpr int row_piece(int c) { return Mode == kWgrad ? c * 1056 : c * 1024; }
+template <int Mode>
+__device__ __forceinline__ constexpr int col_piece(int c) {
+  return Mode == kFwd ? c * 1024
+       : Mode == kDgrad ? c * 1024 + 16 * (c & 3) + 128 * ((c >> 2) & 1) + 256 * (c >> 3)
+                        : c * 1024 + 16 * (c & 1) + 128 * ((c >> 1) & 1) + 256 * (c >> 2);
+}
+__device__ __forceinline__ int row_unit(int row, int slot) { return slot ^ ((row >> 1) & 7); }
+__device__ __forceinline__ int col_unit(int row, int slot) { return slot ^ (((row >> 1) & 1) | ((row >> 4) & 3) << 1); }
+
+// Keeps a wave's common address in scalar registers, apart from the lanes'
+// offsets: left alone, the compiler holds their sums, two vector registers each.
+__device__ __forceinline__ const char *uniform(const char *p) {
+  asm("" : "+s"(p));
+  return p;
+}
+
+struct WideTile {
+  int e, first, count;  // group, its first row, its rows
+  int i0, j0, ni, nj;   // the tile's first output row and column, and how many exist from there
+  int nr;               // terms of the sum
+};
+
+template <typename Tr, int Mode, int TI, bool Gather>
+__device__ __forceinline__ void wide_body(const GroupedArgs &a, const WideTile t, uint8_t *s_l0, uint8_t *s_l1, uint8_t *s_r0, uint8_t *s_r1) {
+  constexpr bool kLAcross = Mode == kWgrad, kRAcross = Mode != kFwd;
+  constexpr int UL = kLAcross ? kUnits : (TI + 1) / 2;  // requests that hold rows of a tile of 32 TI
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wi = wave >> 2, wj = wave & 3;
+  const int p16 = lane & 15, q4 = lane >> 4;
+  const int steps = (t.nr + kBR - 1) / kBR;
+
+  // ---- requests. Unit i is piece 8 i + wave: a straight operand's tile rows
+  // 64 i + tid / 8, an across operand's r = 16 i + tid / 32 of the step. Rows and
+  // columns past the output's end repeat the last one; what they give is not stored.
+  // Byte offsets are 32 bits from a base that is the same for the workgroup.
+  const char *lbase, *rbase;
+  uint32_t lv[kLAcross ? 1 : UL], rv[kRAcross ? 1 : kUnits];
+  int lr, rr;  // this thread's r in a step: straight the first of its unit's eight, across that of unit 0
+  const int col_wave = col_piece<Mode>(wave);  // adds to col_piece(8 i)
+  if constexpr (kLAcross) {
+    lr = tid >> 5;
+    lbase = (const char *)(a.w + (int64_t)t.first * a.ld_w + t.i0);
+    lv[0] = (uint32_t)(lr * a.ld_w + min(8 * (tid & 31), t.ni - 8)) * 2;
+  } else {
+    const int row0 = tid >> 3;
+    lr = 8 * row_unit(row0, tid & 7);
+    constexpr bool gather = Mode == kFwd && Gather;
+    const int64_t from = gather ? 0 : (int64_t)t.first + t.i0;
+    const int64_t have = max((Mode == kFwd ? a.a_rows : a.P) - from, (int64_t)1);
+    lbase = (const char *)(a.rows + min(from, (int64_t)(Mode == kFwd ? a.a_rows : a.P) - 1) * a.ld_rows);
+#pragma unroll
+    for (int i = 0; i < UL; ++i) {
+      int row = min(row0 + 64 * i, t.ni - 1);
+      if (gather) row = a.a_row[t.first + t.i0 + row];
+      // a masked row reads some row that exists; its results are set to zero at the end
+      row = (int)min(max((int64_t)row, (int64_t)0), have - 1);
+      lv[i] = (uint32_t)(row * a.ld_rows + lr) * 2;
+    }
+  }
+  if constexpr (kRAcross) {
+    rr = tid >> 5;
+    const int col = min(8 * (tid & 31), t.nj - 8);
+    if constexpr (Mode == kWgrad) {
+      rbase = (const char *)(a.rows + t.j0);
+      rv[0] = (uint32_t)col * 2;
+    } else {
+      rbase = (const char *)(a.w + (int64_t)t.e * a.N * a.K + t.j0);
+      rv[0] = (uint32_t)(rr * a.ld_w + col) * 2;
+    }
+  } else {
+    const int row0 = tid >> 3;
+    rr = 8 * col_unit(row0, tid & 7);
+    rbase = (const char *)(a.w + ((int64_t)t.e * a.N + t.j0) * a.K);
+#pragma unroll
+    for (int j = 0; j < kUnits; ++j) rv[j] = (uint32_t)(min(row0 + 64 * j, t.nj - 1) * a.ld_w + rr) * 2;
+  }
+  int rrow[kUnits];  // weight gradient: the rows of A of the next requested step, -1: zeros
+  auto fetch_rows = [&](int s) __attribute__((always_inline)) {
+    if constexpr (Mode == kWgrad) {
+#pragma unroll
+      for (int i = 0; i < kUnits; ++i) {
+        const int r = s * kBR + rr + 16 * i, p = t.first + min(r, t.nr - 1);
+        const int at = Gather ? a.a_row[p] : p;
+        rrow[i] = (r < t.nr) & (at < a.a_rows) ? at : -1;
+      }
+    }
+  };
+  // `s` is the step asked for, lbase and rbase stand at it; `whole`: every r of the step exists
+  const int64_t lstep = kLAcross ? kBR * a.ld_w * 2 : kBR * 2, rstep = Mode == kDgrad ? kBR * a.ld_w * 2 : Mode == kFwd ? kBR * 2 : 0;
+  auto request_l = [&](int s, int i, uint8_t *buf, auto whole) __attribute__((always_inline)) {
+    const char *p = uniform(lbase + (kLAcross ? (lstep >> 2) * i : 0)) + lv[kLAcross ? 0 : i];
+    if constexpr (!decltype(whole)::value) p = s * kBR + lr + (kLAcross ? 16 * i : 0) < t.nr ? p : (const char *)&g_zeros;
+    load_lds16(p, buf + row_piece<Mode>(8 * i) + row_piece<Mode>(1) * wave);
+  };
+  auto request_r = [&](int s, int i, uint8_t *buf, auto whole) __attribute__((always_inline)) {
+    const char *p;
+    if constexpr (Mode == kWgrad) {
+      p = rbase + (uint64_t)((uint32_t)rrow[i] * (uint32_t)(a.ld_rows * 2) + rv[0]);
+      p = rrow[i] >= 0 ? p : (const char *)&g_zeros;
+    } else {
+      p = uniform(rbase + (kRAcross ? (rstep >> 2) * i : 0)) + rv[kRAcross ? 0 : i];
+      if constexpr (!decltype(whole)::value) p = s * kBR + rr + (kRAcross ? 16 * i : 0) < t.nr ? p : (const char *)&g_zeros;
+    }
+    load_lds16(p, buf + col_piece<Mode>(8 * i) + col_wave);
+  };
+
+  // ---- operand fetches: half ks, fetch h of it (r = 32 ks + 8 q4 + 4 h + x, in the weight
+  // gradient 32 ks + 16 h + 4 q4 + x: any order does, if both operands have it).
+  // Every address is a lane's part, kept in one register, and a constant: the constant
+  // and the lane's part of a piece's number add up without carries into each other's gap bits.
+  constexpr int kC0 = Mode == kWgrad ? 8 : 2;  // pieces from fetch h = 0 to h = 1
+  const int cl = (Mode == kWgrad ? 2 : 4) * q4 + (p16 >> 3), odd = 512 * ((p16 >> 2) & 1);
+  const int col_row = 16 * (p16 >> 2) + (p16 & 3);
+  uint32_t lat[2], rat[2];  // of half 0 and 1 (across operands: the first serves both)
+#pragma unroll
+  for (int ks = 0; ks < 2; ++ks) {
+    lat[ks] = kLAcross ? row_piece<Mode>(cl) + odd + 32 * wi + 8 * (p16 & 3)
+                       : (16 * wi + p16) * 128 + 16 * row_unit(p16, 4 * ks + q4);
+    rat[ks] = kRAcross ? col_piece<Mode>(cl) + odd + 128 * wj + 32 * (p16 & 3)
+                       : (64 * wj + col_row) * 128 + 16 * col_unit(col_row, 4 * ks + q4);
+    asm("" : "+v"(lat[ks]), "+v"(rat[ks]));
+  }
+  auto read_l = [&](const uint8_t *b, int i, int ks) __attribute__((always_inline)) {
+    if constexpr (kLAcross) {
+      const s4 x = read_lds_tr(b + lat[0] + row_piece<Mode>(16 * ks) + 64 * i), y = read_lds_tr(b + lat[0] + row_piece<Mode>(16 * ks + kC0) + 64 * i);
+      return s8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+    } else {
+      return *reinterpret_cast<const s8 *>(b + lat[ks] + 4096 * i);
+    }
+  };
+  auto read_r = [&](const uint8_t *b, int j, int ks) __attribute__((always_inline)) {
+    if constexpr (kRAcross) {
+      const s4 x = read_lds_tr(b + rat[0] + col_piece<Mode>(16 * ks) + 8 * j), y = read_lds_tr(b + rat[0] + col_piece<Mode>(16 * ks + kC0) + 8 * j);
+      return s8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+    } else {
+      return *reinterpret_cast<const s8 *>(b + rat[ks] + 512 * j);
+    }
+  };
+
+  f4 acc[TI][kTJ];
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int j = 0; j < kTJ; ++j) acc[i][j] = f4{0.f, 0.f, 0.f, 0.f};
+  s8 l0[TI], r0[kTJ], l1[TI], r1[kTJ];
+
+  // this wave's requests have landed and its reads are done, and everyone's behind the barrier
+  auto meet = [&]() __attribute__((always_inline)) {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  auto step = [&](int s, uint8_t *bl, uint8_t *br, uint8_t *nl, uint8_t *nr, auto whole) __attribute__((always_inline)) {
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): half 0's operands, before half 1's are asked for
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+      if (i == 0) {
+#pragma unroll
+        for (int j = 0; j < kTJ; ++j) r1[j] = read_r(br, j, 1);
+      }
+      l1[i] = read_l(bl, i, 1);
+#pragma unroll
+      for (int j = 0; j < kTJ; ++j) acc[i][j] = Tr::mfma(r0[j], l0[i], acc[i][j]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    meet();
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+      constexpr int per = (2 * kUnits + TI - 1) / TI;  // requests beside a row of blocks
+#pragma unroll
+      for (int y = i * per; y < (i + 1) * per; ++y) {
+        if (y < UL) request_l(s + 2, y, bl, whole); 
+        if (y >= kUnits && y < 2 * kUnits) request_r(s + 2, y - kUnits, br, whole);
+      }
+      if (i == 0) {
+#pragma unroll
+        for (int j = 0; j < kTJ; ++j) r0[j] = read_r(nr, j, 0);
+      }
+      l0[i] = read_l(nl, i, 0);
+#pragma unroll
+      for (int j = 0; j < kTJ; ++j) acc[i][j] = Tr::mfma(r1[j], l1[i], acc[i][j]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    lbase += lstep;
+    rbase += rstep;
+    fetch_rows(s + 3);
+  };
+  if (steps > 0) {
+    constexpr std::false_type partly{};
+    fetch_rows(0);
+#pragma unroll
+    for (int i = 0; i < UL; ++i) request_l(0, i, s_l0, partly);
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) request_r(0, i, s_r0, partly);
+    lbase += lstep;
+    rbase += rstep;
+    fetch_rows(1);
+#pragma unroll
+    for (int i = 0; i < UL; ++i) request_l(1, i, s_l1, partly);
+#pragma unroll
+    for (int i = 0; i < kUnits; ++i) request_r(1, i, s_r1, partly);
+    lbase += lstep;
+    rbase += rstep;
+    fetch_rows(2);
+    meet();
+#pragma unroll
+    for (int j = 0; j < kTJ; ++j) r0[j] = read_r(s_r0, j, 0);
+#pragma unroll
+    for (int i = 0; i < TI; ++i) l0[i] = read_l(s_l0, i, 0);
+    int s = 0;
+    for (; (s + 4) * kBR <= t.nr; s += 2) {  // steps s + 2 and s + 3 are whole
+      step(s, s_l0, s_r0, s_l1, s_r1, std::true_type{});
+      step(s + 1, s_l1, s_r1, s_l0, s_r0, std::true_type{});
+    }
+    for (; s < steps; s += 2) {  // an odd number of steps ends with one of zeros
+      step(s, s_l0, s_r0, s_l1, s_r1, partly);
+      step(s + 1, s_l1, s_r1, s_l0, s_r0, partly);
+    }
+  }
+
+  // ---- results
+  const int64_t obase = Mode == kWgrad ? (int64_t)t.e * a.N * a.K : (int64_t)t.first * a.ld_out;
+  const int64_t ldo = Mode == kWgrad ? a.K : a.ld_out;
+  if (Mode == kWgrad && a.accumulate && t.count == 0) return;
+  const int col = 64 * wj + 16 * q4;
+#pragma unroll
+  for (int i = 0; i < TI; ++i) {
+    const int row = 16 * (wi + 2 * i) + p16;
+    if (row >= t.ni || col >= t.nj) continue;
+    bool masked = false;
+    if (Mode == kFwd) {
+      const int at = a.a_row ? a.a_row[t.first + t.i0 + row] : t.first + t.i0 + row;
+      masked = at < 0 || at >= a.a_rows;
+    }
+    const int64_t at = obase + (int64_t)(t.i0 + row) * ldo + t.j0 + col;
+    f4 (&v)[kTJ] = acc[i];  // by reference: a copied row would be held as one vector of 16 through the loop, which spills
+    if (masked) {
+#pragma unroll
+      for (int c = 0; c < kTJ; ++c) v[c] = f4{0.f, 0.f, 0.f, 0.f};
+    }
+    if (a.out_f32) {
+      float *o = static_cast<float *>(a.out) + at;
+      if (a.vec_out && col + 16 <= t.nj) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (Mode == kWgrad && a.accumulate) v[c] += reinterpret_cast<const f4 *>(o)[c];
+          reinterpret_cast<f4 *>(o)[c] = v[c];
+        }
+      } else {
+#pragma unroll
+        for (int x = 0; x < 16; ++x)
+          if (col + x < t.nj) o[x] = v[x >> 2][x & 3] + (Mode == kWgrad && a.accumulate ? o[x] : 0.f);
+      }
+    } else {
+      uint16_t *o = static_cast<uint16_t *>(a.out) + at;
+      if (a.vec_out && col + 16 <= t.nj) {
+#pragma unroll
+        for (int c = 0; c < 4; c += 2) {
+          u4 w;
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            w[x] = (uint32_t)Tr::from(v[c + (x >> 1)][2 * (x & 1)]) | (uint32_t)Tr::from(v[c + (x >> 1)][2 * (x & 1) + 1]) << 16;
+          reinterpret_cast<u4 *>(o)[c >> 1] = w;
+        }
+      } else {
+#pragma unroll
+        for (int x = 0; x < 16; ++x)
+          if (col + x < t.nj) o[x] = Tr::from(v[x >> 2][x & 3]);
+      }
+    }
+  }
+}
+
+template <typename Tr, int Mode, bool Gather>
+__global__ __launch_bounds__(kWideThreads, 2) void grouped_wide_kernel(GroupedArgs a) {
+  // four arrays rather than one: the compiler then knows that reading one does not depend on a request into another
+  __shared__ __attribute__((aligned(16))) uint8_t s_l0[kWideBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t s_l1[kWideBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t s_r0[kWideBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t s_r1[kWideBytes];
+  WideTile t;
+  if constexpr (Mode == kWgrad) {
+    const int tj = (a.K + kWide - 1) / kWide, ti = (a.N + kWide - 1) / kWide;
+    const int per = ti * tj;
+    t.e = blockIdx.x / per;
+    const int x = blockIdx.x - t.e * per;
+    t.i0 = x / tj * kWide;
+    t.j0 = (x - x / tj * tj) * kWide;
+    t.first = min(max(a.offsets[t.e], 0), a.P);
+    t.count = max(min(max(a.offsets[t.e + 1], 0), a.P) - t.first, 0);
+    t.nr = t.count;
+    t.ni = a.N - t.i0;
+    t.nj = a.K - t.j0;
+    wide_body<Tr, Mode, 8, Gather>(a, t, s_l0, s_l1, s_r0, s_r1);
+  } else {
+    const int J = Mode == kFwd ? a.N : a.K;
+    const int tj = (J + kWide - 1) / kWide;
+    int item;
+    const GroupTile g = find_group(a.offsets, a.G, a.P, kWide, [&](int total) {
+      item = xcd_item(blockIdx.x, total * tj);
+      return item < 0 ? -1 : item / tj;
+    });
+    if (g.e < 0) return;
+    t.e = g.e;
+    const int x = item - g.before * tj, mt = (g.count + kWide - 1) / kWide;
+    const int jt = x / mt;
+    t.i0 = (x - jt * mt) * kWide;
+    t.j0 = jt * kWide;
+    t.first = g.first;
+    t.count = g.count;
+    t.ni = t.count - t.i0;
+    t.nj = J - t.j0;
+    t.nr = Mode == kFwd ? a.K : a.N;
+    if (t.ni > 128) wide_body<Tr, Mode, 8, Gather>(a, t, s_l0, s_l1, s_r0, s_r1);
+    else if (t.ni > 64) wide_body<Tr, Mode, 4, Gather>(a, t, s_l0, s_l1, s_r0, s_r1);
+    else wide_body<Tr, Mode, 2, Gather>(a, t, s_l0, s_l1, s_r0, s_r1);
+  }
+}
+
 template <typename Tr, int Mode, bool Vec>
 hipError_t launch(const GroupedArgs &a, hipStream_t s) {
+  if constexpr (Vec) {
+    const int64_t used = a.G < a.P ? a.G : a.P;
+    const int64_t tiles = Mode == kWgrad ? (int64_t)a.G * cdiv(a.N, kWide) * cdiv(a.K, kWide)
+                                         : (a.P + used * (kWide - 1)) / kWide * cdiv(Mode == kFwd ? a.N : a.K, kWide);
+    if (a.a_rows > 0 && a.wide) {
+      if (!grid_fits(xcd_grid(tiles), kWideThreads) || tiles >= INT32_MAX / 2) return hipErrorInvalidConfiguration;
+      const dim3 grid((unsigned)xcd_grid(tiles));
+      if (Mode != kDgrad && a.a_row) grouped_wide_kernel<Tr, Mode, Mode != kDgrad><<<grid, kWideThreads, 0, s>>>(a);
+      else grouped_wide_kernel<Tr, Mode, false><<<grid, kWideThreads, 0, s>>>(a);
+      return hipGetLastError();
+    }
+  }
   constexpr int BI = 128, BJ = 128;
   int64_t tiles;
   if (Mode == kWgrad) {
