@@ -38,6 +38,15 @@ __device__ __forceinline__ void load_lds16(const void *src, void *dst) {
                                    (__attribute__((address_space(3))) void *)dst, 16, 0, 0);
 }
 
+// Orders what a wave's lanes write to LDS before and read from it behind this
+// point. The hardware runs a wave's LDS accesses in order; this keeps the compiler from
+// moving them, or from running the lanes of a branch past it one side after the other.
+__device__ __forceinline__ void wave_sync() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_wave_barrier();
+  asm volatile("" ::: "memory");
+}
+
 // Lane p of each 16-lane group names four 16-bit elements of row p / 4 of a
 // 4 x 16 block (columns 4 (p % 4) ..); it receives column p, rows 0..3.
 __device__ __forceinline__ s4 read_lds_tr(const void *p) {

@@ -334,8 +334,11 @@ struct WideTile {
 };
 
 template <typename Tr, int Mode, int TI, bool Gather>
-__device__ __forceinline__ void wide_body(const GroupedArgs &a, const WideTile t, uint8_t *s_l0, uint8_t *s_l1, uint8_t *s_r0, uint8_t *s_r1) {
-  constexpr bool kLAcross = Mode == kWgrad, kRAcross = Mode != kFwd;
+__device__ __forceinline__ void wide_body(const GroupedArgs &a, const WideTile t, uint8_t *s_l0, uint8_t *s_l1, uint8_t *s_r0, uint8_t *s_r1, uint8_t *s_out) {
+#ifndef NEAR
+#define NEAR (Mode == kWgrad)
+#endif
+  constexpr bool kLAcross = Mode == kWgrad, kRAcross = Mode != kFwd, kNear = NEAR;
   constexpr int UL = kLAcross ? kUnits : (TI + 1) / 2;  // requests that hold rows of a tile of 32 TI
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -395,7 +398,7 @@ __device__ __forceinline__ void wide_body(const GroupedArgs &a, const WideTile t
       for (int i = 0; i < kUnits; ++i) {
         const int r = s * kBR + rr + 16 * i, p = t.first + min(r, t.nr - 1);
         const int at = Gather ? a.a_row[p] : p;
-        rrow[i] = (r < t.nr) & (at < a.a_rows) ? at : -1;
+        rrow[i] = ((r < t.nr) & (at < a.a_rows)) ? at : -1;
       }
     }
   };
@@ -500,8 +503,36 @@ __device__ __forceinline__ void wide_body(const GroupedArgs &a, const WideTile t
     rbase += rstep;
     fetch_rows(s + 3);
   };
+  // The weight gradient's variant of a step. Both its operands come from LDS
+  // in pairs of 8-byte fetches, and a half held ahead spills; here the next
+  // step is requested at the step's begin, operands are fetched one row of blocks ahead, and the meeting
+  // stands at the end.
+  auto step_near = [&](int s, uint8_t *bl, uint8_t *br, uint8_t *nl, uint8_t *nr, auto whole) __attribute__((always_inline)) {
+    s8 l[2], r[2][kTJ];
+#pragma unroll
+    for (int j = 0; j < kTJ; ++j) r[0][j] = read_r(br, j, 0);
+    l[0] = read_l(bl, 0, 0);
+#pragma unroll
+    for (int x = 0; x < 2 * TI; ++x) {
+      const int ks = x / TI, i = x % TI;
+      if (x < UL) request_l(s + 1, x, nl, whole);
+      else if (x < UL + kUnits) request_r(s + 1, x - UL, nr, whole);
+      if (x + 1 < 2 * TI) l[(x + 1) & 1] = read_l(bl, (x + 1) % TI, (x + 1) / TI);
+      if (x == TI - 2) {
+#pragma unroll
+        for (int j = 0; j < kTJ; ++j) r[1][j] = read_r(br, j, 1);
+      }
+#pragma unroll
+      for (int j = 0; j < kTJ; ++j) acc[i][j] = Tr::mfma(r[ks][j], l[x & 1], acc[i][j]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    lbase += lstep;
+    rbase += rstep;
+    fetch_rows(s + 2);
+    meet();
+  };
+  constexpr std::false_type partly{};
   if (steps > 0) {
-    constexpr std::false_type partly{};
     fetch_rows(0);
 #pragma unroll
     for (int i = 0; i < UL; ++i) request_l(0, i, s_l0, partly);
@@ -510,78 +541,115 @@ __device__ __forceinline__ void wide_body(const GroupedArgs &a, const WideTile t
     lbase += lstep;
     rbase += rstep;
     fetch_rows(1);
+    if constexpr (kNear) {
+      meet();
+      int s = 0;
+      for (; (s + 3) * kBR <= t.nr; s += 2) {  // steps s + 1 and s + 2 are whole
+        step_near(s, s_l0, s_r0, s_l1, s_r1, std::true_type{});
+        step_near(s + 1, s_l1, s_r1, s_l0, s_r0, std::true_type{});
+      }
+      for (; s < steps; s += 2) {  // an odd number of steps ends with one of zeros
+        step_near(s, s_l0, s_r0, s_l1, s_r1, partly);
+        step_near(s + 1, s_l1, s_r1, s_l0, s_r0, partly);
+      }
+    } else {
 #pragma unroll
-    for (int i = 0; i < UL; ++i) request_l(1, i, s_l1, partly);
+      for (int i = 0; i < UL; ++i) request_l(1, i, s_l1, partly);
 #pragma unroll
-    for (int i = 0; i < kUnits; ++i) request_r(1, i, s_r1, partly);
-    lbase += lstep;
-    rbase += rstep;
-    fetch_rows(2);
-    meet();
+      for (int i = 0; i < kUnits; ++i) request_r(1, i, s_r1, partly);
+      lbase += lstep;
+      rbase += rstep;
+      fetch_rows(2);
+      meet();
 #pragma unroll
-    for (int j = 0; j < kTJ; ++j) r0[j] = read_r(s_r0, j, 0);
+      for (int j = 0; j < kTJ; ++j) r0[j] = read_r(s_r0, j, 0);
 #pragma unroll
-    for (int i = 0; i < TI; ++i) l0[i] = read_l(s_l0, i, 0);
-    int s = 0;
-    for (; (s + 4) * kBR <= t.nr; s += 2) {  // steps s + 2 and s + 3 are whole
-      step(s, s_l0, s_r0, s_l1, s_r1, std::true_type{});
-      step(s + 1, s_l1, s_r1, s_l0, s_r0, std::true_type{});
-    }
-    for (; s < steps; s += 2) {  // an odd number of steps ends with one of zeros
-      step(s, s_l0, s_r0, s_l1, s_r1, partly);
-      step(s + 1, s_l1, s_r1, s_l0, s_r0, partly);
+      for (int i = 0; i < TI; ++i) l0[i] = read_l(s_l0, i, 0);
+      int s = 0;
+      for (; (s + 4) * kBR <= t.nr; s += 2) {  // steps s + 2 and s + 3 are whole
+        step(s, s_l0, s_r0, s_l1, s_r1, std::true_type{});
+        step(s + 1, s_l1, s_r1, s_l0, s_r0, std::true_type{});
+      }
+      for (; s < steps; s += 2) {
+        step(s, s_l0, s_r0, s_l1, s_r1, partly);
+        step(s + 1, s_l1, s_r1, s_l0, s_r0, partly);
+      }
     }
   }
 
-  // ---- results
+  // ---- results. A wave passes 16 rows of its columns at a time through 2 KiB of
+  // LDS of its own, so that it stores whole 128-byte lines (from the accumulators' places it
+  // would store 16 bytes of each line at once, which ran at 2.5 TB/s where lines run at
+  // twice that). 16-byte unit u of row r lies in slot u ^ (r & 7).
   const int64_t obase = Mode == kWgrad ? (int64_t)t.e * a.N * a.K : (int64_t)t.first * a.ld_out;
   const int64_t ldo = Mode == kWgrad ? a.K : a.ld_out;
   if (Mode == kWgrad && a.accumulate && t.count == 0) return;
-  const int col = 64 * wj + 16 * q4;
+  uint8_t *mine = s_out + 2048 * wave;
 #pragma unroll
   for (int i = 0; i < TI; ++i) {
-    const int row = 16 * (wi + 2 * i) + p16;
-    if (row >= t.ni || col >= t.nj) continue;
+    const int row0 = 16 * (wi + 2 * i);
+    if (row0 >= t.ni) break;
     bool masked = false;
     if (Mode == kFwd) {
-      const int at = a.a_row ? a.a_row[t.first + t.i0 + row] : t.first + t.i0 + row;
+      int at = t.first + t.i0 + min(row0 + p16, t.ni - 1);
+      if (Gather) at = a.a_row[at];
       masked = at < 0 || at >= a.a_rows;
     }
-    const int64_t at = obase + (int64_t)(t.i0 + row) * ldo + t.j0 + col;
     f4 (&v)[kTJ] = acc[i];  // by reference: a copied row would be held as one vector of 16 through the loop, which spills
     if (masked) {
 #pragma unroll
       for (int c = 0; c < kTJ; ++c) v[c] = f4{0.f, 0.f, 0.f, 0.f};
     }
     if (a.out_f32) {
-      float *o = static_cast<float *>(a.out) + at;
-      if (a.vec_out && col + 16 <= t.nj) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (Mode == kWgrad && a.accumulate) v[c] += reinterpret_cast<const f4 *>(o)[c];
-          reinterpret_cast<f4 *>(o)[c] = v[c];
+      for (int h = 0; h < 2; ++h) {  // columns 32 h ..: the lanes of two q4
+        if (q4 >> 1 == h) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) *reinterpret_cast<f4 *>(mine + 128 * p16 + 16 * ((4 * (q4 & 1) + c) ^ (p16 & 7))) = v[c];
         }
-      } else {
+        wave_sync();
 #pragma unroll
-        for (int x = 0; x < 16; ++x)
-          if (col + x < t.nj) o[x] = v[x >> 2][x & 3] + (Mode == kWgrad && a.accumulate ? o[x] : 0.f);
+        for (int x = 0; x < 2; ++x) {
+          const int r = 8 * x + (lane >> 3), col = 64 * wj + 32 * h + 4 * (lane & 7);
+          f4 w = *reinterpret_cast<const f4 *>(mine + 128 * r + 16 * ((lane & 7) ^ (r & 7)));
+          if (row0 + r >= t.ni || col >= t.nj) continue;
+          float *o = static_cast<float *>(a.out) + obase + (int64_t)(t.i0 + row0 + r) * ldo + t.j0 + col;
+          if (a.vec_out && col + 4 <= t.nj) {
+            if (Mode == kWgrad && a.accumulate) w += *reinterpret_cast<const f4 *>(o);
+            *reinterpret_cast<f4 *>(o) = w;
+          } else {
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              if (col + y < t.nj) o[y] = w[y] + (Mode == kWgrad && a.accumulate ? o[y] : 0.f);
+          }
+        }
+        wave_sync();
       }
     } else {
-      uint16_t *o = static_cast<uint16_t *>(a.out) + at;
-      if (a.vec_out && col + 16 <= t.nj) {
 #pragma unroll
-        for (int c = 0; c < 4; c += 2) {
-          u4 w;
+      for (int c = 0; c < 4; c += 2) {
+        u4 w;
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            w[x] = (uint32_t)Tr::from(v[c + (x >> 1)][2 * (x & 1)]) | (uint32_t)Tr::from(v[c + (x >> 1)][2 * (x & 1) + 1]) << 16;
-          reinterpret_cast<u4 *>(o)[c >> 1] = w;
-        }
-      } else {
-#pragma unroll
-        for (int x = 0; x < 16; ++x)
-          if (col + x < t.nj) o[x] = Tr::from(v[x >> 2][x & 3]);
+        for (int x = 0; x < 4; ++x)
+          w[x] = (uint32_t)Tr::from(v[c + (x >> 1)][2 * (x & 1)]) | (uint32_t)Tr::from(v[c + (x >> 1)][2 * (x & 1) + 1]) << 16;
+        *reinterpret_cast<u4 *>(mine + 128 * p16 + 16 * ((2 * q4 + (c >> 1)) ^ (p16 & 7))) = w;
       }
+      wave_sync();
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int r = 8 * x + (lane >> 3), col = 64 * wj + 8 * (lane & 7);
+        const s8 w = *reinterpret_cast<const s8 *>(mine + 128 * r + 16 * ((lane & 7) ^ (r & 7)));
+        if (row0 + r >= t.ni || col >= t.nj) continue;
+        uint16_t *o = static_cast<uint16_t *>(a.out) + obase + (int64_t)(t.i0 + row0 + r) * ldo + t.j0 + col;
+        if (a.vec_out && col + 8 <= t.nj) {
+          *reinterpret_cast<s8 *>(o) = w;
+        } else {
+#pragma unroll
+          for (int y = 0; y < 8; ++y)
+            if (col + y < t.nj) o[y] = (uint16_t)w[y];
+        }
+      }
+      wave_sync();
     }
   }
 }
@@ -593,6 +661,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void grouped_wide_kernel(GroupedAr
   __shared__ __attribute__((aligned(16))) uint8_t s_l1[kWideBytes];
   __shared__ __attribute__((aligned(16))) uint8_t s_r0[kWideBytes];
   __shared__ __attribute__((aligned(16))) uint8_t s_r1[kWideBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t s_out[kWideThreads / 64 * 2048];
   WideTile t;
   if constexpr (Mode == kWgrad) {
     const int tj = (a.K + kWide - 1) / kWide, ti = (a.N + kWide - 1) / kWide;
@@ -606,7 +675,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void grouped_wide_kernel(GroupedAr
     t.nr = t.count;
     t.ni = a.N - t.i0;
     t.nj = a.K - t.j0;
-    wide_body<Tr, Mode, 8, Gather>(a, t, s_l0, s_l1, s_r0, s_r1);
+    wide_body<Tr, Mode, 8, Gather>(a, t, s_l0, s_l1, s_r0, s_r1, s_out);
   } else {
     const int J = Mode == kFwd ? a.N : a.K;
     const int tj = (J + kWide - 1) / kWide;
@@ -626,9 +695,9 @@ __global__ __launch_bounds__(kWideThreads, 2) void grouped_wide_kernel(GroupedAr
     t.ni = t.count - t.i0;
     t.nj = J - t.j0;
     t.nr = Mode == kFwd ? a.K : a.N;
-    if (t.ni > 128) wide_body<Tr, Mode, 8, Gather>(a, t, s_l0, s_l1, s_r0, s_r1);
-    else if (t.ni > 64) wide_body<Tr, Mode, 4, Gather>(a, t, s_l0, s_l1, s_r0, s_r1);
-    else wide_body<Tr, Mode, 2, Gather>(a, t, s_l0, s_l1, s_r0, s_r1);
+    if (t.ni > 128) wide_body<Tr, Mode, 8, Gather>(a, t, s_l0, s_l1, s_r0, s_r1, s_out);
+    else if (t.ni > 64) wide_body<Tr, Mode, 4, Gather>(a, t, s_l0, s_l1, s_r0, s_r1, s_out);
+    else wide_body<Tr, Mode, 2, Gather>(a, t, s_l0, s_l1, s_r0, s_r1, s_out);
   }
 }
 
