@@ -300,7 +300,6 @@ constexpr int kTJ = 4;                  // 16 x 16 blocks of a wave along the co
 constexpr int kWide = 256;              // rows and columns of a tile
 constexpr int kWideThreads = 512;
 constexpr int kUnits = 4;               // requests of a thread for each operand of a step, 16 bytes each
-constexpr int kWideBytes = 35 * 1024;   // an operand of a step with its gaps
 
 // Where 1 KiB piece c (what one wave requests at once) of an operand lies in LDS.
 // A straight operand's piece is eight rows of 128 bytes, whose 16-byte units are swapped
@@ -333,12 +332,10 @@ struct WideTile {
   int nr;               // terms of the sum
 };
 
-template <typename Tr, int Mode, int TI, bool Gather>
-__device__ __forceinline__ void wide_body(const GroupedArgs &a, const WideTile t, uint8_t *s_l0, uint8_t *s_l1, uint8_t *s_r0, uint8_t *s_r1, uint8_t *s_out) {
-#ifndef NEAR
-#define NEAR (Mode == kWgrad)
-#endif
-  constexpr bool kLAcross = Mode == kWgrad, kRAcross = Mode != kFwd, kNear = NEAR;
+template <typename Tr, int Mode, int TI, bool Gather, int Stages>
+__device__ __forceinline__ void wide_body(const GroupedArgs &a, const WideTile t, uint8_t *s_l0, uint8_t *s_l1, uint8_t *s_l2,
+                                          uint8_t *s_r0, uint8_t *s_r1, uint8_t *s_r2) {
+  constexpr bool kLAcross = Mode == kWgrad, kRAcross = Mode != kFwd, kNear = Mode == kWgrad;
   constexpr int UL = kLAcross ? kUnits : (TI + 1) / 2;  // requests that hold rows of a tile of 32 TI
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -461,13 +458,18 @@ __device__ __forceinline__ void wide_body(const GroupedArgs &a, const WideTile t
     for (int j = 0; j < kTJ; ++j) acc[i][j] = f4{0.f, 0.f, 0.f, 0.f};
   s8 l0[TI], r0[kTJ], l1[TI], r1[kTJ];
 
-  // this wave's requests have landed and its reads are done, and everyone's behind the barrier
-  auto meet = [&]() __attribute__((always_inline)) {
+  // This wave's requests but the last `open` steps' have landed and its reads are done, and
+  // everyone's behind the barrier.
+  constexpr int kAsks = UL + kUnits;
+  auto meet = [&](auto open) __attribute__((always_inline)) {
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+    __builtin_amdgcn_s_waitcnt(0x0070 | decltype(open)::value * kAsks);  // vmcnt, lgkmcnt(0)
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   };
+  constexpr std::integral_constant<int, 0> none{};
+  constexpr std::integral_constant<int, Stages - 2> ahead{};
+  // One step out of buffers bl, br; nl, nr hold the next.
   auto step = [&](int s, uint8_t *bl, uint8_t *br, uint8_t *nl, uint8_t *nr, auto whole) __attribute__((always_inline)) {
     __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): half 0's operands, before half 1's are asked for
 #pragma unroll
@@ -481,14 +483,14 @@ __device__ __forceinline__ void wide_body(const GroupedArgs &a, const WideTile t
       for (int j = 0; j < kTJ; ++j) acc[i][j] = Tr::mfma(r0[j], l0[i], acc[i][j]);
       __builtin_amdgcn_sched_barrier(0);
     }
-    meet();
+    meet(ahead);
 #pragma unroll
     for (int i = 0; i < TI; ++i) {
-      constexpr int per = (2 * kUnits + TI - 1) / TI;  // requests beside a row of blocks
+      constexpr int per = (kAsks + TI - 1) / TI;  // requests beside a row of blocks
 #pragma unroll
       for (int y = i * per; y < (i + 1) * per; ++y) {
-        if (y < UL) request_l(s + 2, y, bl, whole); 
-        if (y >= kUnits && y < 2 * kUnits) request_r(s + 2, y - kUnits, br, whole);
+        if (y < UL) request_l(s + Stages, y, bl, whole);
+        else if (y < kAsks) request_r(s + Stages, y - UL, br, whole);
       }
       if (i == 0) {
 #pragma unroll
@@ -501,7 +503,6 @@ __device__ __forceinline__ void wide_body(const GroupedArgs &a, const WideTile t
     }
     lbase += lstep;
     rbase += rstep;
-    fetch_rows(s + 3);
   };
   // The weight gradient's variant of a step. Both its operands come from LDS
   // in pairs of 8-byte fetches, and a half held ahead spills; here the next
@@ -529,7 +530,7 @@ __device__ __forceinline__ void wide_body(const GroupedArgs &a, const WideTile t
     lbase += lstep;
     rbase += rstep;
     fetch_rows(s + 2);
-    meet();
+    meet(none);
   };
   constexpr std::false_type partly{};
   if (steps > 0) {
@@ -542,7 +543,7 @@ __device__ __forceinline__ void wide_body(const GroupedArgs &a, const WideTile t
     rbase += rstep;
     fetch_rows(1);
     if constexpr (kNear) {
-      meet();
+      meet(none);
       int s = 0;
       for (; (s + 3) * kBR <= t.nr; s += 2) {  // steps s + 1 and s + 2 are whole
         step_near(s, s_l0, s_r0, s_l1, s_r1, std::true_type{});
@@ -554,28 +555,35 @@ __device__ __forceinline__ void wide_body(const GroupedArgs &a, const WideTile t
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < UL; ++i) request_l(1, i, s_l1, partly);
+      for (int x = 1; x < Stages; ++x) {
 #pragma unroll
-      for (int i = 0; i < kUnits; ++i) request_r(1, i, s_r1, partly);
-      lbase += lstep;
-      rbase += rstep;
-      fetch_rows(2);
-      meet();
+        for (int i = 0; i < UL; ++i) request_l(x, i, x == 1 ? s_l1 : s_l2, partly);
+#pragma unroll
+        for (int i = 0; i < kUnits; ++i) request_r(x, i, x == 1 ? s_r1 : s_r2, partly);
+        lbase += lstep;
+        rbase += rstep;
+      }
+      meet(std::integral_constant<int, Stages - 1>{});
 #pragma unroll
       for (int j = 0; j < kTJ; ++j) r0[j] = read_r(s_r0, j, 0);
 #pragma unroll
       for (int i = 0; i < TI; ++i) l0[i] = read_l(s_l0, i, 0);
+      auto round = [&](int s, auto whole) __attribute__((always_inline)) {
+        if constexpr (Stages == 2) {
+          step(s, s_l0, s_r0, s_l1, s_r1, whole);
+          step(s + 1, s_l1, s_r1, s_l0, s_r0, whole);
+        } else {
+          step(s, s_l0, s_r0, s_l1, s_r1, whole);
+          step(s + 1, s_l1, s_r1, s_l2, s_r2, whole);
+          step(s + 2, s_l2, s_r2, s_l0, s_r0, whole);
+        }
+      };
       int s = 0;
-      for (; (s + 4) * kBR <= t.nr; s += 2) {  // steps s + 2 and s + 3 are whole
-        step(s, s_l0, s_r0, s_l1, s_r1, std::true_type{});
-        step(s + 1, s_l1, s_r1, s_l0, s_r0, std::true_type{});
-      }
-      for (; s < steps; s += 2) {
-        step(s, s_l0, s_r0, s_l1, s_r1, partly);
-        step(s + 1, s_l1, s_r1, s_l0, s_r0, partly);
-      }
+      for (; (s + 2 * Stages) * kBR <= t.nr; s += Stages) round(s, std::true_type{});  // the steps it asks for are whole
+      for (; s < steps; s += Stages) round(s, partly);  // a part of a round ends with steps of zeros
     }
   }
+  meet(none);  // the buffers are free
 
   // ---- results. A wave passes 16 rows of its columns at a time through 2 KiB of
   // LDS of its own, so that it stores whole 128-byte lines (from the accumulators' places it
@@ -584,7 +592,7 @@ __device__ __forceinline__ void wide_body(const GroupedArgs &a, const WideTile t
   const int64_t obase = Mode == kWgrad ? (int64_t)t.e * a.N * a.K : (int64_t)t.first * a.ld_out;
   const int64_t ldo = Mode == kWgrad ? a.K : a.ld_out;
   if (Mode == kWgrad && a.accumulate && t.count == 0) return;
-  uint8_t *mine = s_out + 2048 * wave;
+  uint8_t *mine = s_l0 + 2048 * wave;
 #pragma unroll
   for (int i = 0; i < TI; ++i) {
     const int row0 = 16 * (wi + 2 * i);
@@ -654,14 +662,17 @@ __device__ __forceinline__ void wide_body(const GroupedArgs &a, const WideTile t
   }
 }
 
-template <typename Tr, int Mode, bool Gather>
+// Rows: of a tile, 256 or 128. Tiles of 128 rows leave LDS for a third buffer.
+template <typename Tr, int Mode, bool Gather, int Rows>
 __global__ __launch_bounds__(kWideThreads, 2) void grouped_wide_kernel(GroupedArgs a) {
-  // four arrays rather than one: the compiler then knows that reading one does not depend on a request into another
-  __shared__ __attribute__((aligned(16))) uint8_t s_l0[kWideBytes];
-  __shared__ __attribute__((aligned(16))) uint8_t s_l1[kWideBytes];
-  __shared__ __attribute__((aligned(16))) uint8_t s_r0[kWideBytes];
-  __shared__ __attribute__((aligned(16))) uint8_t s_r1[kWideBytes];
-  __shared__ __attribute__((aligned(16))) uint8_t s_out[kWideThreads / 64 * 2048];
+  constexpr int kLBytes = row_piece<Mode>(Rows / 8), kRBytes = col_piece<Mode>(kWide / 8), Stages = Rows == 256 ? 2 : 3;
+  // arrays of their own rather than one: the compiler then knows that reading one does not depend on a request into another
+  __shared__ __attribute__((aligned(16))) uint8_t s_l0[kLBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t s_l1[kLBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t s_l2[Stages == 3 ? kLBytes : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t s_r0[kRBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t s_r1[kRBytes];
+  __shared__ __attribute__((aligned(16))) uint8_t s_r2[Stages == 3 ? kRBytes : 16];
   WideTile t;
   if constexpr (Mode == kWgrad) {
     const int tj = (a.K + kWide - 1) / kWide, ti = (a.N + kWide - 1) / kWide;
@@ -675,44 +686,56 @@ __global__ __launch_bounds__(kWideThreads, 2) void grouped_wide_kernel(GroupedAr
     t.nr = t.count;
     t.ni = a.N - t.i0;
     t.nj = a.K - t.j0;
-    wide_body<Tr, Mode, 8, Gather>(a, t, s_l0, s_l1, s_r0, s_r1, s_out);
+    wide_body<Tr, Mode, 8, Gather, Stages>(a, t, s_l0, s_l1, s_l2, s_r0, s_r1, s_r2);
   } else {
     const int J = Mode == kFwd ? a.N : a.K;
     const int tj = (J + kWide - 1) / kWide;
     int item;
-    const GroupTile g = find_group(a.offsets, a.G, a.P, kWide, [&](int total) {
+    const GroupTile g = find_group(a.offsets, a.G, a.P, Rows, [&](int total) {
       item = xcd_item(blockIdx.x, total * tj);
       return item < 0 ? -1 : item / tj;
     });
     if (g.e < 0) return;
     t.e = g.e;
-    const int x = item - g.before * tj, mt = (g.count + kWide - 1) / kWide;
+    const int x = item - g.before * tj, mt = (g.count + Rows - 1) / Rows;
     const int jt = x / mt;
-    t.i0 = (x - jt * mt) * kWide;
+    t.i0 = (x - jt * mt) * Rows;
     t.j0 = jt * kWide;
     t.first = g.first;
     t.count = g.count;
     t.ni = t.count - t.i0;
     t.nj = J - t.j0;
     t.nr = Mode == kFwd ? a.K : a.N;
-    if (t.ni > 128) wide_body<Tr, Mode, 8, Gather>(a, t, s_l0, s_l1, s_r0, s_r1, s_out);
-    else if (t.ni > 64) wide_body<Tr, Mode, 4, Gather>(a, t, s_l0, s_l1, s_r0, s_r1, s_out);
-    else wide_body<Tr, Mode, 2, Gather>(a, t, s_l0, s_l1, s_r0, s_r1, s_out);
+    if (Rows == 256 && t.ni > 128) wide_body<Tr, Mode, 8, Gather, Stages>(a, t, s_l0, s_l1, s_l2, s_r0, s_r1, s_r2);
+    else if (t.ni > 64) wide_body<Tr, Mode, 4, Gather, Stages>(a, t, s_l0, s_l1, s_l2, s_r0, s_r1, s_r2);
+    else wide_body<Tr, Mode, 2, Gather, Stages>(a, t, s_l0, s_l1, s_l2, s_r0, s_r1, s_r2);
   }
+}
+
+template <typename Tr, int Mode, int Rows>
+hipError_t launch_wide(const GroupedArgs &a, hipStream_t s) {
+  const int64_t used = a.G < a.P ? a.G : a.P;  // groups that can have rows
+  const int64_t tiles = Mode == kWgrad ? (int64_t)a.G * cdiv(a.N, kWide) * cdiv(a.K, kWide)
+                                       : (a.P + used * (Rows - 1)) / Rows * cdiv(Mode == kFwd ? a.N : a.K, kWide);
+  if (!grid_fits(xcd_grid(tiles), kWideThreads) || tiles >= INT32_MAX / 2) return hipErrorInvalidConfiguration;
+  const dim3 grid((unsigned)xcd_grid(tiles));
+  if (Mode != kDgrad && a.a_row) grouped_wide_kernel<Tr, Mode, Mode != kDgrad, Rows><<<grid, kWideThreads, 0, s>>>(a);
+  else grouped_wide_kernel<Tr, Mode, false, Rows><<<grid, kWideThreads, 0, s>>>(a);
+  return hipGetLastError();
 }
 
 template <typename Tr, int Mode, bool Vec>
 hipError_t launch(const GroupedArgs &a, hipStream_t s) {
   if constexpr (Vec) {
-    const int64_t used = a.G < a.P ? a.G : a.P;
-    const int64_t tiles = Mode == kWgrad ? (int64_t)a.G * cdiv(a.N, kWide) * cdiv(a.K, kWide)
-                                         : (a.P + used * (kWide - 1)) / kWide * cdiv(Mode == kFwd ? a.N : a.K, kWide);
-    if (a.a_rows > 0 && a.wide) {
-      if (!grid_fits(xcd_grid(tiles), kWideThreads) || tiles >= INT32_MAX / 2) return hipErrorInvalidConfiguration;
-      const dim3 grid((unsigned)xcd_grid(tiles));
-      if (Mode != kDgrad && a.a_row) grouped_wide_kernel<Tr, Mode, Mode != kDgrad><<<grid, kWideThreads, 0, s>>>(a);
-      else grouped_wide_kernel<Tr, Mode, false><<<grid, kWideThreads, 0, s>>>(a);
-      return hipGetLastError();
+    if (a.wide) {
+      // Tiles of 128 rows and three buffers where groups hold few rows, of 256 and two where they
+      // hold many, by the average. Forward at 256 experts, N = 1024, K = 2048: 159 against 170 us at
+      // 2 rows a group, 214 / 234 at 64, 380 / 385 at 256; 16 groups of 1024 rows: 301 / 284. Input gradient:
+      // 162 / 171 at 2, 240 / 250 at 64, 305 / 288 at 128.
+      if constexpr (Mode != kWgrad) {
+        if (a.P < (int64_t)(Mode == kFwd ? 256 : 96) * a.G) return launch_wide<Tr, Mode, 128>(a, s);
+      }
+      return launch_wide<Tr, Mode, 256>(a, s);
     }
   }
   constexpr int BI = 128, BJ = 128;
