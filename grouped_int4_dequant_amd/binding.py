@@ -509,79 +509,106 @@ def prefill_chunked(layer: Layer, x: torch.Tensor, logits: torch.Tensor, chunk: 
 _CODES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
+def _current_stream(device: torch.device) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):  # the same handle without a Stream object: 0.1 against 1.9 us
+    def _current_stream(device: torch.device) -> int:  # noqa: F811
+        return torch._C._cuda_getCurrentRawStream(device.index)
+
+
 class _Call:
     """One call: its device and stream, and the checks of its tensors."""
+
+    __slots__ = ("dtype", "device", "code", "stream", "given")
 
     def __init__(self, lead: torch.Tensor, name: str, stream):
         if not isinstance(lead, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
-        if lead.dtype not in (torch.bfloat16, torch.float16):
+        self.dtype = lead.dtype
+        if self.dtype is not torch.bfloat16 and self.dtype is not torch.float16:
             raise TypeError(f"{name} must be bfloat16 or float16, got {lead.dtype}")
         if not lead.is_cuda:
             raise ValueError(f"{name} must be on the GPU")
-        self.dtype, self.device = lead.dtype, lead.device
-        self.code = _CODES[lead.dtype]
-        self.stream = torch.cuda.current_stream(lead.device) if stream is None else stream
-        if self.stream.device != lead.device:
-            raise ValueError(f"stream must be of {lead.device}, got {self.stream.device}")
+        self.device = lead.device
+        self.code = 0 if self.dtype is torch.bfloat16 else 1
+        self.given = stream
+        if stream is None:
+            self.stream = _current_stream(self.device)
+        elif stream.device != self.device:
+            raise ValueError(f"stream must be of {lead.device}, got {stream.device}")
+        else:
+            self.stream = stream.cuda_stream
 
     def need(self, t, name, dtype, shape):
         """A contiguous tensor of the call's device."""
-        _need(t, name, dtype, shape)
-        self._here(t, name)
+        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == self.device and t.is_contiguous()):
+            _need(t, name, dtype, shape)
+            raise ValueError(f"{name} must be on {self.device}, got {t.device}")
         return t
 
-    def rows(self, t, name, shape, dtypes=None):
-        """A matrix with contiguous columns and a row stride of at least its width."""
+    def rows(self, t, name, shape, other=None):
+        """A matrix of the call's type (or of `other`) with contiguous columns and a row stride of at least its width."""
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
-        if t.dtype not in (dtypes or (self.dtype,)):
-            raise TypeError(f"{name} must be {' or '.join(map(str, dtypes or (self.dtype,)))}, got {t.dtype}")
-        if tuple(t.shape) != tuple(shape):
+        if t.dtype is not self.dtype and (other is None or t.dtype is not other):
+            raise TypeError(f"{name} must be {self.dtype}{'' if other is None else f' or {other}'}, got {t.dtype}")
+        if t.shape != shape:
             raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-        if (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        if t.device != self.device:
+            raise ValueError(f"{name} must be on {self.device}, got {t.device}")
+        if not t.is_contiguous() and ((shape[1] > 1 and t.stride(1) != 1) or (shape[0] > 1 and t.stride(0) < shape[1])):
             raise ValueError(f"{name} must have contiguous columns and rows that do not overlap")
-        self._here(t, name)
         return t
 
     def result(self, t, name, shape, dtype):
         """The given result matrix, or a new one of `dtype` (None: the call's type)."""
         if t is not None:
-            if dtype is not None and t.dtype != dtype:
+            if dtype is not None and t.dtype is not dtype:
                 raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-            return self.rows(t, name, shape, (self.dtype, torch.float32))
+            return self.rows(t, name, shape, torch.float32)
         return self.new(shape, self._type(dtype, name))
 
     def whole(self, t, name, shape, dtype):
         """The given contiguous result, or a new one of `dtype` (None: the call's type)."""
         if t is None:
             return self.new(shape, self._type(dtype, name))
-        if t.dtype not in (self.dtype, torch.float32) or (dtype is not None and t.dtype != dtype):
+        if t.dtype not in (self.dtype, torch.float32) or (dtype is not None and t.dtype is not dtype):
             raise TypeError(f"{name} must be {dtype or self.dtype}, got {t.dtype}")
         return self.need(t, name, t.dtype, shape)
 
     def _type(self, dtype, name):
-        dtype = self.dtype if dtype is None else dtype
-        if dtype not in (self.dtype, torch.float32):
+        if dtype is None:
+            return self.dtype
+        if dtype is not self.dtype and dtype is not torch.float32:
             raise TypeError(f"{name} must be {self.dtype} or float32, not {dtype}")
         return dtype
 
     def new(self, shape, dtype):
-        with torch.cuda.stream(self.stream):
+        """A new tensor that belongs to the call's stream."""
+        if self.given is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.given):
             return torch.empty(shape, dtype=dtype, device=self.device)
 
-    def _here(self, t, name):
-        if t.device != self.device:
-            raise ValueError(f"{name} must be on {self.device}, got {t.device}")
-
     def __call__(self, what, *args):
-        with torch.cuda.device(self.device):
-            _check(getattr(load(), what)(*args, self.stream.cuda_stream), what)
+        f = getattr(_lib or load(), what)
+        if torch.cuda.current_device() == self.device.index:
+            status = f(*args, self.stream)
+        else:
+            with torch.cuda.device(self.device):
+                status = f(*args, self.stream)
+        if status != MOE_OK:
+            _check(status, what)
 
 
 def _ld(t: Optional[torch.Tensor]) -> int:
     """Row stride of a matrix; its width where it has at most one row."""
-    return 0 if t is None else t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if t is None:
+        return 0
+    n, width = t.shape
+    return t.stride(0) if n > 1 else width
 
 
 def _groups(c: _Call, offsets: torch.Tensor, G: int) -> torch.Tensor:
@@ -670,7 +697,7 @@ def combine(o: torch.Tensor, pair_pos: torch.Tensor, weights: Optional[torch.Ten
     if weights is not None:
         c.need(weights, "weights", torch.float32, (T, k))
     if add is not None:
-        c.rows(add, "add", (T, d), (c.dtype, torch.float32))
+        c.rows(add, "add", (T, d), torch.float32)
     y = c.result(out, "out", (T, d), out_dtype)
     c("moe_combine", c.code, o.data_ptr(), _ld(o), P, pair_pos.data_ptr(), _ptr(weights), T, k, d, _ptr(add),
       c.code if add is None else _CODES[add.dtype], _ld(add), y.data_ptr(), _CODES[y.dtype], _ld(y))
@@ -703,18 +730,16 @@ def adapter_plan(row_adapter: torch.Tensor, n: int, stream=None):
     sorted by adapter (row_adapter int32 [T]; outside [0, n): no adapter, sorted
     behind the others). One plan serves every projection of the batch."""
     _need(row_adapter, "row_adapter", torch.int32, (row_adapter.numel(),))
-    dev = row_adapter.device
-    s = torch.cuda.current_stream(dev) if stream is None else stream
-    if s.device != dev:
-        raise ValueError(f"stream must be of {dev}, got {s.device}")
     if n < 1:
         raise ValueError("n must be at least 1")
-    T = row_adapter.numel()
-    with torch.cuda.stream(s):
+    dev, T = row_adapter.device, row_adapter.numel()
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"stream must be of {dev}, got {stream.device}")
+    with torch.cuda.stream(torch.cuda.current_stream(dev) if stream is None else stream):
         rows = torch.empty(T, dtype=torch.int32, device=dev)
         offsets = torch.empty(n + 1, dtype=torch.int32, device=dev)
-        _check(load().moe_adapter_plan(row_adapter.data_ptr(), T, n, rows.data_ptr(), offsets.data_ptr(), s.cuda_stream),
-               "moe_adapter_plan")
+        _check(load().moe_adapter_plan(row_adapter.data_ptr(), T, n, rows.data_ptr(), offsets.data_ptr(),
+                                       torch.cuda.current_stream(dev).cuda_stream), "moe_adapter_plan")
     return rows, offsets
 
 
@@ -744,7 +769,7 @@ def adapter_forward(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scale: Op
     c = _Call(x, "x", stream)
     T, K, N, r, n, rows, offsets = _adapter_args(c, x, A, B, scale, plan)
     if base is not None:
-        c.rows(base, "base", (T, N), (c.dtype, torch.float32))
+        c.rows(base, "base", (T, N), torch.float32)
         out_dtype = base.dtype if out_dtype is None and out is None else out_dtype
     y = c.result(out, "out", (T, N), out_dtype)
     if base is not None and base.dtype != y.dtype:
@@ -771,7 +796,7 @@ def adapter_backward(dy: torch.Tensor, x: torch.Tensor, A: torch.Tensor, B: torc
     T, K, N, r, n, rows, offsets = _adapter_args(c, x, A, B, scale, plan)
     c.rows(dy, "dy", (T, N))
     if dx_base is not None:
-        c.rows(dx_base, "dx_base", (T, K), (c.dtype, torch.float32))
+        c.rows(dx_base, "dx_base", (T, K), torch.float32)
     dx = c.result(dx, "dx", (T, K), None if dx_base is None else dx_base.dtype)
     if accumulate and (dA is None or dB is None):
         raise ValueError("accumulate needs the tensors to add to in dA and dB")
@@ -780,8 +805,8 @@ def adapter_backward(dy: torch.Tensor, x: torch.Tensor, A: torch.Tensor, B: torc
     need = adapter_backward_workspace_bytes(T, r)
     if ws is None:
         ws = c.new(max(need, 1), torch.uint8)
-    else:
-        c._here(ws, "ws")
+    elif ws.device != c.device:
+        raise ValueError(f"ws must be on {c.device}, got {ws.device}")
     c("moe_adapter_backward", c.code, dy.data_ptr(), _ld(dy), x.data_ptr(), _ld(x), T, K, N, r, n, A.data_ptr(),
       B.data_ptr(), _ptr(scale), rows.data_ptr(), offsets.data_ptr(), _ptr(dx_base), _ld(dx_base), dx.data_ptr(),
       _CODES[dx.dtype], _ld(dx), dA.data_ptr(), dB.data_ptr(), _CODES[dA.dtype], int(accumulate), ws.data_ptr(),
