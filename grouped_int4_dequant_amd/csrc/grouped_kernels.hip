@@ -34,57 +34,106 @@ __device__ __forceinline__ int across_unit(int row, int slot) {
   return slot ^ (((((row & 3) | ((row >> 1) & 12))) & (Cols / 16 - 1)) << 1);
 }
 
-// Load `n` 16-bit elements one by one (operands whose rows are not whole aligned
-// 16-byte units).
-__device__ __forceinline__ u4 load_elems(const uint16_t *p, int64_t n) {
-  u4 v = {0u, 0u, 0u, 0u};
+// Forward: sorted row p takes no row of A. Its results are zeros whatever the
+// weights hold (a product of zeros would pass on their infinities and NaN).
+template <int Mode>
+__device__ __forceinline__ bool masked_row(const GroupedArgs &a, int p) {
+  if (Mode != kFwd) return false;
+  const int at = a.a_row ? a.a_row[p] : p;
+  return at < 0 || at >= a.a_rows;
+}
+
+// Four consecutive results from element `at` on, of which `left` exist.
+template <typename Tr>
+__device__ __forceinline__ void store4(const GroupedArgs &a, int64_t at, f4 v, int left, bool add) {
+  if (a.out_f32) {
+    float *o = static_cast<float *>(a.out) + at;
+    if (a.vec_out) {
+      if (add) v += *reinterpret_cast<const f4 *>(o);
+      *reinterpret_cast<f4 *>(o) = v;
+    } else {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t x = i < n ? (uint32_t)p[i] : 0u;
-    v[i >> 1] |= x << (16 * (i & 1));
+      for (int x = 0; x < 4; ++x)
+        if (x < left) o[x] = v[x] + (add ? o[x] : 0.f);
+    }
+  } else {
+    uint16_t *o = static_cast<uint16_t *>(a.out) + at;
+    if (a.vec_out) {
+      *reinterpret_cast<u2 *>(o) = u2{(uint32_t)Tr::from(v[0]) | (uint32_t)Tr::from(v[1]) << 16,
+                                      (uint32_t)Tr::from(v[2]) | (uint32_t)Tr::from(v[3]) << 16};
+    } else {
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (x < left) o[x] = Tr::from(v[x]);
+    }
+  }
+}
+
+// Eight 16-bit elements at p, of which the first n exist. Rows that are not whole aligned
+// units are read all the same 16 bytes at a time (global loads need no alignment), but
+// for a row's last elements.
+typedef u4 __attribute__((aligned(2))) u4_any;
+template <bool Vec>
+__device__ __forceinline__ u4 load_unit(const uint16_t *p, int n) {
+  u4 v = {0u, 0u, 0u, 0u};
+  if (Vec) {
+    if (n > 0) v = *reinterpret_cast<const u4 *>(p);
+  } else if (n >= 8) {
+    v = *reinterpret_cast<const u4_any *>(p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t x = i < n ? (uint32_t)p[i] : 0u;
+      v[i >> 1] |= x << (16 * (i & 1));
+    }
   }
   return v;
 }
 
-template <typename Tr, int Mode, bool Vec, int BI, int BJ, int WI, int WJ>
-__global__ __launch_bounds__(64 * WI * WJ) void grouped_kernel(GroupedArgs a) {
-  constexpr int kThreads = 64 * WI * WJ;
-  constexpr int TI = BI / WI / 16, TJ = BJ / WJ / 16;  // 16 x 16 blocks of a wave
-  constexpr int UL = BI * 8 / kThreads, UR = BJ * 8 / kThreads;  // 16-byte units a thread stages per step
-  static_assert(UL >= 1 && UR >= 1 && BI * 8 % kThreads == 0 && BJ * 8 % kThreads == 0, "whole units per thread");
+// ---------------------------------------------------------------- small tiles
+// 64 x 64 outputs a workgroup of four waves, 64 r a step, any sizes and
+// alignment. The next step's operands are loaded into registers while this one's matrix
+// instructions run, and go to the other LDS buffer behind them. For calls whose wide
+// tiles would leave most CUs idle, and for operands the wide tiles cannot request.
+constexpr int kSmall = 64;
+
+template <typename Tr, int Mode, bool Vec>
+__global__ __launch_bounds__(256) void grouped_small_kernel(GroupedArgs a) {
+  constexpr int B = kSmall, U = B * 8 / 256;  // 16-byte units a thread stages of each operand and step
   constexpr bool kLAcross = Mode == kWgrad, kRAcross = Mode != kFwd;
-  __shared__ __attribute__((aligned(16))) uint8_t s_l[2][BI * kBR * 2];
-  __shared__ __attribute__((aligned(16))) uint8_t s_r[2][BJ * kBR * 2];
+  __shared__ __attribute__((aligned(16))) uint8_t s_l[2][B * kBR * 2];
+  __shared__ __attribute__((aligned(16))) uint8_t s_r[2][B * kBR * 2];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int p16 = lane & 15, q4 = lane >> 4;
 
   // ---- which tile
-  int e, first, count, i0, j0, ni, nj;  // ni, nj: rows and columns of the output that exist from i0, j0
-  int nr;                               // length of the sum
+  int e, first, count, i0, j0, ni, nj, nr;
   if (Mode == kWgrad) {
-    const int tj = (a.K + BJ - 1) / BJ, ti = (a.N + BI - 1) / BI;
-    const int per = ti * tj;
+    const int tj = (a.K + B - 1) / B, ti = (a.N + B - 1) / B, per = ti * tj;
     e = blockIdx.x / per;
+    if (e >= a.G) return;
     const int t = blockIdx.x - e * per;
-    i0 = t / tj * BI;
-    j0 = (t - t / tj * tj) * BJ;
+    i0 = t / tj * B;
+    j0 = (t - t / tj * tj) * B;
     first = min(max(a.offsets[e], 0), a.P);
     count = max(min(max(a.offsets[e + 1], 0), a.P) - first, 0);
     nr = count;
     ni = a.N - i0;
     nj = a.K - j0;
   } else {
-    const int J = Mode == kFwd ? a.N : a.K;
-    const int tj = (J + BJ - 1) / BJ;
-    const int m = blockIdx.x / tj;
-    const GroupTile g = find_group(a.offsets, a.G, a.P, BI, [&](int) { return m; });
+    const int J = Mode == kFwd ? a.N : a.K, tj = (J + B - 1) / B;
+    int item;
+    const GroupTile g = find_group(a.offsets, a.G, a.P, B, [&](int total) {
+      item = xcd_item(blockIdx.x, total * tj);
+      return item < 0 ? -1 : item / tj;
+    });
     if (g.e < 0) return;
     e = g.e;
-    const int t = blockIdx.x - g.before * tj, mt = (g.count + BI - 1) / BI;
+    const int t = item - g.before * tj, mt = (g.count + B - 1) / B;
     const int jt = t / mt;
-    i0 = (t - jt * mt) * BI;
-    j0 = jt * BJ;
+    i0 = (t - jt * mt) * B;
+    j0 = jt * B;
     first = g.first;
     count = g.count;
     ni = count - i0;
@@ -93,190 +142,224 @@ __global__ __launch_bounds__(64 * WI * WJ) void grouped_kernel(GroupedArgs a) {
   }
   const int steps = (nr + kBR - 1) / kBR;
 
-  // ---- what this thread stages: unit u = tid + kThreads i of each tile
-  const uint16_t *lp[UL], *rp[UR];  // at step 0; nullptr: zeros at every step
+  // ---- staging. Unit u = tid + 256 i: a straight operand's row u / 8, an
+  // across operand's r = u / 8, eight r or columns at 8 (slot's unit).
+  const uint16_t *lp[U], *rp[U];  // at step 0; nullptr: zeros
   const uint16_t *L = Mode == kWgrad ? a.w : a.rows;
   const int64_t ldl = Mode == kWgrad ? a.ld_w : a.ld_rows;
   const uint16_t *R = Mode == kWgrad ? a.rows : a.w + (int64_t)e * a.N * a.K;
   const int64_t ldr = Mode == kWgrad ? a.ld_rows : a.ld_w;
-  int lu[UL], ru[UR];  // straight: first r of the unit; across: its row r
+  const int urow = tid >> 3;
+  const int lslot = 8 * (kLAcross ? across_unit<B>(urow, tid & 7) : straight_unit(urow, tid & 7));
+  const int rslot = 8 * (kRAcross ? across_unit<B>(urow, tid & 7) : straight_unit(urow, tid & 7));
 #pragma unroll
-  for (int i = 0; i < UL; ++i) {
-    const int u = tid + kThreads * i;
+  for (int i = 0; i < U; ++i) {
+    const int row = urow + 32 * i;  // the slots' swap goes by bits that 32 i leaves alone
     if (kLAcross) {
-      constexpr int per = BI / 8;
-      const int row = u / per, col = 8 * across_unit<BI>(row, u % per);
-      lu[i] = row;
-      lp[i] = col < ni ? L + (int64_t)(first + row) * ldl + i0 + col : nullptr;
+      lp[i] = lslot < ni ? L + (int64_t)(first + row) * ldl + i0 + lslot : nullptr;
     } else {
-      const int row = u >> 3;
-      lu[i] = 8 * straight_unit(row, u & 7);
       int64_t at = first + i0 + row;
       bool ok = row < ni;
-      if (Mode == kFwd && a.a_row && ok) {
-        at = a.a_row[at];
-        ok = at >= 0 && at < a.a_rows;
-      } else if (Mode == kFwd) {
-        ok = ok && at < a.a_rows;
-      }
-      lp[i] = ok ? L + at * ldl + lu[i] : nullptr;
+      if (Mode == kFwd && a.a_row && ok) at = a.a_row[at];
+      if (Mode == kFwd) ok = ok && at >= 0 && at < a.a_rows;
+      lp[i] = ok ? L + at * ldl + lslot : nullptr;
     }
+    if (kRAcross) rp[i] = rslot < nj ? R + j0 + rslot + (Mode == kDgrad ? (int64_t)row * ldr : 0) : nullptr;
+    else rp[i] = row < nj ? R + (int64_t)(j0 + row) * ldr + rslot : nullptr;
   }
+  u4 lreg[U], rreg[U];
+  auto load = [&](int s) {
 #pragma unroll
-  for (int i = 0; i < UR; ++i) {
-    const int u = tid + kThreads * i;
-    if (kRAcross) {
-      constexpr int per = BJ / 8;
-      const int row = u / per, col = 8 * across_unit<BJ>(row, u % per);
-      ru[i] = row;
-      rp[i] = col < nj ? R + j0 + col + (Mode == kDgrad ? (int64_t)row * ldr : 0) : nullptr;
-    } else {
-      const int row = u >> 3;
-      ru[i] = 8 * straight_unit(row, u & 7);
-      rp[i] = row < nj ? R + (int64_t)(j0 + row) * ldr + ru[i] : nullptr;
-    }
-  }
-  // rows of A that the weight gradient's next step gathers
-  int rrow[UR];
-  auto fetch_rows = [&](int s) {
-    if (Mode != kWgrad) return;
-#pragma unroll
-    for (int i = 0; i < UR; ++i) {
-      const int r = s * kBR + ru[i];
-      int at = -1;
-      if (r < nr) at = a.a_row ? a.a_row[first + r] : first + r;
-      rrow[i] = at >= 0 && at < a.a_rows ? at : -1;
-    }
-  };
-  auto stage = [&](int s, int buf) {
-#pragma unroll
-    for (int i = 0; i < UL; ++i) {
-      const int r = s * kBR + lu[i];
-      const uint16_t *p = lp[i];
-      if (p) p += kLAcross ? (int64_t)s * kBR * ldl : s * kBR;
-      const bool ok = p && r < nr;
-      uint8_t *dst = s_l[buf] + 16 * (kThreads * i);
-      if (Vec) {
-        load_lds16(ok ? (const void *)p : (const void *)&g_zeros, dst + 1024 * wave);
-      } else {
-        const int left = kLAcross ? ni - 8 * across_unit<BI>(lu[i], (tid + kThreads * i) % (BI / 8)) : nr - r;
-        *reinterpret_cast<u4 *>(dst + 16 * tid) = load_elems(p, ok ? left : 0);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < UR; ++i) {
-      const int r = s * kBR + ru[i];
-      const uint16_t *p = rp[i];
-      bool ok = p && r < nr;
+    for (int i = 0; i < U; ++i) {
+      const int r = s * kBR + urow + 32 * i;  // across operands: the unit's r
+      if (kLAcross) lreg[i] = load_unit<Vec>(lp[i] + (int64_t)s * kBR * ldl, lp[i] && r < nr ? ni - lslot : 0);
+      else lreg[i] = load_unit<Vec>(lp[i] + s * kBR, lp[i] ? nr - s * kBR - lslot : 0);
       if (Mode == kWgrad) {
-        ok = p && rrow[i] >= 0;
-        if (ok) p += (int64_t)rrow[i] * ldr;
-      } else if (p) {
-        p += kRAcross ? (int64_t)s * kBR * ldr : s * kBR;
-      }
-      uint8_t *dst = s_r[buf] + 16 * (kThreads * i);
-      if (Vec) {
-        load_lds16(ok ? (const void *)p : (const void *)&g_zeros, dst + 1024 * wave);
+        int at = -1;
+        if (rp[i] && r < nr) at = a.a_row ? a.a_row[first + r] : first + r;
+        const bool ok = at >= 0 && at < a.a_rows;
+        rreg[i] = load_unit<Vec>(rp[i] + (ok ? at * ldr : 0), ok ? nj - rslot : 0);
+      } else if (kRAcross) {
+        rreg[i] = load_unit<Vec>(rp[i] + (int64_t)s * kBR * ldr, rp[i] && r < nr ? nj - rslot : 0);
       } else {
-        const int left = kRAcross ? nj - 8 * across_unit<BJ>(ru[i], (tid + kThreads * i) % (BJ / 8)) : nr - r;
-        *reinterpret_cast<u4 *>(dst + 16 * tid) = load_elems(p, ok ? left : 0);
+        rreg[i] = load_unit<Vec>(rp[i] + s * kBR, rp[i] ? nr - s * kBR - rslot : 0);
       }
     }
   };
-
-  const int wi = wave / WJ * (BI / WI), wj = wave % WJ * (BJ / WJ);
-  f4 acc[TI][TJ];
+  auto keep = [&](int buf) {
 #pragma unroll
-  for (int i = 0; i < TI; ++i)
-#pragma unroll
-    for (int j = 0; j < TJ; ++j) acc[i][j] = f4{0.f, 0.f, 0.f, 0.f};
-
-  // operand of 16 rows (or columns) from c0, r = 32 ks + 8 q4 ..+7
-  auto straight = [&](const uint8_t *t, int c0, int ks) {
-    const int row = c0 + p16;
-    return *reinterpret_cast<const s8 *>(t + row * 128 + 16 * straight_unit(row, 4 * ks + q4));
+    for (int i = 0; i < U; ++i) {
+      *reinterpret_cast<u4 *>(s_l[buf] + 16 * (tid + 256 * i)) = lreg[i];
+      *reinterpret_cast<u4 *>(s_r[buf] + 16 * (tid + 256 * i)) = rreg[i];
+    }
   };
-  auto across = [&](const uint8_t *t, int c0, int ks, auto cols) {
-    constexpr int C = decltype(cols)::value;
-    s8 v;
+
+  const int wi = (wave >> 1) * 32, wj = (wave & 1) * 32;
+  f4 acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) acc[i][j] = f4{0.f, 0.f, 0.f, 0.f};
+  auto fetch = [&](const uint8_t *t, int c0, int ks, bool across) {
+    if (!across) return *reinterpret_cast<const s8 *>(t + (c0 + p16) * 128 + 16 * straight_unit(c0 + p16, 4 * ks + q4));
+    s4 x[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int row = 32 * ks + 8 * q4 + 4 * h + (p16 >> 2);
-      const int c = c0 + 4 * (p16 & 3);
-      const s4 x = read_lds_tr(t + row * (2 * C) + 16 * across_unit<C>(row, c >> 3) + 2 * (c & 7));
-      v[4 * h] = x[0]; v[4 * h + 1] = x[1]; v[4 * h + 2] = x[2]; v[4 * h + 3] = x[3];
+      const int row = 32 * ks + 8 * q4 + 4 * h + (p16 >> 2), c = c0 + 4 * (p16 & 3);
+      x[h] = read_lds_tr(t + row * 128 + 16 * across_unit<B>(row, c >> 3) + 2 * (c & 7));
     }
-    return v;
+    return s8{x[0][0], x[0][1], x[0][2], x[0][3], x[1][0], x[1][1], x[1][2], x[1][3]};
   };
-
   if (steps > 0) {
-    fetch_rows(0);
-    stage(0, 0);
-    fetch_rows(1);
+    load(0);
+    keep(0);
   }
   for (int s = 0; s < steps; ++s) {
     const int buf = s & 1;
-    __builtin_amdgcn_s_waitcnt(0);
     __syncthreads();
-    s8 lf[2][TI], rf[2][TJ];
+    if (s + 1 < steps) load(s + 1);
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
+      s8 l[2], r[2];
 #pragma unroll
-      for (int i = 0; i < TI; ++i)
-        lf[ks][i] = kLAcross ? across(s_l[buf], wi + 16 * i, ks, std::integral_constant<int, BI>{}) : straight(s_l[buf], wi + 16 * i, ks);
+      for (int i = 0; i < 2; ++i) {
+        l[i] = fetch(s_l[buf], wi + 16 * i, ks, kLAcross);
+        r[i] = fetch(s_r[buf], wj + 16 * i, ks, kRAcross);
+      }
 #pragma unroll
-      for (int j = 0; j < TJ; ++j)
-        rf[ks][j] = kRAcross ? across(s_r[buf], wj + 16 * j, ks, std::integral_constant<int, BJ>{}) : straight(s_r[buf], wj + 16 * j, ks);
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = Tr::mfma(r[j], l[i], acc[i][j]);
     }
-    if (s + 1 < steps) {
-      stage(s + 1, buf ^ 1);
-      fetch_rows(s + 2);
-    }
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-      for (int i = 0; i < TI; ++i)
-#pragma unroll
-        for (int j = 0; j < TJ; ++j) acc[i][j] = Tr::mfma(rf[ks][j], lf[ks][i], acc[i][j]);
+    if (s + 1 < steps) keep(buf ^ 1);
   }
 
-  // ---- results: lane holds column p16 of block i (an output row) and four
-  // consecutive output columns of block j
+  // ---- results: lane holds output row p16 and four consecutive columns of each block
   const int64_t obase = Mode == kWgrad ? (int64_t)e * a.N * a.K : (int64_t)first * a.ld_out;
   const int64_t ldo = Mode == kWgrad ? a.K : a.ld_out;
   if (Mode == kWgrad && a.accumulate && count == 0) return;
 #pragma unroll
-  for (int i = 0; i < TI; ++i) {
+  for (int i = 0; i < 2; ++i) {
     const int row = wi + 16 * i + p16;
     if (row >= ni) continue;
+    const bool masked = masked_row<Mode>(a, first + i0 + row);
 #pragma unroll
-    for (int j = 0; j < TJ; ++j) {
+    for (int j = 0; j < 2; ++j) {
       const int col = wj + 16 * j + 4 * q4;
       if (col >= nj) continue;
-      const int64_t at = obase + (int64_t)(i0 + row) * ldo + j0 + col;
-      f4 v = acc[i][j];
-      if (a.out_f32) {
-        float *o = static_cast<float *>(a.out) + at;
-        if (a.vec_out) {
-          if (Mode == kWgrad && a.accumulate) v += *reinterpret_cast<const f4 *>(o);
-          *reinterpret_cast<f4 *>(o) = v;
-        } else {
+      store4<Tr>(a, obase + (int64_t)(i0 + row) * ldo + j0 + col, masked ? f4{0.f, 0.f, 0.f, 0.f} : acc[i][j], nj - col, Mode == kWgrad && a.accumulate);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- few rows
+// Calls of a few rows read each touched group's weights once and are bound by
+// that, so the weights are spread over all CUs: a workgroup takes up to 16 rows of
+// a group and 32 output columns (forward) or 64 (input gradient); its eight waves share the sum
+// and join in LDS, in order. Weights go straight from memory to operand registers.
+constexpr int kFewRows = 16;
+
+template <typename Tr, int Mode>
+__global__ __launch_bounds__(512) void grouped_few_kernel(GroupedArgs a) {
+  constexpr int kCols = Mode == kFwd ? 32 : 64, NB = kCols / 16;  // 16-column blocks
+  __shared__ __attribute__((aligned(16))) f4 s_part[8][Mode == kFwd ? 1 : NB][64];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int p16 = lane & 15, q4 = lane >> 4;
+  const int J = Mode == kFwd ? a.N : a.K, nr = Mode == kFwd ? a.K : a.N;
+  const int tj = (J + kCols - 1) / kCols;
+  const GroupTile g = find_group(a.offsets, a.G, a.P, kFewRows, [&](int) { return (int)blockIdx.x / tj; });
+  if (g.e < 0) return;
+  const int t = blockIdx.x - g.before * tj, mt = (g.count + kFewRows - 1) / kFewRows;
+  const int jt = t / mt, i0 = (t - jt * mt) * kFewRows, j0 = jt * kCols;
+  const int ni = min(g.count - i0, kFewRows), nj = min(J - j0, kCols);
+  int64_t at = g.first + i0 + p16;
+  bool ok = p16 < ni;
+  if (Mode == kFwd && a.a_row && ok) at = a.a_row[at];
+  if (Mode == kFwd) ok = ok && at >= 0 && at < a.a_rows;
+  const uint16_t *x = ok ? a.rows + at * a.ld_rows : nullptr;
+  const uint16_t *W = a.w + (int64_t)g.e * a.N * a.K;
+  const s8 zero = {0, 0, 0, 0, 0, 0, 0, 0};
+  f4 acc[NB];
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            if (col + x < nj) o[x] = v[x] + (Mode == kWgrad && a.accumulate ? o[x] : 0.f);
-        }
-      } else {
-        uint16_t *o = static_cast<uint16_t *>(a.out) + at;
-        if (a.vec_out) {
-          *reinterpret_cast<u2 *>(o) = u2{(uint32_t)Tr::from(v[0]) | (uint32_t)Tr::from(v[1]) << 16,
-                                          (uint32_t)Tr::from(v[2]) | (uint32_t)Tr::from(v[3]) << 16};
-        } else {
+  for (int j = 0; j < NB; ++j) acc[j] = f4{0.f, 0.f, 0.f, 0.f};
+  if constexpr (Mode == kFwd) {
+    // wave: columns 16 (wave / 4) .., every fourth 32 of k
+    const int n = j0 + 16 * (wave >> 2) + p16;
+    const uint16_t *w = n < a.N ? W + (int64_t)n * a.K : nullptr;
+    constexpr int kDeep = 8;
+    for (int k0 = 32 * (wave & 3); k0 < nr; k0 += 128 * kDeep) {
+      s8 wv[kDeep], xv[kDeep];
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            if (col + x < nj) o[x] = Tr::from(v[x]);
+      for (int u = 0; u < kDeep; ++u) {
+        const int k = k0 + 128 * u + 8 * q4;
+        wv[u] = w && k < nr ? *reinterpret_cast<const s8 *>(w + k) : zero;
+      }
+#pragma unroll
+      for (int u = 0; u < kDeep; ++u) {
+        const int k = k0 + 128 * u + 8 * q4;
+        xv[u] = x && k < nr ? *reinterpret_cast<const s8 *>(x + k) : zero;
+      }
+#pragma unroll
+      for (int u = 0; u < kDeep; ++u) acc[0] = Tr::mfma(wv[u], xv[u], acc[0]);
+    }
+    s_part[wave][0][lane] = acc[0];
+  } else {
+    // wave: every eighth 32 of n. A lane reads four columns 4 p16 .. of rows n = 8 q4 .. + 7 and
+    // hands the matrix instruction number c the eight values of column 4 p16 + c.
+    const int col = 4 * p16;
+    constexpr int kDeep = 2;
+    for (int n0 = 32 * wave; n0 < nr; n0 += 256 * kDeep) {
+      u2 wv[kDeep][8];
+      s8 xv[kDeep];
+#pragma unroll
+      for (int u = 0; u < kDeep; ++u) {
+        const int n = n0 + 256 * u + 8 * q4;
+#pragma unroll
+        for (int y = 0; y < 8; ++y)
+          wv[u][y] = n < nr && col < nj ? *reinterpret_cast<const u2 *>(W + (int64_t)(n + y) * a.K + j0 + col) : u2{0u, 0u};
+        xv[u] = x && n < nr ? *reinterpret_cast<const s8 *>(x + n) : zero;
+      }
+#pragma unroll
+      for (int u = 0; u < kDeep; ++u) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          u4 v;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const uint32_t lo = wv[u][2 * y][c >> 1], hi = wv[u][2 * y + 1][c >> 1];
+            v[y] = c & 1 ? (lo >> 16) | (hi & 0xffff0000u) : (lo & 0xffffu) | (hi << 16);
+          }
+          acc[c] = Tr::mfma(__builtin_bit_cast(s8, v), xv[u], acc[c]);
         }
       }
     }
+#pragma unroll
+    for (int c = 0; c < NB; ++c) s_part[wave][c][lane] = acc[c];
+  }
+  __syncthreads();
+  // lane: row p16; forward: wave 0 and 1 take a 16-column block each, columns 4 q4 ..;
+  // input gradient: block c's operand row m is column 4 m + c, so a lane has 4 (4 q4 + reg) + c
+  if (Mode == kFwd) {
+    if (wave < 2) {
+      f4 v = s_part[4 * wave][0][lane];
+#pragma unroll
+      for (int y = 1; y < 4; ++y) v += s_part[4 * wave + y][0][lane];
+      const int col = 16 * wave + 4 * q4;
+      if (!ok) v = f4{0.f, 0.f, 0.f, 0.f};
+      if (p16 < ni && col < nj) store4<Tr>(a, (int64_t)(g.first + i0 + p16) * a.ld_out + j0 + col, v, nj - col, false);
+    }
+  } else if (wave < 4) {  // wave: the four columns 4 (4 q4 + wave) ..
+    f4 v;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      float sum = 0.f;
+#pragma unroll
+      for (int y = 0; y < 8; ++y) sum += reinterpret_cast<const float *>(&s_part[y][c][lane])[wave];
+      v[c] = sum;
+    }
+    const int col = 4 * (4 * q4 + wave);
+    if (p16 < ni && col < nj) store4<Tr>(a, (int64_t)(g.first + i0 + p16) * a.ld_out + j0 + col, v, nj - col, false);
   }
 }
 
@@ -678,6 +761,7 @@ __global__ __launch_bounds__(kWideThreads, 2) void grouped_wide_kernel(GroupedAr
     const int tj = (a.K + kWide - 1) / kWide, ti = (a.N + kWide - 1) / kWide;
     const int per = ti * tj;
     t.e = blockIdx.x / per;
+    if (t.e >= a.G) return;
     const int x = blockIdx.x - t.e * per;
     t.i0 = x / tj * kWide;
     t.j0 = (x - x / tj * tj) * kWide;
@@ -717,17 +801,36 @@ hipError_t launch_wide(const GroupedArgs &a, hipStream_t s) {
   const int64_t used = a.G < a.P ? a.G : a.P;  // groups that can have rows
   const int64_t tiles = Mode == kWgrad ? (int64_t)a.G * cdiv(a.N, kWide) * cdiv(a.K, kWide)
                                        : (a.P + used * (Rows - 1)) / Rows * cdiv(Mode == kFwd ? a.N : a.K, kWide);
-  if (!grid_fits(xcd_grid(tiles), kWideThreads) || tiles >= INT32_MAX / 2) return hipErrorInvalidConfiguration;
-  const dim3 grid((unsigned)xcd_grid(tiles));
+  const int64_t wgs = Mode == kWgrad ? tiles : xcd_grid(tiles);  // the weight gradient's kernel takes its tile by number
+  if (!grid_fits(wgs, kWideThreads) || tiles >= INT32_MAX / 2) return hipErrorInvalidConfiguration;
+  const dim3 grid((unsigned)wgs);
   if (Mode != kDgrad && a.a_row) grouped_wide_kernel<Tr, Mode, Mode != kDgrad, Rows><<<grid, kWideThreads, 0, s>>>(a);
   else grouped_wide_kernel<Tr, Mode, false, Rows><<<grid, kWideThreads, 0, s>>>(a);
   return hipGetLastError();
 }
 
+#ifndef FEWP
+#define FEWP 64
+#endif
+#ifndef SMALLT
+#define SMALLT 128
+#endif
 template <typename Tr, int Mode, bool Vec>
 hipError_t launch(const GroupedArgs &a, hipStream_t s) {
+  const int64_t used = a.G < a.P ? a.G : a.P;  // groups that can have rows
+  const int J = Mode == kFwd ? a.N : a.K;
   if constexpr (Vec) {
-    if (a.wide) {
+    if constexpr (Mode != kWgrad) {
+      if (a.P <= FEWP) {
+        const int64_t wgs = (a.P + used * (kFewRows - 1)) / kFewRows * cdiv(J, Mode == kFwd ? 32 : 64);
+        if (!grid_fits(wgs, 512)) return hipErrorInvalidConfiguration;
+        grouped_few_kernel<Tr, Mode><<<dim3((unsigned)wgs), 512, 0, s>>>(a);
+        return hipGetLastError();
+      }
+    }
+    const int64_t at_least = Mode == kWgrad ? (int64_t)a.G * cdiv(a.N, kWide) * cdiv(a.K, kWide)
+                                            : (used > a.P / kWide ? used : a.P / kWide) * cdiv(J, kWide);
+    if (a.wide && at_least >= SMALLT) {
       // Tiles of 128 rows and three buffers where groups hold few rows, of 256 and two where they
       // hold many, by the average. Forward at 256 experts, N = 1024, K = 2048: 159 against 170 us at
       // 2 rows a group, 214 / 234 at 64, 380 / 385 at 256; 16 groups of 1024 rows: 301 / 284. Input gradient:
@@ -738,16 +841,10 @@ hipError_t launch(const GroupedArgs &a, hipStream_t s) {
       return launch_wide<Tr, Mode, 256>(a, s);
     }
   }
-  constexpr int BI = 128, BJ = 128;
-  int64_t tiles;
-  if (Mode == kWgrad) {
-    tiles = (int64_t)a.G * cdiv(a.N, BI) * cdiv(a.K, BJ);
-  } else {
-    const int64_t used = a.G < a.P ? a.G : a.P;  // groups that can have rows
-    tiles = (a.P + used * (BI - 1)) / BI * cdiv(Mode == kFwd ? a.N : a.K, BJ);
-  }
-  if (!grid_fits(tiles, 256)) return hipErrorInvalidConfiguration;
-  grouped_kernel<Tr, Mode, Vec, BI, BJ, 2, 2><<<dim3((unsigned)tiles), dim3(256), 0, s>>>(a);
+  const int64_t tiles = Mode == kWgrad ? (int64_t)a.G * cdiv(a.N, kSmall) * cdiv(a.K, kSmall)
+                                       : (a.P + used * (kSmall - 1)) / kSmall * cdiv(J, kSmall);
+  if (!grid_fits(xcd_grid(tiles), 256)) return hipErrorInvalidConfiguration;
+  grouped_small_kernel<Tr, Mode, Vec><<<dim3((unsigned)(Mode == kWgrad ? tiles : xcd_grid(tiles))), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 

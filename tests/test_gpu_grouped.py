@@ -43,13 +43,14 @@ def strided(t, extra, fill):
 LAYOUTS = {
     "one_row": ([1], 0), "one_of_many": ([0, 0, 1, 0], 0), "edges": ([0, 15, 16, 17, 0, 127, 128, 129, 0], 0),
     "all_in_one": ([0, 700, 0], 0), "tail": ([33, 0, 5], 9), "single_rows": ([1] * 70, 0), "all_empty": ([0, 0, 0], 4),
-    "many": ([(7 * i) % 23 for i in range(130)], 0), "short_long": ([3, 513, 64, 2, 0, 255], 0),
+    "many": ([(7 * i) % 23 for i in range(130)], 0), "wide": ([(37 * i) % 301 for i in range(140)], 3), "wide_long": ([700, 0, 513, 1030] * 9, 0), "short_long": ([3, 513, 64, 2, 0, 255], 0),
 }
 #          N, K
-SIZES = {"tile": (128, 64), "small": (8, 8), "mid": (264, 200), "odd": (77, 131), "one": (1, 1), "odd_n": (65, 128), "odd_k": (128, 67),
+SIZES = {"wide": (1032, 1160), "tile": (128, 64), "small": (8, 8), "mid": (264, 200), "odd": (77, 131), "one": (1, 1), "odd_n": (65, 128), "odd_k": (128, 67),
          "deep": (40, 1544)}
 CASES = [(l, s, t, o) for l in LAYOUTS for s, t, o in (("mid", BF, BF), ("odd", FP, F4))]
 CASES += [(l, s, t, o) for s in SIZES for l, t, o in (("edges", FP, FP), ("short_long", BF, F4))]
+CASES += [("wide_long", "wide", BF, BF), ("wide_long", "wide", FP, F4), ("wide", "wide", BF, F4), ("single_rows", "wide", FP, FP), ("one_row", "wide", BF, F4)]
 IDS = [f"{l}-{s}-{str(t)[6:]}-{str(o)[6:]}" for l, s, t, o in CASES]
 
 
@@ -158,6 +159,28 @@ def test_infinities_and_nan_stay_in_their_sums(moe, dtype, K):
     hit = torch.zeros(4, N, K, dtype=torch.bool, device="cuda")
     hit[2, 0], hit[0, :, 1] = True, True
     assert torch.equal(G0[~hit], G1[~hit]) and not torch.isfinite(G1[hit]).any()
+
+
+@pytest.mark.parametrize("P,N,K", [(5, 64, 64), (300, 40, 72), (300, 33, 70), (1200, 1024, 512)])
+def test_masked_rows_are_zeros(moe, P, N, K):
+    """A masked row gives zeros whatever the weights hold, and no gradient."""
+    g, G = gen(5), 70
+    offsets = torch.linspace(0, P, G + 1).to(torch.int32).cuda()
+    A, W, dC = rnd(g, 20, K), rnd(g, G, N, K, scale=0.1), rnd(g, P, N)
+    a_row = torch.randint(0, 20, (P,), generator=g, dtype=torch.int32)
+    a_row[::3], a_row[1::7] = -1, 20
+    masked = ((a_row < 0) | (a_row >= 20)).cuda()
+    a_row = a_row.cuda()
+    value, mag, _ = R.grouped(A, W, offsets, a_row, P)
+    C = moe.grouped_gemm(A, W, offsets, a_row=a_row)
+    R.within(C, value, R.stored(value, R.sums(K, mag), BF), "C")
+    W[:, 3] = float("inf")
+    W[:, 5] = float("nan")
+    assert (moe.grouped_gemm(A, W, offsets, a_row=a_row)[masked] == 0).all()
+    kept = torch.where(masked[:, None], 0.0, dC.float()).to(BF)
+    D = moe.grouped_gemm_wgrad(dC, A, offsets, a_row=a_row, out_dtype=F4)
+    value, mag = R.grouped_wgrad(kept, A, offsets, torch.where(masked, 0, a_row))
+    R.within(D, value, R.stored(value, R.sums(P, mag), F4), "dW")
 
 
 @pytest.mark.parametrize("layout", ["edges", "many"])
