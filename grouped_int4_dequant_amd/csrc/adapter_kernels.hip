@@ -5,10 +5,15 @@
 //   g[t] = scale_a B_a^T dy[t],  dx[t] = dx_base[t] + A_a^T g[t]
 //   dA_a = sum_t g[t] x[t]^T,  dB_a = sum_t dy[t] h[t]^T
 //
-// Rows come sorted by adapter (rows[], offsets[]). x A^T and dy B have 16-bit operands on
-// both sides and run on the 16-bit matrix instructions; their results h and g stay fp32, and the
-// products they enter run on the fp32 matrix instruction, so that nothing is
-// rounded between the two factors of an adapter.
+// Rows come sorted by adapter (rows[], offsets[]); a workgroup takes up to 16
+// or 32 rows of one adapter and forms both products of them, so h and g never leave
+// the chip (but for the copies that dA and dB sum over). x A^T and dy B have
+// 16-bit operands on both sides and run on the 16-bit matrix instructions. Their
+// results h and g are fp32 and enter the second product as sums of
+// 16-bit parts (three exact ones in bf16; two in fp16, at the scale of the row's
+// largest value, 22 bits), so that nothing is rounded between the two factors
+// beyond fp32's own precision: the 16-bit matrix instructions at two or three times the work are
+// still three to five times faster than the fp32 one.
 
 #include "grouped_device.h"
 
@@ -17,14 +22,14 @@ namespace {
 
 constexpr int kWaves = 8;                // waves of a workgroup
 constexpr int kAdThreads = 64 * kWaves;
-constexpr int kRowBlocks = 2;            // 16-row blocks of a workgroup
-constexpr int kAdRows = 16 * kRowBlocks;
 
-// Eight elements of which `left` exist (no more than eight are read).
+typedef s8 __attribute__((aligned(2))) s8_any;
+// Eight elements of which `left` exist (no more are read).
 __device__ __forceinline__ s8 load8(const uint16_t *p, int left, bool vec) {
   s8 v = {0, 0, 0, 0, 0, 0, 0, 0};
-  if (vec) {
-    if (left > 0) v = *reinterpret_cast<const s8 *>(p);
+  if (left >= 8) {
+    if (vec) v = *reinterpret_cast<const s8 *>(p);
+    else v = *reinterpret_cast<const s8_any *>(p);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -34,8 +39,9 @@ __device__ __forceinline__ s8 load8(const uint16_t *p, int left, bool vec) {
 }
 
 // The rows of a workgroup: places [at, at + n) of the sorted order, adapter e
-// (-1: rows without one), or n == 0.
+// (-1: rows without one), or n <= 0.
 struct RowBlock { int e, at, n; };
+template <int kAdRows>
 __device__ __forceinline__ RowBlock find_rows(const int32_t *offsets, int adapters, int T, int m) {
   const GroupTile g = find_group(offsets, adapters, T, kAdRows, [&](int) { return m; });
   RowBlock b;
@@ -60,11 +66,24 @@ __device__ __forceinline__ int row_of(const int32_t *rows, const RowBlock &b, in
   return t >= 0 && t < T ? t : -1;
 }
 
+// LDS of a workgroup: the waves' partial first products ([wave][row block][rank tile][lane]),
+// and before and after that each wave's own staging area.
+template <int RT>
+constexpr int kStageBytes = 16 * RT * 144;   // 16 RT rank rows of 64 columns, 16 bytes apart from each other's banks
+template <int RT>
+constexpr int kAdLds = kWaves * kStageBytes<RT>;
+
 // Sum the waves' partial products and scale them. part[w][rb][rt][lane] holds
 // row 16 rb + lane % 16, columns 16 rt + 4 (lane / 16) .. of wave w. The sums
 // replace wave 0's partials.
 template <int RB, int RT>
-__device__ __forceinline__ void join_waves(f4 *part, float scale) {
+__device__ __forceinline__ void join_waves(f4 *part, const f4 (&acc)[RB][RT], float scale) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __syncthreads();
+#pragma unroll
+  for (int b = 0; b < RB; ++b)
+#pragma unroll
+    for (int j = 0; j < RT; ++j) part[((wave * RB + b) * RT + j) * 64 + lane] = acc[b][j];
   __syncthreads();
   for (int u = threadIdx.x; u < RB * RT * 64; u += kAdThreads) {
     f4 s = part[u];
@@ -75,98 +94,232 @@ __device__ __forceinline__ void join_waves(f4 *part, float scale) {
   __syncthreads();
 }
 
-// x A^T of the block's rows, inputs split over the waves.
+// x A^T of the block's rows, inputs split over the waves: acc[b][j] holds row
+// 16 b + p16, rank 16 j + 4 q4 .. of this wave's share.
 template <typename Tr, int RB, int RT>
 __device__ __forceinline__ void down_product(const uint16_t *x, int64_t ld_x, const int (&row)[RB], const uint16_t *A, int r,
-                                             int K, bool vec, f4 *part) {
+                                             int K, bool vec, f4 (&acc)[RB][RT]) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, p16 = lane & 15, q4 = lane >> 4;
-  f4 acc[RB][RT];
+  constexpr int kDeep = RB * RT == 1 ? 8 : RT <= 2 ? 4 / RB : 1;  // steps whose loads are in flight together
+  for (int k0 = 32 * wave; k0 < K; k0 += 32 * kWaves * kDeep) {
+    s8 xv[kDeep][RB], av[kDeep][RT];
 #pragma unroll
-  for (int b = 0; b < RB; ++b)
+    for (int u = 0; u < kDeep; ++u) {
+      const int k = k0 + 32 * kWaves * u + 8 * q4;
 #pragma unroll
-    for (int j = 0; j < RT; ++j) acc[b][j] = f4{0.f, 0.f, 0.f, 0.f};
-  for (int k0 = 32 * wave; k0 < K; k0 += 32 * kWaves) {
-    const int k = k0 + 8 * q4;
-    s8 xv[RB], av[RT];
+      for (int j = 0; j < RT; ++j) av[u][j] = load8(A + (int64_t)min(16 * j + p16, r - 1) * K + k, 16 * j + p16 < r ? K - k : 0, vec);
+    }
 #pragma unroll
-    for (int b = 0; b < RB; ++b) xv[b] = load8(x + (int64_t)max(row[b], 0) * ld_x + k, row[b] >= 0 ? K - k : 0, vec);
+    for (int u = 0; u < kDeep; ++u) {  // behind A's: the row numbers may still be on their way
+      const int k = k0 + 32 * kWaves * u + 8 * q4;
 #pragma unroll
-    for (int j = 0; j < RT; ++j) av[j] = load8(A + (int64_t)min(16 * j + p16, r - 1) * K + k, 16 * j + p16 < r ? K - k : 0, vec);
+      for (int b = 0; b < RB; ++b) xv[u][b] = load8(x + (int64_t)max(row[b], 0) * ld_x + k, row[b] >= 0 ? K - k : 0, vec);
+    }
 #pragma unroll
-    for (int b = 0; b < RB; ++b)
+    for (int u = 0; u < kDeep; ++u)
 #pragma unroll
-      for (int j = 0; j < RT; ++j) acc[b][j] = Tr::mfma(av[j], xv[b], acc[b][j]);
+      for (int b = 0; b < RB; ++b)
+#pragma unroll
+        for (int j = 0; j < RT; ++j) acc[b][j] = Tr::mfma(av[u][j], xv[u][b], acc[b][j]);
   }
-#pragma unroll
-  for (int b = 0; b < RB; ++b)
-#pragma unroll
-    for (int j = 0; j < RT; ++j) part[((wave * RB + b) * RT + j) * 64 + lane] = acc[b][j];
 }
 
-__device__ __forceinline__ f4 mfma32(float a, float b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
+// ------------------------------------------------------- the second product
+// out[i][c] = sum_j h[i][j] m[j][c] with h fp32 in `part` as join_waves left
+// it. h is cut into 16-bit parts; the matrix instruction's 32 terms hold 32 ranks of a part, or, at one
+// rank tile, 16 ranks of two parts.
+template <typename Tr> constexpr int kParts = 2;
+template <> constexpr int kParts<Bf16> = 3;
+template <typename Tr, int RT> constexpr int kTerms = RT == 1 ? (kParts<Tr> + 1) / 2 : kParts<Tr> * RT / 2;  // instructions per block
 
-// Sixteen consecutive values of base or y.
+// Part `n` of v. bf16: the leading, middle and last eight bits, exact. fp16: the nearest, and what is left.
+// An infinity or NaN is all in the first part.
+__device__ __forceinline__ bool finite(float v) { return (__builtin_bit_cast(uint32_t, v) & 0x7f800000u) != 0x7f800000u; }
 template <typename Tr>
-__device__ __forceinline__ void load16(const void *p, int64_t at, bool f32, bool vec, int left, float *f) {
-  if (f32) {
-    const float *q = static_cast<const float *>(p) + at;
+__device__ __forceinline__ uint16_t part_of(float v, int n);
+template <>
+__device__ __forceinline__ uint16_t part_of<Bf16>(float v, int n) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (vec && left >= 16) {
-        const f4 v = reinterpret_cast<const f4 *>(q)[i];
-        f[4 * i] = v[0]; f[4 * i + 1] = v[1]; f[4 * i + 2] = v[2]; f[4 * i + 3] = v[3];
-      } else {
+  for (int i = 0; i < n; ++i) v = finite(v) ? v - __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, v) & 0xffff0000u) : 0.f;
+  return (uint16_t)(__builtin_bit_cast(uint32_t, v) >> 16);
+}
+template <>
+__device__ __forceinline__ uint16_t part_of<Fp16>(float v, int n) {
+  if (n) v = finite(v) ? v - Fp16::to(Fp16::from(v)) : 0.f;
+  return Fp16::from(v);
+}
+
+template <typename Tr, int RB, int RT>
+struct Cut {
+  s8 v[RB][kTerms<Tr, RT>];  // operand of row p16
+  float unscale[RB];         // what a sum is multiplied by (1 in bf16)
+};
+
+template <typename Tr, int RB, int RT>
+__device__ __forceinline__ void cut(const f4 *part, Cut<Tr, RB, RT> &c) {
+  const int lane = threadIdx.x & 63, p16 = lane & 15, q4 = lane >> 4;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) f[4 * i + x] = 4 * i + x < left ? q[4 * i + x] : 0.f;
+  for (int b = 0; b < RB; ++b) {
+    float scale = 1.f;
+    c.unscale[b] = 1.f;
+    if constexpr (kParts<Tr> == 2) {  // powers of two that bring the row's largest value to [2^14, 2^15)
+      float top = 0.f;
+#pragma unroll
+      for (int j = 0; j < RT; ++j) {
+        const f4 h = part[(b * RT + j) * 64 + lane];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) top = fmaxf(top, fabsf(h[x]));
+      }
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      if (finite(top) && top > 0.f) {
+        const int e = min(max(__builtin_amdgcn_frexp_expf(top), -100), 100);
+        scale = ldexpf(1.f, 15 - e);
+        c.unscale[b] = ldexpf(1.f, e - 15);
       }
     }
-  } else {
-    const uint16_t *q = static_cast<const uint16_t *>(p) + at;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const s8 v = load8(q + 8 * i, left - 8 * i, vec && left >= 16);
+    for (int m = 0; m < kTerms<Tr, RT>; ++m) {
+      const int n = RT == 1 ? 2 * m + (q4 >> 1) : m / (RT / 2 ? RT / 2 : 1);
+      const int j = RT == 1 ? 8 * (q4 & 1) : 32 * (m % (RT / 2 ? RT / 2 : 1)) + 8 * q4;  // first of this lane's eight ranks
+      const f4 *q = part + (b * RT + (j >> 4)) * 64 + p16 + 16 * ((j >> 2) & 3);
+      const f4 lo = q[0], hi = q[16];
 #pragma unroll
-      for (int x = 0; x < 8; ++x) f[8 * i + x] = Tr::to((uint16_t)v[x]);
+      for (int x = 0; x < 8; ++x) {
+        const float h = (x < 4 ? lo[x & 3] : hi[x & 3]) * scale;
+        if constexpr (RT == 1) {
+          const uint16_t a = part_of<Tr>(h, 2 * m), z = 2 * m + 1 < kParts<Tr> ? part_of<Tr>(h, 2 * m + 1) : (uint16_t)0;
+          c.v[b][m][x] = (short)(q4 >> 1 ? z : a);
+        } else {
+          c.v[b][m][x] = (short)part_of<Tr>(h, n);
+        }
+      }
     }
   }
 }
-template <typename Tr>
-__device__ __forceinline__ void store16(void *p, int64_t at, bool f32, bool vec, int left, const float *f) {
-  if (f32) {
-    float *q = static_cast<float *>(p) + at;
-    if (vec && left >= 16) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) reinterpret_cast<f4 *>(q)[i] = f4{f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]};
+
+// Eight consecutive values of base or y from element `at` on, of which `left` exist, as they lie in memory.
+template <bool F32> struct Eight { u4 v[F32 ? 2 : 1]; };
+template <bool F32>
+__device__ __forceinline__ Eight<F32> load_out(const void *p, int64_t at, bool vec, int left) {
+  Eight<F32> e;
+  if constexpr (F32) {
+    const uint32_t *q = static_cast<const uint32_t *>(p) + at;
+    if (vec && left >= 8) {
+      e.v[0] = reinterpret_cast<const u4 *>(q)[0];
+      e.v[1] = reinterpret_cast<const u4 *>(q)[1];
     } else {
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
+      for (int i = 0; i < 8; ++i) e.v[i >> 2][i & 3] = i < left ? q[i] : 0u;
+    }
+  } else {
+    e.v[0] = __builtin_bit_cast(u4, load8(static_cast<const uint16_t *>(p) + at, left, vec));
+  }
+  return e;
+}
+template <typename Tr, bool F32>
+__device__ __forceinline__ float value_of(const Eight<F32> &e, int i) {
+  if constexpr (F32) return __builtin_bit_cast(float, (uint32_t)e.v[i >> 2][i & 3]);
+  else return Tr::to((uint16_t)(e.v[0][i >> 1] >> (16 * (i & 1))));
+}
+template <typename Tr, bool F32>
+__device__ __forceinline__ void store_out(void *p, int64_t at, bool vec, int left, const float *f) {
+  if constexpr (F32) {
+    float *q = static_cast<float *>(p) + at;
+    if (vec && left >= 8) {
+      reinterpret_cast<f4 *>(q)[0] = f4{f[0], f[1], f[2], f[3]};
+      reinterpret_cast<f4 *>(q)[1] = f4{f[4], f[5], f[6], f[7]};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
         if (i < left) q[i] = f[i];
     }
   } else {
     uint16_t *q = static_cast<uint16_t *>(p) + at;
-    if (vec && left >= 16) {
+    if (vec && left >= 8) {
+      u4 v;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        u4 v;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) v[x] = (uint32_t)Tr::from(f[8 * i + 2 * x]) | (uint32_t)Tr::from(f[8 * i + 2 * x + 1]) << 16;
-        reinterpret_cast<u4 *>(q)[i] = v;
-      }
+      for (int x = 0; x < 4; ++x) v[x] = (uint32_t)Tr::from(f[2 * x]) | (uint32_t)Tr::from(f[2 * x + 1]) << 16;
+      *reinterpret_cast<u4 *>(q) = v;
     } else {
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
+      for (int i = 0; i < 8; ++i)
         if (i < left) q[i] = Tr::from(f[i]);
     }
   }
 }
 
-// Forward. blockIdx.x: block of rows, blockIdx.y: slice of 64 kWaves columns of y (every
-// slice forms h for itself).
-template <typename Tr, int RT>
-__global__ __launch_bounds__(kAdThreads) void adapter_kernel(AdapterArgs a, int slice) {
-  constexpr int RB = kRowBlocks;
+// What the second product adds to and writes.
+struct OutRows {
+  const void *base;
+  int64_t ld_base;
+  void *out;
+  int64_t ld_out;
+  bool vec;
+};
+
+// A wave's 64 columns from n0 on: four 16-column blocks. Block c, operand row m
+// is column 32 (c / 2) + 8 (m / 4) + 4 (c % 2) + m % 4, so that a lane
+// ends with two runs of eight columns, n0 + 8 q4 and n0 + 32 + 8 q4.
+template <bool F32, int RB>
+__device__ __forceinline__ void load_base(const OutRows &o, const int (&row)[RB], int n0, int end, Eight<F32> (&f)[RB][2]) {
+  const int q4 = (threadIdx.x & 63) >> 4;
+#pragma unroll
+  for (int b = 0; b < RB; ++b)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int col = n0 + 32 * h + 8 * q4;
+      f[b][h] = load_out<F32>(o.base, (int64_t)max(row[b], 0) * o.ld_base + col, o.vec, o.base && row[b] >= 0 ? end - col : 0);
+    }
+}
+template <typename Tr, bool F32, int RB, int RT>
+__device__ __forceinline__ void finish(const OutRows &o, const int (&row)[RB], int n0, int end, const Cut<Tr, RB, RT> &h,
+                                       const s8 (&m)[4][RT / 2 ? RT / 2 : 1], const Eight<F32> (&base)[RB][2]) {
+  const int q4 = (threadIdx.x & 63) >> 4;
+#pragma unroll
+  for (int b = 0; b < RB; ++b)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      float f[8];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        f4 acc = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int u = 0; u < kTerms<Tr, RT>; ++u) acc = Tr::mfma(m[2 * x + c][u % (RT / 2 ? RT / 2 : 1)], h.v[b][u], acc);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) f[4 * c + y] = value_of<Tr, F32>(base[b][x], 4 * c + y) + acc[y] * h.unscale[b];
+      }
+      const int col = n0 + 32 * x + 8 * q4;
+      if (row[b] >= 0 && col < end) store_out<Tr, F32>(o.out, (int64_t)row[b] * o.ld_out + col, o.vec, end - col, f);
+    }
+}
+
+// Rows without an adapter: out = base.
+template <typename Tr, bool F32, int RB>
+__device__ __forceinline__ void copy_rows(const OutRows &o, const int (&row)[RB], int begin, int end) {
+  const int wave = threadIdx.x >> 6, q4 = (threadIdx.x & 63) >> 4;
+  for (int n0 = begin + 64 * wave; n0 < end; n0 += 64 * kWaves) {
+    Eight<F32> e[RB][2];
+    load_base<F32, RB>(o, row, n0, end, e);
+#pragma unroll
+    for (int b = 0; b < RB; ++b)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int col = n0 + 32 * x + 8 * q4;
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = value_of<Tr, F32>(e[b][x], i);
+        if (row[b] >= 0 && col < end) store_out<Tr, F32>(o.out, (int64_t)row[b] * o.ld_out + col, o.vec, end - col, f);
+      }
+  }
+}
+
+// Forward. blockIdx.x: block of rows, blockIdx.y: slice of y's columns (every slice forms h for itself).
+template <typename Tr, int RT, int RB, bool F32>
+__global__ __launch_bounds__(kAdThreads, RT <= 2 ? 4 : 2) void adapter_kernel(AdapterArgs a, int slice) {
+  constexpr int NM = RT / 2 ? RT / 2 : 1;
   __shared__ __attribute__((aligned(16))) f4 s_part[kWaves * RB * RT * 64];
-  const RowBlock blk = find_rows(a.offsets, a.n, a.T, blockIdx.x);
+  const RowBlock blk = find_rows<16 * RB>(a.offsets, a.n, a.T, blockIdx.x);
   if (blk.n <= 0) return;
   const bool same = a.base == a.y && a.ld_base == a.ld_y;
   if (blk.e < 0 && same) return;
@@ -174,81 +327,60 @@ __global__ __launch_bounds__(kAdThreads) void adapter_kernel(AdapterArgs a, int 
   int row[RB];
 #pragma unroll
   for (int b = 0; b < RB; ++b) row[b] = row_of(a.rows, blk, 16 * b + p16, a.T);
-  f4 h[RB][RT];
+  const OutRows o{a.base, a.ld_base, a.y, a.ld_y, a.vec_y != 0};
+  const int begin = blockIdx.y * slice, end = min(a.N, begin + slice);
+  if (blk.e < 0) {
+    copy_rows<Tr, F32, RB>(o, row, begin, end);
+    return;
+  }
+  const uint16_t *B = a.B + (int64_t)blk.e * a.N * a.r;
+  s8 m[4][NM];
+  Eight<F32> f[RB][2];
+  auto ask = [&](int n0) {  // a chunk's B and base
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int n = n0 + 32 * (c >> 1) + 8 * (p16 >> 2) + 4 * (c & 1) + (p16 & 3);
+#pragma unroll
+      for (int u = 0; u < NM; ++u) {
+        const int j = RT == 1 ? 8 * (q4 & 1) : 32 * u + 8 * q4;
+        m[c][u] = load8(B + (int64_t)n * a.r + j, n < end ? a.r - j : 0, a.vec_b);
+      }
+    }
+    load_base<F32, RB>(o, row, n0, end, f);
+  };
+  int n0 = begin + 64 * wave;
+  if (n0 < end) ask(n0);  // the first chunk's, beside the first product
+  f4 acc[RB][RT];
 #pragma unroll
   for (int b = 0; b < RB; ++b)
 #pragma unroll
-    for (int j = 0; j < RT; ++j) h[b][j] = f4{0.f, 0.f, 0.f, 0.f};
-  if (blk.e >= 0) {
-    down_product<Tr, RB, RT>(a.x, a.ld_x, row, a.A + (int64_t)blk.e * a.r * a.K, a.r, a.K, a.vec_x, s_part);
-    join_waves<RB, RT>(s_part, a.scale ? a.scale[blk.e] : 1.f);
-#pragma unroll
-    for (int b = 0; b < RB; ++b)
-#pragma unroll
-      for (int j = 0; j < RT; ++j) h[b][j] = s_part[(b * RT + j) * 64 + lane];
-  }
-  // wave's 64 columns: block c holds, as its row m, column 16 (m / 4) + 4 c +
-  // m % 4, so that a lane ends with 16 consecutive columns of its row of y
-  const uint16_t *B = a.B + (int64_t)max(blk.e, 0) * a.N * a.r;
-  const int n_end = min(a.N, (int)(blockIdx.y + 1) * slice);
-  for (int n0 = blockIdx.y * slice + 64 * wave; n0 < n_end; n0 += 64 * kWaves) {
-    f4 acc[RB][4];
-#pragma unroll
-    for (int b = 0; b < RB; ++b)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) acc[b][c] = f4{0.f, 0.f, 0.f, 0.f};
-    if (blk.e >= 0) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int n = n0 + 16 * (p16 >> 2) + 4 * c + (p16 & 3);
-#pragma unroll
-        for (int j = 0; j < RT; ++j) {
-          const int left = n < a.N ? a.r - (16 * j + 4 * q4) : 0;
-          const uint16_t *q = B + (int64_t)n * a.r + 16 * j + 4 * q4;
-          uint16_t w[4] = {0, 0, 0, 0};
-          if (a.vec_b) {
-            if (left > 0) {
-              const u2 v = *reinterpret_cast<const u2 *>(q);
-              w[0] = (uint16_t)v[0]; w[1] = (uint16_t)(v[0] >> 16); w[2] = (uint16_t)v[1]; w[3] = (uint16_t)(v[1] >> 16);
-            }
-          } else {
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              if (x < left) w[x] = q[x];
-          }
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-#pragma unroll
-            for (int b = 0; b < RB; ++b) acc[b][c] = mfma32(Tr::to(w[x]), h[b][j][x], acc[b][c]);
-        }
-      }
-    }
-    const int col = n0 + 16 * q4;
-    if (col >= n_end) continue;
-    const int left = n_end - col;
-#pragma unroll
-    for (int b = 0; b < RB; ++b) {
-      if (row[b] < 0) continue;
-      float f[16];
-      if (a.base) {
-        load16<Tr>(a.base, (int64_t)row[b] * a.ld_base + col, a.y_f32, a.vec_y, left, f);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) f[i] = 0.f;
-      }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) f[i] += acc[b][i >> 2][i & 3];
-      store16<Tr>(a.y, (int64_t)row[b] * a.ld_y + col, a.y_f32, a.vec_y, left, f);
-    }
+    for (int j = 0; j < RT; ++j) acc[b][j] = f4{0.f, 0.f, 0.f, 0.f};
+  down_product<Tr, RB, RT>(a.x, a.ld_x, row, a.A + (int64_t)blk.e * a.r * a.K, a.r, a.K, a.vec_x, acc);
+  join_waves<RB, RT>(s_part, acc, a.scale ? a.scale[blk.e] : 1.f);
+  Cut<Tr, RB, RT> h;
+  cut<Tr, RB, RT>(s_part, h);
+  for (; n0 < end; n0 += 64 * kWaves) {
+    finish<Tr, F32, RB, RT>(o, row, n0, end, h, m, f);
+    if (n0 + 64 * kWaves < end) ask(n0 + 64 * kWaves);
   }
 }
 
+// Four consecutive values of column `c` of a tile of 16-bit rows of `bytes` bytes in LDS, for the lane's place in
+// its 16: rows row0 + 0 .. 3 of column c0 + step (p16 / 4) + p16 % 4.
+__device__ __forceinline__ s4 column4(const uint8_t *t, int bytes, int row0, int c0, int step) {
+  const int p16 = threadIdx.x & 15;
+  return read_lds_tr(t + (row0 + (p16 >> 2)) * bytes + 2 * (c0 + step * (p16 & 3)));
+}
+
 // Gradient by rows: g and h of every sorted place into the workspace, and dx.
-template <typename Tr, int RT>
-__global__ __launch_bounds__(kAdThreads) void adapter_rows_grad_kernel(AdapterGradArgs a, int slice) {
-  constexpr int RB = kRowBlocks;
-  __shared__ __attribute__((aligned(16))) f4 s_part[kWaves * RB * RT * 64];
-  const RowBlock blk = find_rows(a.offsets, a.n, a.T, blockIdx.x);
+// Both operands that lie across (B for g, A for dx) pass through a staging area of the wave.
+template <typename Tr, int RT, int RB, bool F32>
+__global__ __launch_bounds__(kAdThreads, RT <= 2 ? 4 : 2) void adapter_rows_grad_kernel(AdapterGradArgs a, int slice) {
+  constexpr int NM = RT / 2 ? RT / 2 : 1;
+  __shared__ __attribute__((aligned(16))) uint8_t s_mem[kAdLds<RT>];
+  static_assert(kAdLds<RT> >= kWaves * RB * RT * 1024, "the partial products fit");
+  f4 *s_part = reinterpret_cast<f4 *>(s_mem);
+  const RowBlock blk = find_rows<16 * RB>(a.offsets, a.n, a.T, blockIdx.x);
   if (blk.n <= 0) return;
   const bool same = a.dx_base == a.dx && a.ld_dx_base == a.ld_dx;
   if (blk.e < 0 && (!a.dx || same)) return;
@@ -256,112 +388,118 @@ __global__ __launch_bounds__(kAdThreads) void adapter_rows_grad_kernel(AdapterGr
   int row[RB];
 #pragma unroll
   for (int b = 0; b < RB; ++b) row[b] = row_of(a.rows, blk, 16 * b + p16, a.T);
-  f4 g[RB][RT];
-#pragma unroll
-  for (int b = 0; b < RB; ++b)
-#pragma unroll
-    for (int j = 0; j < RT; ++j) g[b][j] = f4{0.f, 0.f, 0.f, 0.f};
-  const uint16_t *A = a.A + (int64_t)max(blk.e, 0) * a.r * a.K;
-  if (blk.e >= 0) {
-    const float scale = a.scale ? a.scale[blk.e] : 1.f;
-    // this workgroup's share of h and g in the workspace (slice 0 writes them)
-    auto keep = [&](float *dst) {
-      if (!dst || blockIdx.y) return;
-      for (int u = threadIdx.x; u < RB * RT * 64; u += kAdThreads) {
-        const int l = u & 63, j = (u >> 6) % RT, b = (u >> 6) / RT;
-        const int i = 16 * b + (l & 15);
-        if (i < blk.n) *reinterpret_cast<f4 *>(dst + ((int64_t)(blk.at + i) * RT + j) * 16 + 4 * (l >> 4)) = s_part[u];
-      }
-    };
-    if (a.dB && blockIdx.y == 0) {
-      down_product<Tr, RB, RT>(a.x, a.ld_x, row, A, a.r, a.K, a.vec_x, s_part);
-      join_waves<RB, RT>(s_part, scale);
-      keep(a.h);
-      __syncthreads();
+  const OutRows o{a.dx_base, a.ld_dx_base, a.dx, a.ld_dx, a.vec_dx != 0};
+  const int begin = blockIdx.y * slice, end = min(a.K, begin + slice);
+  if (blk.e < 0) {
+    copy_rows<Tr, F32, RB>(o, row, begin, end);
+    return;
+  }
+  uint8_t *mine = s_mem + wave * kStageBytes<RT>;
+  const uint16_t *A = a.A + (int64_t)blk.e * a.r * a.K;
+  const uint16_t *B = a.B + (int64_t)blk.e * a.N * a.r;
+  const float scale = a.scale ? a.scale[blk.e] : 1.f;
+  // the block's h or g into the workspace (slice 0 writes them)
+  auto keep = [&](float *dst) {
+    if (!dst || blockIdx.y) return;
+    for (int u = threadIdx.x; u < RB * RT * 64; u += kAdThreads) {
+      const int l = u & 63, j = (u >> 6) % RT, b = (u >> 6) / RT;
+      const int i = 16 * b + (l & 15);
+      if (i < blk.n) *reinterpret_cast<f4 *>(dst + ((int64_t)(blk.at + i) * RT + j) * 16 + 4 * (l >> 4)) = s_part[u];
     }
-    // g: dy rows by B, columns split over the waves; B lies across
-    const uint16_t *B = a.B + (int64_t)blk.e * a.N * a.r;
-    for (int n0 = 32 * wave; n0 < a.N; n0 += 32 * kWaves) {
-      const int n = n0 + 8 * q4;
-      s8 dv[RB];
+  };
+  f4 acc[RB][RT];
+  auto clear = [&]() {
 #pragma unroll
-      for (int b = 0; b < RB; ++b) dv[b] = load8(a.dy + (int64_t)max(row[b], 0) * a.ld_dy + n, row[b] >= 0 ? a.N - n : 0, a.vec_dy);
+    for (int b = 0; b < RB; ++b)
+#pragma unroll
+      for (int j = 0; j < RT; ++j) acc[b][j] = f4{0.f, 0.f, 0.f, 0.f};
+  };
+  if (a.dB && blockIdx.y == 0) {
+    clear();
+    down_product<Tr, RB, RT>(a.x, a.ld_x, row, A, a.r, a.K, a.vec_x, acc);
+    join_waves<RB, RT>(s_part, acc, scale);
+    keep(a.h);
+    __syncthreads();
+  }
+  // g: 32 columns of dy at a time, split over the waves; 32 rows of B are staged as 16 RT ranks each
+  clear();
+  constexpr int kDeep = RT <= 2 ? 4 / RB : 1;  // steps whose loads are in flight together
+  static_assert(RT * 1024 <= kStageBytes<RT>, "a step of B fits");
+  for (int n0 = 32 * wave; n0 < a.N; n0 += 32 * kWaves * kDeep) {
+    s8 dv[kDeep][RB], bv[kDeep][RT];
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u) {
+      const int n1 = n0 + 32 * kWaves * u, n = n1 + 8 * q4;
+#pragma unroll
+      for (int b = 0; b < RB; ++b) dv[u][b] = load8(a.dy + (int64_t)max(row[b], 0) * a.ld_dy + n, row[b] >= 0 ? a.N - n : 0, a.vec_dy);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        const int unit = lane + 64 * i, nb = n1 + unit / (2 * RT), j = 8 * (unit % (2 * RT));
+        bv[u][i] = load8(B + (int64_t)nb * a.r + j, nb < a.N ? a.r - j : 0, a.vec_b);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u) {
+#pragma unroll
+      for (int i = 0; i < RT; ++i) *reinterpret_cast<s8 *>(mine + 16 * (lane + 64 * i)) = bv[u][i];
+      wave_sync();
 #pragma unroll
       for (int j = 0; j < RT; ++j) {
-        s8 bv = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (16 * j + p16 < a.r) {
+        const s4 lo = column4(mine, 32 * RT, 8 * q4, 16 * j, 4), hi = column4(mine, 32 * RT, 8 * q4 + 4, 16 * j, 4);
+        const s8 w = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
 #pragma unroll
-          for (int x = 0; x < 8; ++x)
-            if (n + x < a.N) bv[x] = (short)B[(int64_t)(n + x) * a.r + 16 * j + p16];
-        }
-#pragma unroll
-        for (int b = 0; b < RB; ++b) g[b][j] = Tr::mfma(bv, dv[b], g[b][j]);
+        for (int b = 0; b < RB; ++b) acc[b][j] = Tr::mfma(w, dv[u][b], acc[b][j]);
       }
+      wave_sync();
     }
-#pragma unroll
-    for (int b = 0; b < RB; ++b)
-#pragma unroll
-      for (int j = 0; j < RT; ++j) s_part[((wave * RB + b) * RT + j) * 64 + lane] = g[b][j];
-    join_waves<RB, RT>(s_part, scale);
-    keep(a.g);
-#pragma unroll
-    for (int b = 0; b < RB; ++b)
-#pragma unroll
-      for (int j = 0; j < RT; ++j) g[b][j] = s_part[(b * RT + j) * 64 + lane];
   }
+  join_waves<RB, RT>(s_part, acc, scale);
+  keep(a.g);
   if (!a.dx) return;
-  // dx: a wave's 64 columns as in the forward kernel
-  const int k_end = min(a.K, (int)(blockIdx.y + 1) * slice);
-  for (int k0 = blockIdx.y * slice + 64 * wave; k0 < k_end; k0 += 64 * kWaves) {
-    f4 acc[RB][4];
+  Cut<Tr, RB, RT> g;
+  cut<Tr, RB, RT>(s_part, g);
+  __syncthreads();  // the staging areas take the partials' place
+  for (int k0 = begin + 64 * wave; k0 < end; k0 += 64 * kWaves) {
+    Eight<F32> f[RB][2];
+    s8 av[2 * RT];
 #pragma unroll
-    for (int b = 0; b < RB; ++b)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) acc[b][c] = f4{0.f, 0.f, 0.f, 0.f};
-    if (blk.e >= 0) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int k = k0 + 16 * (p16 >> 2) + 4 * c + (p16 & 3);
-#pragma unroll
-        for (int j = 0; j < RT; ++j)
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int i = 16 * j + 4 * q4 + x;
-            const float w = i < a.r && k < a.K ? Tr::to(A[(int64_t)i * a.K + k]) : 0.f;
-#pragma unroll
-            for (int b = 0; b < RB; ++b) acc[b][c] = mfma32(w, g[b][j][x], acc[b][c]);
-          }
-      }
+    for (int i = 0; i < 2 * RT; ++i) {
+      const int unit = lane + 64 * i, j = unit >> 3, col = k0 + 8 * (unit & 7);
+      av[i] = load8(A + (int64_t)j * a.K + col, j < a.r ? end - col : 0, a.vec_x);
     }
-    const int col = k0 + 16 * q4;
-    if (col >= k_end) continue;
-    const int left = k_end - col;
+    load_base<F32, RB>(o, row, k0, end, f);
 #pragma unroll
-    for (int b = 0; b < RB; ++b) {
-      if (row[b] < 0) continue;
-      float f[16];
-      if (a.dx_base) {
-        load16<Tr>(a.dx_base, (int64_t)row[b] * a.ld_dx_base + col, a.dx_f32, a.vec_dx, left, f);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) f[i] = 0.f;
-      }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) f[i] += acc[b][i >> 2][i & 3];
-      store16<Tr>(a.dx, (int64_t)row[b] * a.ld_dx + col, a.dx_f32, a.vec_dx, left, f);
+    for (int i = 0; i < 2 * RT; ++i) {
+      const int unit = lane + 64 * i;
+      *reinterpret_cast<s8 *>(mine + (unit >> 3) * 144 + 16 * (unit & 7)) = av[i];
     }
+    wave_sync();
+    s8 m[4][NM];
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int u = 0; u < NM; ++u) {
+        const int j = RT == 1 ? 8 * (q4 & 1) : 32 * u + 8 * q4, c0 = 32 * (c >> 1) + 4 * (c & 1);
+        const s4 lo = column4(mine, 144, j, c0, 8), hi = column4(mine, 144, j + 4, c0, 8);
+        m[c][u] = s8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+      }
+    wave_sync();
+    finish<Tr, F32, RB, RT>(o, row, k0, end, g, m, f);
   }
 }
 
+__device__ __forceinline__ f4 mfma32(float a, float b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
+
 // Gradient of the adapters: out[c][j] = sum over the adapter's rows of
 // v[row][c] * m[place][j], v = x (dA, c = k) or dy (dB, c = n), m = g or h.
-// A workgroup owns 128 columns of one adapter and up to four 16-wide rank
-// tiles; its waves take every eighth group of four rows. Lane (p16, q4) reads
-// eight consecutive columns 8 p16 .. of row q4, and the matrix instruction
-// number x takes column 8 p16 + x.
+// A workgroup owns 64 columns of one adapter; its waves take every eighth
+// group of four rows, and join in LDS. Lane (p16, q4) reads four consecutive columns 4 p16 .. of
+// row q4, and the fp32 matrix instruction number x takes column 4 p16 + x. Rows are asked for
+// kRowsDeep groups at a time, their numbers one batch earlier.
+constexpr int kRowsDeep = 8;
 template <typename Tr, int RT>
-__global__ __launch_bounds__(kAdThreads) void adapter_weights_grad_kernel(AdapterGradArgs a, int tiles_a, int tiles_all, int rank_tiles) {
-  __shared__ __attribute__((aligned(16))) f4 s_part[kWaves / 2 * RT * 8 * 64];
+__global__ __launch_bounds__(kAdThreads) void adapter_weights_grad_kernel(AdapterGradArgs a, int tiles_a, int tiles_all) {
+  __shared__ __attribute__((aligned(16))) f4 s_part[kWaves * (RT < 4 ? RT : 4) * 4 * 64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, p16 = lane & 15, q4 = lane >> 4;
   const int e = blockIdx.x / tiles_all;
   int tile = blockIdx.x - e * tiles_all;
@@ -372,71 +510,90 @@ __global__ __launch_bounds__(kAdThreads) void adapter_weights_grad_kernel(Adapte
   const float *m = is_a ? a.g : a.h;
   const int C = is_a ? a.K : a.N;
   const bool vec = is_a ? a.vec_x : a.vec_dy;
-  const int c0 = 128 * tile, j0 = 16 * RT * blockIdx.y, ldm = 16 * rank_tiles;
+  const int c0 = 64 * tile;
   const int first = min(max(a.offsets[e], 0), a.T);
   const int count = max(min(max(a.offsets[e + 1], 0), a.T) - first, 0);
   void *out = is_a ? a.dA : a.dB;
   if (count == 0 && a.accumulate) return;
-  f4 acc[RT][8];
+  f4 acc[RT][4];
 #pragma unroll
   for (int j = 0; j < RT; ++j)
 #pragma unroll
-    for (int x = 0; x < 8; ++x) acc[j][x] = f4{0.f, 0.f, 0.f, 0.f};
-  const int c = c0 + 8 * p16;
-  for (int i = 4 * wave + q4; i < (count + 3) / 4 * 4; i += 4 * kWaves) {
-    int t = -1;
-    if (i < count) t = a.rows[first + i];
-    const bool ok = t >= 0 && t < a.T;
-    const s8 vv = load8(v + (int64_t)(ok ? t : 0) * ld + c, ok ? C - c : 0, vec);
-    float mv[RT];
+    for (int x = 0; x < 4; ++x) acc[j][x] = f4{0.f, 0.f, 0.f, 0.f};
+  const int c = c0 + 4 * p16, left = C - c;
+  int at[kRowsDeep];
+  auto numbers = [&](int i0) {
 #pragma unroll
-    for (int j = 0; j < RT; ++j) mv[j] = ok ? m[(int64_t)(first + i) * ldm + j0 + 16 * j + p16] : 0.f;
-#pragma unroll
-    for (int x = 0; x < 8; ++x) {
-      const float f = Tr::to((uint16_t)vv[x]);
-#pragma unroll
-      for (int j = 0; j < RT; ++j) acc[j][x] = mfma32(f, mv[j], acc[j][x]);
+    for (int u = 0; u < kRowsDeep; ++u) {
+      const int i = i0 + 4 * kWaves * u + 4 * wave + q4;
+      at[u] = i < count ? a.rows[first + i] : -1;
     }
+  };
+  numbers(0);
+  for (int i0 = 0; i0 < count; i0 += 4 * kWaves * kRowsDeep) {
+    u2 vv[kRowsDeep];
+    float mv[kRowsDeep][RT];
+#pragma unroll
+    for (int u = 0; u < kRowsDeep; ++u) {
+      const int i = i0 + 4 * kWaves * u + 4 * wave + q4;
+      const bool ok = at[u] >= 0 && at[u] < a.T;
+      const uint16_t *q = v + (int64_t)(ok ? at[u] : 0) * ld + c;
+      vv[u] = u2{0u, 0u};
+      if (ok && left >= 4 && vec) {
+        vv[u] = *reinterpret_cast<const u2 *>(q);
+      } else if (ok) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (x < left) vv[u][x >> 1] |= (uint32_t)q[x] << (16 * (x & 1));
+      }
+#pragma unroll
+      for (int j = 0; j < RT; ++j) mv[u][j] = ok ? m[(int64_t)(first + i) * (16 * RT) + 16 * j + p16] : 0.f;
+    }
+    numbers(i0 + 4 * kWaves * kRowsDeep);
+#pragma unroll
+    for (int u = 0; u < kRowsDeep; ++u)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const float w = Tr::to((uint16_t)(vv[u][x >> 1] >> (16 * (x & 1))));
+#pragma unroll
+        for (int j = 0; j < RT; ++j) acc[j][x] = mfma32(w, mv[u][j], acc[j][x]);
+      }
   }
-  // join the waves: the upper half hands its sums to the lower half, three times
+  // Join the waves through LDS, up to four rank tiles at a time. A block x of a rank tile has, in lane
+  // (p16, q4), rank p16 of columns 4 (4 q4 + reg) + x; a thread adds up the waves' four
+  // values x of one (p16, q4, reg): four consecutive columns.
+  constexpr int JT = RT < 4 ? RT : 4;
 #pragma unroll
-  for (int half = kWaves / 2; half; half >>= 1) {
+  for (int j0 = 0; j0 < RT; j0 += JT) {
     __syncthreads();
-    if (wave >= half && wave < 2 * half) {
 #pragma unroll
-      for (int j = 0; j < RT; ++j)
+    for (int j = 0; j < JT; ++j)
 #pragma unroll
-        for (int x = 0; x < 8; ++x) s_part[((wave - half) * RT * 8 + j * 8 + x) * 64 + lane] = acc[j][x];
-    }
+      for (int x = 0; x < 4; ++x) s_part[((wave * JT + j) * 4 + x) * 64 + lane] = acc[j0 + j][x];
     __syncthreads();
-    if (wave < half) {
+    for (int t = threadIdx.x; t < JT * 256; t += kAdThreads) {
+      // neighbours: dA's columns, dB's ranks
+      const int l = is_a ? (t >> 4 & 15) + 16 * (t >> 2 & 3) : (t & 15) + 16 * (t >> 6 & 3), reg = is_a ? t & 3 : t >> 4 & 3, j = t >> 8;
+      f4 sum = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int j = 0; j < RT; ++j)
+      for (int w = 0; w < kWaves; ++w)
 #pragma unroll
-        for (int x = 0; x < 8; ++x) acc[j][x] += s_part[(wave * RT * 8 + j * 8 + x) * 64 + lane];
-    }
-  }
-  if (wave) return;
-  // lane: rank column p16, columns c0 + 8 (4 q4 + reg) + x
+        for (int x = 0; x < 4; ++x) sum[x] += reinterpret_cast<const float *>(&s_part[((w * JT + j) * 4 + x) * 64 + l])[reg];
+      const int i = 16 * (j0 + j) + (l & 15), col = c0 + 4 * (4 * (l >> 4) + reg);
+      if (i >= a.r) continue;
+      const int64_t at1 = is_a ? ((int64_t)e * a.r + i) * a.K + col : ((int64_t)e * a.N + col) * a.r + i;
 #pragma unroll
-  for (int j = 0; j < RT; ++j) {
-    const int i = j0 + 16 * j + p16;
-    if (i >= a.r) continue;
-#pragma unroll
-    for (int reg = 0; reg < 4; ++reg)
-#pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        const int col = c0 + 8 * (4 * q4 + reg) + x;
-        if (col >= C) continue;
-        const int64_t at = is_a ? ((int64_t)e * a.r + i) * a.K + col : ((int64_t)e * a.N + col) * a.r + i;
-        const float s = acc[j][x][reg];
+      for (int x = 0; x < 4; ++x) {
+        if (col + x >= C) break;
+        const int64_t to = at1 + (is_a ? x : (int64_t)x * a.r);
         if (a.g_f32) {
-          float *o = static_cast<float *>(out) + at;
-          *o = s + (a.accumulate ? *o : 0.f);
+          float *w = static_cast<float *>(out) + to;
+          *w = sum[x] + (a.accumulate ? *w : 0.f);
         } else {
-          static_cast<uint16_t *>(out)[at] = Tr::from(s);
+          static_cast<uint16_t *>(out)[to] = Tr::from(sum[x]);
         }
       }
+    }
   }
 }
 
@@ -524,37 +681,54 @@ int slices_for(int64_t blocks, int cols) {
   return (int)(want < 1 ? 1 : want);
 }
 
-int64_t row_blocks(int T, int n) {
+int64_t row_blocks(int T, int n, int rows) {
   const int64_t used = (n < T ? n : T) + 1;
-  return (T + used * (kAdRows - 1)) / kAdRows;
+  return (T + used * (rows - 1)) / rows;
 }
 
-template <typename Tr, int RT>
+// 16 rows a workgroup where adapters have few rows each or the batch has few, else 32.
+#ifndef RB1T
+#define RB1T 8192
+#endif
+bool few_rows(int T, int n) { return T < RB1T || T <= 16 * (int64_t)n; }
+
+template <typename Tr, int RT, int RB, bool F32>
 hipError_t run_forward(const AdapterArgs &a, hipStream_t s) {
-  const int64_t blocks = row_blocks(a.T, a.n);
+  const int64_t blocks = row_blocks(a.T, a.n, 16 * RB);
   if (!grid_fits(blocks, kAdThreads)) return hipErrorInvalidConfiguration;
   const int slices = slices_for(blocks, a.N);
   const int slice = (int)(cdiv(a.N, (int64_t)slices * 64) * 64);
-  adapter_kernel<Tr, RT><<<dim3((unsigned)blocks, (unsigned)cdiv(a.N, slice)), kAdThreads, 0, s>>>(a, slice);
+  adapter_kernel<Tr, RT, RB, F32><<<dim3((unsigned)blocks, (unsigned)cdiv(a.N, slice)), kAdThreads, 0, s>>>(a, slice);
   return hipGetLastError();
 }
+template <typename Tr, int RT>
+hipError_t run_forward(const AdapterArgs &a, hipStream_t s) {
+  if constexpr (RT < 8) {  // at eight rank tiles 32 rows' operands spill
+    if (!few_rows(a.T, a.n)) return a.y_f32 ? run_forward<Tr, RT, 2, true>(a, s) : run_forward<Tr, RT, 2, false>(a, s);
+  }
+  return a.y_f32 ? run_forward<Tr, RT, 1, true>(a, s) : run_forward<Tr, RT, 1, false>(a, s);
+}
 
+template <typename Tr, int RT, int RB, bool F32>
+hipError_t run_rows_grad(const AdapterGradArgs &a, hipStream_t s) {
+  const int64_t blocks = row_blocks(a.T, a.n, 16 * RB);
+  if (blocks == 0) return hipSuccess;
+  if (!grid_fits(blocks, kAdThreads)) return hipErrorInvalidConfiguration;
+  const int slices = a.dx ? slices_for(blocks, a.K) : 1;
+  const int slice = (int)(cdiv(a.K, (int64_t)slices * 64) * 64);
+  adapter_rows_grad_kernel<Tr, RT, RB, F32><<<dim3((unsigned)blocks, (unsigned)cdiv(a.K, slice)), kAdThreads, 0, s>>>(a, slice);
+  return hipGetLastError();
+}
 template <typename Tr, int RT>
 hipError_t run_grad(const AdapterGradArgs &a, hipStream_t s) {
-  const int64_t blocks = row_blocks(a.T, a.n);
-  const int64_t weight_blocks = (int64_t)a.n * (cdiv(a.K, 128) + cdiv(a.N, 128));
-  if (!grid_fits(blocks, kAdThreads) || !grid_fits(weight_blocks, kAdThreads)) return hipErrorInvalidConfiguration;
-  if (blocks > 0) {
-    const int slices = a.dx ? slices_for(blocks, a.K) : 1;
-    const int slice = (int)(cdiv(a.K, (int64_t)slices * 64) * 64);
-    adapter_rows_grad_kernel<Tr, RT><<<dim3((unsigned)blocks, (unsigned)cdiv(a.K, slice)), kAdThreads, 0, s>>>(a, slice);
-    const hipError_t err = hipGetLastError();
-    if (err != hipSuccess) return err;
-  }
-  if (!a.dA && !a.dB) return hipSuccess;
-  constexpr int WT = RT < 4 ? RT : 4;
-  const int ta = a.dA ? (int)cdiv(a.K, 128) : 0, tb = a.dB ? (int)cdiv(a.N, 128) : 0;
-  adapter_weights_grad_kernel<Tr, WT><<<dim3((unsigned)((int64_t)a.n * (ta + tb)), (unsigned)(RT / WT)), kAdThreads, 0, s>>>(a, ta, ta + tb, RT);
+  const int ta = a.dA ? (int)cdiv(a.K, 64) : 0, tb = a.dB ? (int)cdiv(a.N, 64) : 0;
+  if (!grid_fits((int64_t)a.n * (ta + tb), kAdThreads)) return hipErrorInvalidConfiguration;
+  hipError_t err;
+  constexpr int kMore = RT < 8 ? 2 : 1;
+  if (few_rows(a.T, a.n)) err = a.dx_f32 ? run_rows_grad<Tr, RT, 1, true>(a, s) : run_rows_grad<Tr, RT, 1, false>(a, s);
+  else err = a.dx_f32 ? run_rows_grad<Tr, RT, kMore, true>(a, s) : run_rows_grad<Tr, RT, kMore, false>(a, s);
+  if (err != hipSuccess || ta + tb == 0) return err;
+  adapter_weights_grad_kernel<Tr, RT><<<dim3((unsigned)((int64_t)a.n * (ta + tb))), kAdThreads, 0, s>>>(a, ta, ta + tb);
   return hipGetLastError();
 }
 

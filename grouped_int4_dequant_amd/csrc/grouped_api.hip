@@ -221,7 +221,7 @@ int moe_adapter_forward(int32_t dtype, const void *x, int64_t ldx, int32_t T, in
   a.vec_x = units(x, ldx, K) && units(A, K, K);
   auto wide = [&](const void *p, int64_t ld) { return aligned(p, 16) && ld * size_of(y_dtype) % 16 == 0; };
   a.vec_y = wide(y, ldy) && (!base || wide(base, ldbase));
-  a.vec_b = r % 4 == 0 && aligned(B, 8);
+  a.vec_b = units(B, r, r);
   return status(launch_adapter(a, dtype == MOE_FP16, stream));
 }
 
@@ -274,6 +274,7 @@ int moe_adapter_backward(int32_t dtype, const void *dy, int64_t lddy, const void
   }
   a.vec_x = units(x, ldx, K) && units(A, K, K);
   a.vec_dy = units(dy, lddy, N);
+  a.vec_b = units(B, r, r);
   auto wide = [&](const void *p, int64_t ld) { return aligned(p, 16) && ld * size_of(dx_dtype) % 16 == 0; };
   a.vec_dx = dx && wide(dx, lddx) && (!dx_base || wide(dx_base, lddx_base));
   return status(launch_adapter_grad(a, dtype == MOE_FP16, stream));

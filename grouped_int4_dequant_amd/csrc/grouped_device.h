@@ -86,7 +86,8 @@ __device__ __forceinline__ GroupTile find_group(const int32_t *offsets, int G, i
   const int g0 = min(lane * run, G), g1 = min(g0 + run, G);
   auto at = [&](int g) { return min(max(offsets[g], 0), P); };
   int mine = 0;
-  int prev = at(g0);
+  const int begin = at(g0);
+  int prev = begin;
   for (int g = g0; g < g1; ++g) {
     const int next = at(g + 1);
     mine += (max(next - prev, 0) + rows - 1) / rows;
@@ -107,6 +108,13 @@ __device__ __forceinline__ GroupTile find_group(const int32_t *offsets, int G, i
   if (m < 0 || past == 0) return t;
   const int owner = __builtin_ctzll(past);
   int before = __shfl(sum - mine, owner);
+  if (run == 1) {  // every lane holds one group: its bounds are in the lane
+    t.e = owner;
+    t.first = __builtin_amdgcn_readfirstlane(__shfl(begin, owner));
+    t.count = __builtin_amdgcn_readfirstlane(__shfl(prev, owner)) - t.first;
+    t.before = __builtin_amdgcn_readfirstlane(before);
+    return t;
+  }
   int g = __shfl(g0, owner);
   const int end = __shfl(g1, owner);
   int a = at(g);

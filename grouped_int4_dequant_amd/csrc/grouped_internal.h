@@ -96,7 +96,7 @@ struct AdapterArgs {
   void *y;
   int32_t y_f32;
   int64_t ld_y;
-  int32_t vec_x, vec_y, vec_b;  // whole aligned units: 16 bytes of x and A, of base and y; 8 bytes of B
+  int32_t vec_x, vec_y, vec_b;  // 16-byte units of x and A, of base and y, of B are aligned
 };
 struct AdapterGradArgs {
   const uint16_t *dy, *x;
@@ -113,7 +113,7 @@ struct AdapterGradArgs {
   void *dA, *dB;            // each nullable: not wanted
   int32_t g_f32, accumulate;
   float *g, *h;             // workspace, fp32 [T][16 rank_tiles(r)] by sorted place: scale B^T dy and scale A x
-  int32_t vec_x, vec_dy, vec_dx, vec_da;
+  int32_t vec_x, vec_dy, vec_dx, vec_b;
 };
 hipError_t launch_adapter_plan(const int32_t *row_adapter, int32_t T, int32_t n, int32_t *rows, int32_t *offsets, hipStream_t s);
 hipError_t launch_adapter(const AdapterArgs &a, bool fp16, hipStream_t s);
