@@ -387,17 +387,15 @@ constexpr int kUnits = 4;               // requests of a thread for each operand
 // Where 1 KiB piece c (what one wave requests at once) of an operand lies in LDS.
 // A straight operand's piece is eight rows of 128 bytes, whose 16-byte units are swapped
 // by row so that the 16 rows of a fetch fall on distinct banks. An across
-// operand's piece is two r of 512 bytes, in order; gaps between the pieces keep the
-// fetches, which take 32 or 4 x 8 bytes of 16 r at once, off each other's banks:
-// the row operand's (in the weight gradient, whose fetch h takes r = 16 h + 4 q4 + x) by 32 bytes a
-// piece, the column operand's by 16 and 128 bytes by the bits of c that vary in a fetch.
+// operand's piece is r = c and r = c + 32, 512 bytes each, so that the four r that 16 lanes fetch
+// together lie in four consecutive pieces. Gaps between the pieces keep those off each other's banks:
+// 32 bytes a piece where a fetch takes 32 consecutive bytes of each r (the row operand), 16 and 128 bytes by
+// the piece's last two bits where it takes four times 8 bytes at 32-byte steps (the column operand).
 template <int Mode>
 __device__ __forceinline__ constexpr int row_piece(int c) { return Mode == kWgrad ? c * 1056 : c * 1024; }
 template <int Mode>
 __device__ __forceinline__ constexpr int col_piece(int c) {
-  return Mode == kFwd ? c * 1024
-       : Mode == kDgrad ? c * 1024 + 16 * (c & 3) + 128 * ((c >> 2) & 1) + 256 * (c >> 3)
-                        : c * 1024 + 16 * (c & 1) + 128 * ((c >> 1) & 1) + 256 * (c >> 2);
+  return Mode == kFwd ? c * 1024 : c * 1024 + 16 * (c & 1) + 128 * ((c >> 1) & 1) + 256 * (c >> 2);
 }
 __device__ __forceinline__ int row_unit(int row, int slot) { return slot ^ ((row >> 1) & 7); }
 __device__ __forceinline__ int col_unit(int row, int slot) { return slot ^ (((row >> 1) & 1) | ((row >> 4) & 3) << 1); }
@@ -427,7 +425,7 @@ __device__ __forceinline__ void wide_body(const GroupedArgs &a, const WideTile t
   const int steps = (t.nr + kBR - 1) / kBR;
 
   // ---- requests. Unit i is piece 8 i + wave: a straight operand's tile rows
-  // 64 i + tid / 8, an across operand's r = 16 i + tid / 32 of the step. Rows and
+  // 64 i + tid / 8, an across operand's r = 8 i + wave of the step in the lower 32 lanes and 32 more in the upper. Rows and
   // columns past the output's end repeat the last one; what they give is not stored.
   // Byte offsets are 32 bits from a base that is the same for the workgroup.
   const char *lbase, *rbase;
@@ -435,7 +433,7 @@ __device__ __forceinline__ void wide_body(const GroupedArgs &a, const WideTile t
   int lr, rr;  // this thread's r in a step: straight the first of its unit's eight, across that of unit 0
   const int col_wave = col_piece<Mode>(wave);  // adds to col_piece(8 i)
   if constexpr (kLAcross) {
-    lr = tid >> 5;
+    lr = wave + (lane & 32);
     lbase = (const char *)(a.w + (int64_t)t.first * a.ld_w + t.i0);
     lv[0] = (uint32_t)(lr * a.ld_w + min(8 * (tid & 31), t.ni - 8)) * 2;
   } else {
@@ -455,7 +453,7 @@ __device__ __forceinline__ void wide_body(const GroupedArgs &a, const WideTile t
     }
   }
   if constexpr (kRAcross) {
-    rr = tid >> 5;
+    rr = wave + (lane & 32);
     const int col = min(8 * (tid & 31), t.nj - 8);
     if constexpr (Mode == kWgrad) {
       rbase = (const char *)(a.rows + t.j0);
@@ -476,7 +474,7 @@ __device__ __forceinline__ void wide_body(const GroupedArgs &a, const WideTile t
     if constexpr (Mode == kWgrad) {
 #pragma unroll
       for (int i = 0; i < kUnits; ++i) {
-        const int r = s * kBR + rr + 16 * i, p = t.first + min(r, t.nr - 1);
+        const int r = s * kBR + rr + 8 * i, p = t.first + min(r, t.nr - 1);
         const int at = Gather ? a.a_row[p] : p;
         rrow[i] = ((r < t.nr) & (at < a.a_rows)) ? at : -1;
       }
@@ -485,8 +483,8 @@ __device__ __forceinline__ void wide_body(const GroupedArgs &a, const WideTile t
   // `s` is the step asked for, lbase and rbase stand at it; `whole`: every r of the step exists
   const int64_t lstep = kLAcross ? kBR * a.ld_w * 2 : kBR * 2, rstep = Mode == kDgrad ? kBR * a.ld_w * 2 : Mode == kFwd ? kBR * 2 : 0;
   auto request_l = [&](int s, int i, uint8_t *buf, auto whole) __attribute__((always_inline)) {
-    const char *p = uniform(lbase + (kLAcross ? (lstep >> 2) * i : 0)) + lv[kLAcross ? 0 : i];
-    if constexpr (!decltype(whole)::value) p = s * kBR + lr + (kLAcross ? 16 * i : 0) < t.nr ? p : (const char *)&g_zeros;
+    const char *p = uniform(lbase + (kLAcross ? (lstep >> 3) * i : 0)) + lv[kLAcross ? 0 : i];
+    if constexpr (!decltype(whole)::value) p = s * kBR + lr + (kLAcross ? 8 * i : 0) < t.nr ? p : (const char *)&g_zeros;
     load_lds16(p, buf + row_piece<Mode>(8 * i) + row_piece<Mode>(1) * wave);
   };
   auto request_r = [&](int s, int i, uint8_t *buf, auto whole) __attribute__((always_inline)) {
@@ -495,31 +493,29 @@ __device__ __forceinline__ void wide_body(const GroupedArgs &a, const WideTile t
       p = rbase + (uint64_t)((uint32_t)rrow[i] * (uint32_t)(a.ld_rows * 2) + rv[0]);
       p = rrow[i] >= 0 ? p : (const char *)&g_zeros;
     } else {
-      p = uniform(rbase + (kRAcross ? (rstep >> 2) * i : 0)) + rv[kRAcross ? 0 : i];
-      if constexpr (!decltype(whole)::value) p = s * kBR + rr + (kRAcross ? 16 * i : 0) < t.nr ? p : (const char *)&g_zeros;
+      p = uniform(rbase + (kRAcross ? (rstep >> 3) * i : 0)) + rv[kRAcross ? 0 : i];
+      if constexpr (!decltype(whole)::value) p = s * kBR + rr + (kRAcross ? 8 * i : 0) < t.nr ? p : (const char *)&g_zeros;
     }
     load_lds16(p, buf + col_piece<Mode>(8 * i) + col_wave);
   };
 
-  // ---- operand fetches: half ks, fetch h of it (r = 32 ks + 8 q4 + 4 h + x, in the weight
-  // gradient 32 ks + 16 h + 4 q4 + x: any order does, if both operands have it).
+  // ---- operand fetches: half ks is r = 32 ks + 8 q4 .. + 7; of an across operand fetch h takes r = 32 ks + 8 q4 + 4 h + x.
   // Every address is a lane's part, kept in one register, and a constant: the constant
   // and the lane's part of a piece's number add up without carries into each other's gap bits.
-  constexpr int kC0 = Mode == kWgrad ? 8 : 2;  // pieces from fetch h = 0 to h = 1
-  const int cl = (Mode == kWgrad ? 2 : 4) * q4 + (p16 >> 3), odd = 512 * ((p16 >> 2) & 1);
+  const int cl = 8 * q4 + (p16 >> 2);
   const int col_row = 16 * (p16 >> 2) + (p16 & 3);
   uint32_t lat[2], rat[2];  // of half 0 and 1 (across operands: the first serves both)
 #pragma unroll
   for (int ks = 0; ks < 2; ++ks) {
-    lat[ks] = kLAcross ? row_piece<Mode>(cl) + odd + 32 * wi + 8 * (p16 & 3)
+    lat[ks] = kLAcross ? row_piece<Mode>(cl) + 32 * wi + 8 * (p16 & 3)
                        : (16 * wi + p16) * 128 + 16 * row_unit(p16, 4 * ks + q4);
-    rat[ks] = kRAcross ? col_piece<Mode>(cl) + odd + 128 * wj + 32 * (p16 & 3)
+    rat[ks] = kRAcross ? col_piece<Mode>(cl) + 128 * wj + 32 * (p16 & 3)
                        : (64 * wj + col_row) * 128 + 16 * col_unit(col_row, 4 * ks + q4);
     asm("" : "+v"(lat[ks]), "+v"(rat[ks]));
   }
   auto read_l = [&](const uint8_t *b, int i, int ks) __attribute__((always_inline)) {
     if constexpr (kLAcross) {
-      const s4 x = read_lds_tr(b + lat[0] + row_piece<Mode>(16 * ks) + 64 * i), y = read_lds_tr(b + lat[0] + row_piece<Mode>(16 * ks + kC0) + 64 * i);
+      const s4 x = read_lds_tr(b + lat[0] + 512 * ks + 64 * i), y = read_lds_tr(b + lat[0] + row_piece<Mode>(4) + 512 * ks + 64 * i);
       return s8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
     } else {
       return *reinterpret_cast<const s8 *>(b + lat[ks] + 4096 * i);
@@ -527,7 +523,7 @@ __device__ __forceinline__ void wide_body(const GroupedArgs &a, const WideTile t
   };
   auto read_r = [&](const uint8_t *b, int j, int ks) __attribute__((always_inline)) {
     if constexpr (kRAcross) {
-      const s4 x = read_lds_tr(b + rat[0] + col_piece<Mode>(16 * ks) + 8 * j), y = read_lds_tr(b + rat[0] + col_piece<Mode>(16 * ks + kC0) + 8 * j);
+      const s4 x = read_lds_tr(b + rat[0] + 512 * ks + 8 * j), y = read_lds_tr(b + rat[0] + col_piece<Mode>(4) + 512 * ks + 8 * j);
       return s8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
     } else {
       return *reinterpret_cast<const s8 *>(b + rat[ks] + 512 * j);
