@@ -521,7 +521,7 @@ if hasattr(torch._C, "_cuda_getCurrentRawStream"):  # the same handle without a 
 class _Call:
     """One call: its device and stream, and the checks of its tensors."""
 
-    __slots__ = ("dtype", "device", "code", "stream", "given")
+    __slots__ = ("dtype", "device", "index", "code", "stream", "given")
 
     def __init__(self, lead: torch.Tensor, name: str, stream):
         if not isinstance(lead, torch.Tensor):
@@ -532,6 +532,7 @@ class _Call:
         if not lead.is_cuda:
             raise ValueError(f"{name} must be on the GPU")
         self.device = lead.device
+        self.index = self.device.index
         self.code = 0 if self.dtype is torch.bfloat16 else 1
         self.given = stream
         if stream is None:
@@ -543,13 +544,15 @@ class _Call:
 
     def need(self, t, name, dtype, shape):
         """A contiguous tensor of the call's device."""
-        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == self.device and t.is_contiguous()):
+        if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.get_device() == self.index and t.is_contiguous()):
             _need(t, name, dtype, shape)
             raise ValueError(f"{name} must be on {self.device}, got {t.device}")
         return t
 
     def rows(self, t, name, shape, other=None):
         """A matrix of the call's type (or of `other`) with contiguous columns and a row stride of at least its width."""
+        if isinstance(t, torch.Tensor) and t.dtype is self.dtype and t.shape == shape and t.get_device() == self.index and t.is_contiguous():
+            return t
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
         if t.dtype is not self.dtype and (other is None or t.dtype is not other):
@@ -594,7 +597,7 @@ class _Call:
 
     def __call__(self, what, *args):
         f = getattr(_lib or load(), what)
-        if torch.cuda.current_device() == self.device.index:
+        if torch.cuda.current_device() == self.index:
             status = f(*args, self.stream)
         else:
             with torch.cuda.device(self.device):
@@ -603,12 +606,9 @@ class _Call:
             _check(status, what)
 
 
-def _ld(t: Optional[torch.Tensor]) -> int:
-    """Row stride of a matrix; its width where it has at most one row."""
-    if t is None:
-        return 0
-    n, width = t.shape
-    return t.stride(0) if n > 1 else width
+def _ld(t: Optional[torch.Tensor], width: int) -> int:
+    """Row stride of a checked matrix; at least its width (that of a single row may be anything)."""
+    return 0 if t is None else max(t.stride(0), width)
 
 
 def _groups(c: _Call, offsets: torch.Tensor, G: int) -> torch.Tensor:
@@ -632,8 +632,8 @@ def grouped_gemm(A: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, a_row:
         c.need(a_row, "a_row", torch.int32, (P,))
     _groups(c, offsets, G)
     C = c.result(out, "out", (P, N), out_dtype)
-    c("moe_grouped_gemm", c.code, A.data_ptr(), _ld(A), A.shape[0], _ptr(a_row), offsets.data_ptr(), G, P, N, K,
-      W.data_ptr(), C.data_ptr(), _CODES[C.dtype], _ld(C))
+    c("moe_grouped_gemm", c.code, A.data_ptr(), _ld(A, K), A.shape[0], _ptr(a_row), offsets.data_ptr(), G, P, N, K,
+      W.data_ptr(), C.data_ptr(), _CODES[C.dtype], _ld(C, N))
     return C
 
 
@@ -650,8 +650,8 @@ def grouped_gemm_dgrad(dC: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor,
     c.need(W, "W", c.dtype, (G, N, K))
     _groups(c, offsets, G)
     dA = c.result(out, "out", (P, K), out_dtype)
-    c("moe_grouped_gemm_dgrad", c.code, dC.data_ptr(), _ld(dC), offsets.data_ptr(), G, P, N, K, W.data_ptr(),
-      dA.data_ptr(), _CODES[dA.dtype], _ld(dA))
+    c("moe_grouped_gemm_dgrad", c.code, dC.data_ptr(), _ld(dC, N), offsets.data_ptr(), G, P, N, K, W.data_ptr(),
+      dA.data_ptr(), _CODES[dA.dtype], _ld(dA, K))
     return dA
 
 
@@ -677,7 +677,7 @@ def grouped_gemm_wgrad(dC: torch.Tensor, A: torch.Tensor, offsets: torch.Tensor,
     if accumulate and out is None:
         raise ValueError("accumulate needs the tensor to add to in `out`")
     dW = c.whole(out, "out", (G, N, K), out_dtype)
-    c("moe_grouped_gemm_wgrad", c.code, dC.data_ptr(), _ld(dC), A.data_ptr(), _ld(A), A.shape[0], _ptr(a_row),
+    c("moe_grouped_gemm_wgrad", c.code, dC.data_ptr(), _ld(dC, N), A.data_ptr(), _ld(A, K), A.shape[0], _ptr(a_row),
       offsets.data_ptr(), G, P, N, K, dW.data_ptr(), _CODES[dW.dtype], int(accumulate))
     return dW
 
@@ -699,8 +699,8 @@ def combine(o: torch.Tensor, pair_pos: torch.Tensor, weights: Optional[torch.Ten
     if add is not None:
         c.rows(add, "add", (T, d), torch.float32)
     y = c.result(out, "out", (T, d), out_dtype)
-    c("moe_combine", c.code, o.data_ptr(), _ld(o), P, pair_pos.data_ptr(), _ptr(weights), T, k, d, _ptr(add),
-      c.code if add is None else _CODES[add.dtype], _ld(add), y.data_ptr(), _CODES[y.dtype], _ld(y))
+    c("moe_combine", c.code, o.data_ptr(), _ld(o, d), P, pair_pos.data_ptr(), _ptr(weights), T, k, d, _ptr(add),
+      c.code if add is None else _CODES[add.dtype], _ld(add, d), y.data_ptr(), _CODES[y.dtype], _ld(y, d))
     return y
 
 
@@ -720,8 +720,8 @@ def combine_backward(dy: torch.Tensor, o: torch.Tensor, pair_pos: torch.Tensor, 
         c.need(weights, "weights", torch.float32, (T, k))
     d_o = c.new((P, d), c.dtype) if d_o is None else c.rows(d_o, "d_o", (P, d))
     dw = c.new((T, k), torch.float32) if dw is None else c.need(dw, "dw", torch.float32, (T, k))
-    c("moe_combine_backward", c.code, dy.data_ptr(), _ld(dy), o.data_ptr(), _ld(o), P, pair_pos.data_ptr(), _ptr(weights),
-      T, k, d, d_o.data_ptr(), _ld(d_o), dw.data_ptr())
+    c("moe_combine_backward", c.code, dy.data_ptr(), _ld(dy, d), o.data_ptr(), _ld(o, d), P, pair_pos.data_ptr(), _ptr(weights),
+      T, k, d, d_o.data_ptr(), _ld(d_o, d), dw.data_ptr())
     return d_o, dw
 
 
@@ -774,8 +774,8 @@ def adapter_forward(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scale: Op
     y = c.result(out, "out", (T, N), out_dtype)
     if base is not None and base.dtype != y.dtype:
         raise TypeError(f"base must be {y.dtype} like the result, got {base.dtype}")
-    c("moe_adapter_forward", c.code, x.data_ptr(), _ld(x), T, K, N, r, n, A.data_ptr(), B.data_ptr(), _ptr(scale),
-      rows.data_ptr(), offsets.data_ptr(), _ptr(base), _ld(base), y.data_ptr(), _CODES[y.dtype], _ld(y))
+    c("moe_adapter_forward", c.code, x.data_ptr(), _ld(x, K), T, K, N, r, n, A.data_ptr(), B.data_ptr(), _ptr(scale),
+      rows.data_ptr(), offsets.data_ptr(), _ptr(base), _ld(base, N), y.data_ptr(), _CODES[y.dtype], _ld(y, N))
     return y
 
 
@@ -807,8 +807,8 @@ def adapter_backward(dy: torch.Tensor, x: torch.Tensor, A: torch.Tensor, B: torc
         ws = c.new(max(need, 1), torch.uint8)
     elif ws.device != c.device:
         raise ValueError(f"ws must be on {c.device}, got {ws.device}")
-    c("moe_adapter_backward", c.code, dy.data_ptr(), _ld(dy), x.data_ptr(), _ld(x), T, K, N, r, n, A.data_ptr(),
-      B.data_ptr(), _ptr(scale), rows.data_ptr(), offsets.data_ptr(), _ptr(dx_base), _ld(dx_base), dx.data_ptr(),
-      _CODES[dx.dtype], _ld(dx), dA.data_ptr(), dB.data_ptr(), _CODES[dA.dtype], int(accumulate), ws.data_ptr(),
+    c("moe_adapter_backward", c.code, dy.data_ptr(), _ld(dy, N), x.data_ptr(), _ld(x, K), T, K, N, r, n, A.data_ptr(),
+      B.data_ptr(), _ptr(scale), rows.data_ptr(), offsets.data_ptr(), _ptr(dx_base), _ld(dx_base, K), dx.data_ptr(),
+      _CODES[dx.dtype], _ld(dx, K), dA.data_ptr(), dB.data_ptr(), _CODES[dA.dtype], int(accumulate), ws.data_ptr(),
       ws.numel() * ws.element_size())
     return dx, dA, dB

@@ -399,17 +399,19 @@ __global__ __launch_bounds__(kAdThreads, RT <= 2 ? 4 : 2) void adapter_rows_grad
   for (int b = 0; b < RB; ++b) row[b] = row_of(a.rows, blk, 16 * b + p16, a.T);
   const OutRows o{a.dx_base, a.ld_dx_base, a.dx, a.ld_dx, a.vec_dx != 0};
   const int begin = blockIdx.y * slice, end = min(a.K, begin + slice);
+  // with dB, the last blockIdx.y forms h, the others g and their slice of dx
+  const bool for_h = a.dB && blockIdx.y + 1 == gridDim.y;
   if (blk.e < 0) {
-    copy_rows<Tr, F32, RB>(o, row, begin, end);
+    if (a.dx && !for_h) copy_rows<Tr, F32, RB>(o, row, begin, end);
     return;
   }
   uint8_t *mine = s_mem + wave * kStageBytes<RT>;
   const uint16_t *A = a.A + (int64_t)blk.e * a.r * a.K;
   const uint16_t *B = a.B + (int64_t)blk.e * a.N * a.r;
   const float scale = a.scale ? a.scale[blk.e] : 1.f;
-  // the block's h or g into the workspace (slice 0 writes them)
+  // the block's h or g into the workspace
   auto keep = [&](float *dst) {
-    if (!dst || blockIdx.y) return;
+    if (!dst) return;
     for (int u = threadIdx.x; u < RB * RT * 64; u += kAdThreads) {
       const int l = u & 63, j = (u >> 6) % RT, b = (u >> 6) / RT;
       const int i = 16 * b + (l & 15);
@@ -423,12 +425,12 @@ __global__ __launch_bounds__(kAdThreads, RT <= 2 ? 4 : 2) void adapter_rows_grad
 #pragma unroll
       for (int j = 0; j < RT; ++j) acc[b][j] = f4{0.f, 0.f, 0.f, 0.f};
   };
-  if (a.dB && blockIdx.y == 0) {
+  if (for_h) {
     clear();
     down_product<Tr, RB, RT>(a.x, a.ld_x, row, A, a.r, a.K, a.vec_x, acc);
     join_waves<RB, RT>(s_part, acc, scale);
     keep(a.h);
-    __syncthreads();
+    return;
   }
   // g: 32 columns of dy at a time, split over the waves; 32 rows of B are staged as 16 RT ranks each
   clear();
@@ -463,7 +465,7 @@ __global__ __launch_bounds__(kAdThreads, RT <= 2 ? 4 : 2) void adapter_rows_grad
     }
   }
   join_waves<RB, RT>(s_part, acc, scale);
-  keep(a.g);
+  if (blockIdx.y == 0) keep(a.g);  // dA's factor
   if (!a.dx) return;
   Cut<Tr, RB, RT> g;
   cut<Tr, RB, RT>(s_part, g);
@@ -685,10 +687,7 @@ __global__ __launch_bounds__(kPlanThreads) void adapter_plan_kernel(const int32_
 // no slice shorter than one pass of the waves.
 int slices_for(int64_t blocks, int cols) {
   const int64_t most = cdiv(cols, 64 * kWaves);
-#ifndef SLW
-#define SLW 512
-#endif
-  int64_t want = cdiv(SLW, blocks);
+  int64_t want = cdiv(512, blocks);
   if (want > most) want = most;
   return (int)(want < 1 ? 1 : want);
 }
@@ -699,10 +698,7 @@ int64_t row_blocks(int T, int n, int rows) {
 }
 
 // 16 rows a workgroup where adapters have few rows each or the batch has few, else 32.
-#ifndef RB1T
-#define RB1T 8192
-#endif
-bool few_rows(int T, int n) { return T < RB1T || T <= 16 * (int64_t)n; }
+bool few_rows(int T, int n) { return T < 8192 || T <= 16 * (int64_t)n; }
 
 template <typename Tr, int RT, int RB, bool F32>
 hipError_t run_forward(const AdapterArgs &a, hipStream_t s) {
@@ -726,7 +722,7 @@ hipError_t run_rows_grad(const AdapterGradArgs &a, hipStream_t s) {
   if (blocks == 0) return hipSuccess;
   const int slice = (int)(cdiv(a.K, (int64_t)(a.dx ? slices_for(blocks, a.K) : 1) * 64) * 64), slices = (int)cdiv(a.K, slice);
   if (!grid_fits(blocks, kAdThreads)) return hipErrorInvalidConfiguration;
-  adapter_rows_grad_kernel<Tr, RT, RB, F32><<<dim3((unsigned)blocks, (unsigned)slices), kAdThreads, 0, s>>>(a, slice);
+  adapter_rows_grad_kernel<Tr, RT, RB, F32><<<dim3((unsigned)blocks, (unsigned)slices + (a.dB != nullptr)), kAdThreads, 0, s>>>(a, slice);
   return hipGetLastError();
 }
 template <typename Tr, int RT>

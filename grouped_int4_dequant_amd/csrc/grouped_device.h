@@ -138,4 +138,53 @@ __device__ __forceinline__ GroupTile find_group(const int32_t *offsets, int G, i
   return t;
 }
 
+// Group number k in an order of roughly falling size: those of at least 3/2 of
+// the average rows first, then of at least the average, of at least half of it, and the rest; ascending in each class.
+// For work whose length goes by the group's rows: the longest starts first, so
+// that the end is not one long piece. The lanes count their runs' groups of the four classes in 16
+// bits each; one prefix sum serves all four.
+__device__ __forceinline__ int group_by_size(const int32_t *offsets, int G, int P, int k) {
+  const int lane = threadIdx.x & 63;
+  const int run = (G + 63) >> 6;
+  const int g0 = min(lane * run, G), g1 = min(g0 + run, G);
+  auto at = [&](int g) { return min(max(offsets[g], 0), P); };
+  const int64_t G2 = 2 * (int64_t)G, P2 = P;
+  auto kind = [&](int n) {  // n against P / G
+    const int64_t x = n * G2;
+    return x >= 3 * P2 ? 0 : x >= 2 * P2 ? 1 : x >= P2 ? 2 : 3;
+  };
+  uint64_t mine = 0;
+  int prev = at(g0);
+  for (int g = g0; g < g1; ++g) {
+    const int next = at(g + 1);
+    mine += 1ull << (16 * kind(max(next - prev, 0)));
+    prev = next;
+  }
+  uint64_t sum = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint64_t v = __shfl_up((unsigned long long)sum, d);
+    if (lane >= d) sum += v;
+  }
+  const uint64_t all = __shfl((unsigned long long)sum, 63);
+  int c = 0;
+  for (; c < 3; ++c) {
+    const int n = (int)(all >> (16 * c) & 0xffff);
+    if (k < n) break;
+    k -= n;
+  }
+  const int upto = (int)(sum >> (16 * c) & 0xffff);
+  const uint64_t past = __ballot(upto > k);
+  if (past == 0) return -1;
+  const int owner = __builtin_ctzll(past);
+  k -= __shfl(upto - (int)(mine >> (16 * c) & 0xffff), owner);  // which of the owner's
+  int g = __shfl(g0, owner);
+  for (int a = at(g);; ++g) {
+    const int b = at(g + 1);
+    if (kind(max(b - a, 0)) == c && k-- == 0) break;
+    a = b;
+  }
+  return __builtin_amdgcn_readfirstlane(g);
+}
+
 }  // namespace moe

@@ -756,9 +756,11 @@ __global__ __launch_bounds__(kWideThreads, 2) void grouped_wide_kernel(GroupedAr
   if constexpr (Mode == kWgrad) {
     const int tj = (a.K + kWide - 1) / kWide, ti = (a.N + kWide - 1) / kWide;
     const int per = ti * tj;
-    t.e = blockIdx.x / per;
-    if (t.e >= a.G) return;
-    const int x = blockIdx.x - t.e * per;
+    const int k = blockIdx.x / per;
+    if (k >= a.G) return;
+    t.e = group_by_size(a.offsets, a.G, a.P, k);
+    if (t.e < 0) return;
+    const int x = blockIdx.x - k * per;
     t.i0 = x / tj * kWide;
     t.j0 = (x - x / tj * tj) * kWide;
     t.first = min(max(a.offsets[t.e], 0), a.P);
@@ -805,19 +807,13 @@ hipError_t launch_wide(const GroupedArgs &a, hipStream_t s) {
   return hipGetLastError();
 }
 
-#ifndef FEWP
-#define FEWP 64
-#endif
-#ifndef SMALLT
-#define SMALLT 128
-#endif
 template <typename Tr, int Mode, bool Vec>
 hipError_t launch(const GroupedArgs &a, hipStream_t s) {
   const int64_t used = a.G < a.P ? a.G : a.P;  // groups that can have rows
   const int J = Mode == kFwd ? a.N : a.K;
   if constexpr (Vec) {
     if constexpr (Mode != kWgrad) {
-      if (a.P <= FEWP) {
+      if (a.P <= 64) {
         const int64_t wgs = (a.P + used * (kFewRows - 1)) / kFewRows * cdiv(J, Mode == kFwd ? 32 : 64);
         if (!grid_fits(wgs, 512)) return hipErrorInvalidConfiguration;
         grouped_few_kernel<Tr, Mode><<<dim3((unsigned)wgs), 512, 0, s>>>(a);
@@ -826,7 +822,7 @@ hipError_t launch(const GroupedArgs &a, hipStream_t s) {
     }
     const int64_t at_least = Mode == kWgrad ? (int64_t)a.G * cdiv(a.N, kWide) * cdiv(a.K, kWide)
                                             : (used > a.P / kWide ? used : a.P / kWide) * cdiv(J, kWide);
-    if (a.wide && at_least >= SMALLT) {
+    if (a.wide && at_least >= 128) {
       // Tiles of 128 rows and three buffers where groups hold few rows, of 256 and two where they
       // hold many, by the average. Forward at 256 experts, N = 1024, K = 2048: 159 against 170 us at
       // 2 rows a group, 214 / 234 at 64, 380 / 385 at 256; 16 groups of 1024 rows: 301 / 284. Input gradient:
