@@ -78,9 +78,10 @@ constexpr int kAdLds = kWaves * kStageBytes<RT>;
 
 // Sum the waves' partial products and scale them. part[w][rb][rt][lane] holds
 // row 16 rb + lane % 16, columns 16 rt + 4 (lane / 16) .. of wave w. The sums
-// replace wave 0's partials.
+// replace wave 0's partials. Columns from r on are zeros, also where the row's
+// values are not finite (there 0 times them was added up).
 template <int RB, int RT>
-__device__ __forceinline__ void join_waves(f4 *part, const f4 (&acc)[RB][RT], float scale) {
+__device__ __forceinline__ void join_waves(f4 *part, const f4 (&acc)[RB][RT], float scale, int r) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   __syncthreads();
 #pragma unroll
@@ -92,7 +93,12 @@ __device__ __forceinline__ void join_waves(f4 *part, const f4 (&acc)[RB][RT], fl
     f4 s = part[u];
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) s += part[w * RB * RT * 64 + u];
-    part[u] = s * scale;
+    s *= scale;
+    const int left = r - 16 * ((u >> 6) % RT) - 4 * ((u & 63) >> 4);
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      if (x >= left) s[x] = 0.f;
+    part[u] = s;
   }
   __syncthreads();
 }
@@ -365,7 +371,7 @@ __global__ __launch_bounds__(kAdThreads, RT <= 2 ? 4 : 2) void adapter_kernel(Ad
 #pragma unroll
     for (int j = 0; j < RT; ++j) acc[b][j] = f4{0.f, 0.f, 0.f, 0.f};
   down_product<Tr, RB, RT>(a.x, a.ld_x, row, a.A + (int64_t)blk.e * a.r * a.K, a.r, a.K, a.vec_x, acc);
-  join_waves<RB, RT>(s_part, acc, a.scale ? a.scale[blk.e] : 1.f);
+  join_waves<RB, RT>(s_part, acc, a.scale ? a.scale[blk.e] : 1.f, a.r);
   Cut<Tr, RB, RT> h;
   cut<Tr, RB, RT>(s_part, h);
   for (; n0 < end; n0 += 64 * kWaves) {
@@ -428,7 +434,7 @@ __global__ __launch_bounds__(kAdThreads, RT <= 2 ? 4 : 2) void adapter_rows_grad
   if (for_h) {
     clear();
     down_product<Tr, RB, RT>(a.x, a.ld_x, row, A, a.r, a.K, a.vec_x, acc);
-    join_waves<RB, RT>(s_part, acc, scale);
+    join_waves<RB, RT>(s_part, acc, scale, a.r);
     keep(a.h);
     return;
   }
@@ -464,7 +470,7 @@ __global__ __launch_bounds__(kAdThreads, RT <= 2 ? 4 : 2) void adapter_rows_grad
       wave_sync();
     }
   }
-  join_waves<RB, RT>(s_part, acc, scale);
+  join_waves<RB, RT>(s_part, acc, scale, a.r);
   if (blockIdx.y == 0) keep(a.g);  // dA's factor
   if (!a.dx) return;
   Cut<Tr, RB, RT> g;
@@ -503,14 +509,14 @@ __device__ __forceinline__ f4 mfma32(float a, float b, f4 c) { return __builtin_
 
 // Gradient of the adapters: out[c][j] = sum over the adapter's rows of
 // v[row][c] * m[place][j], v = x (dA, c = k) or dy (dB, c = n), m = g or h.
-// A workgroup owns 64 columns of one adapter; its waves take every eighth
-// group of four rows, and join in LDS. Lane (p16, q4) reads four consecutive columns 4 p16 .. of
+// Split: a workgroup owns 64 columns of one adapter; its waves take every eighth
+// group of four rows, and join in LDS. Else every wave owns 64 columns and takes all rows,
+// for adapters of few rows, where the join would be most of the work. Lane (p16, q4) reads four consecutive columns 4 p16 .. of
 // row q4, and the fp32 matrix instruction number x takes column 4 p16 + x. Rows are asked for
 // kRowsDeep groups at a time, their numbers one batch earlier.
 constexpr int kRowsDeep = 8;
-template <typename Tr, int RT>
+template <typename Tr, int RT, bool Split>
 __global__ __launch_bounds__(kAdThreads) void adapter_weights_grad_kernel(AdapterGradArgs a, int tiles_a, int tiles_all) {
-  __shared__ __attribute__((aligned(16))) f4 s_part[kWaves * (RT < 4 ? RT : 4) * 4 * 64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, p16 = lane & 15, q4 = lane >> 4;
   const int e = blockIdx.x / tiles_all;
   int tile = blockIdx.x - e * tiles_all;
@@ -521,7 +527,10 @@ __global__ __launch_bounds__(kAdThreads) void adapter_weights_grad_kernel(Adapte
   const float *m = is_a ? a.g : a.h;
   const int C = is_a ? a.K : a.N;
   const bool vec = is_a ? a.vec_x : a.vec_dy;
-  const int c0 = 64 * tile;
+  const int c0 = 64 * (Split ? tile : kWaves * tile + wave);
+  if (c0 >= C) return;  // only without Split, which has no barrier
+  constexpr int kApart = Split ? 4 * kWaves : 4;  // rows from one of a wave's groups to the next
+  const int own = q4 + (Split ? 4 * wave : 0);
   const int first = min(max(a.offsets[e], 0), a.T);
   const int count = max(min(max(a.offsets[e + 1], 0), a.T) - first, 0);
   void *out = is_a ? a.dA : a.dB;
@@ -536,17 +545,17 @@ __global__ __launch_bounds__(kAdThreads) void adapter_weights_grad_kernel(Adapte
   auto numbers = [&](int i0) {
 #pragma unroll
     for (int u = 0; u < kRowsDeep; ++u) {
-      const int i = i0 + 4 * kWaves * u + 4 * wave + q4;
+      const int i = i0 + kApart * u + own;
       at[u] = i < count ? a.rows[first + i] : -1;
     }
   };
   numbers(0);
-  for (int i0 = 0; i0 < count; i0 += 4 * kWaves * kRowsDeep) {
+  for (int i0 = 0; i0 < count; i0 += kApart * kRowsDeep) {
     u2 vv[kRowsDeep];
     float mv[kRowsDeep][RT];
 #pragma unroll
     for (int u = 0; u < kRowsDeep; ++u) {
-      const int i = i0 + 4 * kWaves * u + 4 * wave + q4;
+      const int i = i0 + kApart * u + own;
       const bool ok = at[u] >= 0 && at[u] < a.T;
       const uint16_t *q = v + (int64_t)(ok ? at[u] : 0) * ld + c;
       vv[u] = u2{0u, 0u};
@@ -560,7 +569,7 @@ __global__ __launch_bounds__(kAdThreads) void adapter_weights_grad_kernel(Adapte
 #pragma unroll
       for (int j = 0; j < RT; ++j) mv[u][j] = ok ? m[(int64_t)(first + i) * (16 * RT) + 16 * j + p16] : 0.f;
     }
-    numbers(i0 + 4 * kWaves * kRowsDeep);
+    numbers(i0 + kApart * kRowsDeep);
 #pragma unroll
     for (int u = 0; u < kRowsDeep; ++u)
 #pragma unroll
@@ -570,39 +579,61 @@ __global__ __launch_bounds__(kAdThreads) void adapter_weights_grad_kernel(Adapte
         for (int j = 0; j < RT; ++j) acc[j][x] = mfma32(w, mv[u][j], acc[j][x]);
       }
   }
-  // Join the waves through LDS, up to four rank tiles at a time. A block x of a rank tile has, in lane
-  // (p16, q4), rank p16 of columns 4 (4 q4 + reg) + x; a thread adds up the waves' four
-  // values x of one (p16, q4, reg): four consecutive columns.
-  constexpr int JT = RT < 4 ? RT : 4;
+  // Block x of a rank tile has, in lane (p16, q4), rank p16 of columns
+  // 4 (4 q4 + reg) + x: the four x are consecutive columns.
+  auto put = [&](int i, int col, f4 sum) {
+    if (i >= a.r || col >= C) return;
+    const int64_t to = is_a ? ((int64_t)e * a.r + i) * a.K + col : ((int64_t)e * a.N + col) * a.r + i;
+    if (is_a && a.vec_da) {
+      if (a.g_f32) {
+        f4 *w = reinterpret_cast<f4 *>(static_cast<float *>(out) + to);
+        *w = a.accumulate ? sum + *w : sum;
+      } else {
+        *reinterpret_cast<u2 *>(static_cast<uint16_t *>(out) + to) = u2{(uint32_t)Tr::from(sum[0]) | (uint32_t)Tr::from(sum[1]) << 16,
+                                                                        (uint32_t)Tr::from(sum[2]) | (uint32_t)Tr::from(sum[3]) << 16};
+      }
+      return;
+    }
 #pragma unroll
-  for (int j0 = 0; j0 < RT; j0 += JT) {
-    __syncthreads();
+    for (int x = 0; x < 4; ++x) {
+      if (col + x >= C) break;
+      const int64_t at1 = to + (is_a ? x : (int64_t)x * a.r);
+      if (a.g_f32) {
+        float *w = static_cast<float *>(out) + at1;
+        *w = sum[x] + (a.accumulate ? *w : 0.f);
+      } else {
+        static_cast<uint16_t *>(out)[at1] = Tr::from(sum[x]);
+      }
+    }
+  };
+  if constexpr (!Split) {
 #pragma unroll
-    for (int j = 0; j < JT; ++j)
+    for (int j = 0; j < RT; ++j)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) s_part[((wave * JT + j) * 4 + x) * 64 + lane] = acc[j0 + j][x];
-    __syncthreads();
-    for (int t = threadIdx.x; t < JT * 256; t += kAdThreads) {
-      // neighbours: dA's columns, dB's ranks
-      const int l = is_a ? (t >> 4 & 15) + 16 * (t >> 2 & 3) : (t & 15) + 16 * (t >> 6 & 3), reg = is_a ? t & 3 : t >> 4 & 3, j = t >> 8;
-      f4 sum = f4{0.f, 0.f, 0.f, 0.f};
+      for (int reg = 0; reg < 4; ++reg)
+        put(16 * j + p16, c0 + 4 * (4 * q4 + reg), f4{acc[j][0][reg], acc[j][1][reg], acc[j][2][reg], acc[j][3][reg]});
+  } else {
+    // Join the waves through LDS, up to four rank tiles at a time; a thread adds up the waves' four
+    // values x of one (p16, q4, reg).
+    constexpr int JT = RT < 4 ? RT : 4;
+    __shared__ __attribute__((aligned(16))) f4 s_part[kWaves * JT * 4 * 64];
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w)
+    for (int j0 = 0; j0 < RT; j0 += JT) {
+      __syncthreads();
 #pragma unroll
-        for (int x = 0; x < 4; ++x) sum[x] += reinterpret_cast<const float *>(&s_part[((w * JT + j) * 4 + x) * 64 + l])[reg];
-      const int i = 16 * (j0 + j) + (l & 15), col = c0 + 4 * (4 * (l >> 4) + reg);
-      if (i >= a.r) continue;
-      const int64_t at1 = is_a ? ((int64_t)e * a.r + i) * a.K + col : ((int64_t)e * a.N + col) * a.r + i;
+      for (int j = 0; j < JT; ++j)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        if (col + x >= C) break;
-        const int64_t to = at1 + (is_a ? x : (int64_t)x * a.r);
-        if (a.g_f32) {
-          float *w = static_cast<float *>(out) + to;
-          *w = sum[x] + (a.accumulate ? *w : 0.f);
-        } else {
-          static_cast<uint16_t *>(out)[to] = Tr::from(sum[x]);
-        }
+        for (int x = 0; x < 4; ++x) s_part[((wave * JT + j) * 4 + x) * 64 + lane] = acc[j0 + j][x];
+      __syncthreads();
+      for (int t = threadIdx.x; t < JT * 256; t += kAdThreads) {
+        // neighbours: dA's columns, dB's ranks
+        const int l = is_a ? (t >> 4 & 15) + 16 * (t >> 2 & 3) : (t & 15) + 16 * (t >> 6 & 3), reg = is_a ? t & 3 : t >> 4 & 3, j = t >> 8;
+        f4 sum = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) sum[x] += reinterpret_cast<const float *>(&s_part[((w * JT + j) * 4 + x) * 64 + l])[reg];
+        put(16 * (j0 + j) + (l & 15), c0 + 4 * (4 * (l >> 4) + reg), sum);
       }
     }
   }
@@ -697,8 +728,13 @@ int64_t row_blocks(int T, int n, int rows) {
   return (T + used * (rows - 1)) / rows;
 }
 
-// 16 rows a workgroup where adapters have few rows each or the batch has few, else 32.
-bool few_rows(int T, int n) { return T < 8192 || T <= 16 * (int64_t)n; }
+// Rows a workgroup, 16 or 32. 16 give more workgroups; 32 read the adapters
+// half as often, and hold in one block the rows of most adapters where those have 8 to 24 on
+// average. At rank 16 and 2048 x 2048, 16 against 32 rows, forward, us: 4096 rows of 16 adapters
+// 19.7 / 23.8, of 64 26.2 / 24.6, of 256 28.6 / 23.7, of 1024 50.9 / 53.8; 8192 rows of 128 35.3 / 39.8,
+// of 512 43.6 / 35.7, of 1024 62.9 / 58.8; 16384 rows of 8 41.8 / 39.1, of 1024 98.5 / 90.8. The
+// gradients follow within a few percent.
+bool few_rows(int T, int n) { return T < 16384 && (T < 8 * (int64_t)n || T > 24 * (int64_t)n); }
 
 template <typename Tr, int RT, int RB, bool F32>
 hipError_t run_forward(const AdapterArgs &a, hipStream_t s) {
@@ -727,14 +763,21 @@ hipError_t run_rows_grad(const AdapterGradArgs &a, hipStream_t s) {
 }
 template <typename Tr, int RT>
 hipError_t run_grad(const AdapterGradArgs &a, hipStream_t s) {
-  const int ta = a.dA ? (int)cdiv(a.K, 64) : 0, tb = a.dB ? (int)cdiv(a.N, 64) : 0;
+  // Waves share an adapter's rows where there are many a adapter. Whole gradients at rank 16 and
+  // 2048 x 2048, shared against not, us: 4096 rows of 16 adapters 37 / 47, of 64 62 / 47, of 256 155 / 63;
+  // 8192 rows of 32 64 / 63, of 128 105 / 71, of 1024 567 / 205; 16384 rows of 8 87 / 188.
+  const bool split = a.T > (int64_t)128 * a.n;
+  const int cols = split ? 64 : 64 * kWaves;
+  const int ta = a.dA ? (int)cdiv(a.K, cols) : 0, tb = a.dB ? (int)cdiv(a.N, cols) : 0;
   if (!grid_fits((int64_t)a.n * (ta + tb), kAdThreads)) return hipErrorInvalidConfiguration;
   hipError_t err;
   constexpr int kMore = RT < 8 ? 2 : 1;
   if (few_rows(a.T, a.n)) err = a.dx_f32 ? run_rows_grad<Tr, RT, 1, true>(a, s) : run_rows_grad<Tr, RT, 1, false>(a, s);
   else err = a.dx_f32 ? run_rows_grad<Tr, RT, kMore, true>(a, s) : run_rows_grad<Tr, RT, kMore, false>(a, s);
   if (err != hipSuccess || ta + tb == 0) return err;
-  adapter_weights_grad_kernel<Tr, RT><<<dim3((unsigned)((int64_t)a.n * (ta + tb))), kAdThreads, 0, s>>>(a, ta, ta + tb);
+  const dim3 grid((unsigned)((int64_t)a.n * (ta + tb)));
+  if (split) adapter_weights_grad_kernel<Tr, RT, true><<<grid, kAdThreads, 0, s>>>(a, ta, ta + tb);
+  else adapter_weights_grad_kernel<Tr, RT, false><<<grid, kAdThreads, 0, s>>>(a, ta, ta + tb);
   return hipGetLastError();
 }
 

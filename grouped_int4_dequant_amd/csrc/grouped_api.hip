@@ -10,6 +10,9 @@ using namespace moe;
 
 namespace {
 
+// Row and column counts in 32 bits leave room for a tile beyond the last one.
+constexpr int32_t kMaxExtent = 1 << 30;
+
 bool aligned(const void *p, size_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
 bool is16(int32_t t) { return t == MOE_BF16 || t == MOE_FP16; }
 // an output type beside operands of type t: t itself, or fp32
@@ -39,7 +42,7 @@ int status(hipError_t e) {
 int check_groups(int32_t dtype, int32_t out, const int32_t *offsets, int32_t G, int32_t P, int32_t N, int32_t K) {
   if (!is16(dtype) || !out_type(out, dtype)) return MOE_EINVAL;
   if (!offsets || !aligned(offsets, 4) || G < 1 || P < 0 || N < 1 || K < 1) return MOE_EINVAL;
-  if (G > MOE_MAX_EXPERTS) return MOE_EUNSUPPORTED;
+  if (G > MOE_MAX_EXPERTS || P > kMaxExtent || N > kMaxExtent || K > kMaxExtent) return MOE_EUNSUPPORTED;
   return MOE_OK;
 }
 
@@ -48,7 +51,7 @@ int check_adapter(int32_t dtype, const uint16_t *x, int64_t ld_x, int32_t T, int
   if (!is16(dtype) || T < 0 || K < 1 || N < 1 || r < 1 || n < 1) return MOE_EINVAL;
   if (!A || !B || !offsets || !aligned(A, 2) || !aligned(B, 2) || !aligned(offsets, 4) || !aligned(scale, 4)) return MOE_EINVAL;
   if (T > 0 && (!x || !rows || !aligned(x, 2) || !aligned(rows, 4) || ld_x < K)) return MOE_EINVAL;
-  if (r > MOE_MAX_ADAPTER_RANK || n > MOE_MAX_ADAPTERS || T > MOE_MAX_TOKENS) return MOE_EUNSUPPORTED;
+  if (r > MOE_MAX_ADAPTER_RANK || n > MOE_MAX_ADAPTERS || T > MOE_MAX_TOKENS || K > kMaxExtent || N > kMaxExtent) return MOE_EUNSUPPORTED;
   return MOE_OK;
 }
 
@@ -141,7 +144,7 @@ int moe_combine(int32_t dtype, const void *o, int64_t ldo, int32_t P, const int3
                 int64_t ldy, hipStream_t stream) {
   if (!is16(dtype) || !out_type(y_dtype, dtype) || (add && !out_type(add_dtype, dtype))) return MOE_EINVAL;
   if (T < 0 || k < 1 || d < 1 || P < 0 || ldo < d || ldy < d || (add && ldadd < d)) return MOE_EINVAL;
-  if (T > MOE_MAX_TOKENS || k > MOE_MAX_EXPERTS) return MOE_EUNSUPPORTED;
+  if (T > MOE_MAX_TOKENS || k > MOE_MAX_EXPERTS || d > kMaxExtent) return MOE_EUNSUPPORTED;
   if (T == 0) return MOE_OK;
   if ((P > 0 && !o) || !pair_pos || !y || !typed(o, dtype) || !typed(y, y_dtype) || !aligned(pair_pos, 4) || !aligned(w, 4)) return MOE_EINVAL;
   if (add && !typed(add, add_dtype)) return MOE_EINVAL;
@@ -168,7 +171,7 @@ int moe_combine_backward(int32_t dtype, const void *dy, int64_t lddy, const void
                          int64_t lddo, float *dw, hipStream_t stream) {
   if (!is16(dtype) || T < 0 || k < 1 || d < 1 || P < 0 || lddy < d) return MOE_EINVAL;
   if ((d_o && lddo < d) || (dw && ldo < d) || (!d_o && !dw)) return MOE_EINVAL;
-  if (T > MOE_MAX_TOKENS || k > MOE_MAX_EXPERTS) return MOE_EUNSUPPORTED;
+  if (T > MOE_MAX_TOKENS || k > MOE_MAX_EXPERTS || d > kMaxExtent) return MOE_EUNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (!dy || !pair_pos || !typed(dy, dtype) || !typed(d_o, dtype) || !aligned(pair_pos, 4) || !aligned(w, 4) || !aligned(dw, 4)) return MOE_EINVAL;
   if (dw && P > 0 && (!o || !typed(o, dtype))) return MOE_EINVAL;
@@ -276,6 +279,7 @@ int moe_adapter_backward(int32_t dtype, const void *dy, int64_t lddy, const void
   a.vec_dy = units(dy, lddy, N);
   a.vec_b = units(B, r, r);
   auto wide = [&](const void *p, int64_t ld) { return aligned(p, 16) && ld * size_of(dx_dtype) % 16 == 0; };
+  a.vec_da = runs(dA, g_dtype, 0) && K % 4 == 0;
   a.vec_dx = dx && wide(dx, lddx) && (!dx_base || wide(dx_base, lddx_base));
   return status(launch_adapter_grad(a, dtype == MOE_FP16, stream));
 }

@@ -40,7 +40,7 @@ struct GroupedArgs {
   int32_t out_f32;          // out is fp32, else the operands' type
   int32_t accumulate;       // fp32 out only: out += result
   int32_t vec;              // every 16-byte unit of the operands is aligned and whole
-  int32_t wide;             // operand rows are at least eight elements wide where they lie across
+  int32_t wide;             // 31-bit byte offsets reach every operand of the wide tiles
   int32_t vec_out;          // four consecutive outputs may be stored at once
 };
 
@@ -114,6 +114,7 @@ struct AdapterGradArgs {
   int32_t g_f32, accumulate;
   float *g, *h;             // workspace, fp32 [T][16 rank_tiles(r)] by sorted place: scale B^T dy and scale A x
   int32_t vec_x, vec_dy, vec_dx, vec_b;
+  int32_t vec_da;           // four consecutive values of dA may be stored at once
 };
 hipError_t launch_adapter_plan(const int32_t *row_adapter, int32_t T, int32_t n, int32_t *rows, int32_t *offsets, hipStream_t s);
 hipError_t launch_adapter(const AdapterArgs &a, bool fp16, hipStream_t s);

@@ -92,8 +92,8 @@ __device__ __forceinline__ u4 load_unit(const uint16_t *p, int n) {
 
 // ---------------------------------------------------------------- small tiles
 // 64 x 64 outputs a workgroup of four waves, 64 r a step, any sizes and
-// alignment. The next step's operands are loaded into registers while this one's matrix
-// instructions run, and go to the other LDS buffer behind them. For calls whose wide
+// alignment. Operands are loaded into registers two steps ahead and go to the other LDS
+// buffer behind the matrix instructions of the step before theirs. For calls whose wide
 // tiles would leave most CUs idle, and for operands the wide tiles cannot request.
 constexpr int kSmall = 64;
 
@@ -140,10 +140,13 @@ __global__ __launch_bounds__(256) void grouped_small_kernel(GroupedArgs a) {
     nj = J - j0;
     nr = Mode == kFwd ? a.K : a.N;
   }
-  const int steps = (nr + kBR - 1) / kBR;
+  // (with no row of A at all nothing is read, and every result is that of a masked row)
+  const int steps = Mode == kFwd && a.a_rows == 0 ? 0 : (nr + kBR - 1) / kBR;
 
   // ---- staging. Unit u = tid + 256 i: a straight operand's row u / 8, an
-  // across operand's r = u / 8, eight r or columns at 8 (slot's unit).
+  // across operand's r = u / 8, eight r or columns at 8 (slot's unit). Straight rows past the
+  // output's end repeat its last, and masked ones read some row that exists: their results are not
+  // stored, or set to zero.
   const uint16_t *lp[U], *rp[U];  // at step 0; nullptr: zeros
   const uint16_t *L = Mode == kWgrad ? a.w : a.rows;
   const int64_t ldl = Mode == kWgrad ? a.ld_w : a.ld_rows;
@@ -158,35 +161,37 @@ __global__ __launch_bounds__(256) void grouped_small_kernel(GroupedArgs a) {
     if (kLAcross) {
       lp[i] = lslot < ni ? L + (int64_t)(first + row) * ldl + i0 + lslot : nullptr;
     } else {
-      int64_t at = first + i0 + row;
-      bool ok = row < ni;
-      if (Mode == kFwd && a.a_row && ok) at = a.a_row[at];
-      if (Mode == kFwd) ok = ok && at >= 0 && at < a.a_rows;
-      lp[i] = ok ? L + at * ldl + lslot : nullptr;
+      int64_t at = first + i0 + min(row, ni - 1);
+      if (Mode == kFwd && a.a_row) at = a.a_row[at];
+      if (Mode == kFwd) at = min(max(at, (int64_t)0), max((int64_t)a.a_rows - 1, (int64_t)0));
+      lp[i] = L + at * ldl + lslot;
     }
     if (kRAcross) rp[i] = rslot < nj ? R + j0 + rslot + (Mode == kDgrad ? (int64_t)row * ldr : 0) : nullptr;
-    else rp[i] = row < nj ? R + (int64_t)(j0 + row) * ldr + rslot : nullptr;
+    else rp[i] = R + (int64_t)(j0 + min(row, nj - 1)) * ldr + rslot;
   }
-  u4 lreg[U], rreg[U];
-  auto load = [&](int s) {
+  u4 lreg[2][U], rreg[2][U];
+  auto load = [&](int s, u4 (&lreg)[U], u4 (&rreg)[U], auto whole) __attribute__((always_inline)) {  // whole: every r of the step exists
+    constexpr bool kAll = decltype(whole)::value;
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       const int r = s * kBR + urow + 32 * i;  // across operands: the unit's r
-      if (kLAcross) lreg[i] = load_unit<Vec>(lp[i] + (int64_t)s * kBR * ldl, lp[i] && r < nr ? ni - lslot : 0);
-      else lreg[i] = load_unit<Vec>(lp[i] + s * kBR, lp[i] ? nr - s * kBR - lslot : 0);
-      if (Mode == kWgrad) {
+      if (Mode == kWgrad) {  // a masked row's dC may hold anything: both operands are zeros
         int at = -1;
-        if (rp[i] && r < nr) at = a.a_row ? a.a_row[first + r] : first + r;
+        if (r < nr) at = a.a_row ? a.a_row[first + r] : first + r;
         const bool ok = at >= 0 && at < a.a_rows;
-        rreg[i] = load_unit<Vec>(rp[i] + (ok ? at * ldr : 0), ok ? nj - rslot : 0);
-      } else if (kRAcross) {
-        rreg[i] = load_unit<Vec>(rp[i] + (int64_t)s * kBR * ldr, rp[i] && r < nr ? nj - rslot : 0);
+        lreg[i] = load_unit<Vec>(lp[i] + (int64_t)s * kBR * ldl, lp[i] && ok ? ni - lslot : 0);
+        rreg[i] = load_unit<Vec>(rp[i] + (ok ? at * ldr : 0), rp[i] && ok ? nj - rslot : 0);
+        continue;
+      }
+      lreg[i] = load_unit<Vec>(lp[i] + s * kBR, kAll ? 8 : nr - s * kBR - lslot);
+      if (kRAcross) {
+        rreg[i] = load_unit<Vec>(rp[i] + (int64_t)s * kBR * ldr, rp[i] && (kAll || r < nr) ? nj - rslot : 0);
       } else {
-        rreg[i] = load_unit<Vec>(rp[i] + s * kBR, rp[i] ? nr - s * kBR - rslot : 0);
+        rreg[i] = load_unit<Vec>(rp[i] + s * kBR, kAll ? 8 : nr - s * kBR - rslot);
       }
     }
   };
-  auto keep = [&](int buf) {
+  auto keep = [&](int buf, const u4 (&lreg)[U], const u4 (&rreg)[U]) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       *reinterpret_cast<u4 *>(s_l[buf] + 16 * (tid + 256 * i)) = lreg[i];
@@ -210,14 +215,17 @@ __global__ __launch_bounds__(256) void grouped_small_kernel(GroupedArgs a) {
     }
     return s8{x[0][0], x[0][1], x[0][2], x[0][3], x[1][0], x[1][1], x[1][2], x[1][3]};
   };
+  constexpr std::false_type partly{};
   if (steps > 0) {
-    load(0);
-    keep(0);
+    load(0, lreg[0], rreg[0], partly);
+    if (steps > 1) load(1, lreg[1], rreg[1], partly);
+    keep(0, lreg[0], rreg[0]);
   }
-  for (int s = 0; s < steps; ++s) {
-    const int buf = s & 1;
+  // step s out of LDS buffer `buf`; registers `buf` receive step s + 2, the others hold s + 1
+  auto step = [&](int s, auto buf_, auto whole) __attribute__((always_inline)) {
+    constexpr int buf = decltype(buf_)::value;
     __syncthreads();
-    if (s + 1 < steps) load(s + 1);
+    if (decltype(whole)::value || s + 2 < steps) load(s + 2, lreg[buf], rreg[buf], whole);
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
       s8 l[2], r[2];
@@ -231,7 +239,18 @@ __global__ __launch_bounds__(256) void grouped_small_kernel(GroupedArgs a) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) acc[i][j] = Tr::mfma(r[j], l[i], acc[i][j]);
     }
-    if (s + 1 < steps) keep(buf ^ 1);
+    if (decltype(whole)::value || s + 1 < steps) keep(buf ^ 1, lreg[buf ^ 1], rreg[buf ^ 1]);
+  };
+  constexpr std::integral_constant<int, 0> even{};
+  constexpr std::integral_constant<int, 1> odd{};
+  int s = 0;
+  for (; (s + 4) * kBR <= nr && s < steps; s += 2) {  // steps s + 2 and s + 3 are whole
+    step(s, even, std::true_type{});
+    step(s + 1, odd, std::true_type{});
+  }
+  for (; s < steps; s += 2) {
+    step(s, even, partly);
+    if (s + 1 < steps) step(s + 1, odd, partly);
   }
 
   // ---- results: lane holds output row p16 and four consecutive columns of each block
@@ -469,7 +488,7 @@ __device__ __forceinline__ void wide_body(const GroupedArgs &a, const WideTile t
 #pragma unroll
     for (int j = 0; j < kUnits; ++j) rv[j] = (uint32_t)(min(row0 + 64 * j, t.nj - 1) * a.ld_w + rr) * 2;
   }
-  int rrow[kUnits];  // weight gradient: the rows of A of the next requested step, -1: zeros
+  int rrow[kUnits];  // weight gradient: the rows of A of the next requested step, -1: zeros (dC's rows are the same r)
   auto fetch_rows = [&](int s) __attribute__((always_inline)) {
     if constexpr (Mode == kWgrad) {
 #pragma unroll
@@ -484,7 +503,8 @@ __device__ __forceinline__ void wide_body(const GroupedArgs &a, const WideTile t
   const int64_t lstep = kLAcross ? kBR * a.ld_w * 2 : kBR * 2, rstep = Mode == kDgrad ? kBR * a.ld_w * 2 : Mode == kFwd ? kBR * 2 : 0;
   auto request_l = [&](int s, int i, uint8_t *buf, auto whole) __attribute__((always_inline)) {
     const char *p = uniform(lbase + (kLAcross ? (lstep >> 3) * i : 0)) + lv[kLAcross ? 0 : i];
-    if constexpr (!decltype(whole)::value) p = s * kBR + lr + (kLAcross ? 8 * i : 0) < t.nr ? p : (const char *)&g_zeros;
+    if constexpr (Mode == kWgrad) p = rrow[i] >= 0 ? p : (const char *)&g_zeros;  // a masked row's dC may hold anything
+    else if constexpr (!decltype(whole)::value) p = s * kBR + lr < t.nr ? p : (const char *)&g_zeros;
     load_lds16(p, buf + row_piece<Mode>(8 * i) + row_piece<Mode>(1) * wave);
   };
   auto request_r = [&](int s, int i, uint8_t *buf, auto whole) __attribute__((always_inline)) {
@@ -812,17 +832,25 @@ hipError_t launch(const GroupedArgs &a, hipStream_t s) {
   const int64_t used = a.G < a.P ? a.G : a.P;  // groups that can have rows
   const int J = Mode == kFwd ? a.N : a.K;
   if constexpr (Vec) {
+    const int64_t at_least = Mode == kWgrad ? (int64_t)a.G * cdiv(a.N, kWide) * cdiv(a.K, kWide)
+                                            : (used > a.P / kWide ? used : a.P / kWide) * cdiv(J, kWide);
+    // Wide tiles where at least half the CUs get one. Against small tiles, us, forward / input gradient / weight
+    // gradient: 16 groups, 1024 rows, 1024 x 1024 (64, 64 and 256 wide tiles) 16.3 / 17.2 / 15.1 against 12.2 / 12.7 / 18.6;
+    // 32 groups, 2048 rows (128, 128, 512) 21.0 / 23.4 / 26.5 against 24.7 / 24.7 / 32.6; 4 groups, 8192 rows (128, 128,
+    // 64) 27.0 / 27.1 / 55.7 against 38.5 / 39.5 / 40.3; 8 groups, 1024 rows (32, 32, 128) 16.3 / 22.9 / 15.8 against 11.0 / 11.6 / 12.9.
+    const bool wide = a.wide && at_least >= 128;
     if constexpr (Mode != kWgrad) {
-      if (a.P <= 64) {
+      // Few rows whose weights are too few for wide tiles. Against small tiles at N = 1024, K = 2048, us, forward / input
+      // gradient: 8 groups, 8 rows 9.4 / 9.0 against 13.2 / 10.5, 64 rows 11.6 / 9.0 against 13.6 / 11.2, 128 rows 18.6 / 11.6
+      // against 13.7 / 11.4. Against wide ones: 64 rows of 256 groups 48 / 40 against 42 / 42.
+      if (!wide && a.P <= 64) {
         const int64_t wgs = (a.P + used * (kFewRows - 1)) / kFewRows * cdiv(J, Mode == kFwd ? 32 : 64);
         if (!grid_fits(wgs, 512)) return hipErrorInvalidConfiguration;
         grouped_few_kernel<Tr, Mode><<<dim3((unsigned)wgs), 512, 0, s>>>(a);
         return hipGetLastError();
       }
     }
-    const int64_t at_least = Mode == kWgrad ? (int64_t)a.G * cdiv(a.N, kWide) * cdiv(a.K, kWide)
-                                            : (used > a.P / kWide ? used : a.P / kWide) * cdiv(J, kWide);
-    if (a.wide && at_least >= 128) {
+    if (wide) {
       // Tiles of 128 rows and three buffers where groups hold few rows, of 256 and two where they
       // hold many, by the average. Forward at 256 experts, N = 1024, K = 2048: 159 against 170 us at
       // 2 rows a group, 214 / 234 at 64, 380 / 385 at 256; 16 groups of 1024 rows: 301 / 284. Input gradient:

@@ -493,6 +493,8 @@ int moe_layer_graph_destroy(moe_layer_graph_t *graph);
  *     taken as the nearest of the two.
  *   - Outputs must not overlap inputs unless stated, and no output row may be
  *     reached twice (row stride at least the width; a permutation of rows).
+ *   - P, N, K and d above 2^30, and calls that would launch 2^32 threads or
+ *     more, are MOE_EUNSUPPORTED.
  *   - stream must belong to the current device.
  */
 #define MOE_BF16 0
@@ -513,8 +515,7 @@ int moe_layer_graph_destroy(moe_layer_graph_t *graph);
  * expert projection of the routed tokens. An infinity or NaN reaches only the
  * results whose sum it enters. Errors: MOE_EINVAL (null or misaligned
  * pointer, unknown type, G, N or K < 1, P or a_rows < 0, a stride below the
- * width), MOE_EUNSUPPORTED (G > MOE_MAX_EXPERTS, or 2^32 or more
- * threads), MOE_EHIP. P == 0 enqueues nothing. One kernel; no workspace.
+ * width), MOE_EUNSUPPORTED (G > MOE_MAX_EXPERTS), MOE_EHIP. P == 0 enqueues nothing. One kernel; no workspace.
  */
 int moe_grouped_gemm(int32_t dtype, const void *A, int64_t lda, int32_t a_rows, const int32_t *a_row,
                      const int32_t *offsets, int32_t G, int32_t P, int32_t N, int32_t K, const void *W, void *C,
@@ -534,7 +535,8 @@ int moe_grouped_gemm_dgrad(int32_t dtype, const void *dC, int64_t lddc, const in
 /*
  * Gradient of moe_grouped_gemm's weights:
  *     dW_e[n][k] = sum_{p in group e} dC[p][n] * A[row(p)][k]
- * for every group; an empty group's dW is zeros. accumulate != 0 (fp32 dW
+ * for every group; an empty group's dW is zeros, and a masked row adds
+ * nothing whatever its dC row holds. accumulate != 0 (fp32 dW
  * only, else MOE_EUNSUPPORTED) adds to what dW holds. A, a_row, a_rows and dC
  * as above; dW dtype or fp32 [G][N][K]. P == 0 still writes the zeros. Errors
  * as moe_grouped_gemm.

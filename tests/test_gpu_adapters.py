@@ -148,6 +148,20 @@ def test_nan_stays_in_its_row(moe):  # noqa: F811
     assert torch.isfinite(dA[0]).all() and torch.isfinite(dB[0]).all() and not torch.isfinite(dA[1]).all()
 
 
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("r", [1, 5, 16, 17, 40, 100])
+def test_infinities_keep_their_sign(moe, dtype, r):  # noqa: F811
+    """An infinite row gives the formula's infinities; ranks that only fill up the
+    kernel's tiles (0 times infinity) have no part in it."""
+    g, ids, x, dy, A, B, scale = problem(70, 2, 72, 40, r, dtype, "mixed")
+    A, B, scale = A.abs() + 0.5, B.abs() + 0.5, scale.abs() + 0.5
+    plan = moe.adapter_plan(ids, 2)
+    hit = int((ids == 1).nonzero()[0, 0])
+    x[hit, 5], dy[hit, 6] = float("inf"), float("-inf")
+    assert (moe.adapter_forward(x, A, B, scale, plan)[hit] == float("inf")).all()
+    assert (moe.adapter_backward(dy, x, A, B, scale, plan)[0][hit] == float("-inf")).all()
+
+
 def test_beside_the_int4_projection(moe):  # noqa: F811
     """A serving step: the shared int4 projection, then the adapters in place on
     its fp32 result; equal to adding them to a copy."""

@@ -183,6 +183,22 @@ def test_masked_rows_are_zeros(moe, P, N, K):
     R.within(D, value, R.stored(value, R.sums(P, mag), F4), "dW")
 
 
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("P,N,K", [(300, 40, 72), (300, 33, 70), (1200, 1024, 512)])
+def test_masked_rows_give_no_weight_gradient(moe, dtype, P, N, K):
+    """dC's rows may hold anything where the row of A is masked."""
+    g, G, rows = gen(15), 70, P - 30
+    offsets = torch.linspace(0, P, G + 1).to(torch.int32).cuda()
+    A, dC = rnd(g, rows, K, dtype=dtype), rnd(g, P, N, dtype=dtype)
+    a_row = torch.randint(0, rows, (P,), generator=g, dtype=torch.int32)
+    a_row[::3], a_row[1::7] = -1, rows
+    masked = ((a_row < 0) | (a_row >= rows)).cuda()
+    a_row = a_row.cuda()
+    want = moe.grouped_gemm_wgrad(torch.where(masked[:, None], 0.0, dC.float()).to(dtype), A, offsets, a_row=a_row, out_dtype=F4)
+    dC[masked] = float("nan")
+    assert torch.equal(moe.grouped_gemm_wgrad(dC, A, offsets, a_row=a_row, out_dtype=F4), want) and torch.isfinite(want).all()
+
+
 @pytest.mark.parametrize("layout", ["edges", "many"])
 def test_gradients_against_differences(moe, layout):
     """The product is linear in A and in W: the change of <C, G> under a change of

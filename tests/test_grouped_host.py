@@ -28,6 +28,7 @@ ADAPTER = dict(dtype=0, x=p, ldx=64, T=8, K=64, N=32, r=16, n=4, A=p, B=p, scale
 AGRAD = dict(dtype=0, dy=p, lddy=32, x=p, ldx=64, T=8, K=64, N=32, r=16, n=4, A=p, B=p, scale=p, rows=p, offsets=p, dx_base=p,
              lddx_base=64, dx=p, dx_dtype=0, lddx=64, dA=p, dB=p, g_dtype=2, acc=0, ws=p, ws_bytes=1 << 20)
 
+LARGE = (1 << 30) + 1
 REFUSED = [
     ("moe_grouped_gemm", GEMM, EINVAL, dict(dtype=2), dict(dtype=3), dict(c_dtype=1), dict(A=None), dict(W=None), dict(C=None),
      dict(offsets=None), dict(A=p + 1), dict(W=p + 1), dict(C=p + 1), dict(a_row=p + 2), dict(offsets=p + 2), dict(G=0), dict(N=0),
@@ -56,6 +57,13 @@ REFUSED = [
      dict(B=None), dict(rows=None), dict(offsets=None), dict(dx=None, dA=None, dB=None), dict(dA=p + 2), dict(ws=None), dict(ws=p + 16),
      dict(lddy=31), dict(lddx=63), dict(lddx_base=63), dict(ldx=63)),
     ("moe_adapter_backward", AGRAD, EUNSUP, dict(r=129), dict(n=1025), dict(T=(1 << 20) + 1), dict(g_dtype=0, acc=1)),
+    ("moe_grouped_gemm", GEMM, EUNSUP, dict(P=LARGE), dict(N=LARGE, ldc=LARGE), dict(K=LARGE, lda=LARGE)),
+    ("moe_grouped_gemm_dgrad", DGRAD, EUNSUP, dict(P=LARGE), dict(N=LARGE, lddc=LARGE), dict(K=LARGE, ldda=LARGE)),
+    ("moe_grouped_gemm_wgrad", WGRAD, EUNSUP, dict(P=LARGE), dict(N=LARGE, lddc=LARGE), dict(K=LARGE, lda=LARGE)),
+    ("moe_combine", COMBINE, EUNSUP, dict(d=LARGE, ldo=LARGE, ldy=LARGE, ldadd=LARGE)),
+    ("moe_combine_backward", CGRAD, EUNSUP, dict(d=LARGE, lddy=LARGE, ldo=LARGE, lddo=LARGE)),
+    ("moe_adapter_forward", ADAPTER, EUNSUP, dict(K=LARGE, ldx=LARGE), dict(N=LARGE, ldy=LARGE, ldbase=LARGE)),
+    ("moe_adapter_backward", AGRAD, EUNSUP, dict(K=LARGE, ldx=LARGE, lddx=LARGE, lddx_base=LARGE), dict(N=LARGE, lddy=LARGE)),
     ("moe_adapter_backward", AGRAD, EWS, dict(ws_bytes=2 * 8 * 16 * 4 - 1), dict(r=17, ws_bytes=2 * 8 * 32 * 4 - 1)),
 ]
 
