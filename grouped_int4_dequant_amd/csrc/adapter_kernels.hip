@@ -14,6 +14,10 @@
 // largest value, 22 bits), so that nothing is rounded between the two factors
 // beyond fp32's own precision: the 16-bit matrix instructions at two or three times the work are
 // still three to five times faster than the fp32 one.
+//
+// Bound by memory, and in decode by the launch. 8192 rows, 16 adapters of rank 32, 2048 x 4096, bf16: 41 us
+// (168 MB, 4.1 TB/s) where base and y stay in the last-level cache, 57 us where they do not. One row: 7 us of kernel.
+// Gradients of 4096 rows, four adapters of rank 16, 2048 x 2048: 24 us for the rows, 16 us for the adapters.
 
 #include "grouped_device.h"
 
@@ -715,7 +719,9 @@ __global__ __launch_bounds__(kPlanThreads) void adapter_plan_kernel(const int32_
 }
 
 // Column slices per row block so that about two workgroups a CU are launched,
-// no slice shorter than one pass of the waves.
+// no slice shorter than one pass of the waves: every slice forms the first product again. With one,
+// two and four workgroups a CU 8192 rows (rank 32, 2048 x 4096) took 57, 58 and 66 us, the gradients of 4096
+// rows (rank 16, 2048 x 2048) 50, 47 and 47.
 int slices_for(int64_t blocks, int cols) {
   const int64_t most = cdiv(cols, 64 * kWaves);
   int64_t want = cdiv(512, blocks);

@@ -5,6 +5,8 @@
 //
 // Both are bound by memory: every element is read once and used for one or two
 // operations. Sums are held in fp32, slots in ascending order and `add` last.
+// bf16, width 2048: 8192 tokens x 8 slots in 69 us, 4.4 TB/s; the gradient of 2048 tokens in
+// 29.5 us, 4.8 TB/s (a copy of 1 GiB runs at 5.2 TB/s).
 
 #include "grouped_device.h"
 
