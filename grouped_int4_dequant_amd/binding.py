@@ -807,6 +807,8 @@ def adapter_backward(dy: torch.Tensor, x: torch.Tensor, A: torch.Tensor, B: torc
         ws = c.new(max(need, 1), torch.uint8)
     elif ws.device != c.device:
         raise ValueError(f"ws must be on {c.device}, got {ws.device}")
+    elif not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
     c("moe_adapter_backward", c.code, dy.data_ptr(), _ld(dy, N), x.data_ptr(), _ld(x, K), T, K, N, r, n, A.data_ptr(),
       B.data_ptr(), _ptr(scale), rows.data_ptr(), offsets.data_ptr(), _ptr(dx_base), _ld(dx_base, K), dx.data_ptr(),
       _CODES[dx.dtype], _ld(dx, K), dA.data_ptr(), dB.data_ptr(), _CODES[dA.dtype], int(accumulate), ws.data_ptr(),

@@ -66,7 +66,7 @@ int moe_grouped_gemm(int32_t dtype, const void *A, int64_t lda, int32_t a_rows, 
   if (st != MOE_OK) return st;
   if (a_rows < 0 || lda < K || ldc < N) return MOE_EINVAL;
   if (P == 0) return MOE_OK;
-  if (!A || !W || !C || !typed(A, dtype) || !typed(W, dtype) || !typed(C, c_dtype) || !aligned(a_row, 4)) return MOE_EINVAL;
+  if ((!A && a_rows > 0) || !W || !C || !typed(A, dtype) || !typed(W, dtype) || !typed(C, c_dtype) || !aligned(a_row, 4)) return MOE_EINVAL;
   GroupedArgs a{};
   a.rows = static_cast<const uint16_t *>(A);
   a.ld_rows = lda;
@@ -118,7 +118,7 @@ int moe_grouped_gemm_wgrad(int32_t dtype, const void *dC, int64_t lddc, const vo
   if (a_rows < 0 || lddc < N || lda < K) return MOE_EINVAL;
   if (!dW || !typed(dW, dw_dtype)) return MOE_EINVAL;
   if (accumulate && dw_dtype != MOE_FP32) return MOE_EUNSUPPORTED;
-  if (P > 0 && (!dC || !A || !typed(dC, dtype) || !typed(A, dtype) || !aligned(a_row, 4))) return MOE_EINVAL;
+  if (P > 0 && (!dC || (!A && a_rows > 0) || !typed(dC, dtype) || !typed(A, dtype) || !aligned(a_row, 4))) return MOE_EINVAL;
   if (P == 0 && accumulate) return MOE_OK;
   GroupedArgs a{};
   a.rows = static_cast<const uint16_t *>(A);
@@ -148,6 +148,7 @@ int moe_combine(int32_t dtype, const void *o, int64_t ldo, int32_t P, const int3
   if (T == 0) return MOE_OK;
   if ((P > 0 && !o) || !pair_pos || !y || !typed(o, dtype) || !typed(y, y_dtype) || !aligned(pair_pos, 4) || !aligned(w, 4)) return MOE_EINVAL;
   if (add && !typed(add, add_dtype)) return MOE_EINVAL;
+  if (add == y && (add_dtype != y_dtype || (T > 1 && ldadd != ldy))) return MOE_EINVAL;
   CombineRowsArgs a{};
   a.o = static_cast<const uint16_t *>(o);
   a.ld_o = ldo;
@@ -206,7 +207,7 @@ int moe_adapter_forward(int32_t dtype, const void *x, int64_t ldx, int32_t T, in
   if (st != MOE_OK) return st;
   if (!out_type(y_dtype, dtype) || (base && ldbase < N) || ldy < N) return MOE_EINVAL;
   if (T == 0) return MOE_OK;
-  if (!y || !typed(y, y_dtype) || !typed(base, y_dtype)) return MOE_EINVAL;
+  if (!y || !typed(y, y_dtype) || !typed(base, y_dtype) || (base == y && T > 1 && ldbase != ldy)) return MOE_EINVAL;
   AdapterArgs a{};
   a.x = static_cast<const uint16_t *>(x);
   a.ld_x = ldx;
@@ -243,6 +244,7 @@ int moe_adapter_backward(int32_t dtype, const void *dy, int64_t lddy, const void
   if (st != MOE_OK) return st;
   if (!dx && !dA && !dB) return MOE_EINVAL;
   if (dx && (!out_type(dx_dtype, dtype) || lddx < K || (dx_base && lddx_base < K) || !typed(dx, dx_dtype) || !typed(dx_base, dx_dtype))) return MOE_EINVAL;
+  if (dx && dx == dx_base && T > 1 && lddx != lddx_base) return MOE_EINVAL;
   if (lddy < N || (T > 0 && (!dy || !typed(dy, dtype)))) return MOE_EINVAL;
   if (dA || dB) {
     if (!out_type(g_dtype, dtype) || !typed(dA, g_dtype) || !typed(dB, g_dtype)) return MOE_EINVAL;

@@ -508,7 +508,8 @@ int moe_layer_graph_destroy(moe_layer_graph_t *graph);
  *     C[p][n] = sum_k A[row(p)][k] * W_e[n][k],  p in group e, n < N, k < K
  *   A     dtype [a_rows][lda]; row(p) = a_row[p] when a_row (int32 [P]) is
  *         non-null, else p. A row index outside [0, a_rows) reads as zeros (a masked row:
- *         its C row is zeros), so no index leaves A. Indices may repeat.
+ *         its C row is zeros), so no index leaves A. Indices may repeat. With a_rows = 0
+ *         all rows are masked and A may be NULL.
  *   W     dtype [G][N][K]
  *   C     dtype or fp32 [P][ldc]
  * With moe_route's sorted_token and offsets as a_row and offsets this is the

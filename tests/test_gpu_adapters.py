@@ -214,6 +214,7 @@ def test_refused_tensors(moe):  # noqa: F811
            (TypeError, lambda: moe.adapter_forward(x, A, B, scale, plan, base=torch.zeros(8, 24, device="cuda"), out_dtype=BF)),
            (ValueError, lambda: moe.adapter_backward(dy, x, A, B, scale, plan, accumulate=True)),
            (ValueError, lambda: moe.adapter_backward(dy, x, A, B, scale, plan, ws=torch.empty(16, dtype=torch.uint8, device="cuda"))),
+           (ValueError, lambda: moe.adapter_backward(dy, x, A, B, scale, plan, ws=torch.empty(1, dtype=torch.uint8, device="cuda").expand(1 << 16))),
            (TypeError, lambda: moe.adapter_plan(ids.long(), 2))]
     for kind, f in bad:
         with pytest.raises(kind):

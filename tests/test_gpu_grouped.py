@@ -131,6 +131,18 @@ def test_no_rows(moe):
     assert D.shape == (3, 8, 16) and (D == 0).all()
 
 
+@pytest.mark.parametrize("P,N,K", [(5, 64, 64), (300, 40, 72), (300, 33, 70), (1200, 1024, 512)])
+def test_no_row_of_the_input(moe, P, N, K):
+    """An input without rows: every row is masked."""
+    g, G = gen(16), 70
+    offsets = torch.linspace(0, P, G + 1).to(torch.int32).cuda()
+    A, W, dC = torch.empty(0, K, dtype=BF, device="cuda"), rnd(g, G, N, K), rnd(g, P, N)
+    W[3], dC[2] = float("nan"), float("inf")
+    a_row = torch.randint(-2, 3, (P,), generator=g, dtype=torch.int32).cuda()
+    assert (moe.grouped_gemm(A, W, offsets, a_row=a_row) == 0).all()
+    assert (moe.grouped_gemm_wgrad(dC, A, offsets, a_row=a_row) == 0).all()
+
+
 @pytest.mark.parametrize("dtype", [BF, FP])
 @pytest.mark.parametrize("K", [72, 75, 128])
 def test_infinities_and_nan_stay_in_their_sums(moe, dtype, K):

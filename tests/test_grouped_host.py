@@ -57,6 +57,9 @@ REFUSED = [
      dict(B=None), dict(rows=None), dict(offsets=None), dict(dx=None, dA=None, dB=None), dict(dA=p + 2), dict(ws=None), dict(ws=p + 16),
      dict(lddy=31), dict(lddx=63), dict(lddx_base=63), dict(ldx=63)),
     ("moe_adapter_backward", AGRAD, EUNSUP, dict(r=129), dict(n=1025), dict(T=(1 << 20) + 1), dict(g_dtype=0, acc=1)),
+    ("moe_combine", COMBINE, EINVAL, dict(y=p, add=p, y_dtype=2), dict(y=p, add=p, ldadd=72)),
+    ("moe_adapter_forward", ADAPTER, EINVAL, dict(base=p, y=p, ldbase=40)),
+    ("moe_adapter_backward", AGRAD, EINVAL, dict(dx_base=p, dx=p, lddx_base=72)),
     ("moe_grouped_gemm", GEMM, EUNSUP, dict(P=LARGE), dict(N=LARGE, ldc=LARGE), dict(K=LARGE, lda=LARGE)),
     ("moe_grouped_gemm_dgrad", DGRAD, EUNSUP, dict(P=LARGE), dict(N=LARGE, lddc=LARGE), dict(K=LARGE, ldda=LARGE)),
     ("moe_grouped_gemm_wgrad", WGRAD, EUNSUP, dict(P=LARGE), dict(N=LARGE, lddc=LARGE), dict(K=LARGE, lda=LARGE)),
