@@ -17,7 +17,7 @@
 //
 // Bound by memory, and in decode by the launch. 8192 rows, 16 adapters of rank 32, 2048 x 4096, bf16: 41 us
 // (168 MB, 4.1 TB/s) where base and y stay in the last-level cache, 57 us where they do not. One row: 7 us of kernel.
-// Gradients of 4096 rows, four adapters of rank 16, 2048 x 2048: 24 us for the rows, 16 us for the adapters.
+// Gradients of 4096 rows, four adapters of rank 16, 2048 x 2048: 19 us for the rows, 16 us for the adapters.
 
 #include "grouped_device.h"
 
@@ -718,13 +718,14 @@ __global__ __launch_bounds__(kPlanThreads) void adapter_plan_kernel(const int32_
   }
 }
 
-// Column slices per row block so that about two workgroups a CU are launched,
-// no slice shorter than one pass of the waves: every slice forms the first product again. With one,
-// two and four workgroups a CU 8192 rows (rank 32, 2048 x 4096) took 57, 58 and 66 us, the gradients of 4096
-// rows (rank 16, 2048 x 2048) 50, 47 and 47.
+// Column slices per row block so that about one workgroup a CU is launched,
+// no slice shorter than one pass of the waves: every slice forms the first product again. One, two
+// and four workgroups a CU, us: forward of 2048 rows of 8 adapters (rank 16, 2048 x 2048) 11.3, 15.7 and -, of 4096
+// of 16 15.4, 19.5 and -; 8192 rows of 16 (rank 32, 2048 x 4096) 58, 58 and 66; gradients of 4096 rows of 4 42.6,
+// 44.6 and 52. Half a workgroup a CU: 13.2 for the 2048 rows.
 int slices_for(int64_t blocks, int cols) {
   const int64_t most = cdiv(cols, 64 * kWaves);
-  int64_t want = cdiv(512, blocks);
+  int64_t want = cdiv(256, blocks);
   if (want > most) want = most;
   return (int)(want < 1 ? 1 : want);
 }
@@ -735,12 +736,14 @@ int64_t row_blocks(int T, int n, int rows) {
 }
 
 // Rows a workgroup, 16 or 32. 16 give more workgroups; 32 read the adapters
-// half as often, and hold in one block the rows of most adapters where those have 8 to 24 on
-// average. At rank 16 and 2048 x 2048, 16 against 32 rows, forward, us: 4096 rows of 16 adapters
-// 19.7 / 23.8, of 64 26.2 / 24.6, of 256 28.6 / 23.7, of 1024 50.9 / 53.8; 8192 rows of 128 35.3 / 39.8,
-// of 512 43.6 / 35.7, of 1024 62.9 / 58.8; 16384 rows of 8 41.8 / 39.1, of 1024 98.5 / 90.8. The
-// gradients follow within a few percent.
-bool few_rows(int T, int n) { return T < 16384 && (T < 8 * (int64_t)n || T > 24 * (int64_t)n); }
+// half as often, which tells sooner at higher rank, and hold in one block the rows of most adapters where those have
+// 8 to 24 on average. At 2048 x 2048, 16 against 32 rows, forward / gradients, us. Rank 16: 2048 rows of 8
+// adapters 11.5 / 23.8 against 19.4 / 26.2; 4096 of 256 23.4 / 56.4 against 20.3 / 52.5, of 1024 50.8 / 182 against
+// 54.2 / 190; 8192 of 32 26.2 / 61.6 against 35.0 / 60.9, of 512 44.2 / 107 against 35.9 / 104; 16384 of 8
+// 40.8 / 86.6 against 39.3 / 82.6. Rank 64: 2048 of 8 20.4 / 42.3 against 25.3 / 52.7; 4096 of 64 48.6 / 101
+// against 44.8 / 96; 8192 of 8 43.2 / 99 against 36.1 / 93.
+template <int RT>
+bool few_rows(int T, int n) { return T < (RT <= 2 ? 16384 : 4096) && (T < 8 * (int64_t)n || T > 24 * (int64_t)n); }
 
 template <typename Tr, int RT, int RB, bool F32>
 hipError_t run_forward(const AdapterArgs &a, hipStream_t s) {
@@ -753,7 +756,7 @@ hipError_t run_forward(const AdapterArgs &a, hipStream_t s) {
 template <typename Tr, int RT>
 hipError_t run_forward(const AdapterArgs &a, hipStream_t s) {
   if constexpr (RT < 8) {  // at eight rank tiles 32 rows' operands spill
-    if (!few_rows(a.T, a.n)) return a.y_f32 ? run_forward<Tr, RT, 2, true>(a, s) : run_forward<Tr, RT, 2, false>(a, s);
+    if (!few_rows<RT>(a.T, a.n)) return a.y_f32 ? run_forward<Tr, RT, 2, true>(a, s) : run_forward<Tr, RT, 2, false>(a, s);
   }
   return a.y_f32 ? run_forward<Tr, RT, 1, true>(a, s) : run_forward<Tr, RT, 1, false>(a, s);
 }
@@ -778,7 +781,7 @@ hipError_t run_grad(const AdapterGradArgs &a, hipStream_t s) {
   if (!grid_fits((int64_t)a.n * (ta + tb), kAdThreads)) return hipErrorInvalidConfiguration;
   hipError_t err;
   constexpr int kMore = RT < 8 ? 2 : 1;
-  if (few_rows(a.T, a.n)) err = a.dx_f32 ? run_rows_grad<Tr, RT, 1, true>(a, s) : run_rows_grad<Tr, RT, 1, false>(a, s);
+  if (few_rows<RT>(a.T, a.n)) err = a.dx_f32 ? run_rows_grad<Tr, RT, 1, true>(a, s) : run_rows_grad<Tr, RT, 1, false>(a, s);
   else err = a.dx_f32 ? run_rows_grad<Tr, RT, kMore, true>(a, s) : run_rows_grad<Tr, RT, kMore, false>(a, s);
   if (err != hipSuccess || ta + tb == 0) return err;
   const dim3 grid((unsigned)((int64_t)a.n * (ta + tb)));

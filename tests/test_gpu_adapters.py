@@ -90,6 +90,18 @@ def test_gradients(moe, T, n, K, N, r, dtype, grads):  # noqa: F811
         R.within(dx, value, R.stored(value, slack, dtype), "dx without base and scale")
 
 
+# 8 to 24 rows an adapter (32 rows a workgroup), many an adapter (rows shared by the waves), a long batch
+FORMS = [(60, 4, 136, 200, 20), (61, 4, 77, 131, 30), (60, 4, 136, 200, 40), (62, 5, 130, 67, 64), (300, 2, 72, 136, 16),
+         (280, 2, 77, 40, 24), (300, 2, 136, 72, 50), (290, 2, 64, 131, 128), (16400, 3, 16, 24, 9), (4100, 9, 24, 16, 36)]
+
+
+@pytest.mark.parametrize("T,n,K,N,r", FORMS)
+@pytest.mark.parametrize("dtype,out", [(BF, F4), (FP, FP)])
+def test_forms(moe, T, n, K, N, r, dtype, out):  # noqa: F811
+    test_forward(moe, T, n, K, N, r, dtype, out)
+    test_gradients(moe, T, n, K, N, r, dtype, out)
+
+
 @pytest.mark.parametrize("kind", ["mixed", "one"])
 def test_gradients_against_differences(moe, kind):  # noqa: F811
     """y is linear in x, in A and in B: <y, G> changes by the gradient times the change."""
