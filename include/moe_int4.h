@@ -618,7 +618,8 @@ int moe_adapter_forward(int32_t dtype, const void *x, int64_t ldx, int32_t T, in
  *          adapter without rows gets zeros. accumulate != 0 (fp32 only, else
  *          MOE_EUNSUPPORTED) adds to what they hold.
  *   ws     moe_adapter_backward_workspace_bytes(T, r) bytes, 256-byte
- *          aligned (needed with dA or dB)
+ *          aligned (needed with dA or dB); calls that may run at the same time, in
+ *          replayed graphs too, need one each
  * g and A_a x[t] are held in fp32. Errors as moe_adapter_forward, and
  * MOE_EWORKSPACE.
  */
