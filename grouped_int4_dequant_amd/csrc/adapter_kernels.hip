@@ -9,17 +9,18 @@
 // or 32 rows of one adapter and forms both products of them, so h and g never leave
 // the chip (but for the copies that dA and dB sum over). x A^T and dy B have
 // 16-bit operands on both sides and run on the 16-bit matrix instructions. Their
-// results h and g are fp32 and enter the second product as sums of
-// 16-bit parts (three exact ones in bf16; two in fp16, at the scale of the row's
-// largest value, 22 bits), so that nothing is rounded between the two factors
-// beyond fp32's own precision: the 16-bit matrix instructions at two or three times the work are
-// still three to five times faster than the fp32 one.
+// results h and g are fp32 and enter the second product whole: in bf16 as sums of three exact
+// 16-bit parts, for which the 16-bit matrix instruction is still five times faster than the fp32
+// one; in fp16, whose exponents cannot hold such parts, on the fp32 instruction. (8192 rows of 16
+// adapters, 2048 x 4096, bf16 and fp16: rank 32 70 and 77 us, rank 64 96 and 119, rank 128 171 and 223.)
 //
 // Bound by memory, and in decode by the launch. 8192 rows, 16 adapters of rank 32, 2048 x 4096, bf16: 41 us
 // (168 MB, 4.1 TB/s) where base and y stay in the last-level cache, 57 us where they do not. One row: 7 us of kernel.
 // Gradients of 4096 rows, four adapters of rank 16, 2048 x 2048: 19 us for the rows, 16 us for the adapters.
 
 #include "grouped_device.h"
+
+#include <type_traits>
 
 namespace moe {
 namespace {
@@ -138,78 +139,99 @@ __device__ __forceinline__ void down_product(const uint16_t *x, int64_t ld_x, co
 }
 
 // ------------------------------------------------------- the second product
-// out[i][c] = sum_j h[i][j] m[j][c] with h fp32 in `part` as join_waves left
-// it. h is cut into 16-bit parts; the matrix instruction's 32 terms hold 32 ranks of a part, or, at one
-// rank tile, 16 ranks of two parts.
-template <typename Tr> constexpr int kParts = 2;
-template <> constexpr int kParts<Bf16> = 3;
-template <typename Tr, int RT> constexpr int kTerms = RT == 1 ? (kParts<Tr> + 1) / 2 : kParts<Tr> * RT / 2;  // instructions per block
+// out[i][c] = sum_j h[i][j] m[j][c] with h fp32 in `part` as join_waves left it, and m 16-bit in operand
+// registers: lane (p16, q4) holds column p16's eight ranks from 32 u + 8 q4 on in register set u, or, at
+// one rank tile, from 8 (q4 & 1) on. times() gives the lane row p16 and columns 4 q4 .. of a 16 x 16 block.
+__device__ __forceinline__ f4 mfma32(float a, float b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
 
-// Part `n` of v. bf16: the leading, middle and last eight bits, exact. fp16: the nearest, and what is left.
-// An infinity or NaN is all in the first part.
-__device__ __forceinline__ bool finite(float v) { return (__builtin_bit_cast(uint32_t, v) & 0x7f800000u) != 0x7f800000u; }
-template <typename Tr>
-__device__ __forceinline__ uint16_t part_of(float v, int n);
-template <>
-__device__ __forceinline__ uint16_t part_of<Bf16>(float v, int n) {
-#pragma unroll
-  for (int i = 0; i < n; ++i) v = finite(v) ? v - __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, v) & 0xffff0000u) : 0.f;
-  return (uint16_t)(__builtin_bit_cast(uint32_t, v) >> 16);
-}
-template <>
-__device__ __forceinline__ uint16_t part_of<Fp16>(float v, int n) {
-  if (n) v = finite(v) ? v - Fp16::to(Fp16::from(v)) : 0.f;
-  return Fp16::from(v);
-}
+template <typename Tr, int RB, int RT> struct Middle;
 
-template <typename Tr, int RB, int RT>
-struct Cut {
-  s8 v[RB][kTerms<Tr, RT>];  // operand of row p16
-  float unscale[RB];         // what a sum is multiplied by (1 in bf16)
-};
+// bf16: h is cut into three parts of eight bits each, exact: bf16 has fp32's exponents (only bits below 2^-133,
+// those of values below 2^-110, are lost). The matrix instruction's 32 terms hold 32 ranks of a part,
+// or, at one rank tile, 16 ranks of two parts.
+template <int RB, int RT>
+struct Middle<Bf16, RB, RT> {
+  static constexpr int kTerms = RT == 1 ? 2 : 3 * RT / 2;  // instructions per block
+  static constexpr int NM = RT / 2 ? RT / 2 : 1;
+  s8 v[RB][kTerms];  // operand of row p16
 
-template <typename Tr, int RB, int RT>
-__device__ __forceinline__ void cut(const f4 *part, Cut<Tr, RB, RT> &c) {
-  const int lane = threadIdx.x & 63, p16 = lane & 15, q4 = lane >> 4;
+  // Part `n` of v: the leading, middle and last eight bits. An infinity or NaN is all in the first part.
+  static __device__ __forceinline__ bool finite(float v) { return (__builtin_bit_cast(uint32_t, v) & 0x7f800000u) != 0x7f800000u; }
+  static __device__ __forceinline__ uint16_t part_of(float v, int n) {
 #pragma unroll
-  for (int b = 0; b < RB; ++b) {
-    float scale = 1.f;
-    c.unscale[b] = 1.f;
-    if constexpr (kParts<Tr> == 2) {  // powers of two that bring the row's largest value to [2^14, 2^15)
-      float top = 0.f;
+    for (int i = 0; i < n; ++i) v = finite(v) ? v - __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, v) & 0xffff0000u) : 0.f;
+    return (uint16_t)(__builtin_bit_cast(uint32_t, v) >> 16);
+  }
+
+  __device__ __forceinline__ void read(const f4 *part) {
+    const int lane = threadIdx.x & 63, p16 = lane & 15, q4 = lane >> 4;
 #pragma unroll
-      for (int j = 0; j < RT; ++j) {
-        const f4 h = part[(b * RT + j) * 64 + lane];
+    for (int b = 0; b < RB; ++b)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) top = fmaxf(top, fabsf(h[x]));
-      }
-      top = fmaxf(top, __shfl_xor(top, 16));
-      top = fmaxf(top, __shfl_xor(top, 32));
-      if (finite(top) && top > 0.f) {
-        const int e = min(max(__builtin_amdgcn_frexp_expf(top), -100), 100);
-        scale = ldexpf(1.f, 15 - e);
-        c.unscale[b] = ldexpf(1.f, e - 15);
-      }
-    }
+      for (int m = 0; m < kTerms; ++m) {
+        const int j = RT == 1 ? 8 * (q4 & 1) : 32 * (m % NM) + 8 * q4;  // first of this lane's eight ranks
+        const f4 *q = part + (b * RT + (j >> 4)) * 64 + p16 + 16 * ((j >> 2) & 3);
+        const f4 lo = q[0], hi = q[16];
 #pragma unroll
-    for (int m = 0; m < kTerms<Tr, RT>; ++m) {
-      const int n = RT == 1 ? 2 * m + (q4 >> 1) : m / (RT / 2 ? RT / 2 : 1);
-      const int j = RT == 1 ? 8 * (q4 & 1) : 32 * (m % (RT / 2 ? RT / 2 : 1)) + 8 * q4;  // first of this lane's eight ranks
-      const f4 *q = part + (b * RT + (j >> 4)) * 64 + p16 + 16 * ((j >> 2) & 3);
-      const f4 lo = q[0], hi = q[16];
-#pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        const float h = (x < 4 ? lo[x & 3] : hi[x & 3]) * scale;
-        if constexpr (RT == 1) {
-          const uint16_t a = part_of<Tr>(h, 2 * m), z = 2 * m + 1 < kParts<Tr> ? part_of<Tr>(h, 2 * m + 1) : (uint16_t)0;
-          c.v[b][m][x] = (short)(q4 >> 1 ? z : a);
-        } else {
-          c.v[b][m][x] = (short)part_of<Tr>(h, n);
+        for (int x = 0; x < 8; ++x) {
+          const float h = x < 4 ? lo[x & 3] : hi[x & 3];
+          if constexpr (RT == 1) {
+            const uint16_t a = part_of(h, 2 * m), z = 2 * m + 1 < 3 ? part_of(h, 2 * m + 1) : (uint16_t)0;
+            v[b][m][x] = (short)(q4 >> 1 ? z : a);
+          } else {
+            v[b][m][x] = (short)part_of(h, m / NM);
+          }
         }
       }
-    }
   }
-}
+  __device__ __forceinline__ f4 times(int b, const s8 (&m)[NM]) const {
+    f4 acc = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int u = 0; u < kTerms; ++u) acc = Bf16::mfma(m[u % NM], v[b][u], acc);
+    return acc;
+  }
+};
+
+// fp16: the fp32 matrix instruction, on h as it is and the columns' values widened. fp16 parts would not
+// do: fp16 spans 40 binary orders, so a rank whose h lies far below its row's largest would lose its bits,
+// though its column may be the only one that another result takes. Instruction x takes rank 8 q4 + x of each 32, or,
+// at one rank tile, rank 8 (q4 & 1) + 4 (q4 / 2) + x.
+template <int RB, int RT>
+struct Middle<Fp16, RB, RT> {
+  static constexpr int NM = RT / 2 ? RT / 2 : 1, kEach = RT == 1 ? 4 : 8;
+  float v[RB][NM * kEach];  // operand of row p16
+
+  __device__ __forceinline__ void read(const f4 *part) {
+    const int lane = threadIdx.x & 63, p16 = lane & 15, q4 = lane >> 4;
+#pragma unroll
+    for (int b = 0; b < RB; ++b)
+#pragma unroll
+      for (int u = 0; u < NM; ++u) {
+        const int j = RT == 1 ? 8 * (q4 & 1) + 4 * (q4 >> 1) : 32 * u + 8 * q4;  // first of this lane's ranks
+        const f4 *q = part + (b * RT + (j >> 4)) * 64 + p16 + 16 * ((j >> 2) & 3);
+#pragma unroll
+        for (int y = 0; y < kEach / 4; ++y)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) v[b][u * kEach + 4 * y + x] = q[16 * y][x];
+      }
+  }
+  __device__ __forceinline__ f4 times(int b, const s8 (&m)[NM]) const {
+    const bool upper = (threadIdx.x & 32) != 0;
+    f4 acc = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int u = 0; u < NM; ++u) {
+      u4 w = __builtin_bit_cast(u4, m[u]);
+      if (RT == 1) {
+        w[0] = upper ? w[2] : w[0];
+        w[1] = upper ? w[3] : w[1];
+      }
+#pragma unroll
+      for (int x = 0; x < kEach; ++x)
+        acc = mfma32(Fp16::to((uint16_t)(w[x >> 1] >> (16 * (x & 1)))), v[b][u * kEach + x], acc);
+    }
+    return acc;
+  }
+};
 
 // Eight consecutive values of base or y from element `at` on, of which `left` exist, as they lie in memory.
 template <bool F32> struct Eight { u4 v[F32 ? 2 : 1]; };
@@ -286,21 +308,19 @@ __device__ __forceinline__ void load_base(const OutRows &o, const int (&row)[RB]
     }
 }
 template <typename Tr, bool F32, int RB, int RT>
-__device__ __forceinline__ void finish(const OutRows &o, const int (&row)[RB], int n0, int end, const Cut<Tr, RB, RT> &h,
+__device__ __forceinline__ void finish(const OutRows &o, const int (&row)[RB], int n0, int end, const Middle<Tr, RB, RT> &h,
                                        const s8 (&m)[4][RT / 2 ? RT / 2 : 1], const Eight<F32> (&base)[RB][2]) {
   const int q4 = (threadIdx.x & 63) >> 4;
 #pragma unroll
-  for (int b = 0; b < RB; ++b)
+  for (int x = 0; x < 2; ++x)
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
+    for (int b = 0; b < RB; ++b) {
       float f[8];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        f4 acc = f4{0.f, 0.f, 0.f, 0.f};
+        const f4 acc = h.times(b, m[2 * x + c]);
 #pragma unroll
-        for (int u = 0; u < kTerms<Tr, RT>; ++u) acc = Tr::mfma(m[2 * x + c][u % (RT / 2 ? RT / 2 : 1)], h.v[b][u], acc);
-#pragma unroll
-        for (int y = 0; y < 4; ++y) f[4 * c + y] = value_of<Tr, F32>(base[b][x], 4 * c + y) + acc[y] * h.unscale[b];
+        for (int y = 0; y < 4; ++y) f[4 * c + y] = value_of<Tr, F32>(base[b][x], 4 * c + y) + acc[y];
       }
       const int col = n0 + 32 * x + 8 * q4;
       if (row[b] >= 0 && col < end) store_out<Tr, F32>(o.out, (int64_t)row[b] * o.ld_out + col, o.vec, end - col, f);
@@ -376,8 +396,8 @@ __global__ __launch_bounds__(kAdThreads, RT <= 2 ? 4 : 2) void adapter_kernel(Ad
     for (int j = 0; j < RT; ++j) acc[b][j] = f4{0.f, 0.f, 0.f, 0.f};
   down_product<Tr, RB, RT>(a.x, a.ld_x, row, a.A + (int64_t)blk.e * a.r * a.K, a.r, a.K, a.vec_x, acc);
   join_waves<RB, RT>(s_part, acc, a.scale ? a.scale[blk.e] : 1.f, a.r);
-  Cut<Tr, RB, RT> h;
-  cut<Tr, RB, RT>(s_part, h);
+  Middle<Tr, RB, RT> h;
+  h.read(s_part);
   for (; n0 < end; n0 += 64 * kWaves) {
     finish<Tr, F32, RB, RT>(o, row, n0, end, h, m, f);
     if (n0 + 64 * kWaves < end) ask(n0 + 64 * kWaves);
@@ -477,8 +497,8 @@ __global__ __launch_bounds__(kAdThreads, RT <= 2 ? 4 : 2) void adapter_rows_grad
   join_waves<RB, RT>(s_part, acc, scale, a.r);
   if (blockIdx.y == 0) keep(a.g);  // dA's factor
   if (!a.dx) return;
-  Cut<Tr, RB, RT> g;
-  cut<Tr, RB, RT>(s_part, g);
+  Middle<Tr, RB, RT> g;
+  g.read(s_part);
   __syncthreads();  // the staging areas take the partials' place
   for (int k0 = begin + 64 * wave; k0 < end; k0 += 64 * kWaves) {
     Eight<F32> f[RB][2];
@@ -508,8 +528,6 @@ __global__ __launch_bounds__(kAdThreads, RT <= 2 ? 4 : 2) void adapter_rows_grad
     finish<Tr, F32, RB, RT>(o, row, k0, end, g, m, f);
   }
 }
-
-__device__ __forceinline__ f4 mfma32(float a, float b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
 
 // Gradient of the adapters: out[c][j] = sum over the adapter's rows of
 // v[row][c] * m[place][j], v = x (dA, c = k) or dy (dB, c = n), m = g or h.
@@ -741,9 +759,13 @@ int64_t row_blocks(int T, int n, int rows) {
 // adapters 11.5 / 23.8 against 19.4 / 26.2; 4096 of 256 23.4 / 56.4 against 20.3 / 52.5, of 1024 50.8 / 182 against
 // 54.2 / 190; 8192 of 32 26.2 / 61.6 against 35.0 / 60.9, of 512 44.2 / 107 against 35.9 / 104; 16384 of 8
 // 40.8 / 86.6 against 39.3 / 82.6. Rank 64: 2048 of 8 20.4 / 42.3 against 25.3 / 52.7; 4096 of 64 48.6 / 101
-// against 44.8 / 96; 8192 of 8 43.2 / 99 against 36.1 / 93.
-template <int RT>
-bool few_rows(int T, int n) { return T < (RT <= 2 ? 16384 : 4096) && (T < 8 * (int64_t)n || T > 24 * (int64_t)n); }
+// against 44.8 / 96; 8192 of 8 43.2 / 99 against 36.1 / 93. Rank 64 in fp16, where the fp32 instruction takes
+// longer than the adapters' reading: 4096 of 64 57 / 105 against 58 / 111; 8192 of 8 78 / 137 against 85 / 146; 8192
+// of 16 at 2048 x 4096 119 against 138; 1000 of 64 35 against 28; 32768 of 8 214 / 455 against 215 / 449.
+template <typename Tr, int RT>
+bool few_rows(int T, int n) {
+  return T < (RT <= 2 || std::is_same_v<Tr, Fp16> ? 16384 : 4096) && (T < 8 * (int64_t)n || T > 24 * (int64_t)n);
+}
 
 template <typename Tr, int RT, int RB, bool F32>
 hipError_t run_forward(const AdapterArgs &a, hipStream_t s) {
@@ -756,7 +778,7 @@ hipError_t run_forward(const AdapterArgs &a, hipStream_t s) {
 template <typename Tr, int RT>
 hipError_t run_forward(const AdapterArgs &a, hipStream_t s) {
   if constexpr (RT < 8) {  // at eight rank tiles 32 rows' operands spill
-    if (!few_rows<RT>(a.T, a.n)) return a.y_f32 ? run_forward<Tr, RT, 2, true>(a, s) : run_forward<Tr, RT, 2, false>(a, s);
+    if (!few_rows<Tr, RT>(a.T, a.n)) return a.y_f32 ? run_forward<Tr, RT, 2, true>(a, s) : run_forward<Tr, RT, 2, false>(a, s);
   }
   return a.y_f32 ? run_forward<Tr, RT, 1, true>(a, s) : run_forward<Tr, RT, 1, false>(a, s);
 }
@@ -781,7 +803,7 @@ hipError_t run_grad(const AdapterGradArgs &a, hipStream_t s) {
   if (!grid_fits((int64_t)a.n * (ta + tb), kAdThreads)) return hipErrorInvalidConfiguration;
   hipError_t err;
   constexpr int kMore = RT < 8 ? 2 : 1;
-  if (few_rows<RT>(a.T, a.n)) err = a.dx_f32 ? run_rows_grad<Tr, RT, 1, true>(a, s) : run_rows_grad<Tr, RT, 1, false>(a, s);
+  if (few_rows<Tr, RT>(a.T, a.n)) err = a.dx_f32 ? run_rows_grad<Tr, RT, 1, true>(a, s) : run_rows_grad<Tr, RT, 1, false>(a, s);
   else err = a.dx_f32 ? run_rows_grad<Tr, RT, kMore, true>(a, s) : run_rows_grad<Tr, RT, kMore, false>(a, s);
   if (err != hipSuccess || ta + tb == 0) return err;
   const dim3 grid((unsigned)((int64_t)a.n * (ta + tb)));

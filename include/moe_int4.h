@@ -598,7 +598,8 @@ int moe_adapter_plan(const int32_t *row_adapter, int32_t T, int32_t n, int32_t *
  *   base   the shared projection's output, of y's type [T][ldbase], or NULL
  *          for zeros; may be y itself with the same stride
  *   y      dtype or fp32 [T][ldy], N columns
- * A_a x[t] is held in fp32. One kernel; no workspace. Errors: MOE_EINVAL,
+ * A_a x[t] and scale[a] A_a x[t] are held in fp32, and enter the product with B_a
+ * whole (in bf16 their bits below 2^-133 are lost). One kernel; no workspace. Errors: MOE_EINVAL,
  * MOE_EUNSUPPORTED (r > MOE_MAX_ADAPTER_RANK, n > MOE_MAX_ADAPTERS,
  * T > MOE_MAX_TOKENS), MOE_EHIP. T == 0 enqueues nothing.
  */
@@ -620,7 +621,7 @@ int moe_adapter_forward(int32_t dtype, const void *x, int64_t ldx, int32_t T, in
  *   ws     moe_adapter_backward_workspace_bytes(T, r) bytes, 256-byte
  *          aligned (needed with dA or dB); calls that may run at the same time, in
  *          replayed graphs too, need one each
- * g and A_a x[t] are held in fp32. Errors as moe_adapter_forward, and
+ * g and A_a x[t] are held in fp32, as in moe_adapter_forward. Errors as there, and
  * MOE_EWORKSPACE.
  */
 size_t moe_adapter_backward_workspace_bytes(int32_t T, int32_t r);
