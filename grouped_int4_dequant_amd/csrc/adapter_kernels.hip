@@ -148,38 +148,49 @@ template <typename Tr, int RB, int RT> struct Middle;
 
 // bf16: h is cut into three parts of eight bits each, exact: bf16 has fp32's exponents (only bits below 2^-133,
 // those of values below 2^-110, are lost). The matrix instruction's 32 terms hold 32 ranks of a part,
-// or, at one rank tile, 16 ranks of two parts.
+// or, at one rank tile, 16 ranks of two parts, the last part in two halves.
 template <int RB, int RT>
 struct Middle<Bf16, RB, RT> {
-  static constexpr int kTerms = RT == 1 ? 2 : 3 * RT / 2;  // instructions per block
   static constexpr int NM = RT / 2 ? RT / 2 : 1;
+  static constexpr int kTerms = RT == 1 ? 2 : 3 * NM;  // instructions per block
   s8 v[RB][kTerms];  // operand of row p16
 
-  // Part `n` of v: the leading, middle and last eight bits. An infinity or NaN is all in the first part.
-  static __device__ __forceinline__ bool finite(float v) { return (__builtin_bit_cast(uint32_t, v) & 0x7f800000u) != 0x7f800000u; }
-  static __device__ __forceinline__ uint16_t part_of(float v, int n) {
-#pragma unroll
-    for (int i = 0; i < n; ++i) v = finite(v) ? v - __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, v) & 0xffff0000u) : 0.f;
-    return (uint16_t)(__builtin_bit_cast(uint32_t, v) >> 16);
+  static __device__ __forceinline__ float top8(float v) { return __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, v) & 0xffff0000u); }
+  static __device__ __forceinline__ short bits(float v) { return (short)(__builtin_bit_cast(uint32_t, v) >> 16); }
+
+  // The parts of v, leading bits first. Unless v is zero all of them have its sign and none is
+  // zero, so that with an infinite weight each part's product is the infinity that v's is: where nothing is left for a part, it
+  // takes half of the one before. Of an infinity or NaN every part is v.
+  static __device__ __forceinline__ void cut(float v, float &a, float &b, float &c) {
+    const bool finite = (__builtin_bit_cast(uint32_t, v) & 0x7f800000u) != 0x7f800000u;
+    a = top8(v);
+    float left = finite ? v - a : v;
+    if (left == 0.f) a = left = 0.5f * a;
+    b = top8(left);
+    c = finite ? left - b : v;
+    if (c == 0.f) b = c = 0.5f * b;
   }
 
   __device__ __forceinline__ void read(const f4 *part) {
     const int lane = threadIdx.x & 63, p16 = lane & 15, q4 = lane >> 4;
 #pragma unroll
-    for (int b = 0; b < RB; ++b)
+    for (int r = 0; r < RB; ++r)
 #pragma unroll
-      for (int m = 0; m < kTerms; ++m) {
-        const int j = RT == 1 ? 8 * (q4 & 1) : 32 * (m % NM) + 8 * q4;  // first of this lane's eight ranks
-        const f4 *q = part + (b * RT + (j >> 4)) * 64 + p16 + 16 * ((j >> 2) & 3);
+      for (int u = 0; u < NM; ++u) {
+        const int j = RT == 1 ? 8 * (q4 & 1) : 32 * u + 8 * q4;  // first of this lane's eight ranks
+        const f4 *q = part + (r * RT + (j >> 4)) * 64 + p16 + 16 * ((j >> 2) & 3);
         const f4 lo = q[0], hi = q[16];
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
-          const float h = x < 4 ? lo[x & 3] : hi[x & 3];
+          float a, b, c;
+          cut(x < 4 ? lo[x & 3] : hi[x & 3], a, b, c);
           if constexpr (RT == 1) {
-            const uint16_t a = part_of(h, 2 * m), z = 2 * m + 1 < 3 ? part_of(h, 2 * m + 1) : (uint16_t)0;
-            v[b][m][x] = (short)(q4 >> 1 ? z : a);
+            v[r][0][x] = bits(q4 >> 1 ? b : a);
+            v[r][1][x] = bits(0.5f * c);
           } else {
-            v[b][m][x] = (short)part_of(h, m / NM);
+            v[r][u][x] = bits(a);
+            v[r][NM + u][x] = bits(b);
+            v[r][2 * NM + u][x] = bits(c);
           }
         }
       }

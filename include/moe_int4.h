@@ -599,7 +599,8 @@ int moe_adapter_plan(const int32_t *row_adapter, int32_t T, int32_t n, int32_t *
  *          for zeros; may be y itself with the same stride
  *   y      dtype or fp32 [T][ldy], N columns
  * A_a x[t] and scale[a] A_a x[t] are held in fp32, and enter the product with B_a
- * whole (in bf16 their bits below 2^-133 are lost). One kernel; no workspace. Errors: MOE_EINVAL,
+ * whole (in bf16 their bits below 2^-133 are lost). Infinities and NaN in x, A, B and
+ * base give what the formula gives. One kernel; no workspace. Errors: MOE_EINVAL,
  * MOE_EUNSUPPORTED (r > MOE_MAX_ADAPTER_RANK, n > MOE_MAX_ADAPTERS,
  * T > MOE_MAX_TOKENS), MOE_EHIP. T == 0 enqueues nothing.
  */
