@@ -611,6 +611,12 @@ def _ld(t: Optional[torch.Tensor], width: int) -> int:
     return 0 if t is None else max(t.stride(0), width)
 
 
+def _sizes(*sizes: int):
+    """Sizes cross the C interface in 32 bits, where ctypes would cut off larger ones."""
+    if max(sizes) > 0x7fffffff:
+        raise ValueError(f"sizes from 2^31 on are not supported, got {max(sizes)}")
+
+
 def _groups(c: _Call, offsets: torch.Tensor, G: int) -> torch.Tensor:
     return c.need(offsets, "offsets", torch.int32, (G + 1,))
 
@@ -628,6 +634,7 @@ def grouped_gemm(A: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor, a_row:
     c.rows(A, "A", (A.shape[0], K))
     c.need(W, "W", c.dtype, (G, N, K))
     P = A.shape[0] if a_row is None else a_row.numel()
+    _sizes(A.shape[0], G, P, N, K)
     if a_row is not None:
         c.need(a_row, "a_row", torch.int32, (P,))
     _groups(c, offsets, G)
@@ -646,6 +653,7 @@ def grouped_gemm_dgrad(dC: torch.Tensor, W: torch.Tensor, offsets: torch.Tensor,
         raise ValueError("dC must be [P][N] and W [G][N][K]")
     G, N, K = W.shape
     P = dC.shape[0]
+    _sizes(G, P, N, K)
     c.rows(dC, "dC", (P, N))
     c.need(W, "W", c.dtype, (G, N, K))
     _groups(c, offsets, G)
@@ -667,6 +675,7 @@ def grouped_gemm_wgrad(dC: torch.Tensor, A: torch.Tensor, offsets: torch.Tensor,
         raise ValueError("offsets must hold the G + 1 group bounds")
     P, N = dC.shape
     K, G = A.shape[1], offsets.numel() - 1
+    _sizes(A.shape[0], G, P, N, K)
     c.rows(dC, "dC", (P, N))
     c.rows(A, "A", (A.shape[0], K))
     if a_row is not None:
@@ -692,6 +701,7 @@ def combine(o: torch.Tensor, pair_pos: torch.Tensor, weights: Optional[torch.Ten
     if o.dim() != 2 or not isinstance(pair_pos, torch.Tensor) or pair_pos.dim() != 2:
         raise ValueError("o must be [P][d] and pair_pos [T][k]")
     (P, d), (T, k) = o.shape, pair_pos.shape
+    _sizes(P, d, T, k)
     c.rows(o, "o", (P, d))
     c.need(pair_pos, "pair_pos", torch.int32, (T, k))
     if weights is not None:
@@ -713,6 +723,7 @@ def combine_backward(dy: torch.Tensor, o: torch.Tensor, pair_pos: torch.Tensor, 
     if dy.dim() != 2 or not isinstance(o, torch.Tensor) or o.dim() != 2 or not isinstance(pair_pos, torch.Tensor) or pair_pos.dim() != 2:
         raise ValueError("dy must be [T][d], o [P][d] and pair_pos [T][k]")
     (P, d), (T, k) = o.shape, pair_pos.shape
+    _sizes(P, d, T, k)
     c.rows(dy, "dy", (T, d))
     c.rows(o, "o", (P, d))
     c.need(pair_pos, "pair_pos", torch.int32, (T, k))
@@ -733,6 +744,7 @@ def adapter_plan(row_adapter: torch.Tensor, n: int, stream=None):
     if n < 1:
         raise ValueError("n must be at least 1")
     dev, T = row_adapter.device, row_adapter.numel()
+    _sizes(T, n)
     if stream is not None and stream.device != dev:
         raise ValueError(f"stream must be of {dev}, got {stream.device}")
     with torch.cuda.stream(torch.cuda.current_stream(dev) if stream is None else stream):
@@ -747,6 +759,7 @@ def _adapter_args(c: _Call, x, A, B, scale, plan):
     if x.dim() != 2 or not isinstance(A, torch.Tensor) or A.dim() != 3 or not isinstance(B, torch.Tensor) or B.dim() != 3:
         raise ValueError("x must be [T][K], A [n][r][K] and B [n][N][r]")
     (T, K), (n, r, _), N = x.shape, A.shape, B.shape[1]
+    _sizes(T, K, n, r, N)
     c.rows(x, "x", (T, K))
     c.need(A, "A", c.dtype, (n, r, K))
     c.need(B, "B", c.dtype, (n, N, r))
@@ -780,6 +793,7 @@ def adapter_forward(x: torch.Tensor, A: torch.Tensor, B: torch.Tensor, scale: Op
 
 
 def adapter_backward_workspace_bytes(T: int, r: int) -> int:
+    _sizes(T, r)
     return int(load().moe_adapter_backward_workspace_bytes(T, r))
 
 

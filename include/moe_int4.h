@@ -493,8 +493,8 @@ int moe_layer_graph_destroy(moe_layer_graph_t *graph);
  *     taken as the nearest of the two.
  *   - Outputs must not overlap inputs unless stated, and no output row may be
  *     reached twice (row stride at least the width; a permutation of rows).
- *   - P, N, K and d above 2^30, and calls that would launch 2^32 threads or
- *     more, are MOE_EUNSUPPORTED.
+ *   - N, K, d and the grouped products' P above 2^30, and calls that would launch
+ *     2^32 threads or more, are MOE_EUNSUPPORTED.
  *   - stream must belong to the current device.
  */
 #define MOE_BF16 0
