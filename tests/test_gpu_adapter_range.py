@@ -9,8 +9,9 @@ from test_gpu_grouped import BF, F4, FP, gen, moe, rnd  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
-#       T, n, r: both row forms (16 and 32 rows a workgroup) at one, two, four and eight rank tiles
-FORMS = [(40, 2, 5), (60, 4, 16), (40, 2, 17), (60, 4, 32), (40, 2, 64), (62, 5, 50), (40, 2, 128)]
+#       T, n, r: one, two, four and eight rank tiles, 32 rows a workgroup (8 to 24 rows an adapter) and 16
+FORMS = [(40, 2, 5), (60, 4, 16), (40, 2, 17), (60, 4, 32), (40, 2, 64), (62, 5, 50), (40, 2, 128),
+         (50, 1, 5), (30, 6, 16), (50, 1, 32), (30, 6, 17), (50, 1, 64), (30, 6, 40)]
 
 
 def spread(r, orders):
