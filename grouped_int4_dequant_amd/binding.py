@@ -505,7 +505,9 @@ def prefill_chunked(layer: Layer, x: torch.Tensor, logits: torch.Tensor, chunk: 
 # Tensors are bf16 or fp16 (one type per call), results of that type or fp32.
 # Activations and results may be row-strided views (their columns contiguous);
 # a call runs on the tensors' device, on `stream` or that device's current
-# stream, and what it allocates belongs to that stream.
+# stream, and what it allocates belongs to that stream. The calls are not recorded
+# for autograd: results carry no gradient function, whatever requires_grad says,
+# and the gradients are the calls named for them.
 _CODES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
@@ -718,7 +720,8 @@ def combine_backward(dy: torch.Tensor, o: torch.Tensor, pair_pos: torch.Tensor, 
                      d_o: Optional[torch.Tensor] = None, dw: Optional[torch.Tensor] = None, stream=None):
     """moe_combine_backward: (d_o [P][d], dw fp32 [T][k]) with d_o[pair_pos[t][j]]
     = weights[t][j] * dy[t] and dw[t][j] = <dy[t], o[pair_pos[t][j]]>. Rows of
-    d_o that no pair names are not written."""
+    d_o that no pair names are not written. Both are formed; the C call takes NULL
+    for the one that is not wanted."""
     c = _Call(dy, "dy", stream)
     if dy.dim() != 2 or not isinstance(o, torch.Tensor) or o.dim() != 2 or not isinstance(pair_pos, torch.Tensor) or pair_pos.dim() != 2:
         raise ValueError("dy must be [T][d], o [P][d] and pair_pos [T][k]")
@@ -805,7 +808,8 @@ def adapter_backward(dy: torch.Tensor, x: torch.Tensor, A: torch.Tensor, B: torc
     """moe_adapter_backward: (dx [T][K], dA [n][r][K], dB [n][N][r]) from dy
     [T][N]. dx_base [T][K] (None: zeros) is added to dx, which is of its type
     (else x's) and may be dx_base itself; dA and dB are of grad_dtype (None:
-    x's type), and with accumulate are added to the given dA and dB (fp32)."""
+    x's type), and with accumulate are added to the given dA and dB (fp32). All three
+    are formed; the C call takes NULL for those that are not wanted."""
     c = _Call(x, "x", stream)
     T, K, N, r, n, rows, offsets = _adapter_args(c, x, A, B, scale, plan)
     c.rows(dy, "dy", (T, N))

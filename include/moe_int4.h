@@ -476,16 +476,20 @@ int moe_layer_graph_destroy(moe_layer_graph_t *graph);
  *
  * Conventions shared by them, beyond those at the top:
  *   - dtype is the type of the operands: MOE_BF16 or MOE_FP16. Results are
- *     of that type or MOE_FP32; any other code is MOE_EINVAL. Products are exact
- *     in fp32, sums are held in fp32 in a fixed order (repeated calls agree
- *     bit for bit) and rounded once, to nearest even, where they are stored.
+ *     of that type or MOE_FP32; any other code is MOE_EINVAL. Products of two
+ *     16-bit operands are exact in fp32, sums are held in fp32 in a fixed order
+ *     (repeated calls agree bit for bit) and rounded once, to nearest even, where
+ *     they are stored.
  *   - A matrix of activations or results is given by its first element and
  *     its row stride in elements (lda, ldc, ...), at least its width; its columns
  *     are contiguous. Weights, adapters and their gradients are contiguous.
  *   - Pointers need the alignment of their element type only (else
  *     MOE_EINVAL). Operands whose rows are whole 16-byte units at 16-byte
- *     alignment take wide loads; others are read element by element, which
- *     is several times slower.
+ *     alignment take wide loads. Others take 64 x 64 tiles and unaligned 16-byte
+ *     loads (the combine reads them element by element) and are two to three times
+ *     slower: 64 groups of 256 rows, 1024 x 2048, bf16, 207 us against 89, their
+ *     weight gradient 409 against 172; adapters of 4096 rows, rank 16, 2048 x 2048,
+ *     61 against 23; combine of 4096 tokens of 8 rows of 2048, 87 against 27.
  *   - The rows of a group are offsets[e] .. offsets[e+1] of the sorted order
  *     (int32 [G+1], device, non-decreasing from 0, as moe_route writes). Groups
  *     may be empty. offsets[G] may be below P: rows from offsets[G] on belong to no
