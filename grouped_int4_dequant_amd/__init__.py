@@ -13,18 +13,22 @@ import os as _os
 # GPU; a value the caller set is kept.
 _os.environ.setdefault("HIP_FORCE_DEV_KERNARG", "1")
 
-from .binding import (ABLATIONS, GRAPH_CONCURRENT, Layer, LayerGraph, ablation_workspace_bytes, adapter_backward,
+from .binding import (ABLATIONS, ACTIVATIONS, GRAPH_CONCURRENT, Layer, LayerGraph, ablation_workspace_bytes, adapter_backward,
                       adapter_backward_workspace_bytes, adapter_forward, adapter_plan, alloc_routing, alloc_workspace,
                       combine, combine_backward, grouped_gemm, grouped_gemm_dgrad, grouped_gemm_wgrad,
                       OVERFLOW_H, OVERFLOW_O, OVERFLOW_X, grouped_gemm_int4, layer_forward, layer_forward_ablation,
                       layer_forward_checked, layer_forward_noalloc, layer_forward_router, load, max_blocks,
                       prefill_chunked, route, route_workspace_bytes, router_logits, router_topk, status_string,
-                      prepared_bytes, workspace_bytes, workspace_layout)
+                      prepared_bytes, workspace_bytes, workspace_layout, linear, linear_backward,
+                      linear_backward_workspace_bytes, residual_norm, residual_norm_backward,
+                      residual_norm_backward_workspace_bytes)
 
-__all__ = ["ABLATIONS", "GRAPH_CONCURRENT", "Layer", "LayerGraph", "ablation_workspace_bytes", "adapter_backward",
+__all__ = ["ABLATIONS", "ACTIVATIONS", "GRAPH_CONCURRENT", "Layer", "LayerGraph", "ablation_workspace_bytes", "adapter_backward",
            "adapter_backward_workspace_bytes", "adapter_forward", "adapter_plan", "alloc_routing", "alloc_workspace",
            "combine", "combine_backward", "grouped_gemm", "grouped_gemm_dgrad", "grouped_gemm_wgrad",
            "OVERFLOW_H", "OVERFLOW_O", "OVERFLOW_X", "grouped_gemm_int4", "layer_forward", "layer_forward_ablation",
            "layer_forward_checked", "layer_forward_noalloc", "layer_forward_router", "load", "max_blocks",
            "prefill_chunked", "route", "route_workspace_bytes", "router_logits", "router_topk", "status_string",
-           "prepared_bytes", "workspace_bytes", "workspace_layout"]
+           "prepared_bytes", "workspace_bytes", "workspace_layout", "linear", "linear_backward",
+           "linear_backward_workspace_bytes", "residual_norm", "residual_norm_backward",
+           "residual_norm_backward_workspace_bytes"]

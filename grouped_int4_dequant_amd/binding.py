@@ -123,6 +123,17 @@ def load() -> ctypes.CDLL:
             getattr(lib, name).restype = ctypes.c_int
         lib.moe_adapter_backward_workspace_bytes.argtypes = [I, I]
         lib.moe_adapter_backward_workspace_bytes.restype = ctypes.c_size_t
+        F, Z = ctypes.c_float, ctypes.c_size_t
+        lib.moe_linear.argtypes = [I, _P, L, I, I, I, _P, _P, I, I, _P, L, _P, L, _P, I, L, _P]
+        lib.moe_linear_backward.argtypes = [I, _P, L, _P, L, I, I, I, _P, _P, L, I, _P, I, L, _P, _P, I, I, _P, Z, _P]
+        lib.moe_residual_norm.argtypes = [I, _P, L, _P, L, I, I, I, _P, _P, I, _P, I, F, F, _P, L, _P, L, _P]
+        lib.moe_residual_norm_backward.argtypes = [I, _P, L, _P, L, _P, L, _P, L, I, I, I, _P, _P, I, _P, I, F, F, _P, L, _P, L,
+                                                   _P, _P, _P, I, I, _P, Z, _P]
+        for name in ("moe_linear", "moe_linear_backward", "moe_residual_norm", "moe_residual_norm_backward"):
+            getattr(lib, name).restype = ctypes.c_int
+        for name in ("moe_linear_backward_workspace_bytes", "moe_residual_norm_backward_workspace_bytes"):
+            getattr(lib, name).argtypes = [I, I, I]
+            getattr(lib, name).restype = Z
         lib.moe_status_string.argtypes = [ctypes.c_int]
         lib.moe_status_string.restype = ctypes.c_char_p
         _lib = lib
@@ -567,6 +578,14 @@ class _Call:
             raise ValueError(f"{name} must have contiguous columns and rows that do not overlap")
         return t
 
+    def vector(self, t, name, shape):
+        """A contiguous tensor of the call's type or fp32."""
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if t.dtype is not self.dtype and t.dtype is not torch.float32:
+            raise TypeError(f"{name} must be {self.dtype} or float32, got {t.dtype}")
+        return self.need(t, name, t.dtype, shape)
+
     def result(self, t, name, shape, dtype):
         """The given result matrix, or a new one of `dtype` (None: the call's type)."""
         if t is not None:
@@ -596,6 +615,16 @@ class _Call:
             return torch.empty(shape, dtype=dtype, device=self.device)
         with torch.cuda.stream(self.given):
             return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def workspace(self, ws, need):
+        """The given workspace, or a new one of `need` bytes that belongs to the call's stream."""
+        if ws is None:
+            return self.new(max(need, 1), torch.uint8)
+        if ws.device != self.device:
+            raise ValueError(f"ws must be on {self.device}, got {ws.device}")
+        if not ws.is_contiguous():
+            raise ValueError("ws must be contiguous")
+        return ws
 
     def __call__(self, what, *args):
         f = getattr(_lib or load(), what)
@@ -821,14 +850,232 @@ def adapter_backward(dy: torch.Tensor, x: torch.Tensor, A: torch.Tensor, B: torc
     dA = c.whole(dA, "dA", (n, r, K), grad_dtype)
     dB = c.whole(dB, "dB", (n, N, r), dA.dtype)
     need = adapter_backward_workspace_bytes(T, r)
-    if ws is None:
-        ws = c.new(max(need, 1), torch.uint8)
-    elif ws.device != c.device:
-        raise ValueError(f"ws must be on {c.device}, got {ws.device}")
-    elif not ws.is_contiguous():
-        raise ValueError("ws must be contiguous")
+    ws = c.workspace(ws, need)
     c("moe_adapter_backward", c.code, dy.data_ptr(), _ld(dy, N), x.data_ptr(), _ld(x, K), T, K, N, r, n, A.data_ptr(),
       B.data_ptr(), _ptr(scale), rows.data_ptr(), offsets.data_ptr(), _ptr(dx_base), _ld(dx_base, K), dx.data_ptr(),
       _CODES[dx.dtype], _ld(dx, K), dA.data_ptr(), dB.data_ptr(), _CODES[dA.dtype], int(accumulate), ws.data_ptr(),
       ws.numel() * ws.element_size())
     return dx, dA, dB
+
+
+# --------------------------------------------- the block around the experts
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4, "swiglu": 5, "geglu": 6}
+
+
+def _activation(act: str, N: int):
+    """(code, columns of the result) of an activation of N columns."""
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}, got {act!r}")
+    if act not in ("swiglu", "geglu"):
+        return ACTIVATIONS[act], N
+    if N % 2:
+        raise ValueError(f"{act} needs an even number of columns, got {N}")
+    return ACTIVATIONS[act], N // 2
+
+
+def linear(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None, act: str = "none",
+           residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+           pre: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """moe_linear: y = act(x @ W^T + bias) + residual. x [T][K], W [N][K], bias
+    [N] of x's type or fp32, act a name of ACTIVATIONS ("swiglu" and "geglu":
+    curve(z[:, :N/2]) * z[:, N/2:]), residual of y's type (may be `out` itself);
+    pre [T][N] of x's type receives x @ W^T + bias for linear_backward.
+    Returns y [T][N], or [T][N/2] if gated."""
+    c = _Call(x, "x", stream)
+    if x.dim() != 2 or not isinstance(W, torch.Tensor) or W.dim() != 2:
+        raise ValueError("x must be [T][K] and W [N][K]")
+    (T, K), N = x.shape, W.shape[0]
+    _sizes(T, N, K)
+    code, cols = _activation(act, N)
+    c.rows(x, "x", (T, K))
+    c.need(W, "W", c.dtype, (N, K))
+    if bias is not None:
+        c.vector(bias, "bias", (N,))
+    if residual is not None:
+        c.rows(residual, "residual", (T, cols), torch.float32)
+        out_dtype = residual.dtype if out_dtype is None and out is None else out_dtype
+    y = c.result(out, "out", (T, cols), out_dtype)
+    if residual is not None and residual.dtype != y.dtype:
+        raise TypeError(f"residual must be {y.dtype} like the result, got {residual.dtype}")
+    if pre is not None:
+        c.rows(pre, "pre", (T, N))
+    c("moe_linear", c.code, x.data_ptr(), _ld(x, K), T, N, K, W.data_ptr(), _ptr(bias), c.code if bias is None else _CODES[bias.dtype],
+      code, _ptr(residual), _ld(residual, cols), _ptr(pre), _ld(pre, N), y.data_ptr(), _CODES[y.dtype], _ld(y, cols))
+    return y
+
+
+def linear_backward_workspace_bytes(T: int, N: int, act: str = "none") -> int:
+    _sizes(T, N)
+    return int(load().moe_linear_backward_workspace_bytes(T, N, _activation(act, N)[0]))
+
+
+def linear_backward(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, pre: Optional[torch.Tensor] = None, act: str = "none",
+                    bias_grad: bool = False, dx: Optional[torch.Tensor] = None, dW: Optional[torch.Tensor] = None,
+                    db: Optional[torch.Tensor] = None, grad_dtype: Optional[torch.dtype] = None, accumulate: bool = False,
+                    ws: Optional[torch.Tensor] = None, stream=None):
+    """moe_linear_backward: (dx [T][K], dW [N][K], db [N] or None) from dy
+    [T][columns of y] and pre [T][N], which linear wrote (not needed without
+    activation). db is formed with bias_grad or where it is given; dW and db are of
+    grad_dtype (None: x's type), and with accumulate are added to the given ones
+    (fp32). The C call takes NULL for those that are not wanted."""
+    c = _Call(dy, "dy", stream)
+    if dy.dim() != 2 or not isinstance(x, torch.Tensor) or x.dim() != 2 or not isinstance(W, torch.Tensor) or W.dim() != 2:
+        raise ValueError("dy must be [T][columns], x [T][K] and W [N][K]")
+    (T, K), N = x.shape, W.shape[0]
+    _sizes(T, N, K)
+    code, cols = _activation(act, N)
+    c.rows(dy, "dy", (T, cols))
+    c.rows(x, "x", (T, K))
+    c.need(W, "W", c.dtype, (N, K))
+    if code:
+        if pre is None:
+            raise ValueError(f"{act} needs pre, which linear wrote")
+        c.rows(pre, "pre", (T, N))
+    bias_grad = bias_grad or db is not None
+    if accumulate and (dW is None or (bias_grad and db is None)):
+        raise ValueError("accumulate needs the tensors to add to in dW and db")
+    dx = c.result(dx, "dx", (T, K), None)
+    dW = c.whole(dW, "dW", (N, K), grad_dtype)
+    db = c.whole(db, "db", (N,), dW.dtype) if bias_grad else None
+    if code or bias_grad:
+        ws = c.workspace(ws, linear_backward_workspace_bytes(T, N, act))
+    c("moe_linear_backward", c.code, dy.data_ptr(), _ld(dy, cols), x.data_ptr(), _ld(x, K), T, N, K, W.data_ptr(),
+      _ptr(pre) if code else None, _ld(pre, N) if code else 0, code, dx.data_ptr(), _CODES[dx.dtype], _ld(dx, K), dW.data_ptr(), _ptr(db),
+      _CODES[dW.dtype], int(accumulate), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size())
+    return dx, dW, db
+
+
+def _norm_args(c: _Call, T: int, d: int, w_o, gate, w_n):
+    """(type of the weights, rows of gate): w_o and w_n [d] and gate [gates][d] or [d], all of one type."""
+    dtype, gates = None, 1
+    if gate is not None:
+        if not isinstance(gate, torch.Tensor):
+            raise TypeError("gate must be a torch.Tensor")
+        gates = 1 if gate.dim() == 1 else gate.shape[0]
+        if gates < 1 or T % gates:
+            raise ValueError(f"gate must have a number of rows that divides {T}, got {gates}")
+    for t, name, shape in ((w_o, "w_o", (d,)), (gate, "gate", (d,) if gate is not None and gate.dim() == 1 else (gates, d)), (w_n, "w_n", (d,))):
+        if t is None:
+            continue
+        c.vector(t, name, shape)
+        if dtype is not None and t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype} like the other weights, got {t.dtype}")
+        dtype = t.dtype
+    return c.dtype if dtype is None else dtype, gates
+
+
+def residual_norm(o: Optional[torch.Tensor], x: Optional[torch.Tensor], w_o: Optional[torch.Tensor] = None,
+                  gate: Optional[torch.Tensor] = None, scale: float = 1.0, w_n: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                  y: Optional[torch.Tensor] = None, n: Optional[torch.Tensor] = None, dtype: Optional[torch.dtype] = None, stream=None):
+    """moe_residual_norm: (y, n) with y = scale * x + gate * norm(o) * w_o and
+    n = norm(y) * w_n. o [T][d] (the block's output) or None (before the first
+    block), x [T][d] (the residual stream, of o's type or fp32) or None, w_o None:
+    o itself, gate [d] or [gates][d] (each row for T / gates consecutive rows)
+    or None, w_n None: no norm behind (n is None). w_o, gate and w_n are of one
+    type, o's or fp32. y is of x's type (without x: o's) and may be x itself; n
+    is of o's type and may be o itself. Without o, y is formed only where it is
+    given, and n is of `dtype` (None: x's, which then must not be fp32)."""
+    lead, name = (o, "o") if o is not None else (x, "x")
+    if lead is None:
+        raise ValueError("o or x must be given")
+    if o is None and isinstance(x, torch.Tensor) and x.dtype is torch.float32:
+        if dtype is None:
+            raise TypeError("n's type must be given in dtype where x is float32 and o is None")
+        lead = torch.empty(0, dtype=dtype, device=x.device)
+    c = _Call(lead, name, stream)
+    if dtype is not None and dtype is not c.dtype:
+        raise TypeError(f"dtype must be {c.dtype}, got {dtype}")
+    first = o if o is not None else x
+    if first.dim() != 2:
+        raise ValueError(f"{name} must be [T][d]")
+    T, d = first.shape
+    _sizes(T, d)
+    if o is not None:
+        c.rows(o, "o", (T, d))
+    stream_type = c.dtype
+    if x is not None:
+        c.rows(x, "x", (T, d), torch.float32)
+        stream_type = x.dtype
+    elif y is not None:
+        stream_type = y.dtype
+    wtype, gates = _norm_args(c, T, d, w_o, gate, w_n)
+    if y is not None:
+        c.rows(y, "y", (T, d), torch.float32)
+        if y.dtype is not stream_type:
+            raise TypeError(f"y must be {stream_type} like x, got {y.dtype}")
+    elif o is not None:
+        y = c.new((T, d), stream_type)
+    if w_n is not None:
+        n = c.new((T, d), c.dtype) if n is None else c.rows(n, "n", (T, d))
+    elif n is not None or y is None:
+        raise ValueError("n needs w_n, and without o one of y and w_n must be given")
+    c("moe_residual_norm", c.code, _ptr(o), _ld(o, d), _ptr(x), _ld(x, d), _CODES[stream_type], T, d, _ptr(w_o), _ptr(gate), gates,
+      _ptr(w_n), _CODES[wtype], scale, eps, _ptr(y), _ld(y, d), _ptr(n), _ld(n, d))
+    return y, n
+
+
+def residual_norm_backward_workspace_bytes(T: int, d: int, gates: int = 1) -> int:
+    _sizes(T, d, gates)
+    return int(load().moe_residual_norm_backward_workspace_bytes(T, d, gates))
+
+
+def residual_norm_backward(dy: Optional[torch.Tensor], dn: Optional[torch.Tensor], o: Optional[torch.Tensor], y: Optional[torch.Tensor],
+                           w_o: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None, scale: float = 1.0,
+                           w_n: Optional[torch.Tensor] = None, eps: float = 1e-6, dx: Optional[torch.Tensor] = None,
+                           d_o: Optional[torch.Tensor] = None, dw_o: Optional[torch.Tensor] = None, dgate: Optional[torch.Tensor] = None,
+                           dw_n: Optional[torch.Tensor] = None, grad_dtype: Optional[torch.dtype] = None, accumulate: bool = False,
+                           ws: Optional[torch.Tensor] = None, stream=None):
+    """moe_residual_norm_backward: (dx, d_o, dw_o, dgate, dw_n) from dy and dn,
+    the gradients of residual_norm's y (None: zeros) and n (None: no norm behind;
+    then w_n and y are not read). o, w_o, gate, scale, w_n and eps as there; y is
+    what it wrote (or x, where it formed n alone with scale 1). Those of what the
+    forward call did not have are None. dx is of dy's type (without it y's) and may be
+    dy itself; dw_o, dgate and dw_n are of grad_dtype (None: the weights' type), and with
+    accumulate are added to the given ones (fp32)."""
+    lead, name = next(((t, n) for t, n in ((o, "o"), (dn, "dn"), (dy, "dy")) if t is not None), (None, None))
+    if lead is None:
+        raise ValueError("dy or dn must be given")
+    c = _Call(lead, name, stream)
+    if lead.dim() != 2:
+        raise ValueError(f"{name} must be [T][d]")
+    T, d = lead.shape
+    _sizes(T, d)
+    if dn is None:
+        if dy is None:
+            raise ValueError("dy or dn must be given")
+        y = w_n = None
+    elif w_n is None or y is None:
+        raise ValueError("dn needs w_n and y")
+    stream_type = (dy if dy is not None else y).dtype
+    for t, what in ((dy, "dy"), (y, "y")):
+        if t is not None:
+            c.rows(t, what, (T, d), torch.float32)
+            if t.dtype is not stream_type:
+                raise TypeError(f"{what} must be {stream_type} like dy, got {t.dtype}")
+    for t, what in ((dn, "dn"), (o, "o")):
+        if t is not None:
+            c.rows(t, what, (T, d))
+    if o is None:
+        w_o = gate = None
+    wtype, gates = _norm_args(c, T, d, w_o, gate, w_n)
+    dx = c.result(dx, "dx", (T, d), stream_type)
+    d_o = None if o is None else c.new((T, d), c.dtype) if d_o is None else c.rows(d_o, "d_o", (T, d))
+    gtype = wtype if grad_dtype is None else grad_dtype
+    grads = []
+    for w, g, what in ((w_o, dw_o, "dw_o"), (gate, dgate, "dgate"), (w_n, dw_n, "dw_n")):
+        if w is None:
+            if g is not None:
+                raise ValueError(f"{what} has nothing that it is the gradient of")
+            grads.append(None)
+            continue
+        if g is None and accumulate:
+            raise ValueError(f"accumulate needs the tensor to add to in {what}")
+        grads.append(c.whole(g, what, tuple(w.shape), gtype))
+    need = any(g is not None for g in grads)
+    if need:
+        ws = c.workspace(ws, residual_norm_backward_workspace_bytes(T, d, gates))
+    c("moe_residual_norm_backward", c.code, _ptr(dy), _ld(dy, d), _ptr(dn), _ld(dn, d), _ptr(o), _ld(o, d), _ptr(y), _ld(y, d),
+      _CODES[stream_type], T, d, _ptr(w_o), _ptr(gate), gates, _ptr(w_n), _CODES[wtype], scale, eps, dx.data_ptr(), _ld(dx, d), _ptr(d_o),
+      _ld(d_o, d), _ptr(grads[0]), _ptr(grads[1]), _ptr(grads[2]), _CODES[gtype] if need else c.code, int(accumulate), _ptr(ws) if need else None,
+      ws.numel() * ws.element_size() if need else 0)
+    return (dx, d_o, *grads)

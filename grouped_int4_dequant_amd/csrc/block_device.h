@@ -1,0 +1,106 @@
+// Device pieces shared by the operators of the block around the experts: runs
+// of eight values of any type and alignment, and sums over a wave.
+#pragma once
+
+#include "block_internal.h"
+#include "grouped_device.h"
+
+namespace moe {
+
+// Global loads and stores of 16 bytes need the alignment of their elements only.
+typedef u4 __attribute__((aligned(2))) u4_elem;
+typedef f4 __attribute__((aligned(4))) f4_elem;
+
+// Eight values as they lie in memory: 16-bit ones in lo, fp32 ones in lo and hi.
+struct Raw8 {
+  u4 lo, hi;
+};
+
+// Values at + 0 .. 7 of p, of which the first `left` exist (the others read as zeros).
+template <bool F32>
+__device__ __forceinline__ Raw8 load_raw8(const void *p, int64_t at, int left) {
+  Raw8 v = {{0u, 0u, 0u, 0u}, {0u, 0u, 0u, 0u}};
+  if constexpr (F32) {
+    const float *q = static_cast<const float *>(p) + at;
+    if (left >= 8) {
+      v.lo = __builtin_bit_cast(u4, (f4) * reinterpret_cast<const f4_elem *>(q));
+      v.hi = __builtin_bit_cast(u4, (f4) * reinterpret_cast<const f4_elem *>(q + 4));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t x = i < left ? __builtin_bit_cast(uint32_t, q[i]) : 0u;
+        if (i < 4) v.lo[i] = x; else v.hi[i - 4] = x;
+      }
+    }
+  } else {
+    const uint16_t *q = static_cast<const uint16_t *>(p) + at;
+    if (left >= 8) {
+      v.lo = *reinterpret_cast<const u4_elem *>(q);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t x = i < left ? (uint32_t)q[i] : 0u;
+        v.lo[i >> 1] |= x << (16 * (i & 1));
+      }
+    }
+  }
+  return v;
+}
+template <typename Tr, bool F32>
+__device__ __forceinline__ void widen8(const Raw8 &v, float *f) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (F32) f[i] = __builtin_bit_cast(float, i < 4 ? v.lo[i] : v.hi[i - 4]);
+    else f[i] = Tr::to((uint16_t)(v.lo[i >> 1] >> (16 * (i & 1))));
+  }
+}
+// The same for an array whose type is known at run time.
+template <typename Tr>
+__device__ __forceinline__ void load8(const void *p, bool f32, int64_t at, int left, float *f) {
+  if (f32) widen8<Tr, true>(load_raw8<true>(p, at, left), f);
+  else widen8<Tr, false>(load_raw8<false>(p, at, left), f);
+}
+
+// Stores the first `left` of eight values, rounded to the array's type.
+template <typename Tr>
+__device__ __forceinline__ void store8(void *p, bool f32, int64_t at, int left, const float *f) {
+  if (f32) {
+    float *q = static_cast<float *>(p) + at;
+    if (left >= 8) {
+      *reinterpret_cast<f4_elem *>(q) = f4{f[0], f[1], f[2], f[3]};
+      *reinterpret_cast<f4_elem *>(q + 4) = f4{f[4], f[5], f[6], f[7]};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < left) q[i] = f[i];
+    }
+  } else {
+    uint16_t *q = static_cast<uint16_t *>(p) + at;
+    if (left >= 8) {
+      u4 v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = (uint32_t)Tr::from(f[2 * i]) | (uint32_t)Tr::from(f[2 * i + 1]) << 16;
+      *reinterpret_cast<u4_elem *>(q) = v;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < left) q[i] = Tr::from(f[i]);
+    }
+  }
+}
+
+template <int Ctrl>
+__device__ __forceinline__ float dpp_f32(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), Ctrl, 0xf, 0xf, false));
+}
+// Sum over the 64 lanes in a fixed order, the same in every lane.
+__device__ __forceinline__ float wave_sum(float v) {
+  v += dpp_f32<0xB1>(v);   // lanes 1,0,3,2 of each four
+  v += dpp_f32<0x4E>(v);   // 2,3,0,1
+  v += dpp_f32<0x124>(v);  // four on, in each 16
+  v += dpp_f32<0x128>(v);  // eight on: every lane holds its 16 lanes' sum
+  auto lane = [&](int l) { return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l)); };
+  return (lane(0) + lane(16)) + (lane(32) + lane(48));
+}
+
+}  // namespace moe

@@ -1,0 +1,82 @@
+// Internal declarations of the operators of the block around the experts: the
+// norms before and after it with its gate and residual, the matrix product with
+// bias, activation and residual, and the whole layer for a few tokens, each in 16
+// bits. Not installed; the public interface is include/moe_int4.h.
+#pragma once
+
+#include "grouped_internal.h"
+
+namespace moe {
+
+// p = o r(o) w_o;  y = scale x + gate p;  n = y r(y) w_n;  r(v) = (mean v^2 + eps)^-1/2
+struct NormArgs {
+  const uint16_t *o;        // nullable: no block
+  int64_t ld_o;
+  const void *x;            // nullable: no residual
+  int64_t ld_x;
+  const void *w_o, *gate, *w_n;  // each nullable
+  int32_t w_f32;            // they are fp32, else the operands' type
+  int32_t stream_f32;       // x and y are
+  int32_t period;           // rows that one row of gate serves
+  int32_t T, d;
+  float scale, eps;
+  void *y;                  // nullable: not wanted
+  int64_t ld_y;
+  uint16_t *n;              // nullable: not wanted
+  int64_t ld_n;
+};
+// The gradients. Rows are cut into chunks that lie in one gate's rows, or hold whole gates' rows; each
+// chunk leaves its column sums in the workspace and a second kernel adds them up.
+struct NormGradArgs {
+  const void *dy;           // nullable: zeros
+  int64_t ld_dy;
+  const uint16_t *dn;       // nullable: no norm behind
+  int64_t ld_dn;
+  const uint16_t *o;        // nullable: no block
+  int64_t ld_o;
+  const void *y;            // with dn
+  int64_t ld_y;
+  const void *w_o, *gate, *w_n;
+  int32_t w_f32, stream_f32, gates, period, T, d;
+  float scale, eps;
+  void *dx;                 // nullable: not wanted
+  int64_t ld_dx;
+  uint16_t *d_o;            // nullable: not wanted
+  int64_t ld_do;
+  void *dw_o, *dgate, *dw_n;  // each nullable: not wanted
+  int32_t g_f32, accumulate;
+  float *part;              // workspace: column sums of dw_o, dgate, dw_n, [3][chunks][pitch]
+  int64_t pitch;
+  int32_t chunk_rows, chunks, per_gate;  // per_gate: chunks of one gate's rows, 0: a chunk holds whole gates
+};
+// chunk_rows, chunks and per_gate for T rows of which every `period` share a gate
+struct NormChunks { int32_t rows, count, per_gate; };
+NormChunks norm_chunks(int32_t T, int32_t period);
+
+// dz = act'(pre) dy and its column sums
+struct ActGradArgs {
+  const uint16_t *dy;       // [T][ld_dy], `cols` columns
+  int64_t ld_dy;
+  const uint16_t *pre;      // [T][ld_pre], N columns; nullable without activation
+  int64_t ld_pre;
+  int32_t T, N, cols, act;  // cols: N, or N / 2 if gated
+  uint16_t *dz;             // [T][N]; nullable without activation
+  float *part;              // nullable: column sums not wanted; [chunks][pitch]
+  int64_t pitch;
+  int32_t chunk_rows, chunks;
+  void *db;                 // [N]
+  int32_t g_f32, accumulate;
+};
+struct ColumnChunks { int32_t rows, count; };
+ColumnChunks column_chunks(int32_t T, int32_t cols);
+
+template <bool Gated>
+hipError_t launch_linear(const LinearArgs<Gated> &a, bool fp16, hipStream_t s);
+hipError_t launch_act_grad(const ActGradArgs &a, bool fp16, hipStream_t s);
+hipError_t launch_dense(const DenseArgs &a, GroupedMode mode, bool fp16, hipStream_t s);
+inline bool is_gated(int32_t act) { return act == MOE_ACT_SWIGLU || act == MOE_ACT_GEGLU; }
+
+hipError_t launch_norm(const NormArgs &a, bool fp16, hipStream_t s);
+hipError_t launch_norm_grad(const NormGradArgs &a, bool fp16, hipStream_t s);
+
+}  // namespace moe

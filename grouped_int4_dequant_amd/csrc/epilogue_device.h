@@ -1,0 +1,215 @@
+// What follows the product of the matrix kernels: bias, activation and
+// residual. Everything is formed in fp32 from the accumulated sum and rounded once.
+#pragma once
+
+#include "block_device.h"
+
+#include <type_traits>
+
+namespace moe {
+
+// e^v for v <= 0, as 2^(v log2 e). The product's rounding error, found with a fused multiply-add, multiplies the
+// result again, so that large |v| keep their bits: within 2^-22 of e^v. The library function costs three times as
+// many instructions.
+__device__ __forceinline__ float exp_of(float v) {
+  const float t = v * 1.44269502e+00f;  // log2 e = 1.44269502 + 1.92596303e-8
+  const float low = fmaf(v, 1.44269502e+00f, -t) + v * 1.92596303e-08f;
+  const float p = __builtin_amdgcn_exp2f(t);
+  return t > -200.f ? fmaf(p, low * 6.93147182e-01f, p) : p;  // (an infinite t has no error to correct)
+}
+// s(v) = 1 / (1 + e^-v) and 1 - s(v), each with all its bits
+struct Sigmoid {
+  float s, rest;
+};
+__device__ __forceinline__ Sigmoid sigmoid_of(float v) {
+  const float e = exp_of(-__builtin_fabsf(v)), big = __builtin_amdgcn_rcpf(1.f + e), small = e * big;
+  return v < 0.f ? Sigmoid{small, big} : Sigmoid{big, small};
+}
+
+constexpr float kGeluC = 7.978845608e-01f;  // sqrt(2 / pi)
+constexpr float kGeluA = 0.044715f;
+
+// The curve that an activation puts a value (the gate's, if gated) through.
+__device__ __forceinline__ float curve_of(int act, float z) {
+  switch (act) {
+    case MOE_ACT_RELU: return z > 0.f || z != z ? z : 0.f;
+    case MOE_ACT_SILU:
+    case MOE_ACT_SWIGLU: return z * sigmoid_of(z).s;
+    case MOE_ACT_GELU: return 0.5f * z * erfcf(z * -7.071067812e-01f);
+    case MOE_ACT_GELU_TANH:
+    case MOE_ACT_GEGLU: return z * sigmoid_of(2.f * kGeluC * fmaf(kGeluA * z * z, z, z)).s;  // (1 + tanh u) / 2 = s(2 u)
+    default: return z;
+  }
+}
+// The curve's derivative.
+__device__ __forceinline__ float slope_of(int act, float z) {
+  switch (act) {
+    case MOE_ACT_RELU: return z > 0.f ? 1.f : 0.f;
+    case MOE_ACT_SILU:
+    case MOE_ACT_SWIGLU: {
+      const Sigmoid g = sigmoid_of(z);
+      return g.s * fmaf(z, g.rest, 1.f);
+    }
+    case MOE_ACT_GELU: return 0.5f * erfcf(z * -7.071067812e-01f) + z * (3.989422804e-01f * exp_of(-0.5f * z * z));
+    case MOE_ACT_GELU_TANH:
+    case MOE_ACT_GEGLU: {
+      const Sigmoid g = sigmoid_of(2.f * kGeluC * fmaf(kGeluA * z * z, z, z));
+      const float both = g.s * g.rest;  // where it is zero the curve is straight, though z^2 may have overflowed
+      return both == 0.f ? g.s : fmaf(z * both, 2.f * kGeluC * fmaf(3.f * kGeluA * z, z, 1.f), g.s);
+    }
+    default: return 1.f;
+  }
+}
+
+typedef u2 __attribute__((aligned(2))) u2_elem;
+
+// Up to four values at + 0 .. 3.
+template <typename Tr>
+__device__ __forceinline__ f4 load4(const void *p, bool f32, int64_t at, int left) {
+  f4 v = {0.f, 0.f, 0.f, 0.f};
+  if (f32) {
+    const float *q = static_cast<const float *>(p) + at;
+    if (left >= 4) return *reinterpret_cast<const f4_elem *>(q);
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (i < left) v[i] = q[i];
+  } else {
+    const uint16_t *q = static_cast<const uint16_t *>(p) + at;
+    if (left >= 4) {
+      const u2 w = *reinterpret_cast<const u2_elem *>(q);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = Tr::to((uint16_t)(w[i >> 1] >> (16 * (i & 1))));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (i < left) v[i] = Tr::to(q[i]);
+    }
+  }
+  return v;
+}
+template <typename Tr>
+__device__ __forceinline__ void store4_of(void *p, bool f32, int64_t at, int left, f4 v) {
+  if (f32) {
+    float *q = static_cast<float *>(p) + at;
+    if (left >= 4) {
+      *reinterpret_cast<f4_elem *>(q) = v;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (i < left) q[i] = v[i];
+    }
+  } else {
+    uint16_t *q = static_cast<uint16_t *>(p) + at;
+    if (left >= 4) {
+      *reinterpret_cast<u2_elem *>(q) = u2{(uint32_t)Tr::from(v[0]) | (uint32_t)Tr::from(v[1]) << 16,
+                                           (uint32_t)Tr::from(v[2]) | (uint32_t)Tr::from(v[3]) << 16};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (i < left) q[i] = Tr::from(v[i]);
+    }
+  }
+}
+
+// Four sums of result row `row`, from result column `col` on, of which `left` exist: z is the product
+// (the gate's if gated), u the product that it multiplies.
+template <typename Tr, typename Args>
+__device__ __forceinline__ void finish4(const Args &a, int row, int col, int left, f4 z, f4 u) {
+  if (a.bias) {
+    z += load4<Tr>(a.bias, a.bias_f32, col, left);
+    if constexpr (Args::kGated) u += load4<Tr>(a.bias, a.bias_f32, a.N / 2 + col, left);
+  }
+  if (a.pre) {
+    store4_of<Tr>(a.pre, false, (int64_t)row * a.ld_pre + col, left, z);
+    if constexpr (Args::kGated) store4_of<Tr>(a.pre, false, (int64_t)row * a.ld_pre + a.N / 2 + col, left, u);
+  }
+  if (a.act != MOE_ACT_NONE) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      z[i] = curve_of(a.act, z[i]);
+      if constexpr (Args::kGated) z[i] *= u[i];
+    }
+  }
+  if (a.res) z += load4<Tr>(a.res, a.out_f32, (int64_t)row * a.ld_res + col, left);
+  store4_of<Tr>(a.out, a.out_f32, (int64_t)row * a.ld_out + col, left, z);
+}
+
+// The same for eight.
+template <typename Tr, typename Args>
+__device__ __forceinline__ void finish8(const Args &a, int row, int col, int left, float (&z)[8], float (&u)[8]) {
+  float f[8];
+  if (a.bias) {
+    load8<Tr>(a.bias, a.bias_f32, col, left, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] += f[i];
+    if constexpr (Args::kGated) {
+      load8<Tr>(a.bias, a.bias_f32, a.N / 2 + col, left, f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) u[i] += f[i];
+    }
+  }
+  if (a.pre) {
+    store8<Tr>(a.pre, false, (int64_t)row * a.ld_pre + col, left, z);
+    if constexpr (Args::kGated) store8<Tr>(a.pre, false, (int64_t)row * a.ld_pre + a.N / 2 + col, left, u);
+  }
+  if (a.act != MOE_ACT_NONE) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      z[i] = curve_of(a.act, z[i]);
+      if constexpr (Args::kGated) z[i] *= u[i];
+    }
+  }
+  if (a.res) {
+    load8<Tr>(a.res, a.out_f32, (int64_t)row * a.ld_res + col, left, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] += f[i];
+  }
+  store8<Tr>(a.out, a.out_f32, (int64_t)row * a.ld_out + col, left, z);
+}
+
+// The results of a wide tile. A lane holds 16 consecutive columns of row p16 of each of its wave's 16-row blocks
+// (gated: eight of the gate and the eight that it multiplies). The sums of a block pass through 4 KiB of LDS of the
+// wave's own, so that eight lanes (gated: four) have a row's consecutive columns and arrays are read and
+// stored as whole lines (gated: halves). The loop over blocks stays one: unrolled, the activations fill the instruction
+// cache and the accumulators' last uses move to scratch.
+template <typename Tr, int TI, typename Args>
+__device__ __forceinline__ void finish_wide(const Args &a, int i0, int j0, int ni, int nj, f4 (&acc)[TI][4], uint8_t *mine) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wi = wave >> 2, wj = wave & 3, p16 = lane & 15, q4 = lane >> 4;
+  constexpr int C = Args::kGated ? 32 : 64;  // result columns of a wave
+  // unit u (four sums) of row r lies in slot u ^ r of sixteen
+  auto unit = [&](int r, int u) __attribute__((always_inline)) { return reinterpret_cast<f4 *>(mine + 256 * r + 16 * (u ^ r)); };
+#pragma unroll 1
+  for (int i = 0; i < TI; ++i) {
+    const int row0 = 16 * (wi + 2 * i);
+    if (row0 >= ni) break;
+#pragma unroll
+    for (int s = 0; s < TI; ++s) {
+      if (s != i) continue;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) *unit(p16, Args::kGated ? 8 * (c >> 1) + 2 * q4 + (c & 1) : 4 * q4 + c) = acc[s][c];
+    }
+    wave_sync();
+#pragma unroll 1
+    for (int x = 0; x < C / 32; ++x) {
+      const int r = Args::kGated ? lane >> 2 : 8 * x + (lane >> 3), g = Args::kGated ? lane & 3 : lane & 7;
+      float z[8], u[8];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const f4 v = *unit(r, 2 * g + c);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) z[4 * c + y] = v[y];
+        if constexpr (Args::kGated) {
+          const f4 w = *unit(r, 8 + 2 * g + c);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) u[4 * c + y] = w[y];
+        }
+      }
+      const int col = C * wj + 8 * g;
+      if (row0 + r < ni && col < nj) finish8<Tr>(a, i0 + row0 + r, j0 + col, nj - col, z, u);
+    }
+    wave_sync();
+  }
+}
+
+}  // namespace moe

@@ -27,6 +27,9 @@ inline bool grid_fits(int64_t blocks, int threads) { return blocks * threads < (
 enum GroupedMode { kFwd = 0, kDgrad = 1, kWgrad = 2 };
 
 struct GroupedArgs {
+  // of the kernels that take them: one matrix for all rows; bias, activation and residual behind the
+  // product; columns in two halves, the first the gate's
+  static constexpr bool kDense = false, kEpilogue = false, kGated = false;
   const uint16_t *rows;     // A (forward, weight gradient) or dC (input gradient)
   int64_t ld_rows;
   const int32_t *a_row;     // nullable: row of `rows` for each sorted row
@@ -42,6 +45,23 @@ struct GroupedArgs {
   int32_t vec;              // every 16-byte unit of the operands is aligned and whole
   int32_t wide;             // 31-bit byte offsets reach every operand of the wide tiles
   int32_t vec_out;          // four consecutive outputs may be stored at once
+};
+
+// One matrix: no groups, no gathered rows (P rows, a_rows = P).
+struct DenseArgs : GroupedArgs {
+  static constexpr bool kDense = true;
+};
+// y = act(x W^T + bias) + residual; z = x W^T + bias goes to `pre`
+template <bool Gated>
+struct LinearArgs : DenseArgs {
+  static constexpr bool kEpilogue = true, kGated = Gated;
+  const void *bias;         // [N], nullable
+  int32_t bias_f32;
+  int32_t act;              // MOE_ACT_*
+  const void *res;          // nullable, of out's type; may be out
+  int64_t ld_res;
+  uint16_t *pre;            // nullable, [P][ld_pre], N columns
+  int64_t ld_pre;
 };
 
 hipError_t launch_grouped(const GroupedArgs &a, GroupedMode mode, bool fp16, hipStream_t s);

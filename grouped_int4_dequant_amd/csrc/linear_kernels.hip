@@ -1,0 +1,216 @@
+// The matrix product with bias, activation and residual, and its gradients, for
+// gfx950.
+//
+//   z = x W^T + b     y = act(z) + r       act(z) = curve(z), or curve(z[:f]) z[f:] if gated (N = 2 f)
+//   dz = act'(z) dy   dx = dz W   dW = dz^T x   db = sum_t dz
+//
+// Many rows are bound by the matrix instructions and take the tiles of grouped_tiles.h,
+// with the epilogue on the accumulators: z, the activation and the residual never make a trip
+// of their own. Few rows are bound by reading W once.
+
+#include "grouped_tiles.h"
+#include "block_internal.h"
+
+namespace moe {
+namespace {
+
+// ---------------------------------------------------------------- few rows
+// At most 64 rows: a workgroup takes 16 rows of W (gated: eight of the gate and the eight that
+// it multiplies), whose sums its eight waves share and join in LDS, in order. W goes straight
+// from memory to operand registers and is read once; x comes from L2.
+template <typename Tr, bool Gated, int RB>
+__global__ __launch_bounds__(512) void linear_few_kernel(LinearArgs<Gated> a) {
+  constexpr int kDeep = RB == 1 ? 8 : RB == 2 ? 4 : 2;
+  __shared__ __attribute__((aligned(16))) f4 s_part[8][RB][64];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int p16 = lane & 15, q4 = lane >> 4;
+  constexpr int C = Gated ? 8 : 16;  // result columns
+  const int J = Gated ? a.N / 2 : a.N, j0 = blockIdx.x * C;
+  const int col = Gated ? j0 + (p16 & 7) : j0 + p16;
+  const uint16_t *w = col < J ? a.w + (int64_t)(Gated && p16 >= 8 ? J + col : col) * a.K : nullptr;
+  const uint16_t *x[RB];
+#pragma unroll
+  for (int b = 0; b < RB; ++b) x[b] = 16 * b + p16 < a.P ? a.rows + (int64_t)(16 * b + p16) * a.ld_rows : nullptr;
+  const s8 zero = {0, 0, 0, 0, 0, 0, 0, 0};
+  f4 acc[RB];
+#pragma unroll
+  for (int b = 0; b < RB; ++b) acc[b] = f4{0.f, 0.f, 0.f, 0.f};
+  for (int k0 = 32 * wave; k0 < a.K; k0 += 256 * kDeep) {
+    s8 wv[kDeep], xv[kDeep][RB];
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u) {
+      const int k = k0 + 256 * u + 8 * q4;
+      wv[u] = w && k < a.K ? *reinterpret_cast<const s8 *>(w + k) : zero;
+    }
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u)
+#pragma unroll
+      for (int b = 0; b < RB; ++b) {
+        const int k = k0 + 256 * u + 8 * q4;
+        xv[u][b] = x[b] && k < a.K ? *reinterpret_cast<const s8 *>(x[b] + k) : zero;
+      }
+#pragma unroll
+    for (int u = 0; u < kDeep; ++u)
+#pragma unroll
+      for (int b = 0; b < RB; ++b) acc[b] = Tr::mfma(wv[u], xv[u][b], acc[b]);
+  }
+#pragma unroll
+  for (int b = 0; b < RB; ++b) s_part[wave][b][lane] = acc[b];
+  __syncthreads();
+  if (wave >= RB) return;
+  f4 v = s_part[0][wave][lane];
+#pragma unroll
+  for (int y = 1; y < 8; ++y) v += s_part[y][wave][lane];
+  // lane: row p16, W's rows 4 q4 ..
+  const int row = 16 * wave + p16;
+  if constexpr (Gated) {
+    f4 u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = __shfl(v[i], (lane + 32) & 63);
+    const int c = j0 + 4 * q4;
+    if (q4 < 2 && row < a.P && c < J) finish4<Tr>(a, row, c, min(J - c, 4), v, u);
+  } else {
+    const int c = j0 + 4 * q4;
+    if (row < a.P && c < J) finish4<Tr>(a, row, c, min(J - c, 4), v, v);
+  }
+}
+
+// ------------------------------------------------------- activation's gradient
+// A workgroup takes 256 columns of a chunk of rows; a thread eight of them, every eighth row. dz is rounded
+// to the operands' type, because it enters the two products as an operand of the matrix instructions; the
+// column sums are of its values before that. Bound by memory.
+template <typename Tr, bool Gated>
+__global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs a) {
+  __shared__ float s_sum[8][Gated ? 2 : 1][256];
+  const int unit = threadIdx.x & 31, r0 = threadIdx.x >> 5;
+  const int col = 256 * blockIdx.x + 8 * unit, left = a.cols - col;
+  const int begin = blockIdx.y * a.chunk_rows, end = min(begin + a.chunk_rows, a.T);
+  float sum[Gated ? 2 : 1][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    sum[0][i] = 0.f;
+    if constexpr (Gated) sum[1][i] = 0.f;
+  }
+  if (left > 0) {
+    for (int row = begin + r0; row < end; row += 8) {
+      float dy[8], z[8], u[8];
+      widen8<Tr, false>(load_raw8<false>(a.dy, (int64_t)row * a.ld_dy + col, left), dy);
+      if (a.act != MOE_ACT_NONE) {
+        widen8<Tr, false>(load_raw8<false>(a.pre, (int64_t)row * a.ld_pre + col, left), z);
+        if constexpr (Gated) widen8<Tr, false>(load_raw8<false>(a.pre, (int64_t)row * a.ld_pre + a.cols + col, left), u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float slope = slope_of(a.act, z[i]);
+          if constexpr (Gated) {
+            const float value = curve_of(a.act, z[i]);
+            z[i] = dy[i] * value;
+            dy[i] = dy[i] * u[i] * slope;
+          } else {
+            dy[i] *= slope;
+          }
+        }
+        store8<Tr>(a.dz, false, (int64_t)row * a.N + col, left, dy);
+        if constexpr (Gated) store8<Tr>(a.dz, false, (int64_t)row * a.N + a.cols + col, left, z);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        sum[0][i] += dy[i];
+        if constexpr (Gated) sum[1][i] += z[i];
+      }
+    }
+  }
+  if (!a.part) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    s_sum[r0][0][8 * unit + i] = sum[0][i];
+    if constexpr (Gated) s_sum[r0][1][8 * unit + i] = sum[1][i];
+  }
+  __syncthreads();
+  const int c = 256 * blockIdx.x + threadIdx.x;
+  if (c >= a.cols) return;
+#pragma unroll
+  for (int h = 0; h < (Gated ? 2 : 1); ++h) {
+    float f = 0.f;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) f += s_sum[r][h][threadIdx.x];
+    a.part[(int64_t)blockIdx.y * a.pitch + h * a.cols + c] = f;
+  }
+}
+
+// db: the chunks' column sums added up in order. 64 columns a workgroup, sixteen waves share the chunks.
+template <typename Tr>
+__global__ __launch_bounds__(1024) void column_sums_kernel(ActGradArgs a) {
+  __shared__ float s_part[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int col = blockIdx.x * 64 + lane;
+  float f = 0.f;
+  if (col < a.N)
+    for (int c = wave; c < a.chunks; c += 16) f += a.part[(int64_t)c * a.pitch + col];
+  s_part[wave][lane] = f;
+  __syncthreads();
+  if (wave != 0 || col >= a.N) return;
+  f = 0.f;
+#pragma unroll
+  for (int w = 0; w < 16; ++w) f += s_part[w][lane];
+  if (a.g_f32) {
+    float *q = static_cast<float *>(a.db) + col;
+    *q = a.accumulate ? *q + f : f;
+  } else {
+    static_cast<uint16_t *>(a.db)[col] = Tr::from(f);
+  }
+}
+
+template <typename Tr, bool Gated>
+hipError_t linear_of(const LinearArgs<Gated> &a, hipStream_t s) {
+  if (a.vec && a.P <= 64) {
+    const dim3 grid((unsigned)cdiv(Gated ? a.N / 2 : a.N, Gated ? 8 : 16));
+    if (a.P <= 16) linear_few_kernel<Tr, Gated, 1><<<grid, 512, 0, s>>>(a);
+    else if (a.P <= 32) linear_few_kernel<Tr, Gated, 2><<<grid, 512, 0, s>>>(a);
+    else linear_few_kernel<Tr, Gated, 4><<<grid, 512, 0, s>>>(a);
+    return hipGetLastError();
+  }
+  return launch_vec<Tr, kFwd, LinearArgs<Gated>>(a, s);
+}
+
+template <typename Tr>
+hipError_t act_grad_of(const ActGradArgs &a, hipStream_t s) {
+  if (a.chunks > 0 && (a.dz || a.part)) {
+    const dim3 grid((unsigned)cdiv(a.cols, 256), (unsigned)a.chunks);
+    if (a.cols != a.N) act_grad_kernel<Tr, true><<<grid, 256, 0, s>>>(a);
+    else act_grad_kernel<Tr, false><<<grid, 256, 0, s>>>(a);
+  }
+  if (a.db) column_sums_kernel<Tr><<<dim3((unsigned)cdiv(a.N, 64)), 1024, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <typename Tr>
+hipError_t dense_of(const DenseArgs &a, GroupedMode mode, hipStream_t s) {
+  return mode == kDgrad ? launch_vec<Tr, kDgrad, DenseArgs>(a, s) : launch_vec<Tr, kWgrad, DenseArgs>(a, s);
+}
+
+}  // namespace
+
+ColumnChunks column_chunks(int32_t T, int32_t cols) {
+  // about 2048 workgroups of 256 columns, of eight rows at least
+  const int64_t blocks = cdiv(cols, 256), most = blocks >= 2048 ? 1 : 2048 / blocks;
+  int64_t rows = cdiv(T > 0 ? T : 1, most);
+  rows = cdiv(rows, 8) * 8;
+  return {(int32_t)rows, (int32_t)cdiv(T, rows)};
+}
+
+template <bool Gated>
+hipError_t launch_linear(const LinearArgs<Gated> &a, bool fp16, hipStream_t s) {
+  return fp16 ? linear_of<Fp16, Gated>(a, s) : linear_of<Bf16, Gated>(a, s);
+}
+template hipError_t launch_linear<false>(const LinearArgs<false> &, bool, hipStream_t);
+template hipError_t launch_linear<true>(const LinearArgs<true> &, bool, hipStream_t);
+
+hipError_t launch_act_grad(const ActGradArgs &a, bool fp16, hipStream_t s) {
+  return fp16 ? act_grad_of<Fp16>(a, s) : act_grad_of<Bf16>(a, s);
+}
+hipError_t launch_dense(const DenseArgs &a, GroupedMode mode, bool fp16, hipStream_t s) {
+  return fp16 ? dense_of<Fp16>(a, mode, s) : dense_of<Bf16>(a, mode, s);
+}
+
+}  // namespace moe

@@ -636,6 +636,116 @@ int moe_adapter_backward(int32_t dtype, const void *dy, int64_t lddy, const void
                          int32_t dx_dtype, int64_t lddx, void *dA, void *dB, int32_t g_dtype, int32_t accumulate, void *ws,
                          size_t ws_bytes, hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The block around the experts in 16 bits: the matrix product with bias,
+ * activation and residual and its gradients (a shared expert, a dense block), the
+ * norms before and after a block with its gate and residual and their gradients,
+ * and the whole layer for a few tokens. The conventions of the 16-bit operators
+ * hold here too; eight consecutive values are read and stored at once at any
+ * alignment of their elements, and only the matrix products are slower where rows
+ * are not whole 16-byte units at 16-byte alignment.
+ */
+
+/* Activations. curve(z) for each of N columns, or gated: curve(z[:N/2]) * z[N/2:]. */
+#define MOE_ACT_NONE      0  /* z */
+#define MOE_ACT_RELU      1  /* max(z, 0); the derivative at 0 is 0 */
+#define MOE_ACT_SILU      2  /* z / (1 + e^-z) */
+#define MOE_ACT_GELU      3  /* z Phi(z), Phi the normal distribution */
+#define MOE_ACT_GELU_TANH 4  /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+#define MOE_ACT_SWIGLU    5  /* gated, with the curve of MOE_ACT_SILU */
+#define MOE_ACT_GEGLU     6  /* gated, with the curve of MOE_ACT_GELU_TANH */
+
+/*
+ * Matrix product with bias, activation and residual:
+ *     z[t][n] = sum_k x[t][k] * W[n][k] + bias[n]       y[t] = act(z[t]) + residual[t]
+ *   x         dtype [T][ldx], K columns
+ *   W         dtype [N][K]
+ *   bias      dtype or fp32 (bias_dtype) [N], or NULL
+ *   act       MOE_ACT_*; gated ones need an even N, and y has N/2 columns (else N)
+ *   residual  of y's type [T][ldres], or NULL; may be y itself with the same stride
+ *   pre       dtype [T][ldpre], N columns: receives z, rounded, for
+ *             moe_linear_backward; or NULL
+ *   y         dtype or fp32 [T][ldy]
+ * The activation takes z before it is rounded. A row's results do not depend on the other rows
+ * of the call, but may differ in the last bits between calls of different T. Errors:
+ * MOE_EINVAL (null or misaligned pointer, unknown type or activation, T < 0, N or K < 1, odd N with a
+ * gated activation, a stride below the width), MOE_EUNSUPPORTED (T, N or K above 2^30), MOE_EHIP. T == 0
+ * enqueues nothing. One kernel; no workspace.
+ */
+int moe_linear(int32_t dtype, const void *x, int64_t ldx, int32_t T, int32_t N, int32_t K, const void *W, const void *bias,
+               int32_t bias_dtype, int32_t act, const void *residual, int64_t ldres, void *pre, int64_t ldpre, void *y,
+               int32_t y_dtype, int64_t ldy, hipStream_t stream);
+
+/*
+ * Gradients of moe_linear (that of residual is dy itself):
+ *     dz = act'(pre) dy       dx = dz W       dW = dz^T x       db = sum_t dz[t]
+ *   dy     dtype [T][lddy], of as many columns as y
+ *   x, W   as above (x with dW, W with dx; else they may be NULL)
+ *   pre    what moe_linear wrote [T][ldpre]; ignored without activation
+ *   dx     dtype or fp32 (dx_dtype) [T][lddx], or NULL (not wanted)
+ *   dW, db dtype or fp32 (g_dtype) [N][K] and [N], each or NULL. accumulate != 0 (fp32
+ *          only, else MOE_EUNSUPPORTED) adds to what they hold. T == 0 writes zeros (or leaves them).
+ *   ws     moe_linear_backward_workspace_bytes(T, N, act) bytes, 256-byte aligned; may be NULL when
+ *          act is MOE_ACT_NONE and db NULL. Calls that may run at the same time, in replayed
+ *          graphs too, need one each.
+ * With an activation dz is rounded to dtype before the two products (they take 16-bit operands), so
+ * dx and dW carry that rounding of each term whatever their type; db does not. Errors as
+ * moe_linear, and MOE_EWORKSPACE.
+ */
+size_t moe_linear_backward_workspace_bytes(int32_t T, int32_t N, int32_t act);
+int moe_linear_backward(int32_t dtype, const void *dy, int64_t lddy, const void *x, int64_t ldx, int32_t T, int32_t N, int32_t K,
+                        const void *W, const void *pre, int64_t ldpre, int32_t act, void *dx, int32_t dx_dtype, int64_t lddx,
+                        void *dW, void *db, int32_t g_dtype, int32_t accumulate, void *ws, size_t ws_bytes, hipStream_t stream);
+
+#define MOE_MAX_NORM_WIDTH 16384
+
+/*
+ * The norms before and after a block, with its gate and residual, in one pass:
+ *     p[t] = o[t] * r(o[t]) * w_o          (w_o NULL: p = o)
+ *     y[t] = scale * x[t] + gate[g] * p[t]
+ *     n[t] = y[t] * r(y[t]) * w_n          r(v) = (mean(v^2) + eps)^(-1/2)
+ *   o      dtype [T][ldo]: the block's output; NULL before the first block (then y = scale * x)
+ *   x      stream_dtype [T][ldx]: the residual stream; NULL: none (then y = gate * p). Not both NULL.
+ *   w_o, w_n, gate   dtype or fp32 (w_dtype) [d], [d], [gates][d]. Each row of gate serves T / gates
+ *          consecutive rows t (one row: a learned scale of each column; one a sequence, or one
+ *          a token: a gate that the model computes). gate NULL: ones, and gates is ignored.
+ *   y      stream_dtype (dtype or fp32) [T][ldy], or NULL (not wanted); may be x itself with the same stride
+ *   n      dtype [T][ldn], or NULL (not wanted; w_n is ignored); may be o itself with the same stride
+ * n is formed from y before y is rounded. Squares are summed in fp32. Errors: MOE_EINVAL (null or misaligned
+ * pointer, unknown type, T < 0, d < 1, gates < 1 or not a divisor of T, neither y nor n, n without w_n, a
+ * stride below the width, eps < 0 or not a number), MOE_EUNSUPPORTED (d > MOE_MAX_NORM_WIDTH, T > 2^30), MOE_EHIP.
+ * T == 0 enqueues nothing. One kernel; no workspace.
+ */
+int moe_residual_norm(int32_t dtype, const void *o, int64_t ldo, const void *x, int64_t ldx, int32_t stream_dtype, int32_t T,
+                      int32_t d, const void *w_o, const void *gate, int32_t gates, const void *w_n, int32_t w_dtype, float scale,
+                      float eps, void *y, int64_t ldy, void *n, int64_t ldn, hipStream_t stream);
+
+/*
+ * Gradients of moe_residual_norm, from dy and dn, those of y and n:
+ *     gy = dy + r(y) (w_n dn - yh mean(w_n dn yh))       yh = y r(y), oh = o r(o)
+ *     dx = scale gy       dgate[g] = sum_{t of g} gy p      dp = gate gy
+ *     d_o = r(o) (w_o dp - oh mean(w_o dp oh))  (w_o NULL: dp)
+ *     dw_o = sum_t dp oh      dw_n = sum_t dn yh
+ *   dy     stream_dtype [T][lddy], or NULL (zeros; then dn is given)
+ *   dn     dtype [T][lddn], or NULL (no norm behind; then w_n and y are ignored)
+ *   o, w_o, gate, gates, w_n, scale, eps   as in the forward call
+ *   y      stream_dtype [T][ldy]: what the forward call wrote (or x, where it formed n alone with scale 1)
+ *   dx     stream_dtype [T][lddx], or NULL; may be dy itself with the same stride
+ *   d_o    dtype [T][lddo], or NULL
+ *   dw_o, dgate, dw_n   dtype or fp32 (g_dtype) [d], [gates][d], [d], each or NULL. accumulate != 0
+ *          (fp32 only, else MOE_EUNSUPPORTED) adds to what they hold. T == 0 writes zeros (or leaves them).
+ *   ws     moe_residual_norm_backward_workspace_bytes(T, d, gates) bytes, 256-byte aligned (needed with
+ *          dw_o, dgate or dw_n; gates 1 without gate); calls that may run at the same time need one each
+ * Column sums are added up in a fixed order. Errors as moe_residual_norm (a result without what it is
+ * formed from is MOE_EINVAL), and MOE_EWORKSPACE.
+ */
+size_t moe_residual_norm_backward_workspace_bytes(int32_t T, int32_t d, int32_t gates);
+int moe_residual_norm_backward(int32_t dtype, const void *dy, int64_t lddy, const void *dn, int64_t lddn, const void *o, int64_t ldo,
+                               const void *y, int64_t ldy, int32_t stream_dtype, int32_t T, int32_t d, const void *w_o,
+                               const void *gate, int32_t gates, const void *w_n, int32_t w_dtype, float scale, float eps, void *dx,
+                               int64_t lddx, void *d_o, int64_t lddo, void *dw_o, void *dgate, void *dw_n, int32_t g_dtype,
+                               int32_t accumulate, void *ws, size_t ws_bytes, hipStream_t stream);
+
 /* Static description of a status code. Never NULL. */
 const char *moe_status_string(int status);
 
