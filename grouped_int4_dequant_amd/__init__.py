@@ -21,7 +21,8 @@ from .binding import (ABLATIONS, ACTIVATIONS, GRAPH_CONCURRENT, Layer, LayerGrap
                       prefill_chunked, route, route_workspace_bytes, router_logits, router_topk, status_string,
                       prepared_bytes, workspace_bytes, workspace_layout, linear, linear_backward,
                       linear_backward_workspace_bytes, residual_norm, residual_norm_backward,
-                      residual_norm_backward_workspace_bytes)
+                      residual_norm_backward_workspace_bytes, MAX_FEW_PAIRS, MAX_FEW_TOKENS, few_tokens_layer,
+                      few_tokens_workspace_bytes)
 
 __all__ = ["ABLATIONS", "ACTIVATIONS", "GRAPH_CONCURRENT", "Layer", "LayerGraph", "ablation_workspace_bytes", "adapter_backward",
            "adapter_backward_workspace_bytes", "adapter_forward", "adapter_plan", "alloc_routing", "alloc_workspace",
@@ -31,4 +32,5 @@ __all__ = ["ABLATIONS", "ACTIVATIONS", "GRAPH_CONCURRENT", "Layer", "LayerGraph"
            "prefill_chunked", "route", "route_workspace_bytes", "router_logits", "router_topk", "status_string",
            "prepared_bytes", "workspace_bytes", "workspace_layout", "linear", "linear_backward",
            "linear_backward_workspace_bytes", "residual_norm", "residual_norm_backward",
-           "residual_norm_backward_workspace_bytes"]
+           "residual_norm_backward_workspace_bytes", "MAX_FEW_PAIRS", "MAX_FEW_TOKENS", "few_tokens_layer",
+           "few_tokens_workspace_bytes"]

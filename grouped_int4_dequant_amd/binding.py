@@ -47,6 +47,11 @@ class MoeWorkspaceLayoutT(ctypes.Structure):
                 ("dec_h", ctypes.c_int64)]
 
 
+class MoeLayer16T(ctypes.Structure):
+    _fields_ = [("dtype", _I32), ("d", _I32), ("f", _I32), ("E", _I32), ("k", _I32), ("f_sh", _I32),
+                ("gu", _P), ("dn", _P), ("sh_gu", _P), ("sh_dn", _P)]
+
+
 _lib = None
 
 
@@ -129,7 +134,10 @@ def load() -> ctypes.CDLL:
         lib.moe_residual_norm.argtypes = [I, _P, L, _P, L, I, I, I, _P, _P, I, _P, I, F, F, _P, L, _P, L, _P]
         lib.moe_residual_norm_backward.argtypes = [I, _P, L, _P, L, _P, L, _P, L, I, I, I, _P, _P, I, _P, I, F, F, _P, L, _P, L,
                                                    _P, _P, _P, I, I, _P, Z, _P]
-        for name in ("moe_linear", "moe_linear_backward", "moe_residual_norm", "moe_residual_norm_backward"):
+        lib.moe_few_tokens_layer.argtypes = [ctypes.POINTER(MoeLayer16T), _P, L, _P, I, _P, L, _P, I, L, _P, _P, _P, Z, _P]
+        lib.moe_few_tokens_workspace_bytes.argtypes = [ctypes.POINTER(MoeLayer16T), I]
+        lib.moe_few_tokens_workspace_bytes.restype = Z
+        for name in ("moe_linear", "moe_linear_backward", "moe_residual_norm", "moe_residual_norm_backward", "moe_few_tokens_layer"):
             getattr(lib, name).restype = ctypes.c_int
         for name in ("moe_linear_backward_workspace_bytes", "moe_residual_norm_backward_workspace_bytes"):
             getattr(lib, name).argtypes = [I, I, I]
@@ -1079,3 +1087,58 @@ def residual_norm_backward(dy: Optional[torch.Tensor], dn: Optional[torch.Tensor
       _ld(d_o, d), _ptr(grads[0]), _ptr(grads[1]), _ptr(grads[2]), _CODES[gtype] if need else c.code, int(accumulate), _ptr(ws) if need else None,
       ws.numel() * ws.element_size() if need else 0)
     return (dx, d_o, *grads)
+
+
+MAX_FEW_TOKENS, MAX_FEW_PAIRS = 64, 512
+
+
+def few_tokens_workspace_bytes(T: int, dtype: torch.dtype, d: int, f: int, E: int, k: int, f_sh: int = 0) -> int:
+    _sizes(T, d, f, E, k, f_sh)
+    L = MoeLayer16T(_CODES[dtype], d, f, E, k, f_sh, None, None, None, None)
+    return int(load().moe_few_tokens_workspace_bytes(ctypes.byref(L), T))
+
+
+def few_tokens_layer(x: torch.Tensor, logits: torch.Tensor, gu: torch.Tensor, dn: torch.Tensor, k: int,
+                     sh_gu: Optional[torch.Tensor] = None, sh_dn: Optional[torch.Tensor] = None, add: Optional[torch.Tensor] = None,
+                     out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                     topk_ids: Optional[torch.Tensor] = None, topk_w: Optional[torch.Tensor] = None,
+                     ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """moe_few_tokens_layer: the whole layer with 16-bit weights for at most
+    MAX_FEW_TOKENS tokens (and MAX_FEW_PAIRS picks), y = sum of the k picked
+    experts' FFN weighted by their gates + the shared expert's + add. x [T][d],
+    logits fp32 [T][E], gu [E][2f][d] (rows 0 .. f-1 the gate's), dn [E][d][f], sh_gu
+    [2 f_sh][d] and sh_dn [d][f_sh] (None: no shared expert), add of y's type [T][d]
+    (may be `out` itself). topk_ids int32 and topk_w fp32 [T][k] receive the picks
+    and their gates where given. Returns y [T][d]."""
+    c = _Call(x, "x", stream)
+    if x.dim() != 2 or not isinstance(gu, torch.Tensor) or gu.dim() != 3 or not isinstance(dn, torch.Tensor) or dn.dim() != 3:
+        raise ValueError("x must be [T][d], gu [E][2f][d] and dn [E][d][f]")
+    (T, d), (E, _, f) = x.shape, dn.shape
+    if (sh_gu is None) != (sh_dn is None):
+        raise ValueError("sh_gu and sh_dn are given together")
+    if sh_dn is not None and (not isinstance(sh_dn, torch.Tensor) or sh_dn.dim() != 2):
+        raise ValueError("sh_gu must be [2 f_sh][d] and sh_dn [d][f_sh]")
+    f_sh = 0 if sh_dn is None else sh_dn.shape[1]
+    _sizes(T, d, f, E, k, f_sh)
+    c.rows(x, "x", (T, d))
+    c.need(logits, "logits", torch.float32, (T, E))
+    c.need(gu, "gu", c.dtype, (E, 2 * f, d))
+    c.need(dn, "dn", c.dtype, (E, d, f))
+    if f_sh:
+        c.need(sh_gu, "sh_gu", c.dtype, (2 * f_sh, d))
+        c.need(sh_dn, "sh_dn", c.dtype, (d, f_sh))
+    if add is not None:
+        c.rows(add, "add", (T, d), torch.float32)
+        out_dtype = add.dtype if out_dtype is None and out is None else out_dtype
+    if topk_ids is not None:
+        c.need(topk_ids, "topk_ids", torch.int32, (T, k))
+    if topk_w is not None:
+        c.need(topk_w, "topk_w", torch.float32, (T, k))
+    y = c.result(out, "out", (T, d), out_dtype)
+    if add is not None and add.dtype != y.dtype:
+        raise TypeError(f"add must be {y.dtype} like the result, got {add.dtype}")
+    L = MoeLayer16T(c.code, d, f, E, k, f_sh, gu.data_ptr(), dn.data_ptr(), _ptr(sh_gu), _ptr(sh_dn))
+    ws = c.workspace(ws, int(load().moe_few_tokens_workspace_bytes(ctypes.byref(L), T)))
+    c("moe_few_tokens_layer", ctypes.byref(L), x.data_ptr(), _ld(x, d), logits.data_ptr(), T, _ptr(add), _ld(add, d), y.data_ptr(),
+      _CODES[y.dtype], _ld(y, d), _ptr(topk_ids), _ptr(topk_w), ws.data_ptr(), ws.numel() * ws.element_size())
+    return y

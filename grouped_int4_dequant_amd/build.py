@@ -17,7 +17,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmoe_int4.so")
 SOURCES = ["moe_api.hip", "routing_kernels.hip", "gemm_kernels.hip", "gemm_kernels_small.hip", "decode_kernels.hip",
            "router_kernels.hip", "grouped_api.hip", "grouped_kernels.hip", "combine_kernels.hip", "adapter_kernels.hip",
-           "block_api.hip", "norm_kernels.hip", "linear_kernels.hip"]
+           "block_api.hip", "norm_kernels.hip", "linear_kernels.hip", "few_layer_kernels.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -9,15 +9,27 @@ using namespace moe;
 
 namespace {
 
+constexpr int32_t kMaxFewWidth = 1 << 20;
+
 size_t pad256(size_t n) { return (n + 255) & ~(size_t)255; }
 // dz, then the chunks' column sums
 size_t dz_bytes(int32_t T, int32_t N, int32_t act) { return act == MOE_ACT_NONE ? 0 : pad256((size_t)T * N * 2); }
+// inner values of the few-token layer: 6 bytes each (three 16-bit parts, or fp32) in rows of whole 16-byte units
+int32_t inner_pitch(int32_t f) { return (f + 7) / 8 * 8; }
+size_t inner_bytes(int32_t rows, int32_t f) { return pad256((size_t)rows * inner_pitch(f) * 6); }
 int64_t sums_pitch(int32_t n) { return ((int64_t)n + 7) / 8 * 8; }
 
 int check_linear(int32_t dtype, int32_t T, int32_t N, int32_t K, int32_t act) {
   if (!is16(dtype) || T < 0 || N < 1 || K < 1 || act < MOE_ACT_NONE || act > MOE_ACT_GEGLU) return MOE_EINVAL;
   if (is_gated(act) && N % 2 != 0) return MOE_EINVAL;
   if (T > kMaxExtent || N > kMaxExtent || K > kMaxExtent) return MOE_EUNSUPPORTED;
+  return MOE_OK;
+}
+
+int check_layer16(const moe_layer16_t *L, int32_t T) {
+  if (!L || !is16(L->dtype) || L->d < 1 || L->f < 1 || L->E < 1 || L->k < 1 || L->k > L->E || L->f_sh < 0 || T < 0) return MOE_EINVAL;
+  if (L->E > MOE_MAX_EXPERTS || L->k > 64 || T > kFewTokens || T * L->k > kFewPairs) return MOE_EUNSUPPORTED;
+  if (L->d > kMaxFewWidth || L->f > kMaxFewWidth || L->f_sh > kMaxFewWidth) return MOE_EUNSUPPORTED;
   return MOE_OK;
 }
 
@@ -252,6 +264,49 @@ int moe_residual_norm_backward(int32_t dtype, const void *dy, int64_t lddy, cons
   a.per_gate = c.per_gate;
   if (T == 0) a.per_gate = 0;
   return status(launch_norm_grad(a, dtype == MOE_FP16, stream));
+}
+
+size_t moe_few_tokens_workspace_bytes(const moe_layer16_t *L, int32_t T) {
+  if (check_layer16(L, T) != MOE_OK) return 0;
+  return pad256(sizeof(FewPlan)) + inner_bytes(T * L->k, L->f) + inner_bytes(T, L->f_sh);
+}
+
+int moe_few_tokens_layer(const moe_layer16_t *L, const void *x, int64_t ldx, const float *logits, int32_t T, const void *add,
+                         int64_t ldadd, void *y, int32_t y_dtype, int64_t ldy, int32_t *topk_ids, float *topk_w, void *ws,
+                         size_t ws_bytes, hipStream_t stream) {
+  const int st = check_layer16(L, T);
+  if (st != MOE_OK) return st;
+  if (!out_type(y_dtype, L->dtype) || ldx < L->d || ldy < L->d || (add && ldadd < L->d)) return MOE_EINVAL;
+  if (T == 0) return MOE_OK;
+  if (!x || !logits || !y || !L->gu || !L->dn || !typed(x, L->dtype) || !aligned(logits, 4) || !typed(y, y_dtype)) return MOE_EINVAL;
+  if (!typed(L->gu, L->dtype) || !typed(L->dn, L->dtype) || !typed(add, y_dtype) || !aligned(topk_ids, 4) || !aligned(topk_w, 4)) return MOE_EINVAL;
+  if (L->f_sh > 0 && (!L->sh_gu || !L->sh_dn || !typed(L->sh_gu, L->dtype) || !typed(L->sh_dn, L->dtype))) return MOE_EINVAL;
+  if (add == y && T > 1 && ldadd != ldy) return MOE_EINVAL;
+  if (ws_bytes < moe_few_tokens_workspace_bytes(L, T)) return MOE_EWORKSPACE;
+  if (!ws || !aligned(ws, 256)) return MOE_EINVAL;
+  FewArgs a{};
+  a.x = static_cast<const uint16_t *>(x);
+  a.ld_x = ldx;
+  a.logits = logits;
+  a.T = T; a.d = L->d; a.f = L->f; a.f_sh = L->f_sh; a.E = L->E; a.k = L->k;
+  a.gu = static_cast<const uint16_t *>(L->gu);
+  a.dn = static_cast<const uint16_t *>(L->dn);
+  a.sh_gu = static_cast<const uint16_t *>(L->sh_gu);
+  a.sh_dn = static_cast<const uint16_t *>(L->sh_dn);
+  a.add = add;
+  a.ld_add = ldadd;
+  a.y = y;
+  a.y_f32 = y_dtype == MOE_FP32;
+  a.ld_y = ldy;
+  a.topk_ids = topk_ids;
+  a.topk_w = topk_w;
+  char *p = static_cast<char *>(ws);
+  a.plan = reinterpret_cast<FewPlan *>(p);
+  a.h = p + pad256(sizeof(FewPlan));
+  a.h_sh = p + pad256(sizeof(FewPlan)) + inner_bytes(T * L->k, L->f);
+  a.pitch = inner_pitch(L->f);
+  a.pitch_sh = inner_pitch(L->f_sh);
+  return status(launch_few_layer(a, L->dtype == MOE_FP16, stream));
 }
 
 }  // extern "C"

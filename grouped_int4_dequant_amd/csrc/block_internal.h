@@ -70,6 +70,35 @@ struct ActGradArgs {
 struct ColumnChunks { int32_t rows, count; };
 ColumnChunks column_chunks(int32_t T, int32_t cols);
 
+// The layer for a few tokens: y[t] = sum_j g_j W_dn (silu(W_g x) * (W_u x)) + shared + add
+constexpr int kFewTokens = MOE_MAX_FEW_TOKENS, kFewPairs = MOE_MAX_FEW_PAIRS;
+// What the first kernel leaves for the second, at the workspace's begin: pairs (token, slot) sorted by expert.
+struct FewPlan {
+  int32_t used;                      // distinct experts
+  int32_t expert[kFewPairs];
+  int32_t start[kFewPairs + 1];      // first sorted pair of each
+  int32_t pair[kFewPairs];           // token * k + slot
+  float gate[kFewPairs];             // by pair
+};
+struct FewArgs {
+  const uint16_t *x;
+  int64_t ld_x;
+  const float *logits;               // [T][E]
+  int32_t T, d, f, f_sh, E, k;
+  const uint16_t *gu, *dn, *sh_gu, *sh_dn;  // [E][2f][d], [E][d][f], [2 f_sh][d], [d][f_sh]
+  const void *add;                   // nullable, of y's type
+  int64_t ld_add;
+  void *y;
+  int32_t y_f32;
+  int64_t ld_y;
+  int32_t *topk_ids;                 // nullable [T][k]
+  float *topk_w;                     // nullable [T][k]
+  FewPlan *plan;                     // workspace
+  void *h, *h_sh;                    // workspace: by pair and by token, see the kernels
+  int32_t pitch, pitch_sh;           // row pitch of h and h_sh in elements
+};
+hipError_t launch_few_layer(const FewArgs &a, bool fp16, hipStream_t s);
+
 template <bool Gated>
 hipError_t launch_linear(const LinearArgs<Gated> &a, bool fp16, hipStream_t s);
 hipError_t launch_act_grad(const ActGradArgs &a, bool fp16, hipStream_t s);

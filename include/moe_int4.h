@@ -746,6 +746,39 @@ int moe_residual_norm_backward(int32_t dtype, const void *dy, int64_t lddy, cons
                                int64_t lddx, void *d_o, int64_t lddo, void *dw_o, void *dgate, void *dw_n, int32_t g_dtype,
                                int32_t accumulate, void *ws, size_t ws_bytes, hipStream_t stream);
 
+#define MOE_MAX_FEW_TOKENS 64
+#define MOE_MAX_FEW_PAIRS 512
+
+/*
+ * A mixture-of-experts layer with 16-bit weights for a few tokens (a decode batch), in two kernels:
+ *     y[t] = sum_j g[t][j] FFN_(ids[t][j])(x[t]) + FFN_shared(x[t]) + add[t]
+ *     FFN(v) = W_dn (silu(W_gu[0:f] v) * (W_gu[f:2f] v))
+ * with ids and g the k picked experts and their gates as moe_route derives them from the logits.
+ *   L         dtype MOE_BF16 or MOE_FP16; gu [E][2f][d], dn [E][d][f]; sh_gu [2 f_sh][d] and
+ *             sh_dn [d][f_sh] of the shared expert, ignored with f_sh == 0 (none). Any widths.
+ *   x         dtype [T][ldx]; logits fp32 [T][E], contiguous
+ *   add       of y's type [T][ldadd], or NULL; may be y itself with the same stride
+ *   y         dtype or fp32 (y_dtype) [T][ldy]
+ *   topk_ids, topk_w   int32 and fp32 [T][k]: the picks, or NULL (not wanted)
+ *   ws        moe_few_tokens_workspace_bytes(L, T) bytes, 256-byte aligned; calls that may run at
+ *             the same time, in replayed graphs too, need one each
+ * Each picked expert's weights are read once for all its tokens. The products of x and of
+ * FFN's inner values are summed in fp32; the inner values are held in fp32 and enter the second product
+ * whole (in bf16 as three 16-bit parts, whose bits below 2^-133 are lost). The k experts are added in slot
+ * order, then the shared one, then `add`. A row's result does not depend on the other rows of the call.
+ * Errors: MOE_EINVAL (null or misaligned pointer, unknown type, T < 0, a size < 1, f_sh < 0, k > E, a stride
+ * below the width), MOE_EUNSUPPORTED (E > MOE_MAX_EXPERTS, k > 64, T > MOE_MAX_FEW_TOKENS,
+ * T * k > MOE_MAX_FEW_PAIRS, d, f or f_sh above 2^20), MOE_EWORKSPACE, MOE_EHIP. T == 0 enqueues nothing.
+ */
+typedef struct moe_layer16 {
+  int32_t dtype, d, f, E, k, f_sh;
+  const void *gu, *dn, *sh_gu, *sh_dn;
+} moe_layer16_t;
+size_t moe_few_tokens_workspace_bytes(const moe_layer16_t *L, int32_t T);
+int moe_few_tokens_layer(const moe_layer16_t *L, const void *x, int64_t ldx, const float *logits, int32_t T, const void *add,
+                         int64_t ldadd, void *y, int32_t y_dtype, int64_t ldy, int32_t *topk_ids, float *topk_w, void *ws,
+                         size_t ws_bytes, hipStream_t stream);
+
 /* Static description of a status code. Never NULL. */
 const char *moe_status_string(int status);
 
