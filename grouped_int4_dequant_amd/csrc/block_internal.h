@@ -72,11 +72,11 @@ ColumnChunks column_chunks(int32_t T, int32_t cols);
 
 // The layer for a few tokens: y[t] = sum_j g_j W_dn (silu(W_g x) * (W_u x)) + shared + add
 constexpr int kFewTokens = MOE_MAX_FEW_TOKENS, kFewPairs = MOE_MAX_FEW_PAIRS;
-// What the first kernel leaves for the second, at the workspace's begin: pairs (token, slot) sorted by expert.
+// What the first kernel leaves for the second, at the workspace's begin: the pairs (token, slot) sorted by
+// expert and cut into blocks of at most 16 pairs of one expert.
 struct FewPlan {
-  int32_t used;                      // distinct experts
-  int32_t expert[kFewPairs];
-  int32_t start[kFewPairs + 1];      // first sorted pair of each
+  int32_t blocks;
+  int32_t expert[kFewPairs], first[kFewPairs], rows[kFewPairs];  // of each block; first: its first sorted pair
   int32_t pair[kFewPairs];           // token * k + slot
   float gate[kFewPairs];             // by pair
 };
@@ -96,6 +96,7 @@ struct FewArgs {
   FewPlan *plan;                     // workspace
   void *h, *h_sh;                    // workspace: by pair and by token, see the kernels
   int32_t pitch, pitch_sh;           // row pitch of h and h_sh in elements
+  int32_t share;                     // gate/up: log2 of the waves that share an item
 };
 hipError_t launch_few_layer(const FewArgs &a, bool fp16, hipStream_t s);
 

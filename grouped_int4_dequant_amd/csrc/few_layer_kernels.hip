@@ -6,14 +6,16 @@
 //
 // A decode batch has little use of each weight, so the bytes of the picked experts set the time.
 //   gate/up  every workgroup repeats the top-k (a token a wave) and sorts the pairs (token,
-//            slot) by expert in LDS; the first one leaves that for the second kernel. Then it walks
-//            over items of 8 columns of h of one expert (or the shared one): 16 rows of W_gu,
-//            eight of the gate and the eight that it multiplies, whose sums its eight waves share and join
-//            in LDS, in order.
-//   down     a workgroup owns 16 columns of y. Its waves take one expert after the other; what an
-//            expert gives each of its pairs goes to LDS, and is added up there by token in slot order.
-// Weights go straight from memory to operand registers and are read once; a matrix instruction
-// takes 16 rows of W and up to 16 pairs (an expert with more reads its weights again from L2).
+//            slot) by expert in LDS, in blocks of at most 16 pairs of one expert; the first one leaves that for
+//            the second kernel. Then it walks over items of 8 columns of h of one block: 16 rows of W_gu,
+//            eight of the gate and the eight that it multiplies. One to eight waves share an item's sum
+//            and join in LDS, in order; the next item's weights are requested before that.
+//   down     a workgroup owns 8 columns of y, its waves take one block after the other. The 16 operand
+//            rows of a matrix instruction are the 8 columns over the first and the second half of the sum, against
+//            up to eight pairs' halves, so that d / 8 workgroups fill the CUs. What a block gives each of its pairs
+//            goes to LDS, and is added up there by token in slot order.
+// Weights go straight from memory to operand registers and are read once (an expert of more than 16
+// pairs again for each 16, from L2).
 
 #include "block_device.h"
 #include "topk_device.h"
@@ -23,7 +25,8 @@
 namespace moe {
 namespace {
 
-constexpr int kWaves = 8;
+constexpr int kWaves = 8;   // of a gate/up workgroup
+constexpr int kDeep = 8;    // 16-byte requests of a lane in flight
 
 // Runs of eight 16-bit values; without Vec rows may end inside one.
 template <bool Vec>
@@ -36,13 +39,21 @@ __device__ __forceinline__ s8 load_w(const uint16_t *p, int left) {
   }
 }
 
+// A barrier that leaves loads from memory in flight.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 struct FewLds {
-  int32_t count[MOE_MAX_EXPERTS];    // pairs of each expert, then its place among the picked ones
+  uint64_t tokens[MOE_MAX_EXPERTS];  // of each expert, a bit a token (kFewTokens of them; a token picks an expert once)
   int32_t ids[kFewPairs];
   float gate[kFewPairs];
-  int32_t expert[kFewPairs], start[kFewPairs + 1], pair[kFewPairs];
-  int32_t fill[kFewPairs];
-  int32_t used;
+  int32_t expert[kFewPairs], first[kFewPairs], rows[kFewPairs], pair[kFewPairs];
+  int32_t start[MOE_MAX_EXPERTS];    // each expert's first sorted pair
+  int32_t blocks;
 };
 
 // Top-k of all tokens and the pairs sorted by expert, by one workgroup.
@@ -50,11 +61,16 @@ template <int VPL>
 __device__ __forceinline__ void make_plan(const FewArgs &a, FewLds &s) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int pairs = a.T * a.k;
-  for (int e = tid; e < a.E; e += 64 * kWaves) s.count[e] = 0;
+  for (int e = tid; e < a.E; e += 64 * kWaves) s.tokens[e] = 0;
+  float v[VPL], next[VPL];
+  if (wave < a.T) topk_load<VPL>(a.logits + (int64_t)wave * a.E, a.E, lane, next);
   for (int t = wave; t < a.T; t += kWaves) {
     int id;
     float g;
-    topk_wave<VPL>(a.logits + (int64_t)t * a.E, a.E, a.k, lane, id, g);
+#pragma unroll
+    for (int r = 0; r < VPL; ++r) v[r] = next[r];
+    if (t + kWaves < a.T) topk_load<VPL>(a.logits + (int64_t)(t + kWaves) * a.E, a.E, lane, next);
+    topk_values<VPL>(v, a.E, a.k, lane, id, g);
     if (lane < a.k) {
       s.ids[t * a.k + lane] = id;
       s.gate[t * a.k + lane] = g;
@@ -63,15 +79,17 @@ __device__ __forceinline__ void make_plan(const FewArgs &a, FewLds &s) {
   __syncthreads();
   // (kFewPairs is the number of threads)
   const int mine = tid < pairs ? s.ids[tid] : -1;
-  if (mine >= 0) atomicAdd(&s.count[mine], 1);
+  const uint64_t bit = 1ull << (tid / a.k & 63);
+  if (mine >= 0) atomicOr(reinterpret_cast<unsigned long long *>(&s.tokens[mine]), (unsigned long long)bit);
   __syncthreads();
   if (wave == 0) {
-    // lane l has the experts of its run: their number and pairs, then what lies before it
+    // lane l has the experts of its run: their blocks and pairs, then what lies before it
     const int run = (a.E + 63) >> 6, e0 = min(lane * run, a.E), e1 = min(e0 + run, a.E);
     int n = 0, p = 0;
     for (int e = e0; e < e1; ++e) {
-      n += s.count[e] > 0;
-      p += s.count[e];
+      const int c = __popcll(s.tokens[e]);
+      n += (c + 15) >> 4;
+      p += c;
     }
     int ns = n, ps = p;
 #pragma unroll
@@ -82,24 +100,21 @@ __device__ __forceinline__ void make_plan(const FewArgs &a, FewLds &s) {
         ps += y;
       }
     }
-    if (lane == 63) {
-      s.used = ns;
-      s.start[ns] = ps;
-    }
-    int u = ns - n, at = ps - p;
+    if (lane == 63) s.blocks = ns;
+    int b = ns - n, at = ps - p;
     for (int e = e0; e < e1; ++e) {
-      const int c = s.count[e];
-      if (c == 0) continue;
-      s.expert[u] = e;
-      s.start[u] = at;
-      s.fill[u] = at;
-      s.count[e] = u++;
-      at += c;
+      s.start[e] = at;
+      for (int left = __popcll(s.tokens[e]); left > 0; left -= 16) {
+        s.expert[b] = e;
+        s.first[b] = at;
+        s.rows[b++] = min(left, 16);
+        at += min(left, 16);
+      }
     }
   }
   __syncthreads();
-  // the order of an expert's pairs is of no consequence: each is a column of its own in the matrix instructions
-  if (mine >= 0) s.pair[atomicAdd(&s.fill[s.count[mine]], 1)] = tid;
+  // an expert's pairs by ascending token: every workgroup has to cut them into the same blocks
+  if (mine >= 0) s.pair[s.start[mine] + __popcll(s.tokens[mine] & (bit - 1))] = tid;
   __syncthreads();
   if (blockIdx.x != 0) return;
   if (tid < pairs) {
@@ -108,15 +123,34 @@ __device__ __forceinline__ void make_plan(const FewArgs &a, FewLds &s) {
     if (a.topk_ids) a.topk_ids[tid] = mine;
     if (a.topk_w) a.topk_w[tid] = s.gate[tid];
   }
-  if (tid < s.used) a.plan->expert[tid] = s.expert[tid];
-  if (tid <= s.used) a.plan->start[tid] = s.start[tid];
-  if (tid == 0) {
-    a.plan->used = s.used;
-    a.plan->start[s.used] = s.start[s.used];
+  if (tid < s.blocks) {
+    a.plan->expert[tid] = s.expert[tid];
+    a.plan->first[tid] = s.first[tid];
+    a.plan->rows[tid] = s.rows[tid];
   }
+  if (tid == 0) a.plan->blocks = s.blocks;
 }
 
-// Inner values. bf16: three parts that add up to the fp32 value, each an array of `rows` rows;
+// One token: its picks are the blocks.
+template <int VPL>
+__device__ __forceinline__ void make_plan_one(const FewArgs &a, FewLds &s) {
+  if (threadIdx.x < 64) {
+    const int lane = threadIdx.x;
+    int id;
+    float g;
+    topk_wave<VPL>(a.logits, a.E, a.k, lane, id, g);
+    if (lane < a.k) s.expert[lane] = id;
+    if (blockIdx.x == 0 && lane < a.k) {
+      a.plan->expert[lane] = id;
+      a.plan->gate[lane] = g;
+      if (a.topk_ids) a.topk_ids[lane] = id;
+      if (a.topk_w) a.topk_w[lane] = g;
+    }
+  }
+  __syncthreads();
+}
+
+// Inner values. bf16: three parts that add up to the fp32 value, each an array of its own;
 // fp16: fp32 (its parts would leave fp16's range).
 template <typename Tr>
 __device__ __forceinline__ void store_inner(void *h, int64_t part, int64_t at, f4 v, int left) {
@@ -146,64 +180,101 @@ __device__ __forceinline__ void store_inner(void *h, int64_t part, int64_t at, f
 
 __device__ __forceinline__ float silu_of(float z) { return z * sigmoid_of(z).s; }
 
-template <typename Tr, int VPL, bool Vec>
+// One: a single token.
+template <typename Tr, int VPL, bool Vec, bool One>
 __global__ __launch_bounds__(64 * kWaves) void few_gate_up_kernel(FewArgs a) {
   __shared__ FewLds s;
   __shared__ __attribute__((aligned(16))) f4 s_part[2][kWaves][64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int p16 = lane & 15, q4 = lane >> 4;
-  make_plan<VPL>(a, s);
+  if constexpr (One) make_plan_one<VPL>(a, s);
+  else make_plan<VPL>(a, s);
   const int per = (a.f + 7) / 8, per_sh = (a.f_sh + 7) / 8;
-  const int items = s.used * per + per_sh;
-  int buf = 0;
-  for (int item = blockIdx.x; item < items; item += gridDim.x) {
-    // the shared expert's items come first
-    const bool shared = item < per_sh;
-    const int u = shared ? 0 : (item - per_sh) / per;
-    const int c0 = 8 * (shared ? item : item - per_sh - u * per), f = shared ? a.f_sh : a.f;
-    const uint16_t *W = shared ? a.sh_gu : a.gu + (int64_t)s.expert[u] * 2 * a.f * a.d;
-    const int col = c0 + (p16 & 7);
-    const uint16_t *w = W + (int64_t)(min(col, f - 1) + (p16 & 8 ? f : 0)) * a.d;  // columns past the last repeat it
-    const int first = shared ? 0 : s.start[u], rows = shared ? a.T : s.start[u + 1] - first;
-    for (int r0 = 0; r0 < rows; r0 += 16) {
-      const bool ok = r0 + p16 < rows;
-      const int pair = !ok ? 0 : shared ? r0 + p16 : s.pair[first + r0 + p16];
-      const uint16_t *x = a.x + (int64_t)(shared ? pair : pair / a.k) * a.ld_x;
-      f4 acc = {0.f, 0.f, 0.f, 0.f};
-      constexpr int kDeep = 8;
-      for (int k0 = 32 * wave; k0 < a.d; k0 += 32 * kWaves * kDeep) {
-        s8 wv[kDeep], xv[kDeep];
+  const int blocks_sh = a.f_sh > 0 ? (a.T + 15) / 16 : 0;
+  const int items_sh = blocks_sh * per_sh, items = items_sh + (One ? a.k : s.blocks) * per;
+  // the waves of a workgroup take kWaves >> share items at a time; `sub` has n steps of 32 k of the sum, from kb on
+  const int slots = kWaves >> a.share, slot = wave >> a.share, sub = wave & ((1 << a.share) - 1);
+  const int n = (((a.d + 31) >> 5) + (1 << a.share) - 1) >> a.share;
+  const int kb = 32 * n * sub + 8 * q4, kend = min(a.d, 32 * n * (sub + 1));
+
+  struct Where {
+    const uint16_t *w, *x;
+    int c0, pair;  // first column; the lane's pair (token, if shared), -1: none
+    bool shared;
+  };
+  auto locate = [&](int item) __attribute__((always_inline)) {
+    Where t;
+    t.shared = item < items_sh;  // the shared expert's items come first
+    const int i = t.shared ? item : item - items_sh, each = t.shared ? per_sh : per;
+    const int b = i / each, f = t.shared ? a.f_sh : a.f;
+    t.c0 = 8 * (i - b * each);
+    const bool ok = item < items;
+    const uint16_t *W = t.shared ? a.sh_gu : a.gu + (int64_t)(ok ? s.expert[b] : 0) * 2 * a.f * a.d;
+    t.w = W + (int64_t)(min(t.c0 + (p16 & 7), f - 1) + (p16 & 8 ? f : 0)) * a.d;  // columns past the last repeat it
+    t.pair = -1;
+    if (One) {
+      if (p16 == 0 && ok) t.pair = t.shared ? 0 : b;
+    } else if (t.shared) {
+      if (16 * b + p16 < a.T) t.pair = 16 * b + p16;
+    } else if (ok && p16 < s.rows[b]) {
+      t.pair = s.pair[s.first[b] + p16];
+    }
+    t.x = a.x + (int64_t)(One || t.pair < 0 ? 0 : t.shared ? t.pair : t.pair / a.k) * a.ld_x;
+    return t;
+  };
+  s8 wv[kDeep], xv[kDeep];
+  auto request = [&](const Where &t, int y0, int item) __attribute__((always_inline)) {
 #pragma unroll
-        for (int y = 0; y < kDeep; ++y) {
-          const int k = k0 + 32 * kWaves * y + 8 * q4;
-          wv[y] = load_w<Vec>(w + k, a.d - k);
-        }
+    for (int y = 0; y < kDeep; ++y) {
+      const int k = kb + 32 * (y0 + y);
+      wv[y] = load_w<Vec>(t.w + k, item < items ? kend - k : 0);
+    }
 #pragma unroll
-        for (int y = 0; y < kDeep; ++y) {
-          const int k = k0 + 32 * kWaves * y + 8 * q4;
-          xv[y] = load_w<Vec>(x + k, ok ? a.d - k : 0);
-        }
+    for (int y = 0; y < kDeep; ++y) {
+      const int k = kb + 32 * (y0 + y);
+      xv[y] = load_w<Vec>(t.x + k, t.pair >= 0 ? kend - k : 0);
+    }
+  };
+  const int rounds = (items + slots - 1) / slots;
+  int buf = 0, round = blockIdx.x;
+  if (round >= rounds) return;
+  Where at = locate(round * slots + slot);
+  request(at, 0, round * slots + slot);
+  for (; round < rounds; round += gridDim.x) {
+    const int item = round * slots + slot;
+    f4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int y = 0; y < kDeep; ++y) acc = Tr::mfma(wv[y], xv[y], acc);
-      }
+    for (int y = 0; y < kDeep; ++y) acc = Tr::mfma(wv[y], xv[y], acc);
+    for (int y0 = kDeep; y0 < n; y0 += kDeep) {
+      request(at, y0, item);
+#pragma unroll
+      for (int y = 0; y < kDeep; ++y) acc = Tr::mfma(wv[y], xv[y], acc);
+    }
+    const Where done = at;
+    if (round + (int)gridDim.x < rounds) {
+      at = locate(item + gridDim.x * slots);
+      request(at, 0, item + gridDim.x * slots);
+    }
+    if (a.share > 0) {
       s_part[buf][wave][lane] = acc;
-      __syncthreads();
-      if (wave == (item & (kWaves - 1))) {
-        f4 v = s_part[buf][0][lane];
-#pragma unroll
-        for (int y = 1; y < kWaves; ++y) v += s_part[buf][y][lane];
-        // lane: pair p16; rows 4 q4 .. of the 16: columns 4 q4 .. of the gate, and behind them what it multiplies
-        f4 h;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = silu_of(v[i]) * __shfl(v[i], (lane + 32) & 63);
-        const int c = c0 + 4 * q4;
-        if (ok && q4 < 2 && c < f) {
-          if (shared) store_inner<Tr>(a.h_sh, (int64_t)a.T * a.pitch_sh, (int64_t)pair * a.pitch_sh + c, h, f - c);
-          else store_inner<Tr>(a.h, (int64_t)a.T * a.k * a.pitch, (int64_t)pair * a.pitch + c, h, f - c);
-        }
+      lds_barrier();
+      if (sub == 0) {
+        acc = s_part[buf][wave][lane];
+        for (int y = 1; y < 1 << a.share; ++y) acc += s_part[buf][wave + y][lane];
       }
-      buf ^= 1;  // a wave may fill the next one while its last reader is at work; the barrier behind that ends both
+      buf ^= 1;  // the next sums may be written while these are read; the barrier behind them ends both
+    }
+    if (sub == 0 && item < items) {
+      // lane: pair p16; rows 4 q4 .. of the 16: columns 4 q4 .. of the gate, and behind them what it multiplies
+      f4 h;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[i] = silu_of(acc[i]) * __shfl(acc[i], (lane + 32) & 63);
+      const int c = done.c0 + 4 * q4, left = (done.shared ? a.f_sh : a.f) - c;
+      if (done.pair >= 0 && q4 < 2 && left > 0) {
+        if (done.shared) store_inner<Tr>(a.h_sh, (int64_t)a.T * a.pitch_sh, (int64_t)done.pair * a.pitch_sh + c, h, left);
+        else store_inner<Tr>(a.h, (int64_t)a.T * a.k * a.pitch, (int64_t)done.pair * a.pitch + c, h, left);
+      }
     }
   }
 }
@@ -237,52 +308,104 @@ struct Inner<Fp16, Vec> {
   }
 };
 
+// As many waves as there are blocks, 4 to 16.
 template <typename Tr, bool Vec>
-__global__ __launch_bounds__(64 * kWaves) void few_down_kernel(FewArgs a) {
-  constexpr int kPitch = 20;  // floats a row of s_o: 16 and a gap that keeps rows off each other's banks
+__global__ __launch_bounds__(1024) void few_down_kernel(FewArgs a) {
+  constexpr int kPitch = 12;  // floats a row of s_o: 8 and a gap that keeps rows off each other's banks
   __shared__ __attribute__((aligned(16))) float s_o[(kFewPairs + kFewTokens) * kPitch];
-  const int tid = threadIdx.x, lane = tid & 63;
+  __shared__ float s_gate[kFewPairs];
+  const int tid = threadIdx.x, lane = tid & 63, waves = blockDim.x >> 6;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int p16 = lane & 15, q4 = lane >> 4;
-  const int n0 = 16 * blockIdx.x, pairs = a.T * a.k;
-  const int row = min(n0 + p16, a.d - 1);  // rows past the last repeat it
-  const int used = a.plan->used, items = used + (a.f_sh > 0);
-  for (int u = wave; u < items; u += kWaves) {
-    const bool shared = u == used;
-    const int f = shared ? a.f_sh : a.f, pitch = shared ? a.pitch_sh : a.pitch;
-    const uint16_t *w = (shared ? a.sh_dn : a.dn + (int64_t)a.plan->expert[u] * a.d * a.f) + (int64_t)row * f;
-    const void *h = shared ? a.h_sh : a.h;
-    const int first = shared ? 0 : a.plan->start[u], rows = shared ? a.T : a.plan->start[u + 1] - first;
-    const int64_t part = (int64_t)(shared ? a.T : pairs) * pitch;
-    for (int r0 = 0; r0 < rows; r0 += 16) {
-      const bool ok = r0 + p16 < rows;
-      const int pair = !ok ? 0 : shared ? r0 + p16 : a.plan->pair[first + r0 + p16];
-      f4 acc = {0.f, 0.f, 0.f, 0.f};
-      constexpr int kDeep = 8;
-      for (int k0 = 0; k0 < f; k0 += 32 * kDeep) {
-        s8 wv[kDeep];
+  const int p16 = lane & 15, q4 = lane >> 4, p8 = p16 & 7;
+  const int n0 = 8 * blockIdx.x, pairs = a.T * a.k;
+  const int row = min(n0 + p8, a.d - 1);  // rows past the last repeat it
+  const bool one = a.T == 1;
+  const int blocks = one ? a.k : a.plan->blocks, blocks_sh = a.f_sh > 0 ? (a.T + 15) / 16 : 0;
+
+  struct Where {
+    const uint16_t *w;
+    const void *h;
+    int64_t part;
+    int kb, kend, n;  // the lane's half of the sum, and its steps of 32
+    int pitch, pair[2], rows;  // the lane's pairs of the block's first and second eight
+    bool shared;
+  };
+  auto locate = [&](int b) __attribute__((always_inline)) {
+    Where t;
+    t.shared = b >= blocks;
+    const int f = t.shared ? a.f_sh : a.f, half = ((f + 63) >> 6) * 32;
+    t.n = half >> 5;
+    t.kb = (p16 & 8 ? half : 0) + 8 * q4;
+    t.kend = p16 & 8 ? f : min(half, f);
+    t.pitch = t.shared ? a.pitch_sh : a.pitch;
+    t.h = t.shared ? a.h_sh : a.h;
+    t.part = (int64_t)(t.shared ? a.T : pairs) * t.pitch;
+    t.w = (t.shared ? a.sh_dn : a.dn + (int64_t)a.plan->expert[b] * a.d * a.f) + (int64_t)row * f;
+    const int first = t.shared ? 16 * (b - blocks) : one ? b : a.plan->first[b];
+    t.rows = t.shared ? min(a.T - first, 16) : one ? 1 : a.plan->rows[b];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int r = 8 * x + p8;
+      t.pair[x] = r >= t.rows ? -1 : t.shared || one ? first + r : a.plan->pair[first + r];
+    }
+    return t;
+  };
+  s8 wv[kDeep];
+  auto request = [&](const Where &t, int y0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int y = 0; y < kDeep; ++y) {
+      const int k = t.kb + 32 * (y0 + y);
+      wv[y] = load_w<Vec>(t.w + k, t.kend - k);
+    }
+  };
+  int b = wave;
+  Where at{};
+  if (b < blocks + blocks_sh) {
+    at = locate(b);
+    request(at, 0);
+  }
+  for (int i = tid; i < pairs; i += blockDim.x) s_gate[i] = a.plan->gate[i];
+  while (b < blocks + blocks_sh) {
+    f4 acc[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) acc[x] = f4{0.f, 0.f, 0.f, 0.f};
+    for (int y0 = 0; y0 < at.n; y0 += kDeep) {
+      if (y0 > 0) request(at, y0);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (8 * x >= at.rows) break;
 #pragma unroll
         for (int y = 0; y < kDeep; ++y) {
-          const int k = k0 + 32 * y + 8 * q4;
-          wv[y] = load_w<Vec>(w + k, f - k);
-        }
-#pragma unroll
-        for (int y = 0; y < kDeep; ++y) {
-          const int k = k0 + 32 * y + 8 * q4;
+          const int k = at.kb + 32 * (y0 + y);
           Inner<Tr, Vec> hv;
-          hv.load(h, part, (int64_t)pair * pitch + k, ok ? f - k : 0);
-          acc = hv.times(wv[y], acc);
+          hv.load(at.h, at.part, (int64_t)max(at.pair[x], 0) * at.pitch + k, at.pair[x] >= 0 ? at.kend - k : 0);
+          acc[x] = hv.times(wv[y], acc[x]);
         }
       }
-      if (ok) *reinterpret_cast<f4 *>(&s_o[((shared ? pairs : 0) + pair) * kPitch + 4 * q4]) = acc;
+    }
+    const Where done = at;
+    b += waves;
+    if (b < blocks + blocks_sh) {
+      at = locate(b);
+      request(at, 0);
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      if (8 * x >= done.rows) break;
+      // lane: pair p16 % 8 and half p16 / 8 of the sum against rows 4 q4 .. of the 16; those of its own half count
+      f4 v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = acc[x][i] + __shfl(acc[x][i], (lane + 40) & 63);
+      if (p16 < 8 && q4 < 2 && done.pair[x] >= 0)
+        *reinterpret_cast<f4 *>(&s_o[((done.shared ? pairs : 0) + done.pair[x]) * kPitch + 4 * q4]) = v;
     }
   }
   __syncthreads();
-  for (int i = tid; i < 16 * a.T; i += 64 * kWaves) {
-    const int t = i >> 4, c = i & 15;
+  for (int i = tid; i < 8 * a.T; i += blockDim.x) {
+    const int t = i >> 3, c = i & 7;
     if (n0 + c >= a.d) continue;
     float y = 0.f;
-    for (int j = 0; j < a.k; ++j) y += a.plan->gate[t * a.k + j] * s_o[(t * a.k + j) * kPitch + c];
+    for (int j = 0; j < a.k; ++j) y += s_gate[t * a.k + j] * s_o[(t * a.k + j) * kPitch + c];
     if (a.f_sh > 0) y += s_o[(pairs + t) * kPitch + c];
     if (a.y_f32) {
       if (a.add) y += static_cast<const float *>(a.add)[t * a.ld_add + n0 + c];
@@ -295,13 +418,21 @@ __global__ __launch_bounds__(64 * kWaves) void few_down_kernel(FewArgs a) {
 }
 
 template <typename Tr, int VPL, bool Vec>
-hipError_t few_of(const FewArgs &a, hipStream_t s) {
-  const int64_t used = a.E < a.T * a.k ? a.E : a.T * a.k;
-  const int64_t items = used * cdiv(a.f, 8) + cdiv(a.f_sh, 8);
-  few_gate_up_kernel<Tr, VPL, Vec><<<dim3((unsigned)(items < 768 ? items : 768)), 64 * kWaves, 0, s>>>(a);
+hipError_t few_of(FewArgs a, hipStream_t s) {
+  const int64_t blocks_sh = a.f_sh > 0 ? cdiv(a.T, 16) : 0;
+  const int64_t pairs = (int64_t)a.T * a.k, blocks = (a.E < pairs ? a.E : pairs) + pairs / 16;  // at most
+  const int64_t items = blocks * cdiv(a.f, 8) + blocks_sh * cdiv(a.f_sh, 8);
+  // a wave's part of a sum is at most kDeep steps, where eight waves can make it so
+  a.share = 0;
+  while (a.share < 3 && ((a.d + 31) / 32 + (1 << a.share) - 1) >> a.share > kDeep) ++a.share;
+  const int64_t rounds = cdiv(items, kWaves >> a.share);
+  const dim3 grid((unsigned)(a.T == 1 || rounds < 512 ? rounds : 512));
+  if (a.T == 1) few_gate_up_kernel<Tr, VPL, Vec, true><<<grid, 64 * kWaves, 0, s>>>(a);
+  else few_gate_up_kernel<Tr, VPL, Vec, false><<<grid, 64 * kWaves, 0, s>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  few_down_kernel<Tr, Vec><<<dim3((unsigned)cdiv(a.d, 16)), 64 * kWaves, 0, s>>>(a);
+  const int64_t waves = blocks + blocks_sh < 4 ? 4 : blocks + blocks_sh > 16 ? 16 : blocks + blocks_sh;
+  few_down_kernel<Tr, Vec><<<dim3((unsigned)cdiv(a.d, 8)), (unsigned)(64 * waves), 0, s>>>(a);
   return hipGetLastError();
 }
 template <typename Tr, int VPL>
@@ -311,11 +442,7 @@ hipError_t few_vec(const FewArgs &a, hipStream_t s) {
 }
 template <typename Tr>
 hipError_t few_experts(const FewArgs &a, hipStream_t s) {
-  if (a.E <= 64) return few_vec<Tr, 1>(a, s);
-  if (a.E <= 128) return few_vec<Tr, 2>(a, s);
-  if (a.E <= 256) return few_vec<Tr, 4>(a, s);
-  if (a.E <= 512) return few_vec<Tr, 8>(a, s);
-  return few_vec<Tr, 16>(a, s);
+  return a.E <= 256 ? few_vec<Tr, 4>(a, s) : few_vec<Tr, 16>(a, s);
 }
 
 }  // namespace

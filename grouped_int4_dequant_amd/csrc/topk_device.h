@@ -69,11 +69,13 @@ __device__ __forceinline__ uint64_t wave_max64(uint64_t v) {
 // Each lane first sorts its own keys, so one round is a wave maximum over the
 // lanes' heads, after which the winning lane shifts its list up by one.
 template <int VPL>
-__device__ __forceinline__ void topk_wave(const float *row, int E, int k, int lane, int &my_id, float &my_gate) {
+__device__ __forceinline__ void topk_load(const float *row, int E, int lane, float (&v)[VPL]) {
   // every load is unconditional (clamped index) so all are in flight at once
-  float v[VPL];
 #pragma unroll
   for (int r = 0; r < VPL; ++r) v[r] = row[min(lane + 64 * r, E - 1)];
+}
+template <int VPL>
+__device__ __forceinline__ void topk_values(const float (&v)[VPL], int E, int k, int lane, int &my_id, float &my_gate) {
   uint64_t key[VPL];
 #pragma unroll
   for (int r = 0; r < VPL; ++r) {
@@ -117,6 +119,12 @@ __device__ __forceinline__ void topk_wave(const float *row, int E, int k, int la
     if (lane == j) { my_ex = ex; my_id = key_index(win); }
   }
   my_gate = my_ex / sum;
+}
+template <int VPL>
+__device__ __forceinline__ void topk_wave(const float *row, int E, int k, int lane, int &my_id, float &my_gate) {
+  float v[VPL];
+  topk_load<VPL>(row, E, lane, v);
+  topk_values<VPL>(v, E, k, lane, my_id, my_gate);
 }
 
 }  // namespace moe
