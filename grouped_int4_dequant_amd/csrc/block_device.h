@@ -103,22 +103,19 @@ __device__ __forceinline__ float wave_sum(float v) {
   return (lane(0) + lane(16)) + (lane(32) + lane(48));
 }
 
-// e^v for v <= 0, as 2^(v log2 e). The product's rounding error, found with a fused multiply-add, multiplies the
-// result again, so that large |v| keep their bits: within 2^-22 of e^v. The library function costs three times as
-// many instructions.
-__device__ __forceinline__ float exp_of(float v) {
-  const float t = v * 1.44269502e+00f;  // log2 e = 1.44269502 + 1.92596303e-8
-  const float low = fmaf(v, 1.44269502e+00f, -t) + v * 1.92596303e-08f;
-  const float p = __builtin_amdgcn_exp2f(t);
-  return t > -200.f ? fmaf(p, low * 6.93147182e-01f, p) : p;  // (an infinite t has no error to correct)
-}
-// s(v) = 1 / (1 + e^-v) and 1 - s(v), each with all its bits
+// s(v) = 1 / (1 + e^-v) and 1 - s(v). e^-|v| is 2^(-|v| log2 e) with the product rounded, which is off by |v| 2^-24 of
+// itself at most: for the small one of the two that is its relative error (and a few 2^-24 more), and nothing to the other.
 struct Sigmoid {
   float s, rest;
 };
 __device__ __forceinline__ Sigmoid sigmoid_of(float v) {
-  const float e = exp_of(-__builtin_fabsf(v)), big = __builtin_amdgcn_rcpf(1.f + e), small = e * big;
+  const float e = __builtin_amdgcn_exp2f(__builtin_fabsf(v) * -1.44269504f);
+  const float big = __builtin_amdgcn_rcpf(1.f + e), small = e * big;
   return v < 0.f ? Sigmoid{small, big} : Sigmoid{big, small};
+}
+// v s(v), by the same way without the case distinction: e^-v may be infinite, its reciprocal is then zero.
+__device__ __forceinline__ float times_sigmoid(float v, float of) {
+  return v * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(of * -1.44269504f));
 }
 
 }  // namespace moe

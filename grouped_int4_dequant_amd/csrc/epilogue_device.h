@@ -16,10 +16,10 @@ __device__ __forceinline__ float curve_of(int act, float z) {
   switch (act) {
     case MOE_ACT_RELU: return z > 0.f || z != z ? z : 0.f;
     case MOE_ACT_SILU:
-    case MOE_ACT_SWIGLU: return z * sigmoid_of(z).s;
+    case MOE_ACT_SWIGLU: return times_sigmoid(z, z);
     case MOE_ACT_GELU: return 0.5f * z * erfcf(z * -7.071067812e-01f);
     case MOE_ACT_GELU_TANH:
-    case MOE_ACT_GEGLU: return z * sigmoid_of(2.f * kGeluC * fmaf(kGeluA * z * z, z, z)).s;  // (1 + tanh u) / 2 = s(2 u)
+    case MOE_ACT_GEGLU: return times_sigmoid(z, 2.f * kGeluC * fmaf(kGeluA * z * z, z, z));  // (1 + tanh u) / 2 = s(2 u)
     default: return z;
   }
 }
@@ -32,7 +32,7 @@ __device__ __forceinline__ float slope_of(int act, float z) {
       const Sigmoid g = sigmoid_of(z);
       return g.s * fmaf(z, g.rest, 1.f);
     }
-    case MOE_ACT_GELU: return 0.5f * erfcf(z * -7.071067812e-01f) + z * (3.989422804e-01f * exp_of(-0.5f * z * z));
+    case MOE_ACT_GELU: return 0.5f * erfcf(z * -7.071067812e-01f) + z * (3.989422804e-01f * __builtin_amdgcn_exp2f(z * z * -7.213475204e-01f));
     case MOE_ACT_GELU_TANH:
     case MOE_ACT_GEGLU: {
       const Sigmoid g = sigmoid_of(2.f * kGeluC * fmaf(kGeluA * z * z, z, z));
@@ -172,7 +172,7 @@ __device__ __forceinline__ void finish_wide(const Args &a, int i0, int j0, int n
       for (int c = 0; c < 4; ++c) *unit(p16, Args::kGated ? 8 * (c >> 1) + 2 * q4 + (c & 1) : 4 * q4 + c) = acc[s][c];
     }
     wave_sync();
-#pragma unroll 1
+#pragma unroll
     for (int x = 0; x < C / 32; ++x) {
       const int r = Args::kGated ? lane >> 2 : 8 * x + (lane >> 3), g = Args::kGated ? lane & 3 : lane & 7;
       float z[8], u[8];

@@ -178,8 +178,6 @@ __device__ __forceinline__ void store_inner(void *h, int64_t part, int64_t at, f
   }
 }
 
-__device__ __forceinline__ float silu_of(float z) { return z * sigmoid_of(z).s; }
-
 // One: a single token.
 template <typename Tr, int VPL, bool Vec, bool One>
 __global__ __launch_bounds__(64 * kWaves) void few_gate_up_kernel(FewArgs a) {
@@ -269,7 +267,7 @@ __global__ __launch_bounds__(64 * kWaves) void few_gate_up_kernel(FewArgs a) {
       // lane: pair p16; rows 4 q4 .. of the 16: columns 4 q4 .. of the gate, and behind them what it multiplies
       f4 h;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) h[i] = silu_of(acc[i]) * __shfl(acc[i], (lane + 32) & 63);
+      for (int i = 0; i < 4; ++i) h[i] = times_sigmoid(acc[i], acc[i]) * __shfl(acc[i], (lane + 32) & 63);
       const int c = done.c0 + 4 * q4, left = (done.shared ? a.f_sh : a.f) - c;
       if (done.pair >= 0 && q4 < 2 && left > 0) {
         if (done.shared) store_inner<Tr>(a.h_sh, (int64_t)a.T * a.pitch_sh, (int64_t)done.pair * a.pitch_sh + c, h, left);

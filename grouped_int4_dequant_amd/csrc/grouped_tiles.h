@@ -61,6 +61,13 @@ __device__ __forceinline__ void group_rows(const Args &a, int e, int &first, int
     count = max(min(max(a.offsets[e + 1], 0), a.P) - first, 0);
   }
 }
+// Place of the item-th tile of a single matrix, in bands of eight row tiles, down each band's columns: the 32
+// tiles that an XCD has at work are a piece of 8 x 4, which read 12 tiles' operands, not 33.
+__device__ __forceinline__ void dense_tile(int item, int ti, int tj, int &it, int &jt) {
+  const int band = item / (8 * tj), h = min(8, ti - 8 * band), x = item - band * 8 * tj;
+  jt = x / h;
+  it = 8 * band + x - jt * h;
+}
 // Columns of the result (forward and input gradient).
 template <int Mode, typename Args>
 __host__ __device__ __forceinline__ int columns_of(const Args &a) {
@@ -848,12 +855,17 @@ __global__ __launch_bounds__(kWideThreads, 2) void grouped_wide_kernel(Args a) {
     const int tj = (a.K + kWide - 1) / kWide, ti = (a.N + kWide - 1) / kWide;
     const int per = ti * tj;
     const int k = blockIdx.x / per;
-    if (k >= a.G) return;
+    if (!Args::kDense && k >= a.G) return;
     if constexpr (Args::kDense) t.e = 0; else t.e = group_by_size(a.offsets, a.G, a.P, k);
     if (t.e < 0) return;
-    const int x = blockIdx.x - k * per;
-    t.i0 = x / tj * kWide;
-    t.j0 = (x - x / tj * tj) * kWide;
+    int x = blockIdx.x - k * per, it = x / tj, jt = x - it * tj;
+    if constexpr (Args::kDense) {
+      x = xcd_item(blockIdx.x, per);
+      if (x < 0) return;
+      dense_tile(x, ti, tj, it, jt);
+    }
+    t.i0 = it * kWide;
+    t.j0 = jt * kWide;
     group_rows(a, t.e, t.first, t.count);
     t.nr = t.count;
     t.ni = a.N - t.i0;
@@ -871,8 +883,9 @@ __global__ __launch_bounds__(kWideThreads, 2) void grouped_wide_kernel(Args a) {
     if (g.e < 0) return;
     t.e = g.e;
     const int x = item - g.before * tj, mt = (g.count + Rows - 1) / Rows;
-    const int jt = x / mt;
-    t.i0 = (x - jt * mt) * Rows;
+    int jt = x / mt, it = x - jt * mt;
+    if constexpr (Args::kDense) dense_tile(x, mt, tj, it, jt);
+    t.i0 = it * Rows;
     t.j0 = jt * C;
     t.first = g.first;
     t.count = g.count;
@@ -890,7 +903,7 @@ hipError_t launch_wide(const Args &a, hipStream_t s) {
   const int64_t used = a.G < a.P ? a.G : a.P;  // groups that can have rows
   const int64_t tiles = Mode == kWgrad ? (int64_t)a.G * cdiv(a.N, kWide) * cdiv(a.K, kWide)
                                        : (a.P + used * (Rows - 1)) / Rows * cdiv(columns_of<Mode>(a), kWide / (Args::kGated ? 2 : 1));
-  const int64_t wgs = Mode == kWgrad ? tiles : xcd_grid(tiles);  // the weight gradient's kernel takes its tile by number
+  const int64_t wgs = Mode == kWgrad && !Args::kDense ? tiles : xcd_grid(tiles);  // the grouped weight gradient's kernel takes its tile by number
   if (!grid_fits(wgs, kWideThreads) || tiles >= INT32_MAX / 2) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)wgs);
   if constexpr (!Args::kDense) {
@@ -932,8 +945,15 @@ hipError_t launch(const Args &a, hipStream_t s) {
       // hold many, by the average. Forward at 256 experts, N = 1024, K = 2048: 159 against 170 us at
       // 2 rows a group, 214 / 234 at 64, 380 / 385 at 256; 16 groups of 1024 rows: 301 / 284. Input gradient:
       // 162 / 171 at 2, 240 / 250 at 64, 305 / 288 at 128.
+      // A single matrix: by the rounds that the tiles make over 256 CUs, a tile of 128 rows taking a little over half
+      // the time of one of 256.
       if constexpr (Mode != kWgrad) {
-        if (a.P < (int64_t)(Mode == kFwd ? 256 : 96) * a.G) return launch_wide<Tr, Mode, 128, Args>(a, s);
+        if constexpr (Args::kDense) {
+          const int64_t tj = cdiv(J, kWide / kPer);
+          if (9 * cdiv(cdiv(a.P, 128) * tj, 256) < 16 * cdiv(cdiv(a.P, 256) * tj, 256)) return launch_wide<Tr, Mode, 128, Args>(a, s);
+        } else if (a.P < (int64_t)(Mode == kFwd ? 256 : 96) * a.G) {
+          return launch_wide<Tr, Mode, 128, Args>(a, s);
+        }
       }
       return launch_wide<Tr, Mode, 256, Args>(a, s);
     }
