@@ -23,19 +23,21 @@ __device__ __forceinline__ float curve_of(int act, float z) {
     default: return z;
   }
 }
-// The curve's derivative.
-__device__ __forceinline__ float slope_of(int act, float z) {
+// The curve's derivative, and its value for the gated ones.
+__device__ __forceinline__ float slope_of(int act, float z, float &value) {
   switch (act) {
     case MOE_ACT_RELU: return z > 0.f ? 1.f : 0.f;
     case MOE_ACT_SILU:
     case MOE_ACT_SWIGLU: {
       const Sigmoid g = sigmoid_of(z);
+      value = z * g.s;
       return g.s * fmaf(z, g.rest, 1.f);
     }
     case MOE_ACT_GELU: return 0.5f * erfcf(z * -7.071067812e-01f) + z * (3.989422804e-01f * __builtin_amdgcn_exp2f(z * z * -7.213475204e-01f));
     case MOE_ACT_GELU_TANH:
     case MOE_ACT_GEGLU: {
       const Sigmoid g = sigmoid_of(2.f * kGeluC * fmaf(kGeluA * z * z, z, z));
+      value = z * g.s;
       const float both = g.s * g.rest;  // where it is zero the curve is straight, though z^2 may have overflowed
       return both == 0.f ? g.s : fmaf(z * both, 2.f * kGeluC * fmaf(3.f * kGeluA * z, z, 1.f), g.s);
     }

@@ -93,17 +93,29 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs a) {
     if constexpr (Gated) sum[1][i] = 0.f;
   }
   if (left > 0) {
+    Raw8 dyv, zv, uv;
+    auto load = [&](int row) __attribute__((always_inline)) {
+      const int n = row < end ? left : 0;
+      dyv = load_raw8<false>(a.dy, (int64_t)row * a.ld_dy + col, n);
+      if (a.act == MOE_ACT_NONE) return;
+      zv = load_raw8<false>(a.pre, (int64_t)row * a.ld_pre + col, n);
+      if constexpr (Gated) uv = load_raw8<false>(a.pre, (int64_t)row * a.ld_pre + a.cols + col, n);
+    };
+    load(begin + r0);
     for (int row = begin + r0; row < end; row += 8) {
       float dy[8], z[8], u[8];
-      widen8<Tr, false>(load_raw8<false>(a.dy, (int64_t)row * a.ld_dy + col, left), dy);
+      widen8<Tr, false>(dyv, dy);
       if (a.act != MOE_ACT_NONE) {
-        widen8<Tr, false>(load_raw8<false>(a.pre, (int64_t)row * a.ld_pre + col, left), z);
-        if constexpr (Gated) widen8<Tr, false>(load_raw8<false>(a.pre, (int64_t)row * a.ld_pre + a.cols + col, left), u);
+        widen8<Tr, false>(zv, z);
+        if constexpr (Gated) widen8<Tr, false>(uv, u);
+      }
+      load(row + 8);
+      if (a.act != MOE_ACT_NONE) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float slope = slope_of(a.act, z[i]);
+          float value;
+          const float slope = slope_of(a.act, z[i], value);
           if constexpr (Gated) {
-            const float value = curve_of(a.act, z[i]);
             z[i] = dy[i] * value;
             dy[i] = dy[i] * u[i] * slope;
           } else {
