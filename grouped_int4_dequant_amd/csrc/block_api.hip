@@ -115,57 +115,48 @@ int moe_linear_backward(int32_t dtype, const void *dy, int64_t lddy, const void 
   const bool fp16 = dtype == MOE_FP16;
   const void *dz = dy;
   int64_t lddz = lddy;
-  if (curved || db) {
-    ActGradArgs a{};
-    a.dy = static_cast<const uint16_t *>(dy);
-    a.ld_dy = lddy;
-    a.pre = static_cast<const uint16_t *>(pre);
-    a.ld_pre = ldpre;
-    a.T = T; a.N = N; a.cols = cols; a.act = act;
-    const ColumnChunks c = column_chunks(T, cols);
-    a.chunk_rows = c.rows;
-    a.chunks = T > 0 ? c.count : 0;
-    if (curved) {
-      a.dz = static_cast<uint16_t *>(ws);
-      dz = ws;
-      lddz = N;
-    }
-    if (db) {
-      a.part = reinterpret_cast<float *>(static_cast<char *>(ws) + dz_bytes(T, N, act));
-      a.pitch = sums_pitch(N);
-      a.db = db;
-      a.g_f32 = g_dtype == MOE_FP32;
-      a.accumulate = accumulate != 0;
-    }
-    const int e = status(launch_act_grad(a, fp16, stream));
-    if (e != MOE_OK) return e;
+  ActGradArgs c{};
+  c.dy = static_cast<const uint16_t *>(dy);
+  c.ld_dy = lddy;
+  c.pre = static_cast<const uint16_t *>(pre);
+  c.ld_pre = ldpre;
+  c.T = T; c.N = N; c.cols = cols; c.act = act;
+  const ColumnChunks n = column_chunks(T, cols);
+  c.chunk_rows = n.rows;
+  c.chunks = T > 0 ? n.count : 0;
+  if (curved) {
+    c.dz = static_cast<uint16_t *>(ws);
+    dz = ws;
+    lddz = N;
   }
-  if (dx && T > 0) {
-    DenseArgs a{};
-    fill_dense(a, dz, lddz, W, K, T, N, K);
-    a.out = dx;
-    a.ld_out = lddx;
-    a.out_f32 = dx_dtype == MOE_FP32;
-    a.vec = units(dz, lddz, N) && units(W, K, K);
-    a.wide = wide_tiles(a, kDgrad);
-    a.vec_out = runs(dx, dx_dtype, lddx) && K % 4 == 0;
-    const int e = status(launch_dense(a, kDgrad, fp16, stream));
-    if (e != MOE_OK) return e;
+  if (db) {
+    c.part = reinterpret_cast<float *>(static_cast<char *>(ws) + dz_bytes(T, N, act));
+    c.pitch = sums_pitch(N);
+    c.db = db;
+    c.g_f32 = g_dtype == MOE_FP32;
+    c.accumulate = accumulate != 0;
+  }
+  DenseArgs dxa{}, dwa{};
+  if (dx) {
+    fill_dense(dxa, dz, lddz, W, K, T, N, K);
+    dxa.out = dx;
+    dxa.ld_out = lddx;
+    dxa.out_f32 = dx_dtype == MOE_FP32;
+    dxa.vec = units(dz, lddz, N) && units(W, K, K);
+    dxa.wide = wide_tiles(dxa, kDgrad);
+    dxa.vec_out = runs(dx, dx_dtype, lddx) && K % 4 == 0;
   }
   if (dW) {
-    DenseArgs a{};
-    fill_dense(a, x, ldx, dz, lddz, T, N, K);
-    a.out = dW;
-    a.ld_out = K;
-    a.out_f32 = g_dtype == MOE_FP32;
-    a.accumulate = accumulate != 0;
-    a.vec = units(dz, lddz, N) && units(x, ldx, K);
-    a.wide = wide_tiles(a, kWgrad);
-    a.vec_out = runs(dW, g_dtype, K) && K % 4 == 0;
-    const int e = status(launch_dense(a, kWgrad, fp16, stream));
-    if (e != MOE_OK) return e;
+    fill_dense(dwa, x, ldx, dz, lddz, T, N, K);
+    dwa.out = dW;
+    dwa.ld_out = K;
+    dwa.out_f32 = g_dtype == MOE_FP32;
+    dwa.accumulate = accumulate != 0;
+    dwa.vec = units(dz, lddz, N) && units(x, ldx, K);
+    dwa.wide = wide_tiles(dwa, kWgrad);
+    dwa.vec_out = runs(dW, g_dtype, K) && K % 4 == 0;
   }
-  return MOE_OK;
+  return status(launch_linear_grad(c, dxa, dwa, fp16, stream));
 }
 
 int moe_residual_norm(int32_t dtype, const void *o, int64_t ldo, const void *x, int64_t ldx, int32_t stream_dtype, int32_t T,

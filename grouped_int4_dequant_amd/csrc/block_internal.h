@@ -102,8 +102,8 @@ hipError_t launch_few_layer(const FewArgs &a, bool fp16, hipStream_t s);
 
 template <bool Gated>
 hipError_t launch_linear(const LinearArgs<Gated> &a, bool fp16, hipStream_t s);
-hipError_t launch_act_grad(const ActGradArgs &a, bool fp16, hipStream_t s);
-hipError_t launch_dense(const DenseArgs &a, GroupedMode mode, bool fp16, hipStream_t s);
+// dz and db, then dx = dz W and dW = dz^T x (each without `out`: not wanted)
+hipError_t launch_linear_grad(const ActGradArgs &c, const DenseArgs &dx, const DenseArgs &dw, bool fp16, hipStream_t s);
 inline bool is_gated(int32_t act) { return act == MOE_ACT_SWIGLU || act == MOE_ACT_GEGLU; }
 
 hipError_t launch_norm(const NormArgs &a, bool fp16, hipStream_t s);

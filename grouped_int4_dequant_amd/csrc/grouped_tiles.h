@@ -139,12 +139,14 @@ __device__ __forceinline__ u4 load_unit(const uint16_t *p, int n) {
 // tiles would leave most CUs idle, and for operands the wide tiles cannot request.
 constexpr int kSmall = 64;
 
-template <typename Tr, int Mode, bool Vec, typename Args>
-__global__ __launch_bounds__(256) void grouped_small_kernel(Args a) {
+typedef uint8_t SmallTile[kSmall * kBR * 2];  // an operand's step in LDS
+
+// Workgroup `block` of a call. Depth: steps ahead, even. A single matrix takes four, since its few tiles leave the CUs
+// to one or two workgroups, whose registers are free: a step is then about 0.4 us.
+template <typename Tr, int Mode, bool Vec, int Depth, typename Args>
+__device__ __forceinline__ void small_body(const Args &a, const int block, SmallTile (&s_l)[2], SmallTile (&s_r)[2]) {
   constexpr int B = kSmall, U = B * 8 / 256;  // 16-byte units a thread stages of each operand and step
   constexpr bool kLAcross = Mode == kWgrad, kRAcross = Mode != kFwd;
-  __shared__ __attribute__((aligned(16))) uint8_t s_l[2][B * kBR * 2];
-  __shared__ __attribute__((aligned(16))) uint8_t s_r[2][B * kBR * 2];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int p16 = lane & 15, q4 = lane >> 4;
@@ -153,9 +155,9 @@ __global__ __launch_bounds__(256) void grouped_small_kernel(Args a) {
   int e, first, count, i0, j0, ni, nj, nr;
   if (Mode == kWgrad) {
     const int tj = (a.K + B - 1) / B, ti = (a.N + B - 1) / B, per = ti * tj;
-    e = blockIdx.x / per;
+    e = block / per;
     if (e >= a.G) return;
-    const int t = blockIdx.x - e * per;
+    const int t = block - e * per;
     i0 = t / tj * B;
     j0 = (t - t / tj * tj) * B;
     group_rows(a, e, first, count);
@@ -167,7 +169,7 @@ __global__ __launch_bounds__(256) void grouped_small_kernel(Args a) {
     const int J = Args::kGated ? a.N / 2 : Mode == kFwd ? a.N : a.K, tj = (J + C - 1) / C;
     int item;
     const GroupTile g = find_rows(a, B, [&](int total) {
-      item = xcd_item(blockIdx.x, total * tj);
+      item = xcd_item(block, total * tj);
       return item < 0 ? -1 : item / tj;
     });
     if (g.e < 0) return;
@@ -212,7 +214,7 @@ __global__ __launch_bounds__(256) void grouped_small_kernel(Args a) {
     else if (Args::kGated) rp[i] = R + (int64_t)(min(j0 + 16 * (row >> 5) + (row & 15), a.N / 2 - 1) + (row & 16 ? a.N / 2 : 0)) * ldr + rslot;
     else rp[i] = R + (int64_t)(j0 + min(row, nj - 1)) * ldr + rslot;
   }
-  u4 lreg[2][U], rreg[2][U];
+  u4 lreg[Depth][U], rreg[Depth][U];
   auto load = [&](int s, u4 (&lreg)[U], u4 (&rreg)[U], auto whole) __attribute__((always_inline)) {  // whole: every r of the step exists
     constexpr bool kAll = decltype(whole)::value;
 #pragma unroll
@@ -260,15 +262,16 @@ __global__ __launch_bounds__(256) void grouped_small_kernel(Args a) {
   };
   constexpr std::false_type partly{};
   if (steps > 0) {
-    load(0, lreg[0], rreg[0], partly);
-    if (steps > 1) load(1, lreg[1], rreg[1], partly);
+#pragma unroll
+    for (int s = 0; s < Depth; ++s)
+      if (s < steps) load(s, lreg[s], rreg[s], partly);
     keep(0, lreg[0], rreg[0]);
   }
-  // step s out of LDS buffer `buf`; registers `buf` receive step s + 2, the others hold s + 1
-  auto step = [&](int s, auto buf_, auto whole) __attribute__((always_inline)) {
-    constexpr int buf = decltype(buf_)::value;
+  // step s out of LDS buffer s % 2; registers s % Depth receive step s + Depth
+  auto step = [&](int s, auto at_, auto whole) __attribute__((always_inline)) {
+    constexpr int at = decltype(at_)::value, buf = at & 1, next = (at + 1) % Depth;
     __syncthreads();
-    if (decltype(whole)::value || s + 2 < steps) load(s + 2, lreg[buf], rreg[buf], whole);
+    if (decltype(whole)::value || s + Depth < steps) load(s + Depth, lreg[at], rreg[at], whole);
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
       s8 l[2], r[2];
@@ -282,19 +285,19 @@ __global__ __launch_bounds__(256) void grouped_small_kernel(Args a) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) acc[i][j] = Tr::mfma(r[j], l[i], acc[i][j]);
     }
-    if (decltype(whole)::value || s + 1 < steps) keep(buf ^ 1, lreg[buf ^ 1], rreg[buf ^ 1]);
+    if (decltype(whole)::value || s + 1 < steps) keep(buf ^ 1, lreg[next], rreg[next]);
   };
-  constexpr std::integral_constant<int, 0> even{};
-  constexpr std::integral_constant<int, 1> odd{};
+  auto round = [&](int s, auto whole) __attribute__((always_inline)) {
+    step(s, std::integral_constant<int, 0>{}, whole);
+    if (decltype(whole)::value || s + 1 < steps) step(s + 1, std::integral_constant<int, 1>{}, whole);
+    if constexpr (Depth == 4) {
+      if (decltype(whole)::value || s + 2 < steps) step(s + 2, std::integral_constant<int, 2>{}, whole);
+      if (decltype(whole)::value || s + 3 < steps) step(s + 3, std::integral_constant<int, 3>{}, whole);
+    }
+  };
   int s = 0;
-  for (; (s + 4) * kBR <= nr && s < steps; s += 2) {  // steps s + 2 and s + 3 are whole
-    step(s, even, std::true_type{});
-    step(s + 1, odd, std::true_type{});
-  }
-  for (; s < steps; s += 2) {
-    step(s, even, partly);
-    if (s + 1 < steps) step(s + 1, odd, partly);
-  }
+  for (; (s + 2 * Depth) * kBR <= nr && s < steps; s += Depth) round(s, std::true_type{});  // the steps it asks for are whole
+  for (; s < steps; s += Depth) round(s, partly);
 
   // ---- results: lane holds output row p16 and four consecutive columns of each block
   if constexpr (Args::kEpilogue) {
@@ -330,6 +333,12 @@ __global__ __launch_bounds__(256) void grouped_small_kernel(Args a) {
       store4<Tr>(a, obase + (int64_t)(i0 + row) * ldo + j0 + col, masked ? f4{0.f, 0.f, 0.f, 0.f} : acc[i][j], nj - col, Mode == kWgrad && a.accumulate);
     }
   }
+}
+
+template <typename Tr, int Mode, bool Vec, typename Args>
+__global__ __launch_bounds__(256) void grouped_small_kernel(Args a) {
+  __shared__ __attribute__((aligned(16))) SmallTile s_l[2], s_r[2];
+  small_body<Tr, Mode, Vec, Args::kDense ? 4 : 2>(a, blockIdx.x, s_l, s_r);
 }
 
 // ---------------------------------------------------------------- few rows
@@ -916,19 +925,25 @@ hipError_t launch_wide(const Args &a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Whether a call takes wide tiles: where at least half the CUs get one. Against small tiles, us, forward / input gradient / weight
+// gradient: 16 groups, 1024 rows, 1024 x 1024 (64, 64 and 256 wide tiles) 16.3 / 17.2 / 15.1 against 12.2 / 12.7 / 18.6;
+// 32 groups, 2048 rows (128, 128, 512) 21.0 / 23.4 / 26.5 against 24.7 / 24.7 / 32.6; 4 groups, 8192 rows (128, 128,
+// 64) 27.0 / 27.1 / 55.7 against 38.5 / 39.5 / 40.3; 8 groups, 1024 rows (32, 32, 128) 16.3 / 22.9 / 15.8 against 11.0 / 11.6 / 12.9.
+template <int Mode, typename Args>
+bool takes_wide(const Args &a) {
+  const int64_t used = a.G < a.P ? a.G : a.P;  // groups that can have rows
+  const int64_t at_least = Mode == kWgrad ? (int64_t)a.G * cdiv(a.N, kWide) * cdiv(a.K, kWide)
+                                          : (used > a.P / kWide ? used : a.P / kWide) * cdiv(columns_of<Mode>(a), kWide / (Args::kGated ? 2 : 1));
+  return a.vec && a.wide && at_least >= 128;
+}
+
 template <typename Tr, int Mode, bool Vec, typename Args>
 hipError_t launch(const Args &a, hipStream_t s) {
   const int64_t used = a.G < a.P ? a.G : a.P;  // groups that can have rows
   const int J = columns_of<Mode>(a);
   constexpr int kPer = Args::kGated ? 2 : 1;  // columns of the product for one of the result
   if constexpr (Vec) {
-    const int64_t at_least = Mode == kWgrad ? (int64_t)a.G * cdiv(a.N, kWide) * cdiv(a.K, kWide)
-                                            : (used > a.P / kWide ? used : a.P / kWide) * cdiv(J, kWide / kPer);
-    // Wide tiles where at least half the CUs get one. Against small tiles, us, forward / input gradient / weight
-    // gradient: 16 groups, 1024 rows, 1024 x 1024 (64, 64 and 256 wide tiles) 16.3 / 17.2 / 15.1 against 12.2 / 12.7 / 18.6;
-    // 32 groups, 2048 rows (128, 128, 512) 21.0 / 23.4 / 26.5 against 24.7 / 24.7 / 32.6; 4 groups, 8192 rows (128, 128,
-    // 64) 27.0 / 27.1 / 55.7 against 38.5 / 39.5 / 40.3; 8 groups, 1024 rows (32, 32, 128) 16.3 / 22.9 / 15.8 against 11.0 / 11.6 / 12.9.
-    const bool wide = a.wide && at_least >= 128;
+    const bool wide = takes_wide<Mode>(a);
     if constexpr (Mode != kWgrad && !Args::kEpilogue) {
       // Few rows whose weights are too few for wide tiles. Against small tiles at N = 1024, K = 2048, us, forward / input
       // gradient: 8 groups, 8 rows 9.4 / 9.0 against 13.2 / 10.5, 64 rows 11.6 / 9.0 against 13.6 / 11.2, 128 rows 18.6 / 11.6
