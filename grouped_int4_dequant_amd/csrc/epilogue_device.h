@@ -95,13 +95,27 @@ __device__ __forceinline__ void store4_of(void *p, bool f32, int64_t at, int lef
   }
 }
 
+// What the epilogue reads for four results of a row, asked for ahead of their sums.
+struct Extra4 {
+  f4 bias, bias_u, res;
+};
+template <typename Tr, typename Args>
+__device__ __forceinline__ Extra4 extra4(const Args &a, int row, int col, int left) {
+  Extra4 e;
+  if (a.bias) {
+    e.bias = load4<Tr>(a.bias, a.bias_f32, col, left);
+    if constexpr (Args::kGated) e.bias_u = load4<Tr>(a.bias, a.bias_f32, a.N / 2 + col, left);
+  }
+  if (a.res) e.res = load4<Tr>(a.res, a.out_f32, (int64_t)row * a.ld_res + col, left);
+  return e;
+}
 // Four sums of result row `row`, from result column `col` on, of which `left` exist: z is the product
 // (the gate's if gated), u the product that it multiplies.
 template <typename Tr, typename Args>
-__device__ __forceinline__ void finish4(const Args &a, int row, int col, int left, f4 z, f4 u) {
+__device__ __forceinline__ void finish4(const Args &a, int row, int col, int left, f4 z, f4 u, const Extra4 &e) {
   if (a.bias) {
-    z += load4<Tr>(a.bias, a.bias_f32, col, left);
-    if constexpr (Args::kGated) u += load4<Tr>(a.bias, a.bias_f32, a.N / 2 + col, left);
+    z += e.bias;
+    if constexpr (Args::kGated) u += e.bias_u;
   }
   if (a.pre) {
     store4_of<Tr>(a.pre, false, (int64_t)row * a.ld_pre + col, left, z);
@@ -114,22 +128,18 @@ __device__ __forceinline__ void finish4(const Args &a, int row, int col, int lef
       if constexpr (Args::kGated) z[i] *= u[i];
     }
   }
-  if (a.res) z += load4<Tr>(a.res, a.out_f32, (int64_t)row * a.ld_res + col, left);
+  if (a.res) z += e.res;
   store4_of<Tr>(a.out, a.out_f32, (int64_t)row * a.ld_out + col, left, z);
 }
 
 // The same for eight.
 template <typename Tr, typename Args>
-__device__ __forceinline__ void finish8(const Args &a, int row, int col, int left, float (&z)[8], float (&u)[8]) {
-  float f[8];
+__device__ __forceinline__ void finish8(const Args &a, int row, int col, int left, float (&z)[8], float (&u)[8], const float (&bias)[2][8], const Raw8 &res) {
   if (a.bias) {
-    load8<Tr>(a.bias, a.bias_f32, col, left, f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] += f[i];
-    if constexpr (Args::kGated) {
-      load8<Tr>(a.bias, a.bias_f32, a.N / 2 + col, left, f);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) u[i] += f[i];
+    for (int i = 0; i < 8; ++i) {
+      z[i] += bias[0][i];
+      if constexpr (Args::kGated) u[i] += bias[1][i];
     }
   }
   if (a.pre) {
@@ -144,7 +154,9 @@ __device__ __forceinline__ void finish8(const Args &a, int row, int col, int lef
     }
   }
   if (a.res) {
-    load8<Tr>(a.res, a.out_f32, (int64_t)row * a.ld_res + col, left, f);
+    float f[8];
+    if (a.out_f32) widen8<Tr, true>(res, f);
+    else widen8<Tr, false>(res, f);
 #pragma unroll
     for (int i = 0; i < 8; ++i) z[i] += f[i];
   }
@@ -161,8 +173,27 @@ __device__ __forceinline__ void finish_wide(const Args &a, int i0, int j0, int n
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wi = wave >> 2, wj = wave & 3, p16 = lane & 15, q4 = lane >> 4;
   constexpr int C = Args::kGated ? 32 : 64;  // result columns of a wave
+  constexpr int X = C / 32;                  // rows of a block that a lane finishes
+  const int g = Args::kGated ? lane & 3 : lane & 7, col = C * wj + 8 * g, left = nj - col;
   // unit u (four sums) of row r lies in slot u ^ r of sixteen
   auto unit = [&](int r, int u) __attribute__((always_inline)) { return reinterpret_cast<f4 *>(mine + 256 * r + 16 * (u ^ r)); };
+  auto row_of = [&](int i, int x) __attribute__((always_inline)) { return 16 * (wi + 2 * i) + (Args::kGated ? lane >> 2 : 8 * x + (lane >> 3)); };
+  float bias[2][8];
+  if (a.bias) {
+    load8<Tr>(a.bias, a.bias_f32, j0 + col, left, bias[0]);
+    if constexpr (Args::kGated) load8<Tr>(a.bias, a.bias_f32, a.N / 2 + j0 + col, left, bias[1]);
+  }
+  Raw8 res[X];  // the residual, one block ahead
+  auto ask = [&](int i) __attribute__((always_inline)) {
+#pragma unroll
+    for (int x = 0; x < X; ++x) {
+      const int64_t at = (int64_t)(i0 + row_of(i, x)) * a.ld_res + j0 + col;
+      const int n = row_of(i, x) < ni ? left : 0;
+      if (a.out_f32) res[x] = load_raw8<true>(a.res, at, n);
+      else res[x] = load_raw8<false>(a.res, at, n);
+    }
+  };
+  if (a.res) ask(0);
 #pragma unroll 1
   for (int i = 0; i < TI; ++i) {
     const int row0 = 16 * (wi + 2 * i);
@@ -174,9 +205,13 @@ __device__ __forceinline__ void finish_wide(const Args &a, int i0, int j0, int n
       for (int c = 0; c < 4; ++c) *unit(p16, Args::kGated ? 8 * (c >> 1) + 2 * q4 + (c & 1) : 4 * q4 + c) = acc[s][c];
     }
     wave_sync();
+    Raw8 now[X];
 #pragma unroll
-    for (int x = 0; x < C / 32; ++x) {
-      const int r = Args::kGated ? lane >> 2 : 8 * x + (lane >> 3), g = Args::kGated ? lane & 3 : lane & 7;
+    for (int x = 0; x < X; ++x) now[x] = res[x];
+    if (a.res && i + 1 < TI) ask(i + 1);
+#pragma unroll
+    for (int x = 0; x < X; ++x) {
+      const int r = row_of(i, x) - row0;
       float z[8], u[8];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
@@ -189,8 +224,7 @@ __device__ __forceinline__ void finish_wide(const Args &a, int i0, int j0, int n
           for (int y = 0; y < 4; ++y) u[4 * c + y] = w[y];
         }
       }
-      const int col = C * wj + 8 * g;
-      if (row0 + r < ni && col < nj) finish8<Tr>(a, i0 + row0 + r, j0 + col, nj - col, z, u);
+      if (row0 + r < ni && left > 0) finish8<Tr>(a, i0 + row0 + r, j0 + col, left, z, u, bias, now[x]);
     }
     wave_sync();
   }

@@ -260,13 +260,29 @@ __device__ __forceinline__ void small_body(const Args &a, const int block, Small
     }
     return s8{x[0][0], x[0][1], x[0][2], x[0][3], x[1][0], x[1][1], x[1][2], x[1][3]};
   };
+  // gated: block 0 holds the gate's columns, block 1 those that it multiplies
+  constexpr int kBlocks = Args::kGated ? 1 : 2;
+  auto col_of = [&](int j) { return Args::kGated ? (wj >> 1) + 4 * q4 : wj + 16 * j + 4 * q4; };
+  Extra4 extra[2][kBlocks];
   constexpr std::false_type partly{};
   if (steps > 0) {
+    if (nr >= Depth * kBR) {
 #pragma unroll
-    for (int s = 0; s < Depth; ++s)
-      if (s < steps) load(s, lreg[s], rreg[s], partly);
-    keep(0, lreg[0], rreg[0]);
+      for (int s = 0; s < Depth; ++s) load(s, lreg[s], rreg[s], std::true_type{});
+    } else {
+#pragma unroll
+      for (int s = 0; s < Depth; ++s)
+        if (s < steps) load(s, lreg[s], rreg[s], partly);
+    }
   }
+  if constexpr (Args::kEpilogue) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < kBlocks; ++j)
+        extra[i][j] = extra4<Tr>(a, i0 + min(wi + 16 * i + p16, ni - 1), j0 + col_of(j), nj - col_of(j));
+  }
+  if (steps > 0) keep(0, lreg[0], rreg[0]);
   // step s out of LDS buffer s % 2; registers s % Depth receive step s + Depth
   auto step = [&](int s, auto at_, auto whole) __attribute__((always_inline)) {
     constexpr int at = decltype(at_)::value, buf = at & 1, next = (at + 1) % Depth;
@@ -305,15 +321,10 @@ __device__ __forceinline__ void small_body(const Args &a, const int block, Small
     for (int i = 0; i < 2; ++i) {
       const int row = wi + 16 * i + p16;
       if (row >= ni) continue;
-      if constexpr (Args::kGated) {  // block 0 the gate's columns, block 1 those that it multiplies
-        const int col = (wj >> 1) + 4 * q4;
-        if (col < nj) finish4<Tr>(a, i0 + row, j0 + col, nj - col, acc[i][0], acc[i][1]);
-      } else {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int col = wj + 16 * j + 4 * q4;
-          if (col < nj) finish4<Tr>(a, i0 + row, j0 + col, nj - col, acc[i][j], acc[i][j]);
-        }
+      for (int j = 0; j < kBlocks; ++j) {
+        const int col = col_of(j);
+        if (col < nj) finish4<Tr>(a, i0 + row, j0 + col, nj - col, acc[i][j], acc[i][1], extra[i][j]);
       }
     }
     return;

@@ -36,6 +36,11 @@ __global__ __launch_bounds__(512) void linear_few_kernel(LinearArgs<Gated> a) {
   f4 acc[RB];
 #pragma unroll
   for (int b = 0; b < RB; ++b) acc[b] = f4{0.f, 0.f, 0.f, 0.f};
+  // the wave that joins a block of rows: lane has row p16, W's rows 4 q4 ..
+  const int row = 16 * wave + p16, c = j0 + 4 * q4;
+  const bool mine = wave < RB && row < a.P && c < J && (!Gated || q4 < 2);
+  Extra4 extra;
+  if (mine) extra = extra4<Tr>(a, row, c, J - c);
   for (int k0 = 32 * wave; k0 < a.K; k0 += 256 * kDeep) {
     s8 wv[kDeep], xv[kDeep][RB];
 #pragma unroll
@@ -62,18 +67,12 @@ __global__ __launch_bounds__(512) void linear_few_kernel(LinearArgs<Gated> a) {
   f4 v = s_part[0][wave][lane];
 #pragma unroll
   for (int y = 1; y < 8; ++y) v += s_part[y][wave][lane];
-  // lane: row p16, W's rows 4 q4 ..
-  const int row = 16 * wave + p16;
+  f4 u = v;
   if constexpr (Gated) {
-    f4 u;
 #pragma unroll
     for (int i = 0; i < 4; ++i) u[i] = __shfl(v[i], (lane + 32) & 63);
-    const int c = j0 + 4 * q4;
-    if (q4 < 2 && row < a.P && c < J) finish4<Tr>(a, row, c, min(J - c, 4), v, u);
-  } else {
-    const int c = j0 + 4 * q4;
-    if (row < a.P && c < J) finish4<Tr>(a, row, c, min(J - c, 4), v, v);
   }
+  if (mine) finish4<Tr>(a, row, c, min(J - c, 4), v, u, extra);
 }
 
 // ------------------------------------------------------- activation's gradient
