@@ -26,10 +26,16 @@ __device__ __forceinline__ Raw8 load_raw8(const void *p, int64_t at, int left) {
       v.lo = __builtin_bit_cast(u4, (f4) * reinterpret_cast<const f4_elem *>(q));
       v.hi = __builtin_bit_cast(u4, (f4) * reinterpret_cast<const f4_elem *>(q + 4));
     } else {
+      uint32_t x[8];  // (all asked for before any is used)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const uint32_t x = i < left ? __builtin_bit_cast(uint32_t, q[i]) : 0u;
-        if (i < 4) v.lo[i] = x; else v.hi[i - 4] = x;
+        x[i] = 0u;
+        if (i < left) x[i] = __builtin_bit_cast(uint32_t, q[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v.lo[i] = x[i];
+        v.hi[i] = x[4 + i];
       }
     }
   } else {
@@ -37,11 +43,14 @@ __device__ __forceinline__ Raw8 load_raw8(const void *p, int64_t at, int left) {
     if (left >= 8) {
       v.lo = *reinterpret_cast<const u4_elem *>(q);
     } else {
+      uint32_t x[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const uint32_t x = i < left ? (uint32_t)q[i] : 0u;
-        v.lo[i >> 1] |= x << (16 * (i & 1));
+        x[i] = 0u;
+        if (i < left) x[i] = q[i];
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v.lo[i] = x[2 * i] | x[2 * i + 1] << 16;
     }
   }
   return v;

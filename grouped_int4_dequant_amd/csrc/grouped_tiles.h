@@ -121,11 +121,14 @@ __device__ __forceinline__ u4 load_unit(const uint16_t *p, int n) {
   } else if (n >= 8) {
     v = *reinterpret_cast<const u4_any *>(p);
   } else {
+    uint32_t x[8];  // (all asked for before any is used)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const uint32_t x = i < n ? (uint32_t)p[i] : 0u;
-      v[i >> 1] |= x << (16 * (i & 1));
+      x[i] = 0u;
+      if (i < n) x[i] = p[i];
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = x[2 * i] | x[2 * i + 1] << 16;
   }
   return v;
 }
@@ -948,13 +951,29 @@ bool takes_wide(const Args &a) {
   return a.vec && a.wide && at_least >= 128;
 }
 
+// A single matrix: rows of its tiles (64: small ones), by the time that they take over 256 CUs. A step of 64 terms costs a CU
+// 0.28 us in a small tile, 0.8 in one of 128 x 256 and 0.95 in one of 256 x 256, each of which has beside its steps a prologue
+// and stores of about 3, 6 and 9 us. 2048 rows, 2048 x 4096, forward: 78 us in small tiles, 58 in those of 128 rows.
+template <int Mode, typename Args>
+int dense_tile_rows(const Args &a) {
+  if (!a.vec || !a.wide) return kSmall;
+  const int64_t rows = Mode == kWgrad ? a.N : a.P, cols = Mode == kWgrad ? a.K : columns_of<Mode>(a), steps = cdiv(Mode == kFwd ? a.K : Mode == kDgrad ? a.N : a.P, kBR);
+  constexpr int kPer = Args::kGated ? 2 : 1;
+  const int64_t n64 = cdiv(rows, kSmall) * cdiv(cols, kSmall / kPer);
+  const int64_t t64 = (n64 > 256 ? n64 : 256) * (28 * steps + 100) / 256 + 200;  // in 10 ns
+  const int64_t t128 = cdiv(cdiv(rows, 128) * cdiv(cols, kWide / kPer), 256) * (80 * steps + 600);
+  const int64_t t256 = cdiv(cdiv(rows, kWide) * cdiv(cols, kWide / kPer), 256) * (95 * steps + 900);
+  if (Mode != kWgrad && t128 < t64 && t128 < t256) return 128;
+  return t256 < t64 ? kWide : kSmall;
+}
+
 template <typename Tr, int Mode, bool Vec, typename Args>
 hipError_t launch(const Args &a, hipStream_t s) {
   const int64_t used = a.G < a.P ? a.G : a.P;  // groups that can have rows
   const int J = columns_of<Mode>(a);
   constexpr int kPer = Args::kGated ? 2 : 1;  // columns of the product for one of the result
   if constexpr (Vec) {
-    const bool wide = takes_wide<Mode>(a);
+    const bool wide = Args::kDense ? dense_tile_rows<Mode>(a) != kSmall : takes_wide<Mode>(a);
     if constexpr (Mode != kWgrad && !Args::kEpilogue) {
       // Few rows whose weights are too few for wide tiles. Against small tiles at N = 1024, K = 2048, us, forward / input
       // gradient: 8 groups, 8 rows 9.4 / 9.0 against 13.2 / 10.5, 64 rows 11.6 / 9.0 against 13.6 / 11.2, 128 rows 18.6 / 11.6
@@ -971,15 +990,9 @@ hipError_t launch(const Args &a, hipStream_t s) {
       // hold many, by the average. Forward at 256 experts, N = 1024, K = 2048: 159 against 170 us at
       // 2 rows a group, 214 / 234 at 64, 380 / 385 at 256; 16 groups of 1024 rows: 301 / 284. Input gradient:
       // 162 / 171 at 2, 240 / 250 at 64, 305 / 288 at 128.
-      // A single matrix: by the rounds that the tiles make over 256 CUs, a tile of 128 rows taking a little over half
-      // the time of one of 256.
       if constexpr (Mode != kWgrad) {
-        if constexpr (Args::kDense) {
-          const int64_t tj = cdiv(J, kWide / kPer);
-          if (9 * cdiv(cdiv(a.P, 128) * tj, 256) < 16 * cdiv(cdiv(a.P, 256) * tj, 256)) return launch_wide<Tr, Mode, 128, Args>(a, s);
-        } else if (a.P < (int64_t)(Mode == kFwd ? 256 : 96) * a.G) {
-          return launch_wide<Tr, Mode, 128, Args>(a, s);
-        }
+        const bool half = Args::kDense ? dense_tile_rows<Mode>(a) == 128 : a.P < (int64_t)(Mode == kFwd ? 256 : 96) * a.G;
+        if (half) return launch_wide<Tr, Mode, 128, Args>(a, s);
       }
       return launch_wide<Tr, Mode, 256, Args>(a, s);
     }

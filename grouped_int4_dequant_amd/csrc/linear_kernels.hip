@@ -20,7 +20,7 @@ namespace {
 // from memory to operand registers and is read once; x comes from L2.
 template <typename Tr, bool Gated, int RB>
 __global__ __launch_bounds__(512) void linear_few_kernel(LinearArgs<Gated> a) {
-  constexpr int kDeep = RB == 1 ? 8 : RB == 2 ? 4 : 2;
+  constexpr int kDeep = 8, kXDeep = RB == 1 ? 8 : RB == 2 ? 4 : 2;  // requests of W, and of each row block of x, in flight
   __shared__ __attribute__((aligned(16))) f4 s_part[8][RB][64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -42,23 +42,27 @@ __global__ __launch_bounds__(512) void linear_few_kernel(LinearArgs<Gated> a) {
   Extra4 extra;
   if (mine) extra = extra4<Tr>(a, row, c, J - c);
   for (int k0 = 32 * wave; k0 < a.K; k0 += 256 * kDeep) {
-    s8 wv[kDeep], xv[kDeep][RB];
+    s8 wv[kDeep];
 #pragma unroll
     for (int u = 0; u < kDeep; ++u) {
       const int k = k0 + 256 * u + 8 * q4;
       wv[u] = w && k < a.K ? *reinterpret_cast<const s8 *>(w + k) : zero;
     }
 #pragma unroll
-    for (int u = 0; u < kDeep; ++u)
+    for (int u0 = 0; u0 < kDeep; u0 += kXDeep) {
+      s8 xv[kXDeep][RB];
 #pragma unroll
-      for (int b = 0; b < RB; ++b) {
-        const int k = k0 + 256 * u + 8 * q4;
-        xv[u][b] = x[b] && k < a.K ? *reinterpret_cast<const s8 *>(x[b] + k) : zero;
-      }
+      for (int u = 0; u < kXDeep; ++u)
 #pragma unroll
-    for (int u = 0; u < kDeep; ++u)
+        for (int b = 0; b < RB; ++b) {
+          const int k = k0 + 256 * (u0 + u) + 8 * q4;
+          xv[u][b] = x[b] && k < a.K ? *reinterpret_cast<const s8 *>(x[b] + k) : zero;
+        }
 #pragma unroll
-      for (int b = 0; b < RB; ++b) acc[b] = Tr::mfma(wv[u], xv[u][b], acc[b]);
+      for (int u = 0; u < kXDeep; ++u)
+#pragma unroll
+        for (int b = 0; b < RB; ++b) acc[b] = Tr::mfma(wv[u0 + u], xv[u][b], acc[b]);
+    }
   }
 #pragma unroll
   for (int b = 0; b < RB; ++b) s_part[wave][b][lane] = acc[b];
@@ -165,8 +169,18 @@ __device__ __forceinline__ void add_chunks(const ActGradArgs &a, int block, floa
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int col = block * 64 + lane;
   float f = 0.f;
-  if (col < a.N)
-    for (int c = wave; c < a.chunks; c += Waves) f += a.part[(int64_t)c * a.pitch + col];
+  if (col < a.N) {
+    for (int c = wave; c < a.chunks; c += 8 * Waves) {
+      float v[8];
+#pragma unroll
+      for (int y = 0; y < 8; ++y) {
+        v[y] = 0.f;
+        if (c + Waves * y < a.chunks) v[y] = a.part[(int64_t)(c + Waves * y) * a.pitch + col];
+      }
+#pragma unroll
+      for (int y = 0; y < 8; ++y) f += v[y];
+    }
+  }
   s_part[64 * wave + lane] = f;
   __syncthreads();
   if (wave != 0 || col >= a.N) return;
@@ -254,7 +268,7 @@ template <typename Tr>
 hipError_t linear_grad_of(const ActGradArgs &c, const DenseArgs &dx, const DenseArgs &dw, hipStream_t s) {
   const bool curved = c.act != MOE_ACT_NONE;
   // one launch for what may run side by side, where both products take small tiles
-  const bool small = dx.out && dw.out && c.T > 0 && !takes_wide<kDgrad>(dx) && !takes_wide<kWgrad>(dw) && dx.vec == dw.vec && !(dx.vec && c.T <= 64);
+  const bool small = dx.out && dw.out && c.T > 0 && dense_tile_rows<kDgrad>(dx) == kSmall && dense_tile_rows<kWgrad>(dw) == kSmall && dx.vec == dw.vec && !(dx.vec && c.T <= 64);
   const bool rows = small && !curved && c.T <= 1024;  // db from dy's rows, without chunks
   if (curved || (c.db && !rows)) {
     const hipError_t e = act_grad_of<Tr>(c, c.db && !small, s);

@@ -349,11 +349,18 @@ __global__ __launch_bounds__(1024) void norm_columns_kernel(NormGradArgs a, int 
   const int64_t kind = j == 0 ? 0 : j == 1 ? 2 : 1;
   const float *p = a.part + kind * a.chunks * a.pitch + col;
   const int begin = j < 2 ? 0 : (j - 2) * a.per_gate, end = j < 2 ? a.chunks : begin + a.per_gate;
-  const int run = (end - begin + 15) / 16;
-  const int c0 = min(begin + wave * run, end), c1 = min(c0 + run, end);
   float f = 0.f;
   if (col < a.d) {
-    for (int c = c0; c < c1; ++c) f += p[(int64_t)c * a.pitch];
+    for (int c = begin + wave; c < end; c += 128) {
+      float v[8];
+#pragma unroll
+      for (int y = 0; y < 8; ++y) {
+        v[y] = 0.f;
+        if (c + 16 * y < end) v[y] = p[(int64_t)(c + 16 * y) * a.pitch];
+      }
+#pragma unroll
+      for (int y = 0; y < 8; ++y) f += v[y];
+    }
   }
   s_part[wave][lane] = f;
   __syncthreads();
