@@ -17,12 +17,14 @@ struct Raw8 {
 };
 
 // Values at + 0 .. 7 of p, of which the first `left` exist (the others read as zeros).
-template <bool F32>
+// Whole: all eight, or (left <= 0) none.
+template <bool F32, bool Whole = false>
 __device__ __forceinline__ Raw8 load_raw8(const void *p, int64_t at, int left) {
   Raw8 v = {{0u, 0u, 0u, 0u}, {0u, 0u, 0u, 0u}};
+  if (Whole && left <= 0) return v;
   if constexpr (F32) {
     const float *q = static_cast<const float *>(p) + at;
-    if (left >= 8) {
+    if (Whole || left >= 8) {
       v.lo = __builtin_bit_cast(u4, (f4) * reinterpret_cast<const f4_elem *>(q));
       v.hi = __builtin_bit_cast(u4, (f4) * reinterpret_cast<const f4_elem *>(q + 4));
     } else {
@@ -40,7 +42,7 @@ __device__ __forceinline__ Raw8 load_raw8(const void *p, int64_t at, int left) {
     }
   } else {
     const uint16_t *q = static_cast<const uint16_t *>(p) + at;
-    if (left >= 8) {
+    if (Whole || left >= 8) {
       v.lo = *reinterpret_cast<const u4_elem *>(q);
     } else {
       uint32_t x[8];
@@ -64,18 +66,19 @@ __device__ __forceinline__ void widen8(const Raw8 &v, float *f) {
   }
 }
 // The same for an array whose type is known at run time.
-template <typename Tr>
+template <typename Tr, bool Whole = false>
 __device__ __forceinline__ void load8(const void *p, bool f32, int64_t at, int left, float *f) {
-  if (f32) widen8<Tr, true>(load_raw8<true>(p, at, left), f);
-  else widen8<Tr, false>(load_raw8<false>(p, at, left), f);
+  if (f32) widen8<Tr, true>(load_raw8<true, Whole>(p, at, left), f);
+  else widen8<Tr, false>(load_raw8<false, Whole>(p, at, left), f);
 }
 
 // Stores the first `left` of eight values, rounded to the array's type.
-template <typename Tr>
+template <typename Tr, bool Whole = false>
 __device__ __forceinline__ void store8(void *p, bool f32, int64_t at, int left, const float *f) {
+  if (Whole && left <= 0) return;
   if (f32) {
     float *q = static_cast<float *>(p) + at;
-    if (left >= 8) {
+    if (Whole || left >= 8) {
       *reinterpret_cast<f4_elem *>(q) = f4{f[0], f[1], f[2], f[3]};
       *reinterpret_cast<f4_elem *>(q + 4) = f4{f[4], f[5], f[6], f[7]};
     } else {
@@ -85,7 +88,7 @@ __device__ __forceinline__ void store8(void *p, bool f32, int64_t at, int left, 
     }
   } else {
     uint16_t *q = static_cast<uint16_t *>(p) + at;
-    if (left >= 8) {
+    if (Whole || left >= 8) {
       u4 v;
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = (uint32_t)Tr::from(f[2 * i]) | (uint32_t)Tr::from(f[2 * i + 1]) << 16;

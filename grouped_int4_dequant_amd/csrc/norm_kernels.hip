@@ -58,7 +58,7 @@ struct RowSum {
 
 __device__ __forceinline__ float root(float squares, float inv_d, float eps) { return 1.f / sqrtf(squares * inv_d + eps); }
 
-template <typename Tr, bool S32, int W, int V>
+template <typename Tr, bool S32, bool Whole, int W, int V>
 __global__ __launch_bounds__(threads_of<W>()) void norm_kernel(NormArgs a) {
   constexpr int kThreads = threads_of<W>(), G = kThreads / (64 * W);
   __shared__ float s_sum[4 * kThreads / 64];
@@ -76,8 +76,8 @@ __global__ __launch_bounds__(threads_of<W>()) void norm_kernel(NormArgs a) {
     const bool ok = row < a.T;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      if (a.o) o[v] = load_raw8<false>(a.o, (int64_t)row * a.ld_o + col[v], ok ? left[v] : 0);
-      if (a.x) x[v] = load_raw8<S32>(a.x, (int64_t)row * a.ld_x + col[v], ok ? left[v] : 0);
+      if (a.o) o[v] = load_raw8<false, Whole>(a.o, (int64_t)row * a.ld_o + col[v], ok ? left[v] : 0);
+      if (a.x) x[v] = load_raw8<S32, Whole>(a.x, (int64_t)row * a.ld_x + col[v], ok ? left[v] : 0);
     }
   };
   int row = blockIdx.x * G + g;
@@ -85,8 +85,8 @@ __global__ __launch_bounds__(threads_of<W>()) void norm_kernel(NormArgs a) {
   float wo[V][8], wn[V][8], gate[V][8];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    if (a.w_o) load8<Tr>(a.w_o, a.w_f32, col[v], left[v], wo[v]);
-    if (a.n) load8<Tr>(a.w_n, a.w_f32, col[v], left[v], wn[v]);
+    if (a.w_o) load8<Tr, Whole>(a.w_o, a.w_f32, col[v], left[v], wo[v]);
+    if (a.n) load8<Tr, Whole>(a.w_n, a.w_f32, col[v], left[v], wn[v]);
   }
   int have = -1;  // row of gate in registers
   const int step = gridDim.x * G;
@@ -107,7 +107,7 @@ __global__ __launch_bounds__(threads_of<W>()) void norm_kernel(NormArgs a) {
       if (a.gate && ok && row / a.period != have) {
         have = row / a.period;
 #pragma unroll
-        for (int v = 0; v < V; ++v) load8<Tr>(a.gate, a.w_f32, (int64_t)have * a.d + col[v], left[v], gate[v]);
+        for (int v = 0; v < V; ++v) load8<Tr, Whole>(a.gate, a.w_f32, (int64_t)have * a.d + col[v], left[v], gate[v]);
       }
       if (a.w_o) {
         float sq = 0.f;
@@ -136,7 +136,7 @@ __global__ __launch_bounds__(threads_of<W>()) void norm_kernel(NormArgs a) {
     }
     if (a.y && ok) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) store8<Tr>(a.y, S32, (int64_t)row * a.ld_y + col[v], left[v], y[v]);
+      for (int v = 0; v < V; ++v) store8<Tr, Whole>(a.y, S32, (int64_t)row * a.ld_y + col[v], left[v], y[v]);
     }
     if (a.n) {
       float sq = 0.f;
@@ -150,7 +150,7 @@ __global__ __launch_bounds__(threads_of<W>()) void norm_kernel(NormArgs a) {
         for (int v = 0; v < V; ++v) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) y[v][i] = y[v][i] * r * wn[v][i];
-          store8<Tr>(a.n, false, (int64_t)row * a.ld_n + col[v], left[v], y[v]);
+          store8<Tr, Whole>(a.n, false, (int64_t)row * a.ld_n + col[v], left[v], y[v]);
         }
       }
     }
@@ -158,10 +158,33 @@ __global__ __launch_bounds__(threads_of<W>()) void norm_kernel(NormArgs a) {
 }
 
 // One chunk of rows for each group of W waves.
-template <typename Tr, bool S32, int W, int V>
-__global__ __launch_bounds__(threads_of<W>()) void norm_grad_kernel(NormGradArgs a) {
+template <typename Tr, bool S32, bool Whole, int W, int V>
+__global__ __launch_bounds__(threads_of<W>(), W == 16 ? 4 : 3) void norm_grad_kernel(NormGradArgs a) {
   constexpr int kThreads = threads_of<W>(), G = kThreads / (64 * W);
   __shared__ float s_sum[4 * kThreads / 64];
+  // w_o, w_n and the gate as every lane uses them, in places of its own: they are read once a row, and leave
+  // registers for three workgroups a CU
+  constexpr bool kLds = 3 * V * 2 * 16 * kThreads <= 100 * 1024;
+  __shared__ f4 s_w[kLds ? 3 * V * 2 * kThreads : 1];
+  f4 own[kLds ? 1 : 3 * V * 2];
+  auto put = [&](int what, int v, const float *f) __attribute__((always_inline)) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const f4 x = {f[4 * h], f[4 * h + 1], f[4 * h + 2], f[4 * h + 3]};
+      if constexpr (kLds) s_w[((what * V + v) * 2 + h) * kThreads + threadIdx.x] = x;
+      else own[(what * V + v) * 2 + h] = x;
+    }
+  };
+  auto get = [&](int what, int v, float *f) __attribute__((always_inline)) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      f4 x;
+      if constexpr (kLds) x = s_w[((what * V + v) * 2 + h) * kThreads + threadIdx.x];
+      else x = own[(what * V + v) * 2 + h];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[4 * h + i] = x[i];
+    }
+  };
   RowSum<W> sum{s_sum};
   const int g = threadIdx.x / (64 * W), tid = threadIdx.x - g * 64 * W;
   const int chunk = blockIdx.x * G + g;
@@ -189,20 +212,27 @@ __global__ __launch_bounds__(threads_of<W>()) void norm_grad_kernel(NormGradArgs
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int n = ok ? left[v] : 0;
-      dy[v] = load_raw8<S32>(a.dy, (int64_t)row * a.ld_dy + col[v], a.dy ? n : 0);
+      dy[v] = load_raw8<S32, Whole>(a.dy, (int64_t)row * a.ld_dy + col[v], a.dy ? n : 0);
       if (a.dn) {
-        dn[v] = load_raw8<false>(a.dn, (int64_t)row * a.ld_dn + col[v], n);
-        y[v] = load_raw8<S32>(a.y, (int64_t)row * a.ld_y + col[v], n);
+        dn[v] = load_raw8<false, Whole>(a.dn, (int64_t)row * a.ld_dn + col[v], n);
+        y[v] = load_raw8<S32, Whole>(a.y, (int64_t)row * a.ld_y + col[v], n);
       }
-      if (a.o) o[v] = load_raw8<false>(a.o, (int64_t)row * a.ld_o + col[v], n);
+      if (a.o) o[v] = load_raw8<false, Whole>(a.o, (int64_t)row * a.ld_o + col[v], n);
     }
   };
   load(begin);
-  float wo[V][8], wn[V][8], gate[V][8], sum_o[V][8], sum_g[V][8], sum_n[V][8];
+  float sum_o[V][8], sum_g[V][8], sum_n[V][8];
+  float f8[8];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    if (a.w_o) load8<Tr>(a.w_o, a.w_f32, col[v], left[v], wo[v]);
-    if (a.dn) load8<Tr>(a.w_n, a.w_f32, col[v], left[v], wn[v]);
+    if (a.w_o) {
+      load8<Tr, Whole>(a.w_o, a.w_f32, col[v], left[v], f8);
+      put(0, v, f8);
+    }
+    if (a.dn) {
+      load8<Tr, Whole>(a.w_n, a.w_f32, col[v], left[v], f8);
+      put(1, v, f8);
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum_o[v][i] = sum_g[v][i] = sum_n[v][i] = 0.f;
   }
@@ -238,77 +268,92 @@ __global__ __launch_bounds__(threads_of<W>()) void norm_grad_kernel(NormGradArgs
     if (a.dn) {
       float sq = 0.f, dot = 0.f;
 #pragma unroll
-      for (int v = 0; v < V; ++v)
+      for (int v = 0; v < V; ++v) {
+        get(1, v, f8);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           sq += yf[v][i] * yf[v][i];
-          dot += yf[v][i] * wn[v][i] * df[v][i];
+          dot += yf[v][i] * f8[i] * df[v][i];
         }
+      }
       sum.two(sq, dot);
       const float r = root(sq, inv_d, a.eps), along = dot * r * inv_d;
       if (ok) {
 #pragma unroll
-        for (int v = 0; v < V; ++v)
+        for (int v = 0; v < V; ++v) {
+          get(1, v, f8);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const float hat = yf[v][i] * r;
             sum_n[v][i] += df[v][i] * hat;
-            gy[v][i] += r * (wn[v][i] * df[v][i] - hat * along);
+            gy[v][i] += r * (f8[i] * df[v][i] - hat * along);
           }
+        }
       }
     }
     if (a.dx && ok) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        float f[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = a.scale * gy[v][i];
-        store8<Tr>(a.dx, S32, (int64_t)row * a.ld_dx + col[v], left[v], f);
+        for (int i = 0; i < 8; ++i) f8[i] = a.scale * gy[v][i];
+        store8<Tr, Whole>(a.dx, S32, (int64_t)row * a.ld_dx + col[v], left[v], f8);
       }
     }
     if (!a.o) continue;
     if (a.gate && ok && row / a.period != have) {
       have = row / a.period;
 #pragma unroll
-      for (int v = 0; v < V; ++v) load8<Tr>(a.gate, a.w_f32, (int64_t)have * a.d + col[v], left[v], gate[v]);
+      for (int v = 0; v < V; ++v) {
+        load8<Tr, Whole>(a.gate, a.w_f32, (int64_t)have * a.d + col[v], left[v], f8);
+        put(2, v, f8);
+      }
     }
     if (a.w_o) {
       // mean(w_o gate gy o), beside the squares
       float dot = 0.f;
 #pragma unroll
-      for (int v = 0; v < V; ++v)
+      for (int v = 0; v < V; ++v) {
+        float w8[8];
+        get(0, v, w8);
+        if (a.gate) get(2, v, f8);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float dp = a.gate ? gate[v][i] * gy[v][i] : gy[v][i];
-          dot += left[v] > i ? wo[v][i] * dp * of[v][i] : 0.f;
+          const float t = w8[i] * gy[v][i] * (a.gate ? f8[i] : 1.f);  // w_o dp
+          dot += left[v] > i ? t * of[v][i] : 0.f;
         }
+      }
       sum.two(squares, dot);
       ro = root(squares, inv_d, a.eps);
       const float along = dot * ro * inv_d;
       if (ok) {
 #pragma unroll
-        for (int v = 0; v < V; ++v)
+        for (int v = 0; v < V; ++v) {
+          float w8[8];
+          get(0, v, w8);
+          if (a.gate) get(2, v, f8);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float hat = of[v][i] * ro;
-            sum_g[v][i] += gy[v][i] * hat * wo[v][i];
-            const float dp = a.gate ? gate[v][i] * gy[v][i] : gy[v][i];
+            const float hat = of[v][i] * ro, dp = a.gate ? f8[i] * gy[v][i] : gy[v][i];
+            sum_g[v][i] += gy[v][i] * hat * w8[i];
             sum_o[v][i] += dp * hat;
-            of[v][i] = ro * (wo[v][i] * dp - hat * along);
+            of[v][i] = ro * (w8[i] * dp - hat * along);
           }
+        }
       }
     } else if (ok) {
 #pragma unroll
-      for (int v = 0; v < V; ++v)
+      for (int v = 0; v < V; ++v) {
+        if (a.gate) get(2, v, f8);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           sum_g[v][i] += gy[v][i] * of[v][i];
-          of[v][i] = a.gate ? gate[v][i] * gy[v][i] : gy[v][i];
+          of[v][i] = a.gate ? f8[i] * gy[v][i] : gy[v][i];
         }
+      }
     }
     if (a.d_o && ok) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) store8<Tr>(a.d_o, false, (int64_t)row * a.ld_do + col[v], left[v], of[v]);
+      for (int v = 0; v < V; ++v) store8<Tr, Whole>(a.d_o, false, (int64_t)row * a.ld_do + col[v], left[v], of[v]);
     }
     if (a.dgate && a.per_gate == 0 && ok && (row + 1 == end || (row + 1) / a.period != have)) {  // the gate's last row
 #pragma unroll
@@ -316,11 +361,11 @@ __global__ __launch_bounds__(threads_of<W>()) void norm_grad_kernel(NormGradArgs
         const int64_t at = (int64_t)have * a.d + col[v];
         if (a.accumulate) {
           float f[8];
-          load8<Tr>(a.dgate, a.g_f32, at, left[v], f);
+          load8<Tr, Whole>(a.dgate, a.g_f32, at, left[v], f);
 #pragma unroll
           for (int i = 0; i < 8; ++i) sum_g[v][i] += f[i];
         }
-        store8<Tr>(a.dgate, a.g_f32, at, left[v], sum_g[v]);
+        store8<Tr, Whole>(a.dgate, a.g_f32, at, left[v], sum_g[v]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum_g[v][i] = 0.f;
       }
@@ -330,9 +375,9 @@ __global__ __launch_bounds__(threads_of<W>()) void norm_grad_kernel(NormGradArgs
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int64_t at = (int64_t)chunk * a.pitch + col[v], kind = (int64_t)a.chunks * a.pitch;
-    if (a.dw_o) store8<Tr>(a.part, true, at, left[v], sum_o[v]);
-    if (a.dgate && a.per_gate) store8<Tr>(a.part, true, at + kind, left[v], sum_g[v]);
-    if (a.dw_n) store8<Tr>(a.part, true, at + 2 * kind, left[v], sum_n[v]);
+    if (a.dw_o) store8<Tr, Whole>(a.part, true, at, left[v], sum_o[v]);
+    if (a.dgate && a.per_gate) store8<Tr, Whole>(a.part, true, at + kind, left[v], sum_g[v]);
+    if (a.dw_n) store8<Tr, Whole>(a.part, true, at + 2 * kind, left[v], sum_n[v]);
   }
 }
 
@@ -377,12 +422,17 @@ __global__ __launch_bounds__(1024) void norm_columns_kernel(NormGradArgs a, int 
   }
 }
 
+template <typename Tr, bool S32, bool Whole, int W, int V>
+hipError_t norm_at(const NormArgs &a, hipStream_t s) {
+  constexpr int G = threads_of<W>() / (64 * W);
+  // as many rows for every workgroup as 1024 workgroups of four waves need
+  const int64_t wgs = cdiv(a.T, G), most = 1024 / (W < 4 ? 1 : W / 4);
+  norm_kernel<Tr, S32, Whole, W, V><<<dim3((unsigned)cdiv(wgs, cdiv(wgs, most))), threads_of<W>(), 0, s>>>(a);
+  return hipGetLastError();
+}
 template <typename Tr, bool S32, int W, int V>
 hipError_t norm_of(const NormArgs &a, hipStream_t s) {
-  constexpr int G = threads_of<W>() / (64 * W);
-  const int64_t wgs = cdiv(a.T, G), most = 2048 / (W < 4 ? 1 : W / 4);
-  norm_kernel<Tr, S32, W, V><<<dim3((unsigned)(wgs < most ? wgs : most)), threads_of<W>(), 0, s>>>(a);
-  return hipGetLastError();
+  return a.d % 8 == 0 ? norm_at<Tr, S32, true, W, V>(a, s) : norm_at<Tr, S32, false, W, V>(a, s);
 }
 template <typename Tr, bool S32>
 hipError_t norm_by_width(const NormArgs &a, hipStream_t s) {
@@ -394,11 +444,15 @@ hipError_t norm_by_width(const NormArgs &a, hipStream_t s) {
   return norm_of<Tr, S32, 16, 2>(a, s);
 }
 
+template <typename Tr, bool S32, bool Whole, int W, int V>
+hipError_t grad_at(const NormGradArgs &a, hipStream_t s) {
+  constexpr int G = threads_of<W>() / (64 * W);
+  norm_grad_kernel<Tr, S32, Whole, W, V><<<dim3((unsigned)cdiv(a.chunks, G)), threads_of<W>(), 0, s>>>(a);
+  return hipGetLastError();
+}
 template <typename Tr, bool S32, int W, int V>
 hipError_t grad_of(const NormGradArgs &a, hipStream_t s) {
-  constexpr int G = threads_of<W>() / (64 * W);
-  norm_grad_kernel<Tr, S32, W, V><<<dim3((unsigned)cdiv(a.chunks, G)), threads_of<W>(), 0, s>>>(a);
-  return hipGetLastError();
+  return a.d % 8 == 0 ? grad_at<Tr, S32, true, W, V>(a, s) : grad_at<Tr, S32, false, W, V>(a, s);
 }
 template <typename Tr, bool S32>
 hipError_t grad_by_width(const NormGradArgs &a, hipStream_t s) {
@@ -429,9 +483,8 @@ hipError_t grad_all(const NormGradArgs &a, hipStream_t s) {
 }  // namespace
 
 NormChunks norm_chunks(int32_t T, int32_t period) {
-  // about 512 chunks: two workgroups a CU at four waves a row, and column sums of a sixteenth of
-  // the rows' bytes at 8192 rows
-  int32_t rows = (int32_t)cdiv(T > 0 ? T : 1, 512);
+  // about 768 chunks: three workgroups a CU at four waves a row
+  int32_t rows = (int32_t)cdiv(T > 0 ? T : 1, 768);
   if (period <= rows) {
     rows = rows / period * period;
     return {rows, (int32_t)cdiv(T, rows), 0};
