@@ -26,7 +26,8 @@ namespace moe {
 namespace {
 
 constexpr int kWaves = 8;   // of a gate/up workgroup
-constexpr int kDeep = 8;    // 16-byte requests of a lane in flight
+// Steps of weights asked for at once. One token's layer is a single round of items: everything is asked for at once there.
+constexpr int deep_of(bool one) { return one ? 16 : 8; }
 
 // Runs of eight 16-bit values; without Vec rows may end inside one.
 template <bool Vec>
@@ -131,66 +132,65 @@ __device__ __forceinline__ void make_plan(const FewArgs &a, FewLds &s) {
   if (tid == 0) a.plan->blocks = s.blocks;
 }
 
-// One token: its picks are the blocks.
+// One token: its picks are the blocks. A workgroup needs the first `need` of them only, the one whose items are
+// those of the last pick leaves all for the second kernel.
 template <int VPL>
-__device__ __forceinline__ void make_plan_one(const FewArgs &a, FewLds &s) {
-  if (threadIdx.x < 64) {
+__device__ __forceinline__ void make_plan_one(const FewArgs &a, FewLds &s, int need, bool writer) {
+  if (need > 0 && threadIdx.x < 64) {
     const int lane = threadIdx.x;
     int id;
     float g;
-    topk_wave<VPL>(a.logits, a.E, a.k, lane, id, g);
-    if (lane < a.k) s.expert[lane] = id;
-    if (blockIdx.x == 0 && lane < a.k) {
+    topk_wave<VPL>(a.logits, a.E, need, lane, id, g);
+    if (lane < need) s.expert[lane] = id;
+    if (writer && lane < a.k) {
       a.plan->expert[lane] = id;
       a.plan->gate[lane] = g;
       if (a.topk_ids) a.topk_ids[lane] = id;
       if (a.topk_w) a.topk_w[lane] = g;
     }
   }
-  __syncthreads();
+  lds_barrier();
 }
 
-// Inner values. bf16: three parts that add up to the fp32 value, each an array of its own;
-// fp16: fp32 (its parts would leave fp16's range).
-template <typename Tr>
-__device__ __forceinline__ void store_inner(void *h, int64_t part, int64_t at, f4 v, int left) {
-  if constexpr (std::is_same_v<Tr, Fp16>) {
-    float *q = static_cast<float *>(h) + at;
+// An inner value as three bf16 parts that add up to it, each an array of its own: leading, middle and
+// last eight bits, cut off rather than rounded, so that no rest changes its sign or leaves the range. Infinities and NaN
+// are all in the first part.
+__device__ __forceinline__ void store_inner(uint16_t *q, int64_t part, f4 v, int left) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < left) q[i] = v[i];
-  } else {
-    uint16_t *q = static_cast<uint16_t *>(h) + at;
+  for (int i = 0; i < 4; ++i) {
+    if (i >= left) break;
+    float rest = v[i];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (i >= left) break;
-      float rest = v[i];
-#pragma unroll
-      for (int p = 0; p < 3; ++p) {
-        // cut off, not rounded: the rest keeps its sign and stays finite; infinities and NaN have none
-        uint32_t b = __builtin_bit_cast(uint32_t, rest);
-        const bool whole = (b & 0x7f800000u) != 0x7f800000u;
-        if (!whole && (b & 0x007fffffu)) b |= 0x00400000u;  // NaN stays NaN
-        q[p * part + i] = (uint16_t)(b >> 16);
-        rest = whole ? rest - __builtin_bit_cast(float, b & 0xffff0000u) : 0.f;
-      }
+    for (int p = 0; p < 3; ++p) {
+      uint32_t b = __builtin_bit_cast(uint32_t, rest);
+      const bool finite = (b & 0x7f800000u) != 0x7f800000u;
+      if (!finite && (b & 0x007fffffu)) b |= 0x00400000u;  // NaN stays NaN
+      q[p * part + i] = (uint16_t)(b >> 16);
+      rest = finite ? rest - __builtin_bit_cast(float, b & 0xffff0000u) : 0.f;
     }
   }
 }
 
 // One: a single token.
 template <typename Tr, int VPL, bool Vec, bool One>
-__global__ __launch_bounds__(64 * kWaves) void few_gate_up_kernel(FewArgs a) {
+__global__ __launch_bounds__(64 * kWaves, 4) void few_gate_up_kernel(FewArgs a) {
+  constexpr int kDeep = deep_of(One), kX = 8;
   __shared__ FewLds s;
   __shared__ __attribute__((aligned(16))) f4 s_part[2][kWaves][64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int p16 = lane & 15, q4 = lane >> 4;
-  if constexpr (One) make_plan_one<VPL>(a, s);
-  else make_plan<VPL>(a, s);
   const int per = (a.f + 7) / 8, per_sh = (a.f_sh + 7) / 8;
   const int blocks_sh = a.f_sh > 0 ? (a.T + 15) / 16 : 0;
-  const int items_sh = blocks_sh * per_sh, items = items_sh + (One ? a.k : s.blocks) * per;
+  const int items_sh = blocks_sh * per_sh;
+  if constexpr (One) {
+    // (every workgroup has one round of items here)
+    const int last = min(((int)blockIdx.x + 1) * (kWaves >> a.share) - 1, items_sh + a.k * per - 1);
+    make_plan_one<VPL>(a, s, last < items_sh ? 0 : (last - items_sh) / per + 1, last == items_sh + a.k * per - 1);
+  } else {
+    make_plan<VPL>(a, s);
+  }
+  const int items = items_sh + (One ? a.k : s.blocks) * per;
   // the waves of a workgroup take kWaves >> share items at a time; `sub` has n steps of 32 k of the sum, from kb on
   const int slots = kWaves >> a.share, slot = wave >> a.share, sub = wave & ((1 << a.share) - 1);
   const int n = (((a.d + 31) >> 5) + (1 << a.share) - 1) >> a.share;
@@ -221,18 +221,21 @@ __global__ __launch_bounds__(64 * kWaves) void few_gate_up_kernel(FewArgs a) {
     t.x = a.x + (int64_t)(One || t.pair < 0 ? 0 : t.shared ? t.pair : t.pair / a.k) * a.ld_x;
     return t;
   };
-  s8 wv[kDeep], xv[kDeep];
+  s8 wv[kDeep], xv[kX];
+  auto request_x = [&](const Where &t, int y0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int y = 0; y < kX; ++y) {
+      const int k = kb + 32 * (y0 + y);
+      xv[y] = load_w<Vec>(t.x + k, t.pair >= 0 ? kend - k : 0);
+    }
+  };
   auto request = [&](const Where &t, int y0, int item) __attribute__((always_inline)) {
 #pragma unroll
     for (int y = 0; y < kDeep; ++y) {
       const int k = kb + 32 * (y0 + y);
       wv[y] = load_w<Vec>(t.w + k, item < items ? kend - k : 0);
     }
-#pragma unroll
-    for (int y = 0; y < kDeep; ++y) {
-      const int k = kb + 32 * (y0 + y);
-      xv[y] = load_w<Vec>(t.x + k, t.pair >= 0 ? kend - k : 0);
-    }
+    request_x(t, y0);
   };
   const int rounds = (items + slots - 1) / slots;
   int buf = 0, round = blockIdx.x;
@@ -242,12 +245,14 @@ __global__ __launch_bounds__(64 * kWaves) void few_gate_up_kernel(FewArgs a) {
   for (; round < rounds; round += gridDim.x) {
     const int item = round * slots + slot;
     f4 acc = {0.f, 0.f, 0.f, 0.f};
+    for (int y0 = 0; y0 < n; y0 += kDeep) {
+      if (y0 > 0) request(at, y0, item);
 #pragma unroll
-    for (int y = 0; y < kDeep; ++y) acc = Tr::mfma(wv[y], xv[y], acc);
-    for (int y0 = kDeep; y0 < n; y0 += kDeep) {
-      request(at, y0, item);
+      for (int h = 0; h < kDeep; h += kX) {
+        if (h > 0) request_x(at, y0 + h);
 #pragma unroll
-      for (int y = 0; y < kDeep; ++y) acc = Tr::mfma(wv[y], xv[y], acc);
+        for (int y = 0; y < kX; ++y) acc = Tr::mfma(wv[h + y], xv[y], acc);
+      }
     }
     const Where done = at;
     if (round + (int)gridDim.x < rounds) {
@@ -270,46 +275,50 @@ __global__ __launch_bounds__(64 * kWaves) void few_gate_up_kernel(FewArgs a) {
       for (int i = 0; i < 4; ++i) h[i] = times_sigmoid(acc[i], acc[i]) * __shfl(acc[i], (lane + 32) & 63);
       const int c = done.c0 + 4 * q4, left = (done.shared ? a.f_sh : a.f) - c;
       if (done.pair >= 0 && q4 < 2 && left > 0) {
-        if (done.shared) store_inner<Tr>(a.h_sh, (int64_t)a.T * a.pitch_sh, (int64_t)done.pair * a.pitch_sh + c, h, left);
-        else store_inner<Tr>(a.h, (int64_t)a.T * a.k * a.pitch, (int64_t)done.pair * a.pitch + c, h, left);
+        if (done.shared) store_inner(a.h_sh + (int64_t)done.pair * a.pitch_sh + c, (int64_t)a.T * a.pitch_sh, h, left);
+        else store_inner(a.h + (int64_t)done.pair * a.pitch + c, (int64_t)a.T * a.k * a.pitch, h, left);
       }
     }
   }
 }
 
-// h of one pair, eight values from k on, times a run of W.
-template <typename Tr, bool Vec>
-struct Inner;
-template <bool Vec>
-struct Inner<Bf16, Vec> {
-  s8 v[3];
-  __device__ __forceinline__ void load(const void *h, int64_t part, int64_t at, int left) {
+// Eight weights times a pair's eight inner values (their three parts), 32 terms a matrix instruction. bf16
+// weights as they are; fp16 ones as two bf16 parts, of eight bits and of the three that are left.
+template <typename Tr>
+__device__ __forceinline__ f4 times_inner(const s8 (&w)[std::is_same_v<Tr, Fp16> ? 2 : 1], const s8 (&h)[3], f4 acc) {
 #pragma unroll
-    for (int p = 0; p < 3; ++p) v[p] = load_w<Vec>(static_cast<const uint16_t *>(h) + p * part + at, left);
-  }
-  __device__ __forceinline__ f4 times(s8 w, f4 acc) const {
+  for (int p = 0; p < 3; ++p) acc = Bf16::mfma(w[0], h[p], acc);
+  if constexpr (std::is_same_v<Tr, Fp16>) {
 #pragma unroll
-    for (int p = 0; p < 3; ++p) acc = Bf16::mfma(w, v[p], acc);
-    return acc;
+    for (int p = 0; p < 3; ++p) acc = Bf16::mfma(w[1], h[p], acc);
   }
-};
-template <bool Vec>
-struct Inner<Fp16, Vec> {
-  Raw8 v;
-  __device__ __forceinline__ void load(const void *h, int64_t, int64_t at, int left) { v = load_raw8<true>(h, at, left); }
-  __device__ __forceinline__ f4 times(s8 w, f4 acc) const {
-    // instruction i takes value i of each lane's run: k = 8 q4 + i
+  return acc;
+}
+template <typename Tr>
+__device__ __forceinline__ void weight_parts(s8 w, s8 (&out)[std::is_same_v<Tr, Fp16> ? 2 : 1]) {
+  if constexpr (std::is_same_v<Tr, Fp16>) {
+    u4 hi, lo;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      acc = __builtin_amdgcn_mfma_f32_16x16x4f32(Fp16::to((uint16_t)w[i]), __builtin_bit_cast(float, i < 4 ? v.lo[i] : v.hi[i - 4]), acc, 0, 0, 0);
-    return acc;
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t x = __builtin_bit_cast(uint32_t, Fp16::to((uint16_t)w[2 * i])), y = __builtin_bit_cast(uint32_t, Fp16::to((uint16_t)w[2 * i + 1]));
+      hi[i] = (x >> 16) | (y & 0xffff0000u);
+      const float rx = __builtin_bit_cast(float, x) - __builtin_bit_cast(float, x & 0xffff0000u);
+      const float ry = __builtin_bit_cast(float, y) - __builtin_bit_cast(float, y & 0xffff0000u);
+      lo[i] = (__builtin_bit_cast(uint32_t, rx) >> 16) | (__builtin_bit_cast(uint32_t, ry) & 0xffff0000u);
+    }
+    out[0] = __builtin_bit_cast(s8, hi);
+    out[1] = __builtin_bit_cast(s8, lo);
+  } else {
+    out[0] = w;
   }
-};
+}
 
-// As many waves as there are blocks, 4 to 16.
+// As many waves as share the blocks evenly, 4 to 12.
+constexpr int kDownWaves = 12;
 template <typename Tr, bool Vec>
-__global__ __launch_bounds__(1024) void few_down_kernel(FewArgs a) {
+__global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewArgs a) {
   constexpr int kPitch = 12;  // floats a row of s_o: 8 and a gap that keeps rows off each other's banks
+  constexpr int kW = 16, kH = std::is_same_v<Tr, Fp16> ? 2 : 4;  // steps of weights asked for at once, and of inner values
   __shared__ __attribute__((aligned(16))) float s_o[(kFewPairs + kFewTokens) * kPitch];
   __shared__ float s_gate[kFewPairs];
   const int tid = threadIdx.x, lane = tid & 63, waves = blockDim.x >> 6;
@@ -321,8 +330,7 @@ __global__ __launch_bounds__(1024) void few_down_kernel(FewArgs a) {
   const int blocks = one ? a.k : a.plan->blocks, blocks_sh = a.f_sh > 0 ? (a.T + 15) / 16 : 0;
 
   struct Where {
-    const uint16_t *w;
-    const void *h;
+    const uint16_t *w, *h;
     int64_t part;
     int kb, kend, n;  // the lane's half of the sum, and its steps of 32
     int pitch, pair[2], rows;  // the lane's pairs of the block's first and second eight
@@ -330,7 +338,8 @@ __global__ __launch_bounds__(1024) void few_down_kernel(FewArgs a) {
   };
   auto locate = [&](int b) __attribute__((always_inline)) {
     Where t;
-    t.shared = b >= blocks;
+    t.shared = b < blocks_sh;  // the shared expert first: nothing of the plan is waited for
+    b -= blocks_sh;
     const int f = t.shared ? a.f_sh : a.f, half = ((f + 63) >> 6) * 32;
     t.n = half >> 5;
     t.kb = (p16 & 8 ? half : 0) + 8 * q4;
@@ -339,7 +348,7 @@ __global__ __launch_bounds__(1024) void few_down_kernel(FewArgs a) {
     t.h = t.shared ? a.h_sh : a.h;
     t.part = (int64_t)(t.shared ? a.T : pairs) * t.pitch;
     t.w = (t.shared ? a.sh_dn : a.dn + (int64_t)a.plan->expert[b] * a.d * a.f) + (int64_t)row * f;
-    const int first = t.shared ? 16 * (b - blocks) : one ? b : a.plan->first[b];
+    const int first = t.shared ? 16 * (b + blocks_sh) : one ? b : a.plan->first[b];
     t.rows = t.shared ? min(a.T - first, 16) : one ? 1 : a.plan->rows[b];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
@@ -348,10 +357,10 @@ __global__ __launch_bounds__(1024) void few_down_kernel(FewArgs a) {
     }
     return t;
   };
-  s8 wv[kDeep];
+  s8 wv[kW];
   auto request = [&](const Where &t, int y0) __attribute__((always_inline)) {
 #pragma unroll
-    for (int y = 0; y < kDeep; ++y) {
+    for (int y = 0; y < kW; ++y) {
       const int k = t.kb + 32 * (y0 + y);
       wv[y] = load_w<Vec>(t.w + k, t.kend - k);
     }
@@ -367,21 +376,62 @@ __global__ __launch_bounds__(1024) void few_down_kernel(FewArgs a) {
     f4 acc[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) acc[x] = f4{0.f, 0.f, 0.f, 0.f};
-    for (int y0 = 0; y0 < at.n; y0 += kDeep) {
+    for (int y0 = 0; y0 < at.n; y0 += kW) {
       if (y0 > 0) request(at, y0);
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        if (8 * x >= at.rows) break;
+      for (int g = 0; g < kW; g += kH) {
+        if (y0 + g >= at.n) break;
+        s8 parts[kH][std::is_same_v<Tr, Fp16> ? 2 : 1];
 #pragma unroll
-        for (int y = 0; y < kDeep; ++y) {
-          const int k = at.kb + 32 * (y0 + y);
-          Inner<Tr, Vec> hv;
-          hv.load(at.h, at.part, (int64_t)max(at.pair[x], 0) * at.pitch + k, at.pair[x] >= 0 ? at.kend - k : 0);
-          acc[x] = hv.times(wv[y], acc[x]);
+        for (int x = 0; x < 2; ++x) {
+          if (8 * x >= at.rows) break;
+          s8 hv[kH][3];
+          const uint16_t *h = at.h + (int64_t)max(at.pair[x], 0) * at.pitch;
+#pragma unroll
+          for (int y = 0; y < kH; ++y) {
+            const int k = at.kb + 32 * (y0 + g + y);
+#pragma unroll
+            for (int p = 0; p < 3; ++p) hv[y][p] = load_w<Vec>(h + p * at.part + k, at.pair[x] >= 0 ? at.kend - k : 0);
+          }
+          if (x == 0) {
+#pragma unroll
+            for (int y = 0; y < kH; ++y) weight_parts<Tr>(wv[g + y], parts[y]);
+          }
+#pragma unroll
+          for (int y = 0; y < kH; ++y) acc[x] = times_inner<Tr>(parts[y], hv[y], acc[x]);
         }
       }
     }
+    // lane: pair p16 % 8 and half p16 / 8 of the sum against rows 4 q4 .. of the 16; those of its own half count.
+    // Where a sum is not finite, parts may have met that the values don't know (an infinite weight times a part
+    // without bits): then it is formed once more, from whole values on the fp32 instruction.
+    const bool counts = (p16 >> 3) == (q4 >> 1);
     const Where done = at;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      if (8 * x >= done.rows) break;
+      bool finite = true;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) finite = finite && __builtin_fabsf(acc[x][i]) < __builtin_inff();
+      if (__ballot(counts && !finite) == 0) continue;
+      f4 again = {0.f, 0.f, 0.f, 0.f};
+      const uint16_t *h = done.h + (int64_t)max(done.pair[x], 0) * done.pitch;
+#pragma unroll 1
+      for (int y = 0; y < done.n; ++y) {
+        const int k = done.kb + 32 * y;
+        const s8 w = load_w<Vec>(done.w + k, done.kend - k);
+        s8 hv[3];
+#pragma unroll
+        for (int p = 0; p < 3; ++p) hv[p] = load_w<Vec>(h + p * done.part + k, done.pair[x] >= 0 ? done.kend - k : 0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {  // instruction i takes value i of each lane's run: k = 8 q4 + i
+          const float v = (Bf16::to((uint16_t)hv[0][i]) + Bf16::to((uint16_t)hv[1][i])) + Bf16::to((uint16_t)hv[2][i]);
+          again = __builtin_amdgcn_mfma_f32_16x16x4f32(Tr::to((uint16_t)w[i]), v, again, 0, 0, 0);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[x][i] = __builtin_fabsf(acc[x][i]) < __builtin_inff() ? acc[x][i] : again[i];
+    }
     b += waves;
     if (b < blocks + blocks_sh) {
       at = locate(b);
@@ -390,7 +440,6 @@ __global__ __launch_bounds__(1024) void few_down_kernel(FewArgs a) {
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       if (8 * x >= done.rows) break;
-      // lane: pair p16 % 8 and half p16 / 8 of the sum against rows 4 q4 .. of the 16; those of its own half count
       f4 v;
 #pragma unroll
       for (int i = 0; i < 4; ++i) v[i] = acc[x][i] + __shfl(acc[x][i], (lane + 40) & 63);
@@ -420,16 +469,16 @@ hipError_t few_of(FewArgs a, hipStream_t s) {
   const int64_t blocks_sh = a.f_sh > 0 ? cdiv(a.T, 16) : 0;
   const int64_t pairs = (int64_t)a.T * a.k, blocks = (a.E < pairs ? a.E : pairs) + pairs / 16;  // at most
   const int64_t items = blocks * cdiv(a.f, 8) + blocks_sh * cdiv(a.f_sh, 8);
-  // a wave's part of a sum is at most kDeep steps, where eight waves can make it so
+  // a wave's part of a sum is what it asks for at once, where eight waves can make it so
   a.share = 0;
-  while (a.share < 3 && ((a.d + 31) / 32 + (1 << a.share) - 1) >> a.share > kDeep) ++a.share;
+  while (a.share < 3 && ((a.d + 31) / 32 + (1 << a.share) - 1) >> a.share > deep_of(a.T == 1)) ++a.share;
   const int64_t rounds = cdiv(items, kWaves >> a.share);
   const dim3 grid((unsigned)(a.T == 1 || rounds < 512 ? rounds : 512));
   if (a.T == 1) few_gate_up_kernel<Tr, VPL, Vec, true><<<grid, 64 * kWaves, 0, s>>>(a);
   else few_gate_up_kernel<Tr, VPL, Vec, false><<<grid, 64 * kWaves, 0, s>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int64_t waves = blocks + blocks_sh < 4 ? 4 : blocks + blocks_sh > 16 ? 16 : blocks + blocks_sh;
+  const int64_t n = blocks + blocks_sh, even = cdiv(n, cdiv(n, kDownWaves)), waves = even < 4 ? 4 : even;
   few_down_kernel<Tr, Vec><<<dim3((unsigned)cdiv(a.d, 8)), (unsigned)(64 * waves), 0, s>>>(a);
   return hipGetLastError();
 }
@@ -440,7 +489,7 @@ hipError_t few_vec(const FewArgs &a, hipStream_t s) {
 }
 template <typename Tr>
 hipError_t few_experts(const FewArgs &a, hipStream_t s) {
-  return a.E <= 256 ? few_vec<Tr, 4>(a, s) : few_vec<Tr, 16>(a, s);
+  return a.E <= 64 ? few_vec<Tr, 1>(a, s) : a.E <= 256 ? few_vec<Tr, 4>(a, s) : few_vec<Tr, 16>(a, s);
 }
 
 }  // namespace

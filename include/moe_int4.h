@@ -764,7 +764,7 @@ int moe_residual_norm_backward(int32_t dtype, const void *dy, int64_t lddy, cons
  *             the same time, in replayed graphs too, need one each
  * Each picked expert's weights are read once for all its tokens. The products of x and of
  * FFN's inner values are summed in fp32; the inner values are held in fp32 and enter the second product
- * whole (in bf16 as three 16-bit parts, whose bits below 2^-133 are lost). The k experts are added in slot
+ * whole (as three 16-bit parts, whose bits below 2^-133 are lost). The k experts are added in slot
  * order, then the shared one, then `add`. A row's result does not depend on the other rows of the call.
  * Errors: MOE_EINVAL (null or misaligned pointer, unknown type, T < 0, a size < 1, f_sh < 0, k > E, a stride
  * below the width), MOE_EUNSUPPORTED (E > MOE_MAX_EXPERTS, k > 64, T > MOE_MAX_FEW_TOKENS,

@@ -120,6 +120,38 @@ def test_infinities_and_nan_stay_in_their_rows(moe):
     assert torch.equal(got[rest], clean[rest]) and torch.isnan(got[3]).all() and not torch.isfinite(got[9]).any()
 
 
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("shape", ["two", "batch", "crowd", "tail_f"])
+def test_infinite_weights_and_inner_values(moe, dtype, shape):
+    """Infinite weights of the second product and inner values beyond the type give the formula's infinities, and only there."""
+    p = problem(shape, dtype, seed=6)
+    p["sh_gu"] = p["sh_dn"] = None
+    T, k = p["x"].shape[0], p["k"]
+    clean = moe.few_tokens_layer(**p, out_dtype=F4)
+    ids = torch.empty((T, k), dtype=torch.int32, device="cuda")
+    e = int(torch.argmax(p["logits"][0]))
+    q = dict(p, dn=p["dn"].clone(), gu=p["gu"].clone())
+    q["dn"][e, 3, 5] = float("inf")       # column 3 of y
+    q["dn"][e, 8, 0] = -float("inf")      # column 8
+    q["gu"][e, 0] = 0.0                   # inner value 0 is zero: zero times infinity
+    got = moe.few_tokens_layer(**q, out_dtype=F4, topk_ids=ids)
+    hit = (ids == e).any(1)
+    base = moe.few_tokens_layer(**dict(q, dn=p["dn"]), out_dtype=F4)
+    cols = [c for c in range(got.shape[1]) if c not in (3, 8)]
+    assert torch.equal(got[:, cols], base[:, cols]) and torch.equal(got[~hit], clean[~hit])
+    x, g = R.d(p["x"]), R.d(q["gu"][e])
+    f = g.shape[0] // 2
+    h5 = R.curve("silu", x @ g[5]) * (x @ g[f + 5])
+    for t in hit.nonzero()[:, 0].tolist():
+        assert torch.isinf(got[t, 3]) and torch.sign(got[t, 3]).item() == torch.sign(h5[t]).item() and torch.isnan(got[t, 8])
+    # an infinite inner value against finite weights
+    q = dict(p, gu=p["gu"].clone())
+    q["gu"][e, 2], q["gu"][e, f + 2] = float("inf"), 0.5
+    x1 = dict(q, x=p["x"].abs() + 1, dn=p["dn"].abs() + 1)
+    got = moe.few_tokens_layer(**x1, out_dtype=F4)
+    assert (got[hit] == float("inf")).all() and torch.isfinite(got[~hit]).all()
+
+
 def test_no_rows(moe):
     p = problem("two", BF)
     y = moe.few_tokens_layer(**dict(p, x=p["x"][:0], logits=p["logits"][:0]))
