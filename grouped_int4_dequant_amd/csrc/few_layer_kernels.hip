@@ -313,32 +313,49 @@ __device__ __forceinline__ void weight_parts(s8 w, s8 (&out)[std::is_same_v<Tr, 
   }
 }
 
-// As many waves as share the blocks evenly, 4 to 12.
-constexpr int kDownWaves = 12;
-template <typename Tr, bool Vec>
-__global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewArgs a) {
+// As many waves as share the blocks evenly: up to 12 for one token, whose blocks are its picks, else 8, whose registers
+// then hold both eights' inner values. 16 tokens of 8 of 256 experts, 2048 x 512: 57 us for 216 MB; 16 waves of half the registers
+// 59, the next block's weights asked for a block ahead 53 (and 26 against 22 in fp16, which then spills).
+constexpr int down_waves(bool one) { return one ? 12 : 8; }
+template <typename Tr, bool Vec, bool One>
+__global__ __launch_bounds__(64 * down_waves(One)) void few_down_kernel(FewArgs a) {
   constexpr int kPitch = 12;  // floats a row of s_o: 8 and a gap that keeps rows off each other's banks
-  constexpr int kW = 16, kH = std::is_same_v<Tr, Fp16> ? 2 : 4;  // steps of weights asked for at once, and of inner values
-  __shared__ __attribute__((aligned(16))) float s_o[(kFewPairs + kFewTokens) * kPitch];
-  __shared__ float s_gate[kFewPairs];
+  constexpr int kW = 16, kH = 4;  // steps of weights asked for at once, and of inner values
+  constexpr int kX = One ? 1 : 2;  // eights of a block's pairs
+  __shared__ __attribute__((aligned(16))) float s_o[(One ? 65 : kFewPairs + kFewTokens) * kPitch];
+  __shared__ FewPlan s;  // what the first kernel left
   const int tid = threadIdx.x, lane = tid & 63, waves = blockDim.x >> 6;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int p16 = lane & 15, q4 = lane >> 4, p8 = p16 & 7;
   const int n0 = 8 * blockIdx.x, pairs = a.T * a.k;
   const int row = min(n0 + p8, a.d - 1);  // rows past the last repeat it
-  const bool one = a.T == 1;
-  const int blocks = one ? a.k : a.plan->blocks, blocks_sh = a.f_sh > 0 ? (a.T + 15) / 16 : 0;
+  const int blocks_sh = a.f_sh > 0 ? (a.T + 15) / 16 : 0;
+  int blocks;
+  if constexpr (One) {
+    blocks = a.k;
+  } else {
+    // all of it in one trip, whatever is in use
+    for (int i = tid; i < pairs; i += blockDim.x) {
+      s.expert[i] = a.plan->expert[i];
+      s.first[i] = a.plan->first[i];
+      s.rows[i] = a.plan->rows[i];
+      s.pair[i] = a.plan->pair[i];
+    }
+    blocks = a.plan->blocks;
+    lds_barrier();
+  }
+  for (int i = tid; i < pairs; i += blockDim.x) s.gate[i] = a.plan->gate[i];
 
   struct Where {
     const uint16_t *w, *h;
     int64_t part;
     int kb, kend, n;  // the lane's half of the sum, and its steps of 32
-    int pitch, pair[2], rows;  // the lane's pairs of the block's first and second eight
+    int pitch, pair[kX], rows;  // the lane's pairs of the block's first and second eight
     bool shared;
   };
   auto locate = [&](int b) __attribute__((always_inline)) {
     Where t;
-    t.shared = b < blocks_sh;  // the shared expert first: nothing of the plan is waited for
+    t.shared = b < blocks_sh;  // the shared expert first
     b -= blocks_sh;
     const int f = t.shared ? a.f_sh : a.f, half = ((f + 63) >> 6) * 32;
     t.n = half >> 5;
@@ -347,13 +364,14 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewArgs a) {
     t.pitch = t.shared ? a.pitch_sh : a.pitch;
     t.h = t.shared ? a.h_sh : a.h;
     t.part = (int64_t)(t.shared ? a.T : pairs) * t.pitch;
-    t.w = (t.shared ? a.sh_dn : a.dn + (int64_t)a.plan->expert[b] * a.d * a.f) + (int64_t)row * f;
-    const int first = t.shared ? 16 * (b + blocks_sh) : one ? b : a.plan->first[b];
-    t.rows = t.shared ? min(a.T - first, 16) : one ? 1 : a.plan->rows[b];
+    const int e = t.shared ? 0 : One ? a.plan->expert[b] : s.expert[b];
+    t.w = (t.shared ? a.sh_dn : a.dn + (int64_t)e * a.d * a.f) + (int64_t)row * f;
+    const int first = t.shared ? 16 * (b + blocks_sh) : One ? b : s.first[b];
+    t.rows = One ? 1 : t.shared ? min(a.T - first, 16) : s.rows[b];
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
+    for (int x = 0; x < kX; ++x) {
       const int r = 8 * x + p8;
-      t.pair[x] = r >= t.rows ? -1 : t.shared || one ? first + r : a.plan->pair[first + r];
+      t.pair[x] = r >= t.rows ? -1 : t.shared || One ? first + r : s.pair[first + r];
     }
     return t;
   };
@@ -371,34 +389,36 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewArgs a) {
     at = locate(b);
     request(at, 0);
   }
-  for (int i = tid; i < pairs; i += blockDim.x) s_gate[i] = a.plan->gate[i];
   while (b < blocks + blocks_sh) {
-    f4 acc[2];
+    f4 acc[kX];
 #pragma unroll
-    for (int x = 0; x < 2; ++x) acc[x] = f4{0.f, 0.f, 0.f, 0.f};
+    for (int x = 0; x < kX; ++x) acc[x] = f4{0.f, 0.f, 0.f, 0.f};
     for (int y0 = 0; y0 < at.n; y0 += kW) {
       if (y0 > 0) request(at, y0);
 #pragma unroll
       for (int g = 0; g < kW; g += kH) {
         if (y0 + g >= at.n) break;
-        s8 parts[kH][std::is_same_v<Tr, Fp16> ? 2 : 1];
+        s8 hv[kX][kH][3];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
+        for (int x = 0; x < kX; ++x) {
           if (8 * x >= at.rows) break;
-          s8 hv[kH][3];
           const uint16_t *h = at.h + (int64_t)max(at.pair[x], 0) * at.pitch;
 #pragma unroll
           for (int y = 0; y < kH; ++y) {
             const int k = at.kb + 32 * (y0 + g + y);
 #pragma unroll
-            for (int p = 0; p < 3; ++p) hv[y][p] = load_w<Vec>(h + p * at.part + k, at.pair[x] >= 0 ? at.kend - k : 0);
+            for (int p = 0; p < 3; ++p) hv[x][y][p] = load_w<Vec>(h + p * at.part + k, at.pair[x] >= 0 ? at.kend - k : 0);
           }
-          if (x == 0) {
+        }
 #pragma unroll
-            for (int y = 0; y < kH; ++y) weight_parts<Tr>(wv[g + y], parts[y]);
+        for (int y = 0; y < kH; ++y) {
+          s8 parts[std::is_same_v<Tr, Fp16> ? 2 : 1];
+          weight_parts<Tr>(wv[g + y], parts);
+#pragma unroll
+          for (int x = 0; x < kX; ++x) {
+            if (8 * x >= at.rows) break;
+            acc[x] = times_inner<Tr>(parts, hv[x][y], acc[x]);
           }
-#pragma unroll
-          for (int y = 0; y < kH; ++y) acc[x] = times_inner<Tr>(parts[y], hv[y], acc[x]);
         }
       }
     }
@@ -408,7 +428,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewArgs a) {
     const bool counts = (p16 >> 3) == (q4 >> 1);
     const Where done = at;
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
+    for (int x = 0; x < kX; ++x) {
       if (8 * x >= done.rows) break;
       bool finite = true;
 #pragma unroll
@@ -438,7 +458,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewArgs a) {
       request(at, 0);
     }
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
+    for (int x = 0; x < kX; ++x) {
       if (8 * x >= done.rows) break;
       f4 v;
 #pragma unroll
@@ -452,7 +472,7 @@ __global__ __launch_bounds__(64 * kDownWaves) void few_down_kernel(FewArgs a) {
     const int t = i >> 3, c = i & 7;
     if (n0 + c >= a.d) continue;
     float y = 0.f;
-    for (int j = 0; j < a.k; ++j) y += s_gate[t * a.k + j] * s_o[(t * a.k + j) * kPitch + c];
+    for (int j = 0; j < a.k; ++j) y += s.gate[t * a.k + j] * s_o[(t * a.k + j) * kPitch + c];
     if (a.f_sh > 0) y += s_o[(pairs + t) * kPitch + c];
     if (a.y_f32) {
       if (a.add) y += static_cast<const float *>(a.add)[t * a.ld_add + n0 + c];
@@ -478,8 +498,10 @@ hipError_t few_of(FewArgs a, hipStream_t s) {
   else few_gate_up_kernel<Tr, VPL, Vec, false><<<grid, 64 * kWaves, 0, s>>>(a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int64_t n = blocks + blocks_sh, even = cdiv(n, cdiv(n, kDownWaves)), waves = even < 4 ? 4 : even;
-  few_down_kernel<Tr, Vec><<<dim3((unsigned)cdiv(a.d, 8)), (unsigned)(64 * waves), 0, s>>>(a);
+  const int64_t n = blocks + blocks_sh, even = cdiv(n, cdiv(n, down_waves(a.T == 1))), waves = even < 4 ? 4 : even;
+  const dim3 groups((unsigned)cdiv(a.d, 8));
+  if (a.T == 1) few_down_kernel<Tr, Vec, true><<<groups, (unsigned)(64 * waves), 0, s>>>(a);
+  else few_down_kernel<Tr, Vec, false><<<groups, (unsigned)(64 * waves), 0, s>>>(a);
   return hipGetLastError();
 }
 template <typename Tr, int VPL>

@@ -92,7 +92,7 @@ __device__ __forceinline__ void topk_values(const float (&v)[VPL], int E, int k,
         key[j] = key[j - 1];
         key[j - 1] = t;
       }
-  float v0 = 0.f, sum = 0.f, my_ex = 0.f;
+  float my_v = 0.f;
   my_id = 0;
   for (int j = 0; j < k; ++j) {
     // wave maximum of the heads: first over the logit half of the key, then
@@ -112,12 +112,13 @@ __device__ __forceinline__ void topk_values(const float (&v)[VPL], int E, int k,
       for (int r = 0; r + 1 < VPL; ++r) key[r] = key[r + 1];
       key[VPL - 1] = 0ull;
     }
-    const float wv = key_value(win);
-    if (j == 0) v0 = wv;
-    const float ex = expf(wv - v0);
-    sum += ex;
-    if (lane == j) { my_ex = ex; my_id = key_index(win); }
+    if (lane == j) { my_v = key_value(win); my_id = key_index(win); }
   }
+  // the exponentials of all slots at once, added up in slot order
+  auto of = [](float x, int l) { return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), l)); };
+  const float my_ex = expf(my_v - of(my_v, 0));
+  float sum = 0.f;
+  for (int j = 0; j < k; ++j) sum += of(my_ex, j);
   my_gate = my_ex / sum;
 }
 template <int VPL>
