@@ -14,9 +14,9 @@ constexpr int32_t kMaxFewWidth = 1 << 20;
 size_t pad256(size_t n) { return (n + 255) & ~(size_t)255; }
 // dz, then the chunks' column sums
 size_t dz_bytes(int32_t T, int32_t N, int32_t act) { return act == MOE_ACT_NONE ? 0 : pad256((size_t)T * N * 2); }
-// inner values of the few-token layer: three 16-bit parts each, in rows of whole 16-byte units
+// inner values of the few-token layer: fp32, in rows of whole 32-byte units
 int32_t inner_pitch(int32_t f) { return (f + 7) / 8 * 8; }
-size_t inner_bytes(int32_t rows, int32_t f) { return pad256((size_t)rows * inner_pitch(f) * 6); }
+size_t inner_bytes(int32_t rows, int32_t f) { return pad256((size_t)rows * inner_pitch(f) * sizeof(float)); }
 int64_t sums_pitch(int32_t n) { return ((int64_t)n + 7) / 8 * 8; }
 
 int check_linear(int32_t dtype, int32_t T, int32_t N, int32_t K, int32_t act) {
@@ -293,8 +293,8 @@ int moe_few_tokens_layer(const moe_layer16_t *L, const void *x, int64_t ldx, con
   a.topk_w = topk_w;
   char *p = static_cast<char *>(ws);
   a.plan = reinterpret_cast<FewPlan *>(p);
-  a.h = reinterpret_cast<uint16_t *>(p + pad256(sizeof(FewPlan)));
-  a.h_sh = reinterpret_cast<uint16_t *>(p + pad256(sizeof(FewPlan)) + inner_bytes(T * L->k, L->f));
+  a.h = reinterpret_cast<float *>(p + pad256(sizeof(FewPlan)));
+  a.h_sh = reinterpret_cast<float *>(p + pad256(sizeof(FewPlan)) + inner_bytes(T * L->k, L->f));
   a.pitch = inner_pitch(L->f);
   a.pitch_sh = inner_pitch(L->f_sh);
   return status(launch_few_layer(a, L->dtype == MOE_FP16, stream));

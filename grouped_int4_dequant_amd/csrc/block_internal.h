@@ -94,7 +94,7 @@ struct FewArgs {
   int32_t *topk_ids;                 // nullable [T][k]
   float *topk_w;                     // nullable [T][k]
   FewPlan *plan;                     // workspace
-  uint16_t *h, *h_sh;                // workspace: inner values by pair and by token, three parts each
+  float *h, *h_sh;                   // workspace: inner values by pair and by token
   int32_t pitch, pitch_sh;           // row pitch of h and h_sh in elements
   int32_t share;                     // gate/up: log2 of the waves that share an item
 };

@@ -10,12 +10,14 @@
 //            the second kernel. Then it walks over items of 8 columns of h of one block: 16 rows of W_gu,
 //            eight of the gate and the eight that it multiplies. One to eight waves share an item's sum
 //            and join in LDS, in order; the next item's weights are requested before that.
-//   down     a workgroup owns 8 columns of y, its waves take one block after the other. The 16 operand
-//            rows of a matrix instruction are the 8 columns over the first and the second half of the sum, against
-//            up to eight pairs' halves, so that d / 8 workgroups fill the CUs. What a block gives each of its pairs
-//            goes to LDS, and is added up there by token in slot order.
-// Weights go straight from memory to operand registers and are read once (an expert of more than 16
-// pairs again for each 16, from L2).
+//   down     a workgroup owns 8 columns of y, its waves take one block after the other. A lane has eight
+//            consecutive terms of the sum in 512, of all 8 columns and of up to four pairs, multiplied in fp32; the lanes'
+//            sums are added up in a fixed order. What a block gives each of its pairs goes to LDS, and is added up there by
+//            token in slot order. The matrix instructions have no part in it: with one or two pairs a block they would be
+//            nearly empty, and laying h out for them took three times the loads of the weights (57 us at 16 tokens of 8
+//            of 256 experts, 2048 x 512).
+// Weights go straight from memory to registers and are read once (by gate/up for each 16 pairs of an expert, by
+// down for each four, from L2).
 
 #include "block_device.h"
 #include "topk_device.h"
@@ -24,6 +26,8 @@
 
 namespace moe {
 namespace {
+
+typedef float f2 __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves = 8;   // of a gate/up workgroup
 // Steps of weights asked for at once. One token's layer is a single round of items: everything is asked for at once there.
@@ -152,22 +156,14 @@ __device__ __forceinline__ void make_plan_one(const FewArgs &a, FewLds &s, int n
   lds_barrier();
 }
 
-// An inner value as three bf16 parts that add up to it, each an array of its own: leading, middle and
-// last eight bits, cut off rather than rounded, so that no rest changes its sign or leaves the range. Infinities and NaN
-// are all in the first part.
-__device__ __forceinline__ void store_inner(uint16_t *q, int64_t part, f4 v, int left) {
+// Stores the first `left` of four inner values.
+__device__ __forceinline__ void store_inner(float *q, f4 v, int left) {
+  if (left >= 4) {
+    *reinterpret_cast<f4 *>(q) = v;
+  } else {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (i >= left) break;
-    float rest = v[i];
-#pragma unroll
-    for (int p = 0; p < 3; ++p) {
-      uint32_t b = __builtin_bit_cast(uint32_t, rest);
-      const bool finite = (b & 0x7f800000u) != 0x7f800000u;
-      if (!finite && (b & 0x007fffffu)) b |= 0x00400000u;  // NaN stays NaN
-      q[p * part + i] = (uint16_t)(b >> 16);
-      rest = finite ? rest - __builtin_bit_cast(float, b & 0xffff0000u) : 0.f;
-    }
+    for (int i = 0; i < 3; ++i)
+      if (i < left) q[i] = v[i];
   }
 }
 
@@ -275,60 +271,56 @@ __global__ __launch_bounds__(64 * kWaves, 4) void few_gate_up_kernel(FewArgs a) 
       for (int i = 0; i < 4; ++i) h[i] = times_sigmoid(acc[i], acc[i]) * __shfl(acc[i], (lane + 32) & 63);
       const int c = done.c0 + 4 * q4, left = (done.shared ? a.f_sh : a.f) - c;
       if (done.pair >= 0 && q4 < 2 && left > 0) {
-        if (done.shared) store_inner(a.h_sh + (int64_t)done.pair * a.pitch_sh + c, (int64_t)a.T * a.pitch_sh, h, left);
-        else store_inner(a.h + (int64_t)done.pair * a.pitch + c, (int64_t)a.T * a.k * a.pitch, h, left);
+        if (done.shared) store_inner(a.h_sh + (int64_t)done.pair * a.pitch_sh + c, h, left);
+        else store_inner(a.h + (int64_t)done.pair * a.pitch + c, h, left);
       }
     }
   }
 }
 
-// Eight weights times a pair's eight inner values (their three parts), 32 terms a matrix instruction. bf16
-// weights as they are; fp16 ones as two bf16 parts, of eight bits and of the three that are left.
-template <typename Tr>
-__device__ __forceinline__ f4 times_inner(const s8 (&w)[std::is_same_v<Tr, Fp16> ? 2 : 1], const s8 (&h)[3], f4 acc) {
-#pragma unroll
-  for (int p = 0; p < 3; ++p) acc = Bf16::mfma(w[0], h[p], acc);
-  if constexpr (std::is_same_v<Tr, Fp16>) {
-#pragma unroll
-    for (int p = 0; p < 3; ++p) acc = Bf16::mfma(w[1], h[p], acc);
-  }
-  return acc;
-}
-template <typename Tr>
-__device__ __forceinline__ void weight_parts(s8 w, s8 (&out)[std::is_same_v<Tr, Fp16> ? 2 : 1]) {
-  if constexpr (std::is_same_v<Tr, Fp16>) {
-    u4 hi, lo;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t x = __builtin_bit_cast(uint32_t, Fp16::to((uint16_t)w[2 * i])), y = __builtin_bit_cast(uint32_t, Fp16::to((uint16_t)w[2 * i + 1]));
-      hi[i] = (x >> 16) | (y & 0xffff0000u);
-      const float rx = __builtin_bit_cast(float, x) - __builtin_bit_cast(float, x & 0xffff0000u);
-      const float ry = __builtin_bit_cast(float, y) - __builtin_bit_cast(float, y & 0xffff0000u);
-      lo[i] = (__builtin_bit_cast(uint32_t, rx) >> 16) | (__builtin_bit_cast(uint32_t, ry) & 0xffff0000u);
-    }
-    out[0] = __builtin_bit_cast(s8, hi);
-    out[1] = __builtin_bit_cast(s8, lo);
-  } else {
-    out[0] = w;
-  }
+// The sum of the values of four lanes 16 apart, in each of them.
+__device__ __forceinline__ float sum_halves(float v) {
+  const uint32_t x = __builtin_bit_cast(uint32_t, v);
+  const auto p = __builtin_amdgcn_permlane16_swap(x, x, false, false);  // rows 0, 0, 2, 2 and 1, 1, 3, 3 of 16 lanes
+  v = __builtin_bit_cast(float, (uint32_t)p[0]) + __builtin_bit_cast(float, (uint32_t)p[1]);
+  const uint32_t y = __builtin_bit_cast(uint32_t, v);
+  const auto q = __builtin_amdgcn_permlane32_swap(y, y, false, false);  // the lower half twice, and the upper
+  return __builtin_bit_cast(float, (uint32_t)q[0]) + __builtin_bit_cast(float, (uint32_t)q[1]);
 }
 
-// As many waves as share the blocks evenly: up to 12 for one token, whose blocks are its picks, else 8, whose registers
-// then hold both eights' inner values. 16 tokens of 8 of 256 experts, 2048 x 512: 57 us for 216 MB; 16 waves of half the registers
-// 59, the next block's weights asked for a block ahead 53 (and 26 against 22 in fp16, which then spills).
+// Sums of eight values over the 64 lanes: lane l ends with those of values 2 (l % 4) and 2 (l % 4) + 1. Lanes that
+// differ in the last two bits swap halves of what they hold first.
+__device__ __forceinline__ void sum_lanes(const float (&v)[8], float &a, float &b) {
+  const int lane = threadIdx.x & 63;
+  const bool hi = lane & 2, odd = lane & 1;
+  float w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float keep = hi ? v[4 + i] : v[i], give = hi ? v[i] : v[4 + i];
+    w[i] = keep + dpp_f32<0x4E>(give);  // lanes 2,3,0,1 of each four
+  }
+  a = (odd ? w[2] : w[0]) + dpp_f32<0xB1>(odd ? w[0] : w[2]);  // 1,0,3,2
+  b = (odd ? w[3] : w[1]) + dpp_f32<0xB1>(odd ? w[1] : w[3]);
+  a += dpp_f32<0x124>(a);  // four on, in each 16
+  b += dpp_f32<0x124>(b);
+  a += dpp_f32<0x128>(a);  // eight on
+  b += dpp_f32<0x128>(b);
+  a = sum_halves(a);
+  b = sum_halves(b);
+}
+
+// As many waves as share the blocks evenly: up to 12 for one token, whose blocks are its picks, else 8.
 constexpr int down_waves(bool one) { return one ? 12 : 8; }
 template <typename Tr, bool Vec, bool One>
 __global__ __launch_bounds__(64 * down_waves(One)) void few_down_kernel(FewArgs a) {
-  constexpr int kPitch = 12;  // floats a row of s_o: 8 and a gap that keeps rows off each other's banks
-  constexpr int kW = 16, kH = 4;  // steps of weights asked for at once, and of inner values
-  constexpr int kX = One ? 1 : 2;  // eights of a block's pairs
-  __shared__ __attribute__((aligned(16))) float s_o[(One ? 65 : kFewPairs + kFewTokens) * kPitch];
+  constexpr int kC = 8;             // columns of a workgroup
+  constexpr int kR = One ? 1 : 4;   // pairs at a time (eight: 16 tokens' blocks 56 us against 51)
+  constexpr int kSpan = 512;        // terms that a wave's lanes hold
+  __shared__ __attribute__((aligned(16))) float s_o[(One ? 65 : kFewPairs + kFewTokens) * kC];
   __shared__ FewPlan s;  // what the first kernel left
   const int tid = threadIdx.x, lane = tid & 63, waves = blockDim.x >> 6;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int p16 = lane & 15, q4 = lane >> 4, p8 = p16 & 7;
-  const int n0 = 8 * blockIdx.x, pairs = a.T * a.k;
-  const int row = min(n0 + p8, a.d - 1);  // rows past the last repeat it
+  const int n0 = kC * blockIdx.x, pairs = a.T * a.k;
   const int blocks_sh = a.f_sh > 0 ? (a.T + 15) / 16 : 0;
   int blocks;
   if constexpr (One) {
@@ -345,135 +337,96 @@ __global__ __launch_bounds__(64 * down_waves(One)) void few_down_kernel(FewArgs 
     lds_barrier();
   }
   for (int i = tid; i < pairs; i += blockDim.x) s.gate[i] = a.plan->gate[i];
+  const int total = blocks + blocks_sh;
 
   struct Where {
-    const uint16_t *w, *h;
-    int64_t part;
-    int kb, kend, n;  // the lane's half of the sum, and its steps of 32
-    int pitch, pair[kX], rows;  // the lane's pairs of the block's first and second eight
+    const uint16_t *w;
+    int f, first, rows;  // terms of the sum; the block's first sorted pair (token, if shared), and how many
     bool shared;
   };
   auto locate = [&](int b) __attribute__((always_inline)) {
     Where t;
     t.shared = b < blocks_sh;  // the shared expert first
     b -= blocks_sh;
-    const int f = t.shared ? a.f_sh : a.f, half = ((f + 63) >> 6) * 32;
-    t.n = half >> 5;
-    t.kb = (p16 & 8 ? half : 0) + 8 * q4;
-    t.kend = p16 & 8 ? f : min(half, f);
-    t.pitch = t.shared ? a.pitch_sh : a.pitch;
-    t.h = t.shared ? a.h_sh : a.h;
-    t.part = (int64_t)(t.shared ? a.T : pairs) * t.pitch;
+    t.f = t.shared ? a.f_sh : a.f;
     const int e = t.shared ? 0 : One ? a.plan->expert[b] : s.expert[b];
-    t.w = (t.shared ? a.sh_dn : a.dn + (int64_t)e * a.d * a.f) + (int64_t)row * f;
-    const int first = t.shared ? 16 * (b + blocks_sh) : One ? b : s.first[b];
-    t.rows = One ? 1 : t.shared ? min(a.T - first, 16) : s.rows[b];
-#pragma unroll
-    for (int x = 0; x < kX; ++x) {
-      const int r = 8 * x + p8;
-      t.pair[x] = r >= t.rows ? -1 : t.shared || One ? first + r : s.pair[first + r];
-    }
+    t.w = (t.shared ? a.sh_dn : a.dn + (int64_t)__builtin_amdgcn_readfirstlane(e) * a.d * a.f) + (int64_t)n0 * t.f;
+    t.first = t.shared ? 16 * (b + blocks_sh) : One ? b : __builtin_amdgcn_readfirstlane(s.first[b]);
+    t.rows = One ? 1 : t.shared ? min(a.T - t.first, 16) : __builtin_amdgcn_readfirstlane(s.rows[b]);
     return t;
   };
-  s8 wv[kW];
-  auto request = [&](const Where &t, int y0) __attribute__((always_inline)) {
+  s8 wv[kC];
+  auto request = [&](const Where &t, int k0) __attribute__((always_inline)) {
+    const uint16_t *w = t.w + k0 + 8 * lane;
+    const int left = t.f - k0 - 8 * lane;
 #pragma unroll
-    for (int y = 0; y < kW; ++y) {
-      const int k = t.kb + 32 * (y0 + y);
-      wv[y] = load_w<Vec>(t.w + k, t.kend - k);
-    }
+    for (int c = 0; c < kC; ++c) wv[c] = load_w<Vec>(w + (int64_t)min(c, a.d - 1 - n0) * t.f, left);  // columns past the last repeat it
+  };
+  float acc[kR][kC];
+  int pair[kR];
+  // 512 terms of N pairs
+  auto multiply = [&](const Where &t, int k0, auto n) __attribute__((always_inline)) {
+    constexpr int N = decltype(n)::value;
+    float hv[N][8];
+    const float *h = (t.shared ? a.h_sh : a.h) + k0 + 8 * lane;
+    const int left = t.f - k0 - 8 * lane, pitch = t.shared ? a.pitch_sh : a.pitch;
+#pragma unroll
+    for (int r = 0; r < N; ++r) widen8<Tr, true>(load_raw8<true, Vec>(h, (int64_t)pair[r] * pitch, left), hv[r]);
+#pragma unroll
+    for (int c = 0; c < kC; ++c)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float w = Tr::to((uint16_t)wv[c][i]);
+#pragma unroll
+        for (int r = 0; r < N; ++r) acc[r][c] = fmaf(w, hv[r][i], acc[r][c]);
+      }
   };
   int b = wave;
   Where at{};
-  if (b < blocks + blocks_sh) {
+  if (b < total) {
     at = locate(b);
     request(at, 0);
   }
-  while (b < blocks + blocks_sh) {
-    f4 acc[kX];
+  while (b < total) {
+    const Where t = at;
+    for (int r0 = 0; r0 < t.rows; r0 += kR) {
+      const int n = min(t.rows - r0, kR);
 #pragma unroll
-    for (int x = 0; x < kX; ++x) acc[x] = f4{0.f, 0.f, 0.f, 0.f};
-    for (int y0 = 0; y0 < at.n; y0 += kW) {
-      if (y0 > 0) request(at, y0);
+      for (int r = 0; r < kR; ++r) {
+        const int q = t.first + r0 + min(r, n - 1);
+        pair[r] = t.shared || One ? q : __builtin_amdgcn_readfirstlane(s.pair[q]);
 #pragma unroll
-      for (int g = 0; g < kW; g += kH) {
-        if (y0 + g >= at.n) break;
-        s8 hv[kX][kH][3];
-#pragma unroll
-        for (int x = 0; x < kX; ++x) {
-          if (8 * x >= at.rows) break;
-          const uint16_t *h = at.h + (int64_t)max(at.pair[x], 0) * at.pitch;
-#pragma unroll
-          for (int y = 0; y < kH; ++y) {
-            const int k = at.kb + 32 * (y0 + g + y);
-#pragma unroll
-            for (int p = 0; p < 3; ++p) hv[x][y][p] = load_w<Vec>(h + p * at.part + k, at.pair[x] >= 0 ? at.kend - k : 0);
-          }
-        }
-#pragma unroll
-        for (int y = 0; y < kH; ++y) {
-          s8 parts[std::is_same_v<Tr, Fp16> ? 2 : 1];
-          weight_parts<Tr>(wv[g + y], parts);
-#pragma unroll
-          for (int x = 0; x < kX; ++x) {
-            if (8 * x >= at.rows) break;
-            acc[x] = times_inner<Tr>(parts, hv[x][y], acc[x]);
-          }
-        }
+        for (int c = 0; c < kC; ++c) acc[r][c] = 0.f;
       }
-    }
-    // lane: pair p16 % 8 and half p16 / 8 of the sum against rows 4 q4 .. of the 16; those of its own half count.
-    // Where a sum is not finite, parts may have met that the values don't know (an infinite weight times a part
-    // without bits): then it is formed once more, from whole values on the fp32 instruction.
-    const bool counts = (p16 >> 3) == (q4 >> 1);
-    const Where done = at;
-#pragma unroll
-    for (int x = 0; x < kX; ++x) {
-      if (8 * x >= done.rows) break;
-      bool finite = true;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) finite = finite && __builtin_fabsf(acc[x][i]) < __builtin_inff();
-      if (__ballot(counts && !finite) == 0) continue;
-      f4 again = {0.f, 0.f, 0.f, 0.f};
-      const uint16_t *h = done.h + (int64_t)max(done.pair[x], 0) * done.pitch;
-#pragma unroll 1
-      for (int y = 0; y < done.n; ++y) {
-        const int k = done.kb + 32 * y;
-        const s8 w = load_w<Vec>(done.w + k, done.kend - k);
-        s8 hv[3];
-#pragma unroll
-        for (int p = 0; p < 3; ++p) hv[p] = load_w<Vec>(h + p * done.part + k, done.pair[x] >= 0 ? done.kend - k : 0);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {  // instruction i takes value i of each lane's run: k = 8 q4 + i
-          const float v = (Bf16::to((uint16_t)hv[0][i]) + Bf16::to((uint16_t)hv[1][i])) + Bf16::to((uint16_t)hv[2][i]);
-          again = __builtin_amdgcn_mfma_f32_16x16x4f32(Tr::to((uint16_t)w[i]), v, again, 0, 0, 0);
+      for (int k0 = 0; k0 < t.f; k0 += kSpan) {
+        if (k0 > 0 || (r0 > 0 && t.f > kSpan)) request(t, k0);
+        if (One || n == 1) multiply(t, k0, std::integral_constant<int, 1>{});
+        else if (n == 2) multiply(t, k0, std::integral_constant<int, One ? 1 : 2>{});
+        else multiply(t, k0, std::integral_constant<int, kR>{});
+      }
+      if (r0 + kR >= t.rows) {
+        b += waves;
+        if (b < total) {
+          at = locate(b);
+          request(at, 0);
         }
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[x][i] = __builtin_fabsf(acc[x][i]) < __builtin_inff() ? acc[x][i] : again[i];
-    }
-    b += waves;
-    if (b < blocks + blocks_sh) {
-      at = locate(b);
-      request(at, 0);
-    }
-#pragma unroll
-    for (int x = 0; x < kX; ++x) {
-      if (8 * x >= done.rows) break;
-      f4 v;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = acc[x][i] + __shfl(acc[x][i], (lane + 40) & 63);
-      if (p16 < 8 && q4 < 2 && done.pair[x] >= 0)
-        *reinterpret_cast<f4 *>(&s_o[((done.shared ? pairs : 0) + done.pair[x]) * kPitch + 4 * q4]) = v;
+      for (int r = 0; r < kR; ++r) {
+        if (r >= n) break;
+        float x, y;
+        sum_lanes(acc[r], x, y);
+        if (lane < 4) *reinterpret_cast<f2 *>(&s_o[((t.shared ? pairs : 0) + pair[r]) * kC + 2 * (2 * ((lane >> 1) & 1) + (lane & 1))]) = f2{x, y};
+      }
     }
   }
   __syncthreads();
-  for (int i = tid; i < 8 * a.T; i += blockDim.x) {
+  for (int i = tid; i < kC * a.T; i += blockDim.x) {
     const int t = i >> 3, c = i & 7;
     if (n0 + c >= a.d) continue;
     float y = 0.f;
-    for (int j = 0; j < a.k; ++j) y += s.gate[t * a.k + j] * s_o[(t * a.k + j) * kPitch + c];
-    if (a.f_sh > 0) y += s_o[(pairs + t) * kPitch + c];
+    for (int j = 0; j < a.k; ++j) y += s.gate[t * a.k + j] * s_o[(t * a.k + j) * kC + c];
+    if (a.f_sh > 0) y += s_o[(pairs + t) * kC + c];
     if (a.y_f32) {
       if (a.add) y += static_cast<const float *>(a.add)[t * a.ld_add + n0 + c];
       static_cast<float *>(a.y)[t * a.ld_y + n0 + c] = y;

@@ -762,9 +762,8 @@ int moe_residual_norm_backward(int32_t dtype, const void *dy, int64_t lddy, cons
  *   topk_ids, topk_w   int32 and fp32 [T][k]: the picks, or NULL (not wanted)
  *   ws        moe_few_tokens_workspace_bytes(L, T) bytes, 256-byte aligned; calls that may run at
  *             the same time, in replayed graphs too, need one each
- * Each picked expert's weights are read once for all its tokens. The products of x and of
- * FFN's inner values are summed in fp32; the inner values are held in fp32 and enter the second product
- * whole (as three 16-bit parts, whose bits below 2^-133 are lost). The k experts are added in slot
+ * Each picked expert's weights are read once for all its tokens (of 16 at most). Sums and FFN's inner
+ * values are held in fp32, and the inner values enter the second product so. The k experts are added in slot
  * order, then the shared one, then `add`. A row's result does not depend on the other rows of the call.
  * Errors: MOE_EINVAL (null or misaligned pointer, unknown type, T < 0, a size < 1, f_sh < 0, k > E, a stride
  * below the width), MOE_EUNSUPPORTED (E > MOE_MAX_EXPERTS, k > 64, T > MOE_MAX_FEW_TOKENS,

@@ -85,7 +85,7 @@ def test_few_layer_limits():
     assert few(dict(d=(1 << 20) + 1), **wide) == EUNSUP and few(dict(f=(1 << 20) + 1)) == EUNSUP and few(dict(f_sh=(1 << 20) + 1)) == EUNSUP
     need = moe.few_tokens_workspace_bytes(8, torch.bfloat16, 64, 32, 16, 2, 8)
     assert few({}, ws_bytes=need - 1) == EWS
-    assert need >= 8 * 2 * 32 * 6 + 8 * 8 * 6 and moe.few_tokens_workspace_bytes(65, torch.bfloat16, 64, 32, 16, 2) == 0
+    assert need >= 8 * 2 * 32 * 4 + 8 * 8 * 4 and moe.few_tokens_workspace_bytes(65, torch.bfloat16, 64, 32, 16, 2) == 0
     assert few({}, T=0, x=None, logits=None, y=None, ws=None, ws_bytes=0) == OK
 
 
