@@ -880,6 +880,7 @@ def adapter_backward(dy: torch.Tensor, x: torch.Tensor, A: torch.Tensor, B: torc
 
 
 # --------------------------------------------- the block around the experts
+# As the operators above: tensors of one device, row-strided views, nothing recorded for autograd.
 ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4, "swiglu": 5, "geglu": 6}
 
 

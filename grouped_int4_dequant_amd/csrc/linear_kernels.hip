@@ -244,7 +244,9 @@ __global__ __launch_bounds__(256) void linear_grad_small_kernel(DenseArgs dg, De
 template <typename Tr, bool Gated>
 hipError_t linear_of(const LinearArgs<Gated> &a, hipStream_t s) {
   if (a.vec && a.P <= 64) {
-    const dim3 grid((unsigned)cdiv(Gated ? a.N / 2 : a.N, Gated ? 8 : 16));
+    const int64_t wgs = cdiv(Gated ? a.N / 2 : a.N, Gated ? 8 : 16);
+    if (!grid_fits(wgs, 512)) return hipErrorInvalidConfiguration;
+    const dim3 grid((unsigned)wgs);
     if (a.P <= 16) linear_few_kernel<Tr, Gated, 1><<<grid, 512, 0, s>>>(a);
     else if (a.P <= 32) linear_few_kernel<Tr, Gated, 2><<<grid, 512, 0, s>>>(a);
     else linear_few_kernel<Tr, Gated, 4><<<grid, 512, 0, s>>>(a);
@@ -264,9 +266,19 @@ hipError_t act_grad_of(const ActGradArgs &a, bool add, hipStream_t s) {
   return hipGetLastError();
 }
 
+// Whether every form that the products of a gradient may take fits a launch: known before the first of a call's
+// kernels is enqueued.
+bool grad_fits(const ActGradArgs &c, const DenseArgs &dx, const DenseArgs &dw) {
+  const int64_t n_w = dw.out ? cdiv(dw.N, kSmall) * cdiv(dw.K, kSmall) : 0, n_d = dx.out ? xcd_grid(cdiv(c.T, kSmall) * cdiv(dx.K, kSmall)) : 0;
+  const int64_t few = dx.out && c.T <= 64 ? cdiv(c.T, kFewRows) * cdiv(dx.K, 64) : 0;
+  return grid_fits(n_w + n_d + cdiv(c.N, 64), 256) && grid_fits(few, 512) && grid_fits(c.db ? cdiv(c.N, 64) : 0, 1024) &&
+         n_w + n_d + cdiv(c.N, 64) < INT32_MAX / 2;
+}
+
 template <typename Tr>
 hipError_t linear_grad_of(const ActGradArgs &c, const DenseArgs &dx, const DenseArgs &dw, hipStream_t s) {
   const bool curved = c.act != MOE_ACT_NONE;
+  if (!grad_fits(c, dx, dw)) return hipErrorInvalidConfiguration;
   // one launch for what may run side by side, where both products take small tiles
   const bool small = dx.out && dw.out && c.T > 0 && dense_tile_rows<kDgrad>(dx) == kSmall && dense_tile_rows<kWgrad>(dw) == kSmall && dx.vec == dw.vec && !(dx.vec && c.T <= 64);
   const bool rows = small && !curved && c.T <= 1024;  // db from dy's rows, without chunks
@@ -276,9 +288,7 @@ hipError_t linear_grad_of(const ActGradArgs &c, const DenseArgs &dx, const Dense
   }
   if (small) {
     const int64_t n_w = cdiv(dw.N, kSmall) * cdiv(dw.K, kSmall), n_d = xcd_grid(cdiv(dx.P, kSmall) * cdiv(dx.K, kSmall)), n_c = c.db ? cdiv(c.N, 64) : 0;
-    const int64_t n = n_w + n_d + n_c;
-    if (!grid_fits(n, 256) || n >= INT32_MAX / 2) return hipErrorInvalidConfiguration;
-    const dim3 grid((unsigned)n);
+    const dim3 grid((unsigned)(n_w + n_d + n_c));
     if (dx.vec) linear_grad_small_kernel<Tr, true><<<grid, 256, 0, s>>>(dx, dw, c, rows, (int)n_w, (int)n_d);
     else linear_grad_small_kernel<Tr, false><<<grid, 256, 0, s>>>(dx, dw, c, rows, (int)n_w, (int)n_d);
     return hipGetLastError();

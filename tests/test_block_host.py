@@ -35,11 +35,13 @@ REFUSED = [
      dict(x=p + 1), dict(W=p + 1), dict(y=p + 1), dict(bias=p + 1), dict(bias_dtype=2, bias=p + 2), dict(res=p + 1), dict(pre=p + 1), dict(T=-1), dict(N=0),
      dict(K=0), dict(ldx=63), dict(ldy=31), dict(ldres=31), dict(ldpre=31), dict(act=5, N=31), dict(act=5, ldpre=31), dict(act=5, ldy=15),
      dict(res=p, y=p, ldres=40), dict(y_dtype=2, y=p + 2)),
-    ("moe_linear", LINEAR, EUNSUP, dict(T=LARGE), dict(N=LARGE, ldy=LARGE, ldres=LARGE, ldpre=LARGE), dict(K=LARGE, ldx=LARGE)),
+    ("moe_linear", LINEAR, EUNSUP, dict(T=1, N=1 << 30, ldy=1 << 30, ldres=1 << 30, ldpre=1 << 30), dict(T=1 << 30, N=1 << 20, ldy=1 << 20, ldres=1 << 20, ldpre=1 << 20),
+     dict(T=LARGE), dict(N=LARGE, ldy=LARGE, ldres=LARGE, ldpre=LARGE), dict(K=LARGE, ldx=LARGE)),
     ("moe_linear_backward", LGRAD, EINVAL, dict(dtype=2), dict(dx_dtype=1), dict(g_dtype=1), dict(act=9), dict(dy=None), dict(x=None), dict(W=None),
      dict(pre=None), dict(dx=None, dW=None, db=None), dict(dy=p + 1), dict(x=p + 1), dict(W=p + 1), dict(pre=p + 1), dict(dW=p + 2), dict(db=p + 2), dict(dx=p + 1),
      dict(ws=None), dict(ws=p + 16), dict(T=-1), dict(N=0), dict(K=0), dict(lddy=31), dict(ldx=63), dict(ldpre=31), dict(lddx=63), dict(act=6, N=33)),
-    ("moe_linear_backward", LGRAD, EUNSUP, dict(g_dtype=0, acc=1), dict(T=LARGE), dict(N=LARGE, lddy=LARGE, ldpre=LARGE), dict(K=LARGE, ldx=LARGE, lddx=LARGE)),
+    ("moe_linear_backward", LGRAD, EUNSUP, dict(g_dtype=0, acc=1), dict(act=0, T=1, N=1 << 29, lddy=1 << 29, K=8, ws_bytes=1 << 40),
+     dict(act=0, db=None, N=1 << 20, lddy=1 << 20, K=1 << 20, ldx=1 << 20, lddx=1 << 20), dict(act=0, db=None, dW=None, T=1, K=1 << 30, ldx=1 << 30, lddx=1 << 30), dict(T=LARGE), dict(N=LARGE, lddy=LARGE, ldpre=LARGE), dict(K=LARGE, ldx=LARGE, lddx=LARGE)),
     ("moe_linear_backward", LGRAD, EWS, dict(ws_bytes=8 * 32 * 2), dict(act=0, ws_bytes=0), dict(db=None, ws_bytes=8 * 32 * 2 - 1)),
     ("moe_residual_norm", NORM, EINVAL, dict(dtype=2), dict(s_dtype=1), dict(w_dtype=1), dict(o=None, x=None), dict(y=None, n=None), dict(w_n=None), dict(o=p + 1),
      dict(x=p + 1), dict(w_o=p + 1), dict(gate=p + 1), dict(w_n=p + 1), dict(y=p + 1), dict(n=p + 1), dict(w_dtype=2, w_o=p + 2), dict(s_dtype=2, x=p + 2),
