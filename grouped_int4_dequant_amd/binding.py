@@ -139,9 +139,10 @@ def load() -> ctypes.CDLL:
         lib.moe_few_tokens_workspace_bytes.restype = Z
         for name in ("moe_linear", "moe_linear_backward", "moe_residual_norm", "moe_residual_norm_backward", "moe_few_tokens_layer"):
             getattr(lib, name).restype = ctypes.c_int
-        for name in ("moe_linear_backward_workspace_bytes", "moe_residual_norm_backward_workspace_bytes"):
-            getattr(lib, name).argtypes = [I, I, I]
-            getattr(lib, name).restype = Z
+        lib.moe_linear_backward_workspace_bytes.argtypes = [I, I, I, I]
+        lib.moe_linear_backward_workspace_bytes.restype = Z
+        lib.moe_residual_norm_backward_workspace_bytes.argtypes = [I, I, I]
+        lib.moe_residual_norm_backward_workspace_bytes.restype = Z
         lib.moe_status_string.argtypes = [ctypes.c_int]
         lib.moe_status_string.restype = ctypes.c_char_p
         _lib = lib
@@ -933,9 +934,9 @@ def linear(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None
     return y
 
 
-def linear_backward_workspace_bytes(T: int, N: int, act: str = "none") -> int:
-    _sizes(T, N)
-    return int(load().moe_linear_backward_workspace_bytes(T, N, _activation(act, N)[0]))
+def linear_backward_workspace_bytes(T: int, N: int, K: int, act: str = "none") -> int:
+    _sizes(T, N, K)
+    return int(load().moe_linear_backward_workspace_bytes(T, N, K, _activation(act, N)[0]))
 
 
 def linear_backward(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, pre: Optional[torch.Tensor] = None, act: str = "none",
@@ -967,12 +968,9 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, pre: Opt
     dx = c.result(dx, "dx", (T, K), None)
     dW = c.whole(dW, "dW", (N, K), grad_dtype)
     db = c.whole(db, "db", (N,), dW.dtype) if bias_grad else None
-    w, w_bytes = None, 0
-    if code or bias_grad:
-        ws = c.workspace(ws, int(load().moe_linear_backward_workspace_bytes(T, N, code)))
-        w, w_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
+    ws = c.workspace(ws, int(load().moe_linear_backward_workspace_bytes(T, N, K, code)))
     c("moe_linear_backward", c.code, dy.data_ptr(), lddy, x.data_ptr(), ldx, T, N, K, W.data_ptr(), z, ldz, code, dx.data_ptr(),
-      _CODES[dx.dtype], _ld(dx, K), dW.data_ptr(), None if db is None else db.data_ptr(), _CODES[dW.dtype], int(accumulate), w, w_bytes)
+      _CODES[dx.dtype], _ld(dx, K), dW.data_ptr(), None if db is None else db.data_ptr(), _CODES[dW.dtype], int(accumulate), ws.data_ptr(), ws.numel() * ws.element_size())
     return dx, dW, db
 
 

@@ -12,12 +12,17 @@ namespace {
 constexpr int32_t kMaxFewWidth = 1 << 20;
 
 size_t pad256(size_t n) { return (n + 255) & ~(size_t)255; }
-// dz, then the chunks' column sums
+// a gradient's workspace: dz, then the chunks' column sums, then dW's parts
 size_t dz_bytes(int32_t T, int32_t N, int32_t act) { return act == MOE_ACT_NONE ? 0 : pad256((size_t)T * N * 2); }
 // inner values of the few-token layer: fp32, in rows of whole 32-byte units
 int32_t inner_pitch(int32_t f) { return (f + 7) / 8 * 8; }
 size_t inner_bytes(int32_t rows, int32_t f) { return pad256((size_t)rows * inner_pitch(f) * sizeof(float)); }
+size_t parts_bytes(const RowParts &p, int32_t N, int32_t K) { return p.count > 1 ? pad256((size_t)p.count * N * K * sizeof(float)) : 0; }
 int64_t sums_pitch(int32_t n) { return ((int64_t)n + 7) / 8 * 8; }
+
+size_t db_bytes(int32_t T, int32_t N, int32_t act) {
+  return pad256((size_t)column_chunks(T, is_gated(act) ? N / 2 : N).count * sums_pitch(N) * sizeof(float) + 1);
+}
 
 int check_linear(int32_t dtype, int32_t T, int32_t N, int32_t K, int32_t act) {
   if (!is16(dtype) || T < 0 || N < 1 || K < 1 || act < MOE_ACT_NONE || act > MOE_ACT_GEGLU) return MOE_EINVAL;
@@ -83,11 +88,10 @@ int moe_linear(int32_t dtype, const void *x, int64_t ldx, int32_t T, int32_t N, 
                        : run_linear<false>(dtype, x, ldx, T, N, K, W, bias, bias_dtype, act, residual, ldres, pre, ldpre, y, y_dtype, ldy, stream);
 }
 
-size_t moe_linear_backward_workspace_bytes(int32_t T, int32_t N, int32_t act) {
-  if (check_linear(MOE_BF16, T, N, 1, act) != MOE_OK) return 0;
-  const ColumnChunks c = column_chunks(T, is_gated(act) ? N / 2 : N);
-  const size_t sums = (size_t)c.count * sums_pitch(N) * sizeof(float);
-  return pad256(dz_bytes(T, N, act) + sums + 1);
+size_t moe_linear_backward_workspace_bytes(int32_t T, int32_t N, int32_t K, int32_t act) {
+  if (check_linear(MOE_BF16, T, N, K, act) != MOE_OK) return 0;
+  const size_t wide = parts_bytes(weight_parts(T, N, K, true), N, K), small = parts_bytes(weight_parts(T, N, K, false), N, K);
+  return dz_bytes(T, N, act) + db_bytes(T, N, act) + (wide > small ? wide : small);
 }
 
 int moe_linear_backward(int32_t dtype, const void *dy, int64_t lddy, const void *x, int64_t ldx, int32_t T, int32_t N, int32_t K,
@@ -107,8 +111,8 @@ int moe_linear_backward(int32_t dtype, const void *dy, int64_t lddy, const void 
     if (!dy || !typed(dy, dtype) || (curved && (!pre || !typed(pre, dtype)))) return MOE_EINVAL;
     if ((dx && (!W || !typed(W, dtype))) || (dW && (!x || !typed(x, dtype)))) return MOE_EINVAL;
   }
-  if (curved || db) {
-    if (ws_bytes < moe_linear_backward_workspace_bytes(T, N, act)) return MOE_EWORKSPACE;
+  if (curved || db || dW) {
+    if (ws_bytes < moe_linear_backward_workspace_bytes(T, N, K, act)) return MOE_EWORKSPACE;
     if (!ws || !aligned(ws, 256)) return MOE_EINVAL;
   }
   if (T == 0 && ((!dW && !db) || accumulate)) return MOE_OK;
@@ -154,9 +158,13 @@ int moe_linear_backward(int32_t dtype, const void *dy, int64_t lddy, const void 
     dwa.accumulate = accumulate != 0;
     dwa.vec = units(dz, lddz, N) && units(x, ldx, K);
     dwa.wide = wide_tiles(dwa, kWgrad);
+    const RowParts p = weight_parts(T, N, K, dwa.wide);
+    dwa.part_rows = p.rows;
+    dwa.G = p.count;
     dwa.vec_out = runs(dW, g_dtype, K) && K % 4 == 0;
   }
-  return status(launch_linear_grad(c, dxa, dwa, fp16, stream));
+  float *parts = reinterpret_cast<float *>(static_cast<char *>(ws) + dz_bytes(T, N, act) + db_bytes(T, N, act));
+  return status(launch_linear_grad(c, dxa, dwa, parts, fp16, stream));
 }
 
 int moe_residual_norm(int32_t dtype, const void *o, int64_t ldo, const void *x, int64_t ldx, int32_t stream_dtype, int32_t T,

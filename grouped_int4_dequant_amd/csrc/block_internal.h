@@ -67,6 +67,10 @@ struct ActGradArgs {
   void *db;                 // [N]
   int32_t g_f32, accumulate;
 };
+// The parts that the rows of a weight gradient are cut into, where its tiles are too few for the CUs: each part's
+// sums go to the workspace in fp32 and are added up in order. wide: whether its operands allow wide tiles.
+struct RowParts { int32_t rows, count; };
+RowParts weight_parts(int32_t T, int32_t N, int32_t K, bool wide);
 struct ColumnChunks { int32_t rows, count; };
 ColumnChunks column_chunks(int32_t T, int32_t cols);
 
@@ -103,7 +107,8 @@ hipError_t launch_few_layer(const FewArgs &a, bool fp16, hipStream_t s);
 template <bool Gated>
 hipError_t launch_linear(const LinearArgs<Gated> &a, bool fp16, hipStream_t s);
 // dz and db, then dx = dz W and dW = dz^T x (each without `out`: not wanted)
-hipError_t launch_linear_grad(const ActGradArgs &c, const DenseArgs &dx, const DenseArgs &dw, bool fp16, hipStream_t s);
+// parts: where dW's parts go when dw has more than one (dw.out is dW all the same).
+hipError_t launch_linear_grad(const ActGradArgs &c, const DenseArgs &dx, const DenseArgs &dw, float *parts, bool fp16, hipStream_t s);
 inline bool is_gated(int32_t act) { return act == MOE_ACT_SWIGLU || act == MOE_ACT_GEGLU; }
 
 hipError_t launch_norm(const NormArgs &a, bool fp16, hipStream_t s);

@@ -47,9 +47,11 @@ struct GroupedArgs {
   int32_t vec_out;          // four consecutive outputs may be stored at once
 };
 
-// One matrix: no groups, no gathered rows (P rows, a_rows = P).
+// One matrix: no groups, no gathered rows (P rows, a_rows = P). The weight gradient's rows may be cut into G parts of
+// `part_rows`, each of which gives a matrix of its own behind the other's in `out`.
 struct DenseArgs : GroupedArgs {
   static constexpr bool kDense = true;
+  int32_t part_rows;
 };
 // y = act(x W^T + bias) + residual; z = x W^T + bias goes to `pre`
 template <bool Gated>

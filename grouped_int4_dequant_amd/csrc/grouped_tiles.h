@@ -36,7 +36,8 @@ __device__ __forceinline__ int straight_unit(int row, int slot) { return slot ^ 
 // 16 lanes fetch together fall on distinct banks.
 __device__ __forceinline__ int across_unit(int row, int slot) { return slot ^ ((row & 3) << 1); }
 
-// The group that holds a row tile, and the rows of a group; a single matrix has one group of all rows.
+// The group that holds a row tile, and the rows of a group; a single matrix has one group of all rows, or, for
+// the weight gradient, parts of `part_rows`.
 template <typename Args, typename Pick>
 __device__ __forceinline__ GroupTile find_rows(const Args &a, int rows, Pick pick) {
   if constexpr (Args::kDense) {
@@ -54,8 +55,8 @@ __device__ __forceinline__ GroupTile find_rows(const Args &a, int rows, Pick pic
 template <typename Args>
 __device__ __forceinline__ void group_rows(const Args &a, int e, int &first, int &count) {
   if constexpr (Args::kDense) {
-    first = 0;
-    count = a.P;
+    first = e * a.part_rows;
+    count = min(a.part_rows, a.P - first);
   } else {
     first = min(max(a.offsets[e], 0), a.P);
     count = max(min(max(a.offsets[e + 1], 0), a.P) - first, 0);
@@ -877,15 +878,20 @@ __global__ __launch_bounds__(kWideThreads, 2) void grouped_wide_kernel(Args a) {
   if constexpr (Mode == kWgrad) {
     const int tj = (a.K + kWide - 1) / kWide, ti = (a.N + kWide - 1) / kWide;
     const int per = ti * tj;
-    const int k = blockIdx.x / per;
-    if (!Args::kDense && k >= a.G) return;
-    if constexpr (Args::kDense) t.e = 0; else t.e = group_by_size(a.offsets, a.G, a.P, k);
-    if (t.e < 0) return;
-    int x = blockIdx.x - k * per, it = x / tj, jt = x - it * tj;
+    int it, jt;
     if constexpr (Args::kDense) {
-      x = xcd_item(blockIdx.x, per);
+      const int x = xcd_item(blockIdx.x, per * a.G);
       if (x < 0) return;
-      dense_tile(x, ti, tj, it, jt);
+      t.e = x / per;
+      dense_tile(x - t.e * per, ti, tj, it, jt);
+    } else {
+      const int k = blockIdx.x / per;
+      if (k >= a.G) return;
+      t.e = group_by_size(a.offsets, a.G, a.P, k);
+      if (t.e < 0) return;
+      const int x = blockIdx.x - k * per;
+      it = x / tj;
+      jt = x - it * tj;
     }
     t.i0 = it * kWide;
     t.j0 = jt * kWide;
@@ -951,19 +957,29 @@ bool takes_wide(const Args &a) {
   return a.vec && a.wide && at_least >= 128;
 }
 
-// A single matrix: rows of its tiles (64: small ones), by the time that they take over 256 CUs. A step of 64 terms costs a CU
-// 0.28 us in a small tile, 0.8 in one of 128 x 256 and 0.95 in one of 256 x 256, each of which has beside its steps a prologue
-// and stores of about 3, 6 and 9 us. 2048 rows, 2048 x 4096, forward: 78 us in small tiles, 58 in those of 128 rows.
+// A single matrix: rows of its tiles (64: small ones), by the time that they take over 256 CUs. us a step of 64 terms and
+// beside the steps, a CU: small tiles 0.28 + 1 a tile (input gradient 0.32; weight gradient, whose operands both lie across,
+// 0.8 + 2.5 for every two tiles), those of 128 x 256 0.7 + 11, those of 256 x 256 1.1 + 13 (weight gradient 1.3 + 11.5). Measured, small /
+// 128 / 256 rows: forward of 512 rows, 2048 x 4096 19 / 45 / 76, 2659, 1896 x 696 28 / 19 / 29, 4096, 4096 x 256 35 / 26 / 21,
+// 4096, 2048 x 2048 79 / 35 / 50; input gradient of 2048 rows, 2048 x 4096 81 / 34 / 45, of 172, 4728 x 3200 27 / 56 / 84; weight
+// gradient (small / 256) of 172 rows, 4728 x 3200 39 / 15, of 4096, 2048 x 2048 108 / 94, of 8192, 1024 x 1024 102 / 179.
+// The weight gradient over `parts` parts of the rows, in 10 ns.
+inline int64_t wgrad_time(int64_t part_rows, int64_t N, int64_t K, int64_t parts, bool wide) {
+  const int64_t steps = cdiv(part_rows, kBR);
+  return wide ? cdiv(cdiv(N, kWide) * cdiv(K, kWide) * parts, 256) * (130 * steps + 1150)
+              : cdiv(cdiv(N, kSmall) * cdiv(K, kSmall) * parts, 512) * (80 * steps + 250);
+}
 template <int Mode, typename Args>
 int dense_tile_rows(const Args &a) {
   if (!a.vec || !a.wide) return kSmall;
-  const int64_t rows = Mode == kWgrad ? a.N : a.P, cols = Mode == kWgrad ? a.K : columns_of<Mode>(a), steps = cdiv(Mode == kFwd ? a.K : Mode == kDgrad ? a.N : a.P, kBR);
+  if constexpr (Mode == kWgrad) return wgrad_time(a.part_rows, a.N, a.K, a.G, true) < wgrad_time(a.part_rows, a.N, a.K, a.G, false) ? kWide : kSmall;
+  const int64_t rows = a.P, cols = columns_of<Mode>(a), steps = cdiv(Mode == kFwd ? a.K : a.N, kBR);
   constexpr int kPer = Args::kGated ? 2 : 1;
-  const int64_t n64 = cdiv(rows, kSmall) * cdiv(cols, kSmall / kPer);
-  const int64_t t64 = (n64 > 256 ? n64 : 256) * (28 * steps + 100) / 256 + 200;  // in 10 ns
-  const int64_t t128 = cdiv(cdiv(rows, 128) * cdiv(cols, kWide / kPer), 256) * (80 * steps + 600);
-  const int64_t t256 = cdiv(cdiv(rows, kWide) * cdiv(cols, kWide / kPer), 256) * (95 * steps + 900);
-  if (Mode != kWgrad && t128 < t64 && t128 < t256) return 128;
+  const int64_t n64 = cdiv(rows, kSmall) * cdiv(cols, kSmall / kPer), n256 = cdiv(rows, kWide) * cdiv(cols, kWide / kPer);  // times in 10 ns
+  const int64_t t64 = (n64 > 256 ? n64 : 256) * ((Mode == kFwd ? 28 : 32) * steps + 100) / 256;
+  const int64_t t128 = cdiv(cdiv(rows, 128) * cdiv(cols, kWide / kPer), 256) * (70 * steps + 1100);
+  const int64_t t256 = cdiv(n256, 256) * (110 * steps + 1300);
+  if (t128 < t64 && t128 < t256) return 128;
   return t256 < t64 ? kWide : kSmall;
 }
 
@@ -973,7 +989,9 @@ hipError_t launch(const Args &a, hipStream_t s) {
   const int J = columns_of<Mode>(a);
   constexpr int kPer = Args::kGated ? 2 : 1;  // columns of the product for one of the result
   if constexpr (Vec) {
-    const bool wide = Args::kDense ? dense_tile_rows<Mode>(a) != kSmall : takes_wide<Mode>(a);
+    bool wide;
+    if constexpr (Args::kDense) wide = dense_tile_rows<Mode>(a) != kSmall;
+    else wide = takes_wide<Mode>(a);
     if constexpr (Mode != kWgrad && !Args::kEpilogue) {
       // Few rows whose weights are too few for wide tiles. Against small tiles at N = 1024, K = 2048, us, forward / input
       // gradient: 8 groups, 8 rows 9.4 / 9.0 against 13.2 / 10.5, 64 rows 11.6 / 9.0 against 13.6 / 11.2, 128 rows 18.6 / 11.6
@@ -991,7 +1009,9 @@ hipError_t launch(const Args &a, hipStream_t s) {
       // 2 rows a group, 214 / 234 at 64, 380 / 385 at 256; 16 groups of 1024 rows: 301 / 284. Input gradient:
       // 162 / 171 at 2, 240 / 250 at 64, 305 / 288 at 128.
       if constexpr (Mode != kWgrad) {
-        const bool half = Args::kDense ? dense_tile_rows<Mode>(a) == 128 : a.P < (int64_t)(Mode == kFwd ? 256 : 96) * a.G;
+        bool half;
+        if constexpr (Args::kDense) half = dense_tile_rows<Mode>(a) == 128;
+        else half = a.P < (int64_t)(Mode == kFwd ? 256 : 96) * a.G;
         if (half) return launch_wide<Tr, Mode, 128, Args>(a, s);
       }
       return launch_wide<Tr, Mode, 256, Args>(a, s);

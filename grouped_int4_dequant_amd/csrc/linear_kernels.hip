@@ -241,6 +241,25 @@ __global__ __launch_bounds__(256) void linear_grad_small_kernel(DenseArgs dg, De
   }
 }
 
+// dW out of the parts' sums, in order. Four elements a thread; bound by memory.
+template <typename Tr>
+__global__ __launch_bounds__(256) void add_parts_kernel(const float *parts, int32_t count, int64_t n, void *out, bool f32, bool accumulate) {
+  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (at >= n) return;
+  const int left = (int)min(n - at, (int64_t)4);
+  f4 sum = {0.f, 0.f, 0.f, 0.f};
+  for (int p = 0; p < count; p += 4) {
+    f4 v[4];
+#pragma unroll
+    for (int y = 0; y < 4; ++y) v[y] = load4<Tr>(parts, true, (int64_t)min(p + y, count - 1) * n + at, left);
+#pragma unroll
+    for (int y = 0; y < 4; ++y)
+      if (p + y < count) sum += v[y];
+  }
+  if (accumulate) sum += load4<Tr>(out, true, at, left);
+  store4_of<Tr>(out, f32, at, left, sum);
+}
+
 template <typename Tr, bool Gated>
 hipError_t linear_of(const LinearArgs<Gated> &a, hipStream_t s) {
   if (a.vec && a.P <= 64) {
@@ -269,35 +288,55 @@ hipError_t act_grad_of(const ActGradArgs &a, bool add, hipStream_t s) {
 // Whether every form that the products of a gradient may take fits a launch: known before the first of a call's
 // kernels is enqueued.
 bool grad_fits(const ActGradArgs &c, const DenseArgs &dx, const DenseArgs &dw) {
-  const int64_t n_w = dw.out ? cdiv(dw.N, kSmall) * cdiv(dw.K, kSmall) : 0, n_d = dx.out ? xcd_grid(cdiv(c.T, kSmall) * cdiv(dx.K, kSmall)) : 0;
+  const int64_t n_w = dw.out ? dw.G * cdiv(dw.N, kSmall) * cdiv(dw.K, kSmall) : 0, n_d = dx.out ? xcd_grid(cdiv(c.T, kSmall) * cdiv(dx.K, kSmall)) : 0;
   const int64_t few = dx.out && c.T <= 64 ? cdiv(c.T, kFewRows) * cdiv(dx.K, 64) : 0;
   return grid_fits(n_w + n_d + cdiv(c.N, 64), 256) && grid_fits(few, 512) && grid_fits(c.db ? cdiv(c.N, 64) : 0, 1024) &&
          n_w + n_d + cdiv(c.N, 64) < INT32_MAX / 2;
 }
 
 template <typename Tr>
-hipError_t linear_grad_of(const ActGradArgs &c, const DenseArgs &dx, const DenseArgs &dw, hipStream_t s) {
+hipError_t linear_grad_of(const ActGradArgs &c, const DenseArgs &dx, const DenseArgs &dw, float *parts, hipStream_t s) {
   const bool curved = c.act != MOE_ACT_NONE;
   if (!grad_fits(c, dx, dw)) return hipErrorInvalidConfiguration;
+  // dW's tiles leave their sums in dW, or in the parts
+  DenseArgs w = dw;
+  const bool cut = dw.out && dw.G > 1;
+  if (cut) {
+    w.out = parts;
+    w.out_f32 = 1;
+    w.accumulate = 0;
+    w.vec_out = dw.K % 4 == 0;
+  }
   // one launch for what may run side by side, where both products take small tiles
-  const bool small = dx.out && dw.out && c.T > 0 && dense_tile_rows<kDgrad>(dx) == kSmall && dense_tile_rows<kWgrad>(dw) == kSmall && dx.vec == dw.vec && !(dx.vec && c.T <= 64);
+  const bool small = dx.out && dw.out && c.T > 0 && dense_tile_rows<kDgrad>(dx) == kSmall && dense_tile_rows<kWgrad>(w) == kSmall && dx.vec == dw.vec &&
+                     !(dx.vec && c.T <= 64);
   const bool rows = small && !curved && c.T <= 1024;  // db from dy's rows, without chunks
   if (curved || (c.db && !rows)) {
     const hipError_t e = act_grad_of<Tr>(c, c.db && !small, s);
     if (e != hipSuccess) return e;
   }
   if (small) {
-    const int64_t n_w = cdiv(dw.N, kSmall) * cdiv(dw.K, kSmall), n_d = xcd_grid(cdiv(dx.P, kSmall) * cdiv(dx.K, kSmall)), n_c = c.db ? cdiv(c.N, 64) : 0;
+    const int64_t n_w = w.G * cdiv(w.N, kSmall) * cdiv(w.K, kSmall), n_d = xcd_grid(cdiv(dx.P, kSmall) * cdiv(dx.K, kSmall)), n_c = c.db ? cdiv(c.N, 64) : 0;
     const dim3 grid((unsigned)(n_w + n_d + n_c));
-    if (dx.vec) linear_grad_small_kernel<Tr, true><<<grid, 256, 0, s>>>(dx, dw, c, rows, (int)n_w, (int)n_d);
-    else linear_grad_small_kernel<Tr, false><<<grid, 256, 0, s>>>(dx, dw, c, rows, (int)n_w, (int)n_d);
-    return hipGetLastError();
-  }
-  if (dx.out && c.T > 0) {
-    const hipError_t e = launch_vec<Tr, kDgrad, DenseArgs>(dx, s);
+    if (dx.vec) linear_grad_small_kernel<Tr, true><<<grid, 256, 0, s>>>(dx, w, c, rows, (int)n_w, (int)n_d);
+    else linear_grad_small_kernel<Tr, false><<<grid, 256, 0, s>>>(dx, w, c, rows, (int)n_w, (int)n_d);
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+  } else {
+    if (dx.out && c.T > 0) {
+      const hipError_t e = launch_vec<Tr, kDgrad, DenseArgs>(dx, s);
+      if (e != hipSuccess) return e;
+    }
+    if (dw.out) {
+      const hipError_t e = launch_vec<Tr, kWgrad, DenseArgs>(w, s);
+      if (e != hipSuccess) return e;
+    }
   }
-  return dw.out ? launch_vec<Tr, kWgrad, DenseArgs>(dw, s) : hipSuccess;
+  if (cut) {
+    const int64_t n = (int64_t)dw.N * dw.K;
+    add_parts_kernel<Tr><<<dim3((unsigned)cdiv(n, 1024)), 256, 0, s>>>(parts, dw.G, n, dw.out, dw.out_f32, dw.accumulate);
+  }
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -310,6 +349,25 @@ ColumnChunks column_chunks(int32_t T, int32_t cols) {
   return {(int32_t)rows, (int32_t)cdiv(T, rows)};
 }
 
+RowParts weight_parts(int32_t T, int32_t N, int32_t K, bool wide) {
+  // The number of parts with the shortest time: that of the tiles, and of writing and reading the parts (4 TB/s) and another
+  // launch; at most 128 MiB. 8192 rows, 512 x 512 100 us uncut, 1024 x 1024 102.
+  RowParts best = {T > 0 ? T : 1, 1};
+  int64_t least = INT64_MAX;
+  for (int32_t count = 1; count <= 32; count *= 2) {
+    const int32_t rows = (int32_t)(cdiv(cdiv(T > 0 ? T : 1, count), kBR) * kBR);
+    if (count > 1 && ((int64_t)(count - 1) * rows >= T || (int64_t)count * N * K > (int64_t)32 << 20)) break;
+    int64_t t = wgrad_time(count > 1 ? rows : T, N, K, count, false);
+    if (wide) t = wgrad_time(count > 1 ? rows : T, N, K, count, true) < t ? wgrad_time(count > 1 ? rows : T, N, K, count, true) : t;
+    if (count > 1) t += 350 + (int64_t)count * N * K * 8 / 40000;
+    if (t < least) {
+      least = t;
+      best = {count > 1 ? rows : (T > 0 ? T : 1), count};
+    }
+  }
+  return best;
+}
+
 template <bool Gated>
 hipError_t launch_linear(const LinearArgs<Gated> &a, bool fp16, hipStream_t s) {
   return fp16 ? linear_of<Fp16, Gated>(a, s) : linear_of<Bf16, Gated>(a, s);
@@ -317,8 +375,8 @@ hipError_t launch_linear(const LinearArgs<Gated> &a, bool fp16, hipStream_t s) {
 template hipError_t launch_linear<false>(const LinearArgs<false> &, bool, hipStream_t);
 template hipError_t launch_linear<true>(const LinearArgs<true> &, bool, hipStream_t);
 
-hipError_t launch_linear_grad(const ActGradArgs &c, const DenseArgs &dx, const DenseArgs &dw, bool fp16, hipStream_t s) {
-  return fp16 ? linear_grad_of<Fp16>(c, dx, dw, s) : linear_grad_of<Bf16>(c, dx, dw, s);
+hipError_t launch_linear_grad(const ActGradArgs &c, const DenseArgs &dx, const DenseArgs &dw, float *parts, bool fp16, hipStream_t s) {
+  return fp16 ? linear_grad_of<Fp16>(c, dx, dw, parts, s) : linear_grad_of<Bf16>(c, dx, dw, parts, s);
 }
 
 }  // namespace moe

@@ -685,14 +685,14 @@ int moe_linear(int32_t dtype, const void *x, int64_t ldx, int32_t T, int32_t N, 
  *   dx     dtype or fp32 (dx_dtype) [T][lddx], or NULL (not wanted)
  *   dW, db dtype or fp32 (g_dtype) [N][K] and [N], each or NULL. accumulate != 0 (fp32
  *          only, else MOE_EUNSUPPORTED) adds to what they hold. T == 0 writes zeros (or leaves them).
- *   ws     moe_linear_backward_workspace_bytes(T, N, act) bytes, 256-byte aligned; may be NULL when
- *          act is MOE_ACT_NONE and db NULL. Calls that may run at the same time, in replayed
+ *   ws     moe_linear_backward_workspace_bytes(T, N, K, act) bytes, 256-byte aligned; may be NULL when
+ *          act is MOE_ACT_NONE and dW and db are NULL. Calls that may run at the same time, in replayed
  *          graphs too, need one each.
  * With an activation dz is rounded to dtype before the two products (they take 16-bit operands), so
  * dx and dW carry that rounding of each term whatever their type; db does not. Errors as
  * moe_linear, and MOE_EWORKSPACE.
  */
-size_t moe_linear_backward_workspace_bytes(int32_t T, int32_t N, int32_t act);
+size_t moe_linear_backward_workspace_bytes(int32_t T, int32_t N, int32_t K, int32_t act);
 int moe_linear_backward(int32_t dtype, const void *dy, int64_t lddy, const void *x, int64_t ldx, int32_t T, int32_t N, int32_t K,
                         const void *W, const void *pre, int64_t ldpre, int32_t act, void *dx, int32_t dx_dtype, int64_t lddx,
                         void *dW, void *db, int32_t g_dtype, int32_t accumulate, void *ws, size_t ws_bytes, hipStream_t stream);

@@ -42,7 +42,8 @@ REFUSED = [
      dict(ws=None), dict(ws=p + 16), dict(T=-1), dict(N=0), dict(K=0), dict(lddy=31), dict(ldx=63), dict(ldpre=31), dict(lddx=63), dict(act=6, N=33)),
     ("moe_linear_backward", LGRAD, EUNSUP, dict(g_dtype=0, acc=1), dict(act=0, T=1, N=1 << 29, lddy=1 << 29, K=8, ws_bytes=1 << 40),
      dict(act=0, db=None, N=1 << 20, lddy=1 << 20, K=1 << 20, ldx=1 << 20, lddx=1 << 20), dict(act=0, db=None, dW=None, T=1, K=1 << 30, ldx=1 << 30, lddx=1 << 30), dict(T=LARGE), dict(N=LARGE, lddy=LARGE, ldpre=LARGE), dict(K=LARGE, ldx=LARGE, lddx=LARGE)),
-    ("moe_linear_backward", LGRAD, EWS, dict(ws_bytes=8 * 32 * 2), dict(act=0, ws_bytes=0), dict(db=None, ws_bytes=8 * 32 * 2 - 1)),
+    ("moe_linear_backward", LGRAD, EWS, dict(ws_bytes=8 * 32 * 2), dict(act=0, ws_bytes=0), dict(db=None, ws_bytes=8 * 32 * 2 - 1),
+     dict(act=0, db=None, T=8192, N=512, K=512, lddy=512, ldx=512, lddx=512, ws_bytes=1 << 20)),
     ("moe_residual_norm", NORM, EINVAL, dict(dtype=2), dict(s_dtype=1), dict(w_dtype=1), dict(o=None, x=None), dict(y=None, n=None), dict(w_n=None), dict(o=p + 1),
      dict(x=p + 1), dict(w_o=p + 1), dict(gate=p + 1), dict(w_n=p + 1), dict(y=p + 1), dict(n=p + 1), dict(w_dtype=2, w_o=p + 2), dict(s_dtype=2, x=p + 2),
      dict(gates=0), dict(gates=3), dict(T=-1), dict(d=0), dict(ldo=63), dict(ldx=63), dict(ldy=63), dict(ldn=63), dict(eps=-1.0), dict(eps=NAN),
@@ -94,15 +95,16 @@ def test_few_layer_limits():
 def test_empty_calls_enqueue_nothing():
     assert call("moe_linear", LINEAR, T=0, x=None, y=None, W=None) == OK
     assert call("moe_linear_backward", LGRAD, T=0, acc=1, dy=None, x=None, dx=None) == OK
-    assert call("moe_linear_backward", LGRAD, T=0, dW=None, db=None, ws=None, ws_bytes=1 << 20, act=0) == OK
+    assert call("moe_linear_backward", LGRAD, T=0, dW=None, db=None, ws=None, ws_bytes=0, act=0) == OK
     assert call("moe_residual_norm", NORM, T=0, o=None, x=None, y=None, n=None) == OK
     assert call("moe_residual_norm_backward", NGRAD, T=0, acc=1, dy=None, dn=None, o=None, y=None, dx=None, d_o=None) == OK
 
 
 def test_workspace_bytes():
     f = moe.linear_backward_workspace_bytes
-    assert f(100, 64, "silu") >= 100 * 64 * 2 + 64 * 4 and f(0, 64, "none") > 0 and f(100, 64, "none") < 100 * 64 * 2
-    assert B.load().moe_linear_backward_workspace_bytes(-1, 64, 0) == 0 and B.load().moe_linear_backward_workspace_bytes(4, 63, 5) == 0
+    assert f(100, 64, 64, "silu") >= 100 * 64 * 2 + 64 * 4 and f(0, 64, 64, "none") > 0 and f(100, 64, 64, "none") < 100 * 64 * 2
+    assert f(8192, 512, 512) > 2 * 512 * 512 * 4 and f(1 << 20, 1 << 13, 1 << 13) < 1 << 28
+    assert B.load().moe_linear_backward_workspace_bytes(-1, 64, 64, 0) == 0 and B.load().moe_linear_backward_workspace_bytes(4, 63, 64, 5) == 0
     g = moe.residual_norm_backward_workspace_bytes
     assert g(100, 64, 1) >= 3 * 64 * 4 and g(0, 64, 3) > 0 and g(100, 64, 3) == 0 and g(100, 16385, 1) == 0 and g(100, 64, 0) == 0
 
@@ -121,9 +123,9 @@ def test_tensors_and_arguments_are_checked():
     with pytest.raises(ValueError, match="given"):
         moe.residual_norm_backward(None, None, None, None)
     with pytest.raises(ValueError, match="act"):
-        moe.linear_backward_workspace_bytes(4, 8, "softplus")
+        moe.linear_backward_workspace_bytes(4, 8, 8, "softplus")
     with pytest.raises(ValueError, match="even"):
-        moe.linear_backward_workspace_bytes(4, 7, "geglu")
+        moe.linear_backward_workspace_bytes(4, 7, 8, "geglu")
 
 
 @pytest.mark.parametrize("act", list(moe.ACTIVATIONS))

@@ -86,7 +86,7 @@ def dense(seed, T, d=128, f=96):
 
 
 def workspaces(moe, T, d, f, byte=255):
-    sizes = (moe.residual_norm_backward_workspace_bytes(T, d, 4), moe.linear_backward_workspace_bytes(T, 2 * f, "swiglu"),
+    sizes = (moe.residual_norm_backward_workspace_bytes(T, d, 4), moe.linear_backward_workspace_bytes(T, 2 * f, d, "swiglu"),
              moe.residual_norm_backward_workspace_bytes(T, d, 1))
     return [torch.full((n,), byte, dtype=torch.uint8, device="cuda") for n in sizes]
 

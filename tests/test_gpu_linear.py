@@ -35,7 +35,8 @@ ACTS = ("none", "relu", "silu", "gelu", "gelu_tanh", "swiglu", "geglu")
 SHAPES = {"one": (1, 1, 1), "two": (1, 2, 8), "decode": (1, 264, 520), "few16": (16, 72, 136), "few17": (17, 40, 1544), "few33": (33, 264, 200),
           "few64": (64, 136, 64), "small65": (65, 128, 72), "small": (129, 200, 328), "odd": (77, 66, 131), "odd_one": (1, 34, 77),
           "odd_k": (70, 64, 67), "wide128": (200, 33032, 72), "wide256": (1290, 6672, 200),
-          "wide_dx": (1290, 264, 6672), "wide_dW": (200, 2824, 2824)}
+          "wide_dx": (1290, 264, 6672), "wide_dW": (200, 2824, 2824),
+          "long": (8200, 136, 72), "long_odd": (5003, 70, 33), "long_wide": (4100, 520, 776)}  # rows cut into parts for dW
 
 
 def problem(shape, act, dtype, out, bias=None, residual=False, pre=False, seed=1):
