@@ -7,6 +7,8 @@
 // Many rows are bound by the matrix instructions and take the tiles of grouped_tiles.h,
 // with the epilogue on the accumulators: z, the activation and the residual never make a trip
 // of their own. Few rows are bound by reading W once.
+// bf16: 8192 rows, 8192 x 2048, swiglu with z stored 243 us on inputs in cache (1130 TFLOP/s; the product alone 218, a
+// library's 203), 265 from memory; 1 row, 4096 x 2048 5.9 us.
 
 #include "grouped_tiles.h"
 #include "block_internal.h"
@@ -17,7 +19,8 @@ namespace {
 // ---------------------------------------------------------------- few rows
 // At most 64 rows: a workgroup takes 16 rows of W (gated: eight of the gate and the eight that
 // it multiplies), whose sums its eight waves share and join in LDS, in order. W goes straight
-// from memory to operand registers and is read once; x comes from L2.
+// from memory to operand registers and is read once; x comes from L2. 4096 x 2048, bf16: 1 row 5.9 us, 16 rows 7.2,
+// 64 rows 12.9.
 template <typename Tr, bool Gated, int RB>
 __global__ __launch_bounds__(512) void linear_few_kernel(LinearArgs<Gated> a) {
   constexpr int kDeep = 8, kXDeep = RB == 1 ? 8 : RB == 2 ? 4 : 2;  // requests of W, and of each row block of x, in flight
@@ -82,7 +85,7 @@ __global__ __launch_bounds__(512) void linear_few_kernel(LinearArgs<Gated> a) {
 // ------------------------------------------------------- activation's gradient
 // A workgroup takes 256 columns of a chunk of rows; a thread eight of them, every eighth row. dz is rounded
 // to the operands' type, because it enters the two products as an operand of the matrix instructions; the
-// column sums are of its values before that. Bound by memory.
+// column sums are of its values before that. Bound by memory: 4096 x 8192, swiglu, 37 us for 168 MB (45 with db).
 template <typename Tr, bool Gated>
 __global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs a) {
   __shared__ float s_sum[8][Gated ? 2 : 1][256];
@@ -225,7 +228,8 @@ __device__ __forceinline__ void add_rows(const ActGradArgs &a, int block, float 
 }
 
 // Both products and db of a gradient whose tiles are few, side by side in one launch: workgroups 0 .. n_w - 1 take
-// dW's tiles, n_d more those of dx, the rest 64 columns of db each. 777 rows, 1032 x 520: 30 us in four launches.
+// dW's tiles, n_d more those of dx, the rest 64 columns of db each. 777 rows, 1032 x 520:
+// 15 us, 30 in four launches.
 template <typename Tr, bool Vec>
 __global__ __launch_bounds__(256) void linear_grad_small_kernel(DenseArgs dg, DenseArgs wg, ActGradArgs c, bool rows, int n_w, int n_d) {
   __shared__ __attribute__((aligned(16))) SmallTile s_l[2], s_r[2];
