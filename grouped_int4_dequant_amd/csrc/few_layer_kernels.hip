@@ -449,6 +449,7 @@ hipError_t few_of(FewArgs a, hipStream_t s) {
   a.share = 0;
   while (a.share < 3 && ((a.d + 31) / 32 + (1 << a.share) - 1) >> a.share > deep_of(a.T == 1)) ++a.share;
   const int64_t rounds = cdiv(items, kWaves >> a.share);
+  if (a.T == 1 && !grid_fits(rounds, 64 * kWaves)) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)(a.T == 1 || rounds < 512 ? rounds : 512));
   if (a.T == 1) few_gate_up_kernel<Tr, VPL, Vec, true><<<grid, 64 * kWaves, 0, s>>>(a);
   else few_gate_up_kernel<Tr, VPL, Vec, false><<<grid, 64 * kWaves, 0, s>>>(a);

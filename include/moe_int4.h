@@ -764,7 +764,8 @@ int moe_residual_norm_backward(int32_t dtype, const void *dy, int64_t lddy, cons
  *             the same time, in replayed graphs too, need one each
  * Each picked expert's weights are read once for all its tokens (of 16 at most). Sums and FFN's inner
  * values are held in fp32, and the inner values enter the second product so. The k experts are added in slot
- * order, then the shared one, then `add`. A row's result does not depend on the other rows of the call.
+ * order, then the shared one, then `add`. A row's result does not depend on the other rows of the call, but may
+ * differ in the last bits between a call of one token and a longer one (the sums are cut in other places).
  * Errors: MOE_EINVAL (null or misaligned pointer, unknown type, T < 0, a size < 1, f_sh < 0, k > E, a stride
  * below the width), MOE_EUNSUPPORTED (E > MOE_MAX_EXPERTS, k > 64, T > MOE_MAX_FEW_TOKENS,
  * T * k > MOE_MAX_FEW_PAIRS, d, f or f_sh above 2^20), MOE_EWORKSPACE, MOE_EHIP. T == 0 enqueues nothing.
