@@ -5,7 +5,7 @@
 //   y[t] = sum_j g[t][j] W_dn h[t][j] + shared + add[t]
 //
 // A decode batch has little use of each weight, so the bytes of the picked experts set the time.
-//   gate/up  every workgroup repeats the top-k (a token a wave) and sorts the pairs (token,
+//   gate/up  every workgroup repeats the top-k (a token a wave, or four) and sorts the pairs (token,
 //            slot) by expert in LDS, in blocks of at most 16 pairs of one expert; the first one leaves that for
 //            the second kernel. Then it walks over items of 8 columns of h of one block: 16 rows of W_gu,
 //            eight of the gate and the eight that it multiplies. One to eight waves share an item's sum
@@ -32,8 +32,10 @@ namespace {
 typedef float f2 __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves = 8;   // of a gate/up workgroup
-// Steps of weights asked for at once. One token's layer is a single round of items: everything is asked for at once there.
-constexpr int deep_of(bool one) { return one ? 16 : 8; }
+// Steps of weights asked for at once. One token's layer is a single round of items: everything is asked for at once there,
+// but for unaligned rows, which are put together from single words and have no registers left for sixteen
+// (283 spilled: 33.0 us against 13.4 at 8 of 256 experts, 1001 x 512).
+constexpr int deep_of(bool one, bool vec) { return one && vec ? 16 : 8; }
 
 // Runs of eight 16-bit values; without Vec rows may end inside one.
 template <bool Vec>
@@ -70,8 +72,24 @@ __device__ __forceinline__ void make_plan(const FewArgs &a, FewLds &s) {
   const int pairs = a.T * a.k;
   for (int e = tid; e < a.E; e += 64 * kWaves) s.tokens[e] = 0;
   float v[VPL], next[VPL];
-  if (wave < a.T) topk_load<VPL>(a.logits + (int64_t)wave * a.E, a.E, lane, next);
-  for (int t = wave; t < a.T; t += kWaves) {
+  // four tokens a wave, where a wave would have several (gate/up of 64 tokens, 8 of 64 experts, 1024 x 512: 48.0 -> 37.8 us; of
+  // 50 tokens, 2 of 16, 1000 x 744: 17.3 -> 15.4; of 9 tokens, 16 of 64: 32.1 -> 29.9)
+  const bool quarters = VPL == 1 && a.k <= 16 && a.T > kWaves;
+  if constexpr (VPL == 1) {
+    if (quarters)
+      for (int t0 = 4 * wave; t0 < a.T; t0 += 4 * kWaves) {
+        const int t = t0 + (lane >> 4), j = lane & 15;
+        int id;
+        float g;
+        topk_quarter<4>(a.logits + (int64_t)min(t, a.T - 1) * a.E, a.E, a.k, lane, id, g);
+        if (t < a.T && j < a.k) {
+          s.ids[t * a.k + j] = id;
+          s.gate[t * a.k + j] = g;
+        }
+      }
+  }
+  if (!quarters && wave < a.T) topk_load<VPL>(a.logits + (int64_t)wave * a.E, a.E, lane, next);
+  for (int t = wave; !quarters && t < a.T; t += kWaves) {
     int id;
     float g;
 #pragma unroll
@@ -172,7 +190,7 @@ __device__ __forceinline__ void store_inner(float *q, f4 v, int left) {
 // One: a single token.
 template <typename Tr, int VPL, bool Vec, bool One>
 __global__ __launch_bounds__(64 * kWaves, 4) void few_gate_up_kernel(FewArgs a) {
-  constexpr int kDeep = deep_of(One), kX = 8;
+  constexpr int kDeep = deep_of(One, Vec), kX = 8;
   __shared__ FewLds s;
   __shared__ __attribute__((aligned(16))) f4 s_part[2][kWaves][64];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -447,7 +465,7 @@ hipError_t few_of(FewArgs a, hipStream_t s) {
   const int64_t items = blocks * cdiv(a.f, 8) + blocks_sh * cdiv(a.f_sh, 8);
   // a wave's part of a sum is what it asks for at once, where eight waves can make it so
   a.share = 0;
-  while (a.share < 3 && ((a.d + 31) / 32 + (1 << a.share) - 1) >> a.share > deep_of(a.T == 1)) ++a.share;
+  while (a.share < 3 && ((a.d + 31) / 32 + (1 << a.share) - 1) >> a.share > deep_of(a.T == 1, Vec)) ++a.share;
   const int64_t rounds = cdiv(items, kWaves >> a.share);
   if (a.T == 1 && !grid_fits(rounds, 64 * kWaves)) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)(a.T == 1 || rounds < 512 ? rounds : 512));

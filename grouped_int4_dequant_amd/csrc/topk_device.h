@@ -128,4 +128,46 @@ __device__ __forceinline__ void topk_wave(const float *row, int E, int k, int la
   topk_values<VPL>(v, E, k, lane, my_id, my_gate);
 }
 
+// The same for four tokens by one wave, 16 lanes each: E <= 16 VPL, k <= 16. `row` is the lane's token's.
+template <int VPL>
+__device__ __forceinline__ void topk_quarter(const float *row, int E, int k, int lane, int &my_id, float &my_gate) {
+  const int l16 = lane & 15, base = lane & 48;
+  uint64_t key[VPL];
+#pragma unroll
+  for (int r = 0; r < VPL; ++r) key[r] = __float_as_uint(row[min(l16 + 16 * r, E - 1)]);
+#pragma unroll
+  for (int r = 0; r < VPL; ++r) {
+    const int e = l16 + 16 * r;
+    key[r] = e < E ? make_key(__uint_as_float((uint32_t)key[r]), e) : 0ull;
+  }
+#pragma unroll
+  for (int i = 1; i < VPL; ++i)
+#pragma unroll
+    for (int j = i; j > 0; --j)
+      if (key[j] > key[j - 1]) {
+        const uint64_t t = key[j];
+        key[j] = key[j - 1];
+        key[j - 1] = t;
+      }
+  float my_v = 0.f;
+  my_id = 0;
+  for (int j = 0; j < k; ++j) {
+    uint64_t win = key[0];
+    win = max64(win, dpp64<0xB1>(win));
+    win = max64(win, dpp64<0x4E>(win));
+    win = max64(win, dpp64<0x124>(win));
+    win = max64(win, dpp64<0x128>(win));
+    if (key[0] == win) {
+#pragma unroll
+      for (int r = 0; r + 1 < VPL; ++r) key[r] = key[r + 1];
+      key[VPL - 1] = 0ull;
+    }
+    if (l16 == j) { my_v = key_value(win); my_id = key_index(win); }
+  }
+  const float my_ex = expf(my_v - __shfl(my_v, base));
+  float sum = 0.f;
+  for (int j = 0; j < k; ++j) sum += __shfl(my_ex, base + j);
+  my_gate = my_ex / sum;
+}
+
 }  // namespace moe

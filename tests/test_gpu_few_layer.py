@@ -26,7 +26,8 @@ def rnd(g, *shape, dtype=BF, scale=1.0):
 #          T, k, E, d, f, f_sh
 SHAPES = {"one": (1, 1, 1, 1, 1, 1), "decode": (1, 8, 256, 520, 72, 40), "two": (2, 2, 16, 256, 128, 128), "odd": (3, 2, 5, 77, 131, 33), "batch": (16, 8, 256, 264, 40, 24),
           "crowd": (50, 2, 3, 136, 200, 0), "all": (64, 8, 8, 72, 24, 16), "most": (64, 8, 300, 40, 16, 8), "many_experts": (7, 6, 1000, 64, 16, 0), "wide": (5, 1, 4, 2312, 1544, 2056),
-          "ks": (8, 64, 70, 64, 16, 0), "tail_d": (20, 4, 9, 129, 64, 64), "tail_f": (20, 4, 9, 128, 65, 0), "deep": (17, 2, 4, 4104, 24, 520)}
+          "ks": (8, 64, 70, 64, 16, 0), "tail_d": (20, 4, 9, 129, 64, 64), "tail_f": (20, 4, 9, 128, 65, 0), "deep": (17, 2, 4, 4104, 24, 520),
+          "broad_odd": (21, 2, 5, 1031, 65, 33), "forty_nine": (49, 3, 49, 72, 520, 8), "ten": (10, 16, 64, 40, 16, 0), "one_odd": (1, 3, 9, 1029, 35, 0)}
 
 
 def problem(shape, dtype, out=None, seed=1, inner=1.0):
