@@ -934,20 +934,25 @@ def linear(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None
     return y
 
 
-def linear_backward_workspace_bytes(T: int, N: int, K: int, act: str = "none") -> int:
+_ROUND_DZ = 0x100
+
+
+def linear_backward_workspace_bytes(T: int, N: int, K: int, act: str = "none", round_dz: bool = False) -> int:
     _sizes(T, N, K)
-    return int(load().moe_linear_backward_workspace_bytes(T, N, K, _activation(act, N)[0]))
+    return int(load().moe_linear_backward_workspace_bytes(T, N, K, _activation(act, N)[0] | (_ROUND_DZ if round_dz else 0)))
 
 
 def linear_backward(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, pre: Optional[torch.Tensor] = None, act: str = "none",
                     bias_grad: bool = False, dx: Optional[torch.Tensor] = None, dW: Optional[torch.Tensor] = None,
                     db: Optional[torch.Tensor] = None, grad_dtype: Optional[torch.dtype] = None, accumulate: bool = False,
-                    ws: Optional[torch.Tensor] = None, stream=None):
+                    ws: Optional[torch.Tensor] = None, stream=None, round_dz: bool = False):
     """moe_linear_backward: (dx [T][K], dW [N][K], db [N] or None) from dy
     [T][columns of y] and pre [T][N], which linear wrote (not needed without
     activation). db is formed with bias_grad or where it is given; dW and db are of
     grad_dtype (None: x's type), and with accumulate are added to the given ones
-    (fp32). The C call takes NULL for those that are not wanted."""
+    (fp32). The C call takes NULL for those that are not wanted. round_dz: the
+    gradient of `pre` is rounded to x's type before the products, in about half the time
+    (MOE_ACT_ROUND_DZ)."""
     c = _Call(dy, "dy", stream)
     if dy.dim() != 2 or not isinstance(x, torch.Tensor) or x.dim() != 2 or not isinstance(W, torch.Tensor) or W.dim() != 2:
         raise ValueError("dy must be [T][columns], x [T][K] and W [N][K]")
@@ -968,6 +973,8 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, pre: Opt
     dx = c.result(dx, "dx", (T, K), None)
     dW = c.whole(dW, "dW", (N, K), grad_dtype)
     db = c.whole(db, "db", (N,), dW.dtype) if bias_grad else None
+    if round_dz:
+        code |= _ROUND_DZ
     ws = c.workspace(ws, int(load().moe_linear_backward_workspace_bytes(T, N, K, code)))
     c("moe_linear_backward", c.code, dy.data_ptr(), lddy, x.data_ptr(), ldx, T, N, K, W.data_ptr(), z, ldz, code, dx.data_ptr(),
       _CODES[dx.dtype], _ld(dx, K), dW.data_ptr(), None if db is None else db.data_ptr(), _CODES[dW.dtype], int(accumulate), ws.data_ptr(), ws.numel() * ws.element_size())

@@ -12,8 +12,14 @@ namespace {
 constexpr int32_t kMaxFewWidth = 1 << 20;
 
 size_t pad256(size_t n) { return (n + 255) & ~(size_t)255; }
-// a gradient's workspace: dz, then the chunks' column sums, then dW's parts
-size_t dz_bytes(int32_t T, int32_t N, int32_t act) { return act == MOE_ACT_NONE ? 0 : pad256((size_t)T * N * 2); }
+// A gradient's workspace: dz, then the chunks' column sums, then what the rows' parts give dW, then W and x in two bf16
+// parts. Its size is that of the types that need most: dz in three parts, and fp16 operands.
+int activation(int32_t act) { return act & ~MOE_ACT_ROUND_DZ; }
+bool curved_act(int32_t act) { return activation(act) != MOE_ACT_NONE; }
+int dz_parts(int32_t act) { return !curved_act(act) ? 0 : act & MOE_ACT_ROUND_DZ ? 1 : 3; }
+size_t dz_part(int32_t T, int32_t N) { return pad256((size_t)T * N * 2); }
+size_t dz_bytes(int32_t T, int32_t N, int32_t act) { return dz_parts(act) * dz_part(T, N); }
+size_t halves_bytes(int32_t rows, int32_t K, int32_t act) { return dz_parts(act) > 1 ? 2 * pad256((size_t)rows * K * 2) : 0; }
 // inner values of the few-token layer: fp32, in rows of whole 32-byte units
 int32_t inner_pitch(int32_t f) { return (f + 7) / 8 * 8; }
 size_t inner_bytes(int32_t rows, int32_t f) { return pad256((size_t)rows * inner_pitch(f) * sizeof(float)); }
@@ -21,6 +27,7 @@ size_t parts_bytes(const RowParts &p, int32_t N, int32_t K) { return p.count > 1
 int64_t sums_pitch(int32_t n) { return ((int64_t)n + 7) / 8 * 8; }
 
 size_t db_bytes(int32_t T, int32_t N, int32_t act) {
+  act = activation(act);
   return pad256((size_t)column_chunks(T, is_gated(act) ? N / 2 : N).count * sums_pitch(N) * sizeof(float) + 1);
 }
 
@@ -46,6 +53,17 @@ void fill_dense(GroupedArgs &a, const void *rows, int64_t ld_rows, const void *w
   a.w = static_cast<const uint16_t *>(w);
   a.ld_w = ld_w;
   a.G = 1; a.P = T; a.N = N; a.K = K;
+}
+// An fp16 matrix that takes part as two bf16 parts at `to`.
+HalvesArgs halves(const void *from, int64_t ld, int32_t rows, int32_t cols, char *to) {
+  HalvesArgs h{};
+  h.from = static_cast<const uint16_t *>(from);
+  h.ld = ld;
+  h.rows = rows;
+  h.cols = cols;
+  h.to = reinterpret_cast<uint16_t *>(to);
+  h.next = (int64_t)pad256((size_t)rows * cols * 2) / 2;
+  return h;
 }
 
 template <bool Gated>
@@ -89,14 +107,15 @@ int moe_linear(int32_t dtype, const void *x, int64_t ldx, int32_t T, int32_t N, 
 }
 
 size_t moe_linear_backward_workspace_bytes(int32_t T, int32_t N, int32_t K, int32_t act) {
-  if (check_linear(MOE_BF16, T, N, K, act) != MOE_OK) return 0;
+  if (check_linear(MOE_BF16, T, N, K, activation(act)) != MOE_OK) return 0;
   const size_t wide = parts_bytes(weight_parts(T, N, K, true), N, K), small = parts_bytes(weight_parts(T, N, K, false), N, K);
-  return dz_bytes(T, N, act) + db_bytes(T, N, act) + (wide > small ? wide : small);
+  return dz_bytes(T, N, act) + db_bytes(T, N, act) + (wide > small ? wide : small) + halves_bytes(N, K, act) + halves_bytes(T, K, act);
 }
 
 int moe_linear_backward(int32_t dtype, const void *dy, int64_t lddy, const void *x, int64_t ldx, int32_t T, int32_t N, int32_t K,
-                        const void *W, const void *pre, int64_t ldpre, int32_t act, void *dx, int32_t dx_dtype, int64_t lddx,
+                        const void *W, const void *pre, int64_t ldpre, int32_t act_flags, void *dx, int32_t dx_dtype, int64_t lddx,
                         void *dW, void *db, int32_t g_dtype, int32_t accumulate, void *ws, size_t ws_bytes, hipStream_t stream) {
+  const int32_t act = activation(act_flags);
   const int st = check_linear(dtype, T, N, K, act);
   if (st != MOE_OK) return st;
   const int32_t cols = is_gated(act) ? N / 2 : N;
@@ -112,11 +131,15 @@ int moe_linear_backward(int32_t dtype, const void *dy, int64_t lddy, const void 
     if ((dx && (!W || !typed(W, dtype))) || (dW && (!x || !typed(x, dtype)))) return MOE_EINVAL;
   }
   if (curved || db || dW) {
-    if (ws_bytes < moe_linear_backward_workspace_bytes(T, N, K, act)) return MOE_EWORKSPACE;
+    if (ws_bytes < moe_linear_backward_workspace_bytes(T, N, K, act_flags)) return MOE_EWORKSPACE;
     if (!ws || !aligned(ws, 256)) return MOE_EINVAL;
   }
   if (T == 0 && ((!dW && !db) || accumulate)) return MOE_OK;
   const bool fp16 = dtype == MOE_FP16;
+  // An fp32 result takes dz whole, in three bf16 parts, a 16-bit one in two. fp16's exponents hold no such
+  // parts: where one of the results is fp32, fp16 operands take part as two bf16 parts each.
+  const bool dx_f32 = dx && dx_dtype == MOE_FP32, dW_f32 = dW && g_dtype == MOE_FP32;
+  const bool split = curved && !(act_flags & MOE_ACT_ROUND_DZ), whole = dx_f32 || dW_f32, bf16_parts = split && fp16 && whole;
   const void *dz = dy;
   int64_t lddz = lddy;
   ActGradArgs c{};
@@ -130,17 +153,35 @@ int moe_linear_backward(int32_t dtype, const void *dy, int64_t lddy, const void 
   c.chunks = T > 0 ? n.count : 0;
   if (curved) {
     c.dz = static_cast<uint16_t *>(ws);
+    c.dz_parts = !split ? 1 : whole ? 3 : 2;
+    c.dz_next = (int64_t)dz_part(T, N) / 2;
     dz = ws;
     lddz = N;
   }
   if (db) {
-    c.part = reinterpret_cast<float *>(static_cast<char *>(ws) + dz_bytes(T, N, act));
+    c.part = reinterpret_cast<float *>(static_cast<char *>(ws) + dz_bytes(T, N, act_flags));
     c.pitch = sums_pitch(N);
     c.db = db;
     c.g_f32 = g_dtype == MOE_FP32;
     c.accumulate = accumulate != 0;
   }
-  DenseArgs dxa{}, dwa{};
+  const RowParts wide_rows = weight_parts(T, N, K, true), small_rows = weight_parts(T, N, K, false);
+  char *const parts = static_cast<char *>(ws) + dz_bytes(T, N, act_flags) + db_bytes(T, N, act_flags);
+  const size_t wide_bytes = parts_bytes(wide_rows, N, K), small_bytes = parts_bytes(small_rows, N, K);
+  HalvesArgs w2{}, x2{};
+  if (bf16_parts) {
+    char *const at = parts + (wide_bytes > small_bytes ? wide_bytes : small_bytes);
+    if (dx && T > 0) {
+      w2 = halves(W, K, N, K, at);
+      W = w2.to;
+    }
+    if (dW) {
+      x2 = halves(x, ldx, T, K, at + halves_bytes(N, K, act_flags));
+      x = x2.to;
+      ldx = K;
+    }
+  }
+  SplitArgs dxa{}, dwa{};
   if (dx) {
     fill_dense(dxa, dz, lddz, W, K, T, N, K);
     dxa.out = dx;
@@ -149,6 +190,10 @@ int moe_linear_backward(int32_t dtype, const void *dy, int64_t lddy, const void 
     dxa.vec = units(dz, lddz, N) && units(W, K, K);
     dxa.wide = wide_tiles(dxa, kDgrad);
     dxa.vec_out = runs(dx, dx_dtype, lddx) && K % 4 == 0;
+    dxa.c_parts = dx_f32 ? 3 : 2;
+    dxa.o_parts = bf16_parts ? 2 : 1;
+    dxa.c_next = c.dz_next;
+    dxa.o_next = w2.next;
   }
   if (dW) {
     fill_dense(dwa, x, ldx, dz, lddz, T, N, K);
@@ -158,13 +203,17 @@ int moe_linear_backward(int32_t dtype, const void *dy, int64_t lddy, const void 
     dwa.accumulate = accumulate != 0;
     dwa.vec = units(dz, lddz, N) && units(x, ldx, K);
     dwa.wide = wide_tiles(dwa, kWgrad);
-    const RowParts p = weight_parts(T, N, K, dwa.wide);
+    const RowParts &p = dwa.wide ? wide_rows : small_rows;
     dwa.part_rows = p.rows;
     dwa.G = p.count;
     dwa.vec_out = runs(dW, g_dtype, K) && K % 4 == 0;
+    dwa.c_parts = dW_f32 ? 3 : 2;
+    dwa.o_parts = bf16_parts ? 2 : 1;
+    dwa.c_next = c.dz_next;
+    dwa.o_next = x2.next;
   }
-  float *parts = reinterpret_cast<float *>(static_cast<char *>(ws) + dz_bytes(T, N, act) + db_bytes(T, N, act));
-  return status(launch_linear_grad(c, dxa, dwa, parts, fp16, stream));
+  float *const sums = reinterpret_cast<float *>(parts);
+  return status(split ? launch_linear_grad_split(c, dxa, dwa, w2, x2, sums, fp16, bf16_parts, stream) : launch_linear_grad(c, dxa, dwa, sums, fp16, stream));
 }
 
 int moe_residual_norm(int32_t dtype, const void *o, int64_t ldo, const void *x, int64_t ldx, int32_t stream_dtype, int32_t T,

@@ -53,14 +53,17 @@ struct NormGradArgs {
 struct NormChunks { int32_t rows, count, per_gate; };
 NormChunks norm_chunks(int32_t T, int32_t period);
 
-// dz = act'(pre) dy and its column sums
+// dz = act'(pre) dy and its column sums. dz enters the products as 16-bit operands: as the sum of two parts, which hold
+// 16 bits of a bf16 dz and 22 of an fp16 one, or of three bf16 parts, which hold it whole (or, if the caller wants that, rounded).
 struct ActGradArgs {
   const uint16_t *dy;       // [T][ld_dy], `cols` columns
   int64_t ld_dy;
   const uint16_t *pre;      // [T][ld_pre], N columns; nullable without activation
   int64_t ld_pre;
   int32_t T, N, cols, act;  // cols: N, or N / 2 if gated
-  uint16_t *dz;             // [T][N]; nullable without activation
+  uint16_t *dz;             // [dz_parts][T][N]; nullable without activation
+  int32_t dz_parts;         // 1: dz rounded
+  int64_t dz_next;          // elements from a part to the next
   float *part;              // nullable: column sums not wanted; [chunks][pitch]
   int64_t pitch;
   int32_t chunk_rows, chunks;
@@ -109,6 +112,17 @@ hipError_t launch_linear(const LinearArgs<Gated> &a, bool fp16, hipStream_t s);
 // dz and db, then dx = dz W and dW = dz^T x (each without `out`: not wanted)
 // parts: where dW's parts go when dw has more than one (dw.out is dW all the same).
 hipError_t launch_linear_grad(const ActGradArgs &c, const DenseArgs &dx, const DenseArgs &dw, float *parts, bool fp16, hipStream_t s);
+// The same with dz in more than one part. w, x: fp16 matrices that take part as two bf16 parts (with c.dz in three), and
+// where those go; `from` null: they are bf16, or not wanted, or dz is of their type.
+struct HalvesArgs {
+  const uint16_t *from;     // [rows][ld]
+  int64_t ld;
+  int32_t rows, cols;
+  uint16_t *to;             // [2][rows][cols]
+  int64_t next;             // elements from a part to the next
+};
+hipError_t launch_linear_grad_split(const ActGradArgs &c, const SplitArgs &dx, const SplitArgs &dw, const HalvesArgs &w, const HalvesArgs &x,
+                                    float *parts, bool fp16, bool bf16_parts, hipStream_t s);
 inline bool is_gated(int32_t act) { return act == MOE_ACT_SWIGLU || act == MOE_ACT_GEGLU; }
 
 hipError_t launch_norm(const NormArgs &a, bool fp16, hipStream_t s);

@@ -28,8 +28,8 @@ enum GroupedMode { kFwd = 0, kDgrad = 1, kWgrad = 2 };
 
 struct GroupedArgs {
   // of the kernels that take them: one matrix for all rows; bias, activation and residual behind the
-  // product; columns in two halves, the first the gate's
-  static constexpr bool kDense = false, kEpilogue = false, kGated = false;
+  // product; columns in two halves, the first the gate's; operands in parts
+  static constexpr bool kDense = false, kEpilogue = false, kGated = false, kSplit = false;
   const uint16_t *rows;     // A (forward, weight gradient) or dC (input gradient)
   int64_t ld_rows;
   const int32_t *a_row;     // nullable: row of `rows` for each sorted row
@@ -52,6 +52,13 @@ struct GroupedArgs {
 struct DenseArgs : GroupedArgs {
   static constexpr bool kDense = true;
   int32_t part_rows;
+};
+// One matrix whose operands come as sums of 16-bit parts (gradients: dC in `c_parts` of them, the other operand in
+// `o_parts`), each part a matrix of its own behind the one before. The product is the sum of those of all pairs of parts.
+struct SplitArgs : DenseArgs {
+  static constexpr bool kSplit = true;
+  int32_t c_parts, o_parts;
+  int64_t c_next, o_next;   // elements from a part to the next
 };
 // y = act(x W^T + bias) + residual; z = x W^T + bias goes to `pre`
 template <bool Gated>

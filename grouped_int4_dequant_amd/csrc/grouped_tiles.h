@@ -69,6 +69,55 @@ __device__ __forceinline__ void dense_tile(int item, int ti, int tj, int &it, in
   jt = x / h;
   it = 8 * band + x - jt * h;
 }
+// Where a kernel stands in the steps of a sum, as it asks for them one after the other. Where operands come in parts, all
+// terms of the smallest pair of parts come first and those of the first parts last: the sum of the small ones has small
+// roundings. (With a block's pairs one after the other, the larger sum is rounded once for each: fp32 gradients of 4096 rows,
+// 8192 x 2048 1.0e-6 off, this way 5.9e-7.)
+template <typename Args>
+struct Steps {
+  int r = 0;          // first term of the step (without parts the caller counts); behind the last step nr or more
+  int c = 0, o = 0;   // the parts
+  __device__ __forceinline__ explicit Steps(const Args &a) {
+    if constexpr (Args::kSplit) {
+      c = a.c_parts - 1;
+      o = a.o_parts - 1;
+    }
+  }
+  static __host__ __device__ __forceinline__ int pairs(const Args &a) {
+    if constexpr (Args::kSplit) return a.c_parts * a.o_parts;
+    else return 1;
+  }
+  // steps of nr terms, and how many from the first on hold kBR terms
+  static __device__ __forceinline__ int count(const Args &a, int nr) { return (nr + kBR - 1) / kBR * pairs(a); }
+  static __device__ __forceinline__ int whole(const Args &a, int nr) {
+    return Args::kSplit && nr % kBR != 0 ? 0 : nr / kBR * pairs(a);
+  }
+  __device__ __forceinline__ int first(int s) const { return Args::kSplit ? r : s * kBR; }
+  // elements from the operands' first terms to the step's parts
+  __device__ __forceinline__ int64_t c_part(const Args &a) const {
+    if constexpr (Args::kSplit) return c * a.c_next;
+    else return 0;
+  }
+  __device__ __forceinline__ int64_t o_part(const Args &a) const {
+    if constexpr (Args::kSplit) return o * a.o_next;
+    else return 0;
+  }
+  // Moves on; what is added to the places of dC's and the other operand's step, where a step of terms is
+  // `c_step` and `o_step` long.
+  __device__ __forceinline__ void next(const Args &a, int nr, int64_t c_step, int64_t o_step, int64_t &c_add, int64_t &o_add) {
+    c_add = c_step;
+    o_add = o_step;
+    if constexpr (Args::kSplit) {
+      const bool end = r + kBR >= nr, c_end = c == 0;
+      const int64_t back = (nr + kBR - 1) / kBR - 1;
+      c_add = end ? (c_end ? (a.c_parts - 1) * a.c_next : -a.c_next) - back * c_step : c_step;
+      o_add = end ? (c_end ? -a.o_next : 0) - back * o_step : o_step;
+      o -= end && c_end;
+      c = !end ? c : c_end ? a.c_parts - 1 : c - 1;
+      r = !end ? r + kBR : o < 0 ? nr : 0;
+    }
+  }
+};
 // Columns of the result (forward and input gradient).
 template <int Mode, typename Args>
 __host__ __device__ __forceinline__ int columns_of(const Args &a) {
@@ -189,7 +238,7 @@ __device__ __forceinline__ void small_body(const Args &a, const int block, Small
     nr = Mode == kFwd ? a.K : a.N;
   }
   // (with no row of A at all nothing is read, and every result is that of a masked row)
-  const int steps = Mode == kFwd && a.a_rows == 0 ? 0 : (nr + kBR - 1) / kBR;
+  const int whole_steps = Steps<Args>::whole(a, nr), steps = Mode == kFwd && a.a_rows == 0 ? 0 : Steps<Args>::count(a, nr);
 
   // ---- staging. Unit u = tid + 256 i: a straight operand's row u / 8, an
   // across operand's r = u / 8, eight r or columns at 8 (slot's unit). Straight rows past the
@@ -219,26 +268,31 @@ __device__ __forceinline__ void small_body(const Args &a, const int block, Small
     else rp[i] = R + (int64_t)(j0 + min(row, nj - 1)) * ldr + rslot;
   }
   u4 lreg[Depth][U], rreg[Depth][U];
+  Steps<Args> at_step(a);
   auto load = [&](int s, u4 (&lreg)[U], u4 (&rreg)[U], auto whole) __attribute__((always_inline)) {  // whole: every r of the step exists
     constexpr bool kAll = decltype(whole)::value;
+    const int r0 = at_step.first(s);
+    const int64_t lpart = at_step.c_part(a), rpart = at_step.o_part(a);
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int r = s * kBR + urow + 32 * i;  // across operands: the unit's r
+      const int r = r0 + urow + 32 * i;  // across operands: the unit's r
       if (Mode == kWgrad) {  // a masked row's dC may hold anything: both operands are zeros
         int at = -1;
         if (r < nr) at = a.a_row ? a.a_row[first + r] : first + r;
         const bool ok = at >= 0 && at < a.a_rows;
-        lreg[i] = load_unit<Vec>(lp[i] + (int64_t)s * kBR * ldl, lp[i] && ok ? ni - lslot : 0);
-        rreg[i] = load_unit<Vec>(rp[i] + (ok ? at * ldr : 0), rp[i] && ok ? nj - rslot : 0);
+        lreg[i] = load_unit<Vec>(lp[i] + lpart + (int64_t)r0 * ldl, lp[i] && ok ? ni - lslot : 0);
+        rreg[i] = load_unit<Vec>(rp[i] + rpart + (ok ? at * ldr : 0), rp[i] && ok ? nj - rslot : 0);
         continue;
       }
-      lreg[i] = load_unit<Vec>(lp[i] + s * kBR, kAll ? 8 : nr - s * kBR - lslot);
+      lreg[i] = load_unit<Vec>(lp[i] + lpart + r0, kAll ? 8 : nr - r0 - lslot);
       if (kRAcross) {
-        rreg[i] = load_unit<Vec>(rp[i] + (int64_t)s * kBR * ldr, rp[i] && (kAll || r < nr) ? nj - rslot : 0);
+        rreg[i] = load_unit<Vec>(rp[i] + rpart + (int64_t)r0 * ldr, rp[i] && (kAll || r < nr) ? nj - rslot : 0);
       } else {
-        rreg[i] = load_unit<Vec>(rp[i] + s * kBR, kAll ? 8 : nr - s * kBR - rslot);
+        rreg[i] = load_unit<Vec>(rp[i] + rpart + r0, kAll ? 8 : nr - r0 - rslot);
       }
     }
+    int64_t unused_c, unused_o;
+    at_step.next(a, nr, 0, 0, unused_c, unused_o);
   };
   auto keep = [&](int buf, const u4 (&lreg)[U], const u4 (&rreg)[U]) __attribute__((always_inline)) {
 #pragma unroll
@@ -270,7 +324,7 @@ __device__ __forceinline__ void small_body(const Args &a, const int block, Small
   Extra4 extra[2][kBlocks];
   constexpr std::false_type partly{};
   if (steps > 0) {
-    if (nr >= Depth * kBR) {
+    if (whole_steps >= Depth) {
 #pragma unroll
       for (int s = 0; s < Depth; ++s) load(s, lreg[s], rreg[s], std::true_type{});
     } else {
@@ -316,7 +370,7 @@ __device__ __forceinline__ void small_body(const Args &a, const int block, Small
     }
   };
   int s = 0;
-  for (; (s + 2 * Depth) * kBR <= nr && s < steps; s += Depth) round(s, std::true_type{});  // the steps it asks for are whole
+  for (; s + 2 * Depth <= whole_steps && s < steps; s += Depth) round(s, std::true_type{});  // the steps it asks for are whole
   for (; s < steps; s += Depth) round(s, partly);
 
   // ---- results: lane holds output row p16 and four consecutive columns of each block
@@ -414,31 +468,48 @@ __global__ __launch_bounds__(512) void grouped_few_kernel(Args a) {
     // wave: every eighth 32 of n. A lane reads four columns 4 p16 .. of rows n = 8 q4 .. + 7 and
     // hands the matrix instruction number c the eight values of column 4 p16 + c.
     const int col = 4 * p16;
-    constexpr int kDeep = 2;
-    for (int n0 = 32 * wave; n0 < nr; n0 += 256 * kDeep) {
-      u2 wv[kDeep][8];
-      s8 xv[kDeep];
+    constexpr int kDeep = 2, kParts = Args::kSplit ? 3 : 1;  // of a row of dC, at most
+    auto multiply = [&](const uint16_t *W) __attribute__((always_inline)) {
+      for (int n0 = 32 * wave; n0 < nr; n0 += 256 * kDeep) {
+        u2 wv[kDeep][8];
+        s8 xv[kDeep][kParts];
 #pragma unroll
-      for (int u = 0; u < kDeep; ++u) {
-        const int n = n0 + 256 * u + 8 * q4;
+        for (int u = 0; u < kDeep; ++u) {
+          const int n = n0 + 256 * u + 8 * q4;
 #pragma unroll
-        for (int y = 0; y < 8; ++y)
-          wv[u][y] = n < nr && col < nj ? *reinterpret_cast<const u2 *>(W + (int64_t)(n + y) * a.K + j0 + col) : u2{0u, 0u};
-        xv[u] = x && n < nr ? *reinterpret_cast<const s8 *>(x + n) : zero;
-      }
+          for (int y = 0; y < 8; ++y)
+            wv[u][y] = n < nr && col < nj ? *reinterpret_cast<const u2 *>(W + (int64_t)(n + y) * a.K + j0 + col) : u2{0u, 0u};
+          xv[u][0] = x && n < nr ? *reinterpret_cast<const s8 *>(x + n) : zero;
+          if constexpr (Args::kSplit) {
 #pragma unroll
-      for (int u = 0; u < kDeep; ++u) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          u4 v;
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const uint32_t lo = wv[u][2 * y][c >> 1], hi = wv[u][2 * y + 1][c >> 1];
-            v[y] = c & 1 ? (lo >> 16) | (hi & 0xffff0000u) : (lo & 0xffffu) | (hi << 16);
+            for (int c = 1; c < kParts; ++c) xv[u][c] = x && n < nr && c < a.c_parts ? *reinterpret_cast<const s8 *>(x + c * a.c_next + n) : zero;
           }
-          acc[c] = Tr::mfma(__builtin_bit_cast(s8, v), xv[u], acc[c]);
+        }
+#pragma unroll
+        for (int u = 0; u < kDeep; ++u) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            u4 v;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const uint32_t lo = wv[u][2 * y][c >> 1], hi = wv[u][2 * y + 1][c >> 1];
+              v[y] = c & 1 ? (lo >> 16) | (hi & 0xffff0000u) : (lo & 0xffffu) | (hi << 16);
+            }
+#pragma unroll
+            for (int q = kParts - 1; q >= 0; --q) {
+              if constexpr (Args::kSplit) {
+                if (q >= a.c_parts) continue;  // (zeros, but the weight may be infinite)
+              }
+              acc[c] = Tr::mfma(__builtin_bit_cast(s8, v), xv[u][q], acc[c]);
+            }
+          }
         }
       }
+    };
+    if constexpr (Args::kSplit) {
+      for (int o = a.o_parts - 1; o >= 0; --o) multiply(W + o * a.o_next);
+    } else {
+      multiply(W);
     }
 #pragma unroll
     for (int c = 0; c < NB; ++c) s_part[wave][c][lane] = acc[c];
@@ -534,7 +605,8 @@ __device__ __forceinline__ void wide_body(const Args &a, const WideTile t, uint8
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wi = wave >> 2, wj = wave & 3;
   const int p16 = lane & 15, q4 = lane >> 4;
-  const int steps = (t.nr + kBR - 1) / kBR;
+  const int steps = Steps<Args>::count(a, t.nr), whole_steps = Steps<Args>::whole(a, t.nr);
+  Steps<Args> at_step(a);
 
   // ---- requests. Unit i is piece 8 i + wave: a straight operand's tile rows
   // 64 i + tid / 8, an across operand's r = 8 i + wave of the step in the lower 32 lanes and 32 more in the upper. Rows and
@@ -591,7 +663,7 @@ __device__ __forceinline__ void wide_body(const Args &a, const WideTile t, uint8
     if constexpr (Mode == kWgrad) {
 #pragma unroll
       for (int i = 0; i < kUnits; ++i) {
-        const int r = s * kBR + rr + 8 * i, p = t.first + min(r, t.nr - 1);
+        const int r = at_step.first(s) + rr + 8 * i, p = t.first + min(r, t.nr - 1);
         const int at = Gather ? a.a_row[p] : p;
         rrow[i] = ((r < t.nr) & (at < a.a_rows)) ? at : -1;
       }
@@ -599,10 +671,16 @@ __device__ __forceinline__ void wide_body(const Args &a, const WideTile t, uint8
   };
   // `s` is the step asked for, lbase and rbase stand at it; `whole`: every r of the step exists
   const int64_t lstep = kLAcross ? kBR * a.ld_w * 2 : kBR * 2, rstep = Mode == kDgrad ? kBR * a.ld_w * 2 : Mode == kFwd ? kBR * 2 : 0;
+  auto advance = [&]() __attribute__((always_inline)) {
+    int64_t l, r;
+    at_step.next(a, t.nr, lstep / 2, rstep / 2, l, r);
+    lbase += 2 * l;
+    rbase += 2 * r;
+  };
   auto request_l = [&](int s, int i, uint8_t *buf, auto whole) __attribute__((always_inline)) {
     const char *p = uniform(lbase + (kLAcross ? (lstep >> 3) * i : 0)) + lv[kLAcross ? 0 : i];
     if constexpr (Mode == kWgrad) p = rrow[i] >= 0 ? p : (const char *)&g_zeros;  // a masked row's dC may hold anything
-    else if constexpr (!decltype(whole)::value) p = s * kBR + lr < t.nr ? p : (const char *)&g_zeros;
+    else if constexpr (!decltype(whole)::value) p = at_step.first(s) + lr < t.nr ? p : (const char *)&g_zeros;
     load_lds16(p, buf + row_piece<Mode>(8 * i) + row_piece<Mode>(1) * wave);
   };
   auto request_r = [&](int s, int i, uint8_t *buf, auto whole) __attribute__((always_inline)) {
@@ -612,7 +690,7 @@ __device__ __forceinline__ void wide_body(const Args &a, const WideTile t, uint8
       p = rrow[i] >= 0 ? p : (const char *)&g_zeros;
     } else {
       p = uniform(rbase + (kRAcross ? (rstep >> 3) * i : 0)) + rv[kRAcross ? 0 : i];
-      if constexpr (!decltype(whole)::value) p = s * kBR + rr + (kRAcross ? 8 * i : 0) < t.nr ? p : (const char *)&g_zeros;
+      if constexpr (!decltype(whole)::value) p = at_step.first(s) + rr + (kRAcross ? 8 * i : 0) < t.nr ? p : (const char *)&g_zeros;
     }
     load_lds16(p, buf + col_piece<Mode>(8 * i) + col_wave);
   };
@@ -698,8 +776,7 @@ __device__ __forceinline__ void wide_body(const Args &a, const WideTile t, uint8
       for (int j = 0; j < kTJ; ++j) acc[i][j] = Tr::mfma(r1[j], l1[i], acc[i][j]);
       __builtin_amdgcn_sched_barrier(0);
     }
-    lbase += lstep;
-    rbase += rstep;
+    advance();
   };
   // The weight gradient's variant of a step. Both its operands come from LDS
   // in pairs of 8-byte fetches, and a half held ahead spills; here the next
@@ -724,25 +801,25 @@ __device__ __forceinline__ void wide_body(const Args &a, const WideTile t, uint8
       for (int j = 0; j < kTJ; ++j) acc[i][j] = Tr::mfma(r[ks][j], l[x & 1], acc[i][j]);
       __builtin_amdgcn_sched_barrier(0);
     }
-    lbase += lstep;
-    rbase += rstep;
+    advance();
     fetch_rows(s + 2);
     meet(none);
   };
   constexpr std::false_type partly{};
+  lbase += 2 * at_step.c_part(a);
+  rbase += 2 * at_step.o_part(a);
   if (steps > 0) {
     fetch_rows(0);
 #pragma unroll
     for (int i = 0; i < UL; ++i) request_l(0, i, s_l0, partly);
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) request_r(0, i, s_r0, partly);
-    lbase += lstep;
-    rbase += rstep;
+    advance();
     fetch_rows(1);
     if constexpr (kNear) {
       meet(none);
       int s = 0;
-      for (; (s + 3) * kBR <= t.nr; s += 2) {  // steps s + 1 and s + 2 are whole
+      for (; s + 3 <= whole_steps; s += 2) {  // steps s + 1 and s + 2 are whole
         step_near(s, s_l0, s_r0, s_l1, s_r1, std::true_type{});
         step_near(s + 1, s_l1, s_r1, s_l0, s_r0, std::true_type{});
       }
@@ -757,8 +834,7 @@ __device__ __forceinline__ void wide_body(const Args &a, const WideTile t, uint8
         for (int i = 0; i < UL; ++i) request_l(x, i, x == 1 ? s_l1 : s_l2, partly);
 #pragma unroll
         for (int i = 0; i < kUnits; ++i) request_r(x, i, x == 1 ? s_r1 : s_r2, partly);
-        lbase += lstep;
-        rbase += rstep;
+        advance();
       }
       meet(std::integral_constant<int, Stages - 1>{});
 #pragma unroll
@@ -776,7 +852,7 @@ __device__ __forceinline__ void wide_body(const Args &a, const WideTile t, uint8
         }
       };
       int s = 0;
-      for (; (s + 2 * Stages) * kBR <= t.nr; s += Stages) round(s, std::true_type{});  // the steps it asks for are whole
+      for (; s + 2 * Stages <= whole_steps; s += Stages) round(s, std::true_type{});  // the steps it asks for are whole
       for (; s < steps; s += Stages) round(s, partly);  // a part of a round ends with steps of zeros
     }
   }
@@ -972,8 +1048,9 @@ inline int64_t wgrad_time(int64_t part_rows, int64_t N, int64_t K, int64_t parts
 template <int Mode, typename Args>
 int dense_tile_rows(const Args &a) {
   if (!a.vec || !a.wide) return kSmall;
-  if constexpr (Mode == kWgrad) return wgrad_time(a.part_rows, a.N, a.K, a.G, true) < wgrad_time(a.part_rows, a.N, a.K, a.G, false) ? kWide : kSmall;
-  const int64_t rows = a.P, cols = columns_of<Mode>(a), steps = cdiv(Mode == kFwd ? a.K : a.N, kBR);
+  const int64_t pairs = Steps<Args>::pairs(a);
+  if constexpr (Mode == kWgrad) return wgrad_time(pairs * a.part_rows, a.N, a.K, a.G, true) < wgrad_time(pairs * a.part_rows, a.N, a.K, a.G, false) ? kWide : kSmall;
+  const int64_t rows = a.P, cols = columns_of<Mode>(a), steps = cdiv(Mode == kFwd ? a.K : a.N, kBR) * pairs;
   constexpr int kPer = Args::kGated ? 2 : 1;
   const int64_t n64 = cdiv(rows, kSmall) * cdiv(cols, kSmall / kPer), n256 = cdiv(rows, kWide) * cdiv(cols, kWide / kPer);  // times in 10 ns
   const int64_t t64 = (n64 > 256 ? n64 : 256) * ((Mode == kFwd ? 28 : 32) * steps + 100) / 256;

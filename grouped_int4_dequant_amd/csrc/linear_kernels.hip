@@ -9,6 +9,9 @@
 // of their own. Few rows are bound by reading W once.
 // bf16: 8192 rows, 8192 x 2048, swiglu with z stored 243 us on inputs in cache (1130 TFLOP/s; the product alone 218, a
 // library's 203), 265 from memory; 1 row, 4096 x 2048 5.9 us.
+// dz is an operand of its two products, which have 16 bits a value, and is laid out as a sum of such: rounded to one, it
+// makes 16-bit results 1.4 times as far off as their own rounding (bf16 2.35e-3 against 1.66e-3) and fp32 ones 2800 times. Two parts for
+// 16-bit results and three for fp32 ones cost as many products: 4096 rows, 8192 x 2048, bf16, each product 115 us a part.
 
 #include "grouped_tiles.h"
 #include "block_internal.h"
@@ -83,9 +86,82 @@ __global__ __launch_bounds__(512) void linear_few_kernel(LinearArgs<Gated> a) {
 }
 
 // ------------------------------------------------------- activation's gradient
-// A workgroup takes 256 columns of a chunk of rows; a thread eight of them, every eighth row. dz is rounded
-// to the operands' type, because it enters the two products as an operand of the matrix instructions; the
-// column sums are of its values before that. Bound by memory: 4096 x 8192, swiglu, 37 us for 168 MB (45 with db).
+// Operands in fp16 whose products are formed of bf16 parts, which have fp32's exponents.
+struct Fp16InBf16 : Fp16 {
+  static __device__ __forceinline__ f4 mfma(s8 a, s8 b, f4 c) { return Bf16::mfma(a, b, c); }
+};
+template <typename Tr>
+struct PartOf { typedef Tr type; };
+template <>
+struct PartOf<Fp16InBf16> { typedef Bf16 type; };
+
+// The value of a 16-bit type next to a finite v, towards zero.
+template <typename P>
+__device__ __forceinline__ uint16_t towards_zero(float v) {
+  if constexpr (std::is_same<P, Bf16>::value) return (uint16_t)(__builtin_bit_cast(uint32_t, v) >> 16);
+  else return (uint16_t)__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(fminf(fmaxf(v, -65504.f), 65504.f), 0.f));
+}
+// v as the sum of `n` (2 or 3, bf16) parts. All are of v's sign, and none is zero unless v is (or is less than two of the type's smallest
+// steps): the product of each with an infinite value is then the infinity that v's is, and the sum of the products too. So a value
+// that its first part would hold whole takes the next smaller one there. The last of two parts is rounded, the last of three exact.
+template <typename P, int N>
+__device__ __forceinline__ void split(float v, uint16_t (&part)[N]) {
+  if (!(__builtin_fabsf(v) < __builtin_inff())) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) part[i] = P::from(v);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i + 1 < N; ++i) {
+    uint16_t p = towards_zero<P>(v);
+    float rest = v - P::to(p);
+    if ((i + 2 < N ? rest == 0.f : (P::from(rest) & 0x7fff) == 0) && (p & 0x7fff) > 1) {
+      --p;  // one step towards zero, whatever the sign
+      rest = v - P::to(p);
+    }
+    part[i] = p;
+    v = rest;
+  }
+  part[N - 1] = P::from(v);
+}
+// The same of eight values, and their first `left` stored: [N][next]
+template <typename P, int N>
+__device__ __forceinline__ void store_parts(uint16_t *to, int64_t at, int64_t next, int left, const float (&v)[8]) {
+  uint16_t part[8][N];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) split<P, N>(v[i], part[i]);
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    uint16_t *q = to + n * next + at;
+    if (left >= 8) {
+      u4 w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = (uint32_t)part[2 * i][n] | (uint32_t)part[2 * i + 1][n] << 16;
+      *reinterpret_cast<u4_elem *>(q) = w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < left) q[i] = part[i][n];
+    }
+  }
+}
+
+// An fp16 matrix as two bf16 parts, exactly. Eight elements a thread; bound by memory.
+__global__ __launch_bounds__(256) void halves_kernel(HalvesArgs a) {
+  const int units = (a.cols + 7) / 8;
+  const int64_t all = (int64_t)a.rows * units;
+  for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < all; u += (int64_t)gridDim.x * 256) {
+    const int64_t row = u / units;
+    const int col = 8 * (int)(u - row * units), left = a.cols - col;
+    float v[8];
+    widen8<Fp16, false>(load_raw8<false>(a.from, row * a.ld + col, left), v);
+    store_parts<Bf16, 2>(a.to, row * a.cols + col, a.next, left, v);
+  }
+}
+
+// A workgroup takes 256 columns of a chunk of rows; a thread eight of them, every eighth row. dz enters the two products
+// as an operand of the matrix instructions, in 16-bit parts; the column sums are of its values before
+// that. Bound by memory: 4096 x 8192, swiglu, 37 us for 168 MB where dz is rounded (45 with db), 62 for 235 MB in two parts.
 template <typename Tr, bool Gated>
 __global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs a) {
   __shared__ float s_sum[8][Gated ? 2 : 1][256];
@@ -128,8 +204,14 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs a) {
             dy[i] *= slope;
           }
         }
-        store8<Tr>(a.dz, false, (int64_t)row * a.N + col, left, dy);
-        if constexpr (Gated) store8<Tr>(a.dz, false, (int64_t)row * a.N + a.cols + col, left, z);
+        auto store = [&](int64_t at, const float (&v)[8]) __attribute__((always_inline)) {
+          typedef typename PartOf<Tr>::type P;
+          if (a.dz_parts == 1) store8<Tr>(a.dz, false, at, left, v);
+          else if (std::is_same<P, Bf16>::value && a.dz_parts == 3) store_parts<P, std::is_same<P, Bf16>::value ? 3 : 2>(a.dz, at, a.dz_next, left, v);
+          else store_parts<P, 2>(a.dz, at, a.dz_next, left, v);
+        };
+        store((int64_t)row * a.N + col, dy);
+        if constexpr (Gated) store((int64_t)row * a.N + a.cols + col, z);
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -230,8 +312,8 @@ __device__ __forceinline__ void add_rows(const ActGradArgs &a, int block, float 
 // Both products and db of a gradient whose tiles are few, side by side in one launch: workgroups 0 .. n_w - 1 take
 // dW's tiles, n_d more those of dx, the rest 64 columns of db each. 777 rows, 1032 x 520:
 // 15 us, 30 in four launches.
-template <typename Tr, bool Vec>
-__global__ __launch_bounds__(256) void linear_grad_small_kernel(DenseArgs dg, DenseArgs wg, ActGradArgs c, bool rows, int n_w, int n_d) {
+template <typename Tr, bool Vec, typename Args>
+__global__ __launch_bounds__(256) void linear_grad_small_kernel(Args dg, Args wg, ActGradArgs c, bool rows, int n_w, int n_d) {
   __shared__ __attribute__((aligned(16))) SmallTile s_l[2], s_r[2];
   const int b = blockIdx.x;
   if (b < n_w) {
@@ -298,12 +380,11 @@ bool grad_fits(const ActGradArgs &c, const DenseArgs &dx, const DenseArgs &dw) {
          n_w + n_d + cdiv(c.N, 64) < INT32_MAX / 2;
 }
 
-template <typename Tr>
-hipError_t linear_grad_of(const ActGradArgs &c, const DenseArgs &dx, const DenseArgs &dw, float *parts, hipStream_t s) {
+template <typename Tr, typename Args>
+hipError_t linear_grad_of(const ActGradArgs &c, const Args &dx, const Args &dw, float *parts, hipStream_t s) {
   const bool curved = c.act != MOE_ACT_NONE;
-  if (!grad_fits(c, dx, dw)) return hipErrorInvalidConfiguration;
   // dW's tiles leave their sums in dW, or in the parts
-  DenseArgs w = dw;
+  Args w = dw;
   const bool cut = dw.out && dw.G > 1;
   if (cut) {
     w.out = parts;
@@ -322,17 +403,17 @@ hipError_t linear_grad_of(const ActGradArgs &c, const DenseArgs &dx, const Dense
   if (small) {
     const int64_t n_w = w.G * cdiv(w.N, kSmall) * cdiv(w.K, kSmall), n_d = xcd_grid(cdiv(dx.P, kSmall) * cdiv(dx.K, kSmall)), n_c = c.db ? cdiv(c.N, 64) : 0;
     const dim3 grid((unsigned)(n_w + n_d + n_c));
-    if (dx.vec) linear_grad_small_kernel<Tr, true><<<grid, 256, 0, s>>>(dx, w, c, rows, (int)n_w, (int)n_d);
-    else linear_grad_small_kernel<Tr, false><<<grid, 256, 0, s>>>(dx, w, c, rows, (int)n_w, (int)n_d);
+    if (dx.vec) linear_grad_small_kernel<Tr, true, Args><<<grid, 256, 0, s>>>(dx, w, c, rows, (int)n_w, (int)n_d);
+    else linear_grad_small_kernel<Tr, false, Args><<<grid, 256, 0, s>>>(dx, w, c, rows, (int)n_w, (int)n_d);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   } else {
     if (dx.out && c.T > 0) {
-      const hipError_t e = launch_vec<Tr, kDgrad, DenseArgs>(dx, s);
+      const hipError_t e = launch_vec<Tr, kDgrad, Args>(dx, s);
       if (e != hipSuccess) return e;
     }
     if (dw.out) {
-      const hipError_t e = launch_vec<Tr, kWgrad, DenseArgs>(w, s);
+      const hipError_t e = launch_vec<Tr, kWgrad, Args>(w, s);
       if (e != hipSuccess) return e;
     }
   }
@@ -380,7 +461,22 @@ template hipError_t launch_linear<false>(const LinearArgs<false> &, bool, hipStr
 template hipError_t launch_linear<true>(const LinearArgs<true> &, bool, hipStream_t);
 
 hipError_t launch_linear_grad(const ActGradArgs &c, const DenseArgs &dx, const DenseArgs &dw, float *parts, bool fp16, hipStream_t s) {
-  return fp16 ? linear_grad_of<Fp16>(c, dx, dw, parts, s) : linear_grad_of<Bf16>(c, dx, dw, parts, s);
+  if (!grad_fits(c, dx, dw)) return hipErrorInvalidConfiguration;
+  return fp16 ? linear_grad_of<Fp16, DenseArgs>(c, dx, dw, parts, s) : linear_grad_of<Bf16, DenseArgs>(c, dx, dw, parts, s);
+}
+
+hipError_t launch_linear_grad_split(const ActGradArgs &c, const SplitArgs &dx, const SplitArgs &dw, const HalvesArgs &w, const HalvesArgs &x,
+                                    float *parts, bool fp16, bool bf16_parts, hipStream_t s) {
+  if (!grad_fits(c, dx, dw)) return hipErrorInvalidConfiguration;
+  for (const HalvesArgs *h : {&w, &x}) {
+    if (!h->from || h->rows == 0) continue;
+    const int64_t n = cdiv((int64_t)h->rows * cdiv(h->cols, 8), 256);
+    halves_kernel<<<dim3((unsigned)(n < 8192 ? n : 8192)), 256, 0, s>>>(*h);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (bf16_parts) return linear_grad_of<Fp16InBf16, SplitArgs>(c, dx, dw, parts, s);
+  return fp16 ? linear_grad_of<Fp16, SplitArgs>(c, dx, dw, parts, s) : linear_grad_of<Bf16, SplitArgs>(c, dx, dw, parts, s);
 }
 
 }  // namespace moe

@@ -654,6 +654,8 @@ int moe_adapter_backward(int32_t dtype, const void *dy, int64_t lddy, const void
 #define MOE_ACT_GELU_TANH 4  /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
 #define MOE_ACT_SWIGLU    5  /* gated, with the curve of MOE_ACT_SILU */
 #define MOE_ACT_GEGLU     6  /* gated, with the curve of MOE_ACT_GELU_TANH */
+/* or-ed to the activation of a gradient: see moe_linear_backward */
+#define MOE_ACT_ROUND_DZ  0x100
 
 /*
  * Matrix product with bias, activation and residual:
@@ -688,9 +690,11 @@ int moe_linear(int32_t dtype, const void *x, int64_t ldx, int32_t T, int32_t N, 
  *   ws     moe_linear_backward_workspace_bytes(T, N, K, act) bytes, 256-byte aligned; may be NULL when
  *          act is MOE_ACT_NONE and dW and db are NULL. Calls that may run at the same time, in replayed
  *          graphs too, need one each.
- * With an activation dz is rounded to dtype before the two products (they take 16-bit operands), so
- * dx and dW carry that rounding of each term whatever their type; db does not. Errors as
- * moe_linear, and MOE_EWORKSPACE.
+ * The two products take 16-bit operands. With an activation dz enters them as a sum of such: exactly for a
+ * result in fp32, and but for 2^-15 of each value (both results in fp16: 2^-22, or 2^-25 if that is more, and infinite
+ * beyond twice fp16's largest value) for one in dtype. With MOE_ACT_ROUND_DZ or-ed to act (in both calls), dz is rounded
+ * to dtype once, and dx and dW carry that rounding of each term whatever their type; the products take half the time,
+ * or less for fp32 results. db is formed of dz before either. Errors as moe_linear, and MOE_EWORKSPACE.
  */
 size_t moe_linear_backward_workspace_bytes(int32_t T, int32_t N, int32_t K, int32_t act);
 int moe_linear_backward(int32_t dtype, const void *dy, int64_t lddy, const void *x, int64_t ldx, int32_t T, int32_t N, int32_t K,
