@@ -461,7 +461,8 @@ __global__ __launch_bounds__(64 * down_waves(One)) void few_down_kernel(FewArgs 
 template <typename Tr, int VPL, bool Vec>
 hipError_t few_of(FewArgs a, hipStream_t s) {
   const int64_t blocks_sh = a.f_sh > 0 ? cdiv(a.T, 16) : 0;
-  const int64_t pairs = (int64_t)a.T * a.k, blocks = (a.E < pairs ? a.E : pairs) + pairs / 16;  // at most
+  // at most; one token's are its picks (a workgroup beyond the last item would write the plan once more)
+  const int64_t pairs = (int64_t)a.T * a.k, blocks = a.T == 1 ? a.k : (a.E < pairs ? a.E : pairs) + pairs / 16;
   const int64_t items = blocks * cdiv(a.f, 8) + blocks_sh * cdiv(a.f_sh, 8);
   // a wave's part of a sum is what it asks for at once, where eight waves can make it so
   a.share = 0;
