@@ -30,6 +30,14 @@ inline bool wide_tiles(const GroupedArgs &a, GroupedMode mode) {
   return !a.a_row || a.a_rows * a.ld_rows < limit;
 }
 
+// For a single matrix those offsets go from the tile's first row on, and from each step's first of 64 terms where rows are the
+// terms; only the columns of a gated product lie apart, in the halves of W.
+inline bool wide_tiles_dense(const DenseArgs &a, bool gated) {
+  const int64_t limit = (int64_t)1 << 30;  // elements
+  if (!a.vec || a.a_rows < 1 || 256 * a.ld_rows >= limit || 256 * a.ld_w >= limit) return false;
+  return !gated || (int64_t)a.N * a.K < limit;
+}
+
 inline int status(hipError_t e) {
   return e == hipSuccess ? MOE_OK : e == hipErrorInvalidConfiguration ? MOE_EUNSUPPORTED : MOE_EHIP;
 }

@@ -76,7 +76,7 @@ int run_linear(int32_t dtype, const void *x, int64_t ldx, int32_t T, int32_t N, 
   a.ld_out = ldy;
   a.out_f32 = y_dtype == MOE_FP32;
   a.vec = units(x, ldx, K) && units(W, K, K);
-  a.wide = wide_tiles(a, kFwd);
+  a.wide = wide_tiles_dense(a, Gated);
   a.bias = bias;
   a.bias_f32 = bias_dtype == MOE_FP32;
   a.act = act;
@@ -188,7 +188,7 @@ int moe_linear_backward(int32_t dtype, const void *dy, int64_t lddy, const void 
     dxa.ld_out = lddx;
     dxa.out_f32 = dx_dtype == MOE_FP32;
     dxa.vec = units(dz, lddz, N) && units(W, K, K);
-    dxa.wide = wide_tiles(dxa, kDgrad);
+    dxa.wide = wide_tiles_dense(dxa, false);
     dxa.vec_out = runs(dx, dx_dtype, lddx) && K % 4 == 0;
     dxa.c_parts = dx_f32 ? 3 : 2;
     dxa.o_parts = bf16_parts ? 2 : 1;
@@ -202,7 +202,7 @@ int moe_linear_backward(int32_t dtype, const void *dy, int64_t lddy, const void 
     dwa.out_f32 = g_dtype == MOE_FP32;
     dwa.accumulate = accumulate != 0;
     dwa.vec = units(dz, lddz, N) && units(x, ldx, K);
-    dwa.wide = wide_tiles(dwa, kWgrad);
+    dwa.wide = wide_tiles_dense(dwa, false);
     const RowParts &p = dwa.wide ? wide_rows : small_rows;
     dwa.part_rows = p.rows;
     dwa.G = p.count;

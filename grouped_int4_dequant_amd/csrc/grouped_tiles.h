@@ -600,6 +600,7 @@ template <typename Tr, int Mode, int TI, bool Gather, int Stages, typename Args>
 __device__ __forceinline__ void wide_body(const Args &a, const WideTile t, uint8_t *s_l0, uint8_t *s_l1, uint8_t *s_l2,
                                           uint8_t *s_r0, uint8_t *s_r1, uint8_t *s_r2) {
   constexpr bool kLAcross = Mode == kWgrad, kRAcross = Mode != kFwd, kNear = Mode == kWgrad;
+  constexpr bool kRows = Mode == kWgrad && Args::kDense;  // terms are consecutive rows, none of them masked
   constexpr int UL = kLAcross ? kUnits : (TI + 1) / 2;  // requests that hold rows of a tile of 32 TI
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -640,8 +641,8 @@ __device__ __forceinline__ void wide_body(const Args &a, const WideTile t, uint8
     rr = wave + (lane & 32);
     const int col = min(8 * (tid & 31), t.nj - 8);
     if constexpr (Mode == kWgrad) {
-      rbase = (const char *)(a.rows + t.j0);
-      rv[0] = (uint32_t)col * 2;
+      rbase = (const char *)(a.rows + (kRows ? (int64_t)t.first * a.ld_rows : 0) + t.j0);
+      rv[0] = (uint32_t)((kRows ? rr * a.ld_rows : 0) + col) * 2;
     } else {
       rbase = (const char *)(a.w + (int64_t)t.e * a.N * a.K + t.j0);
       rv[0] = (uint32_t)(rr * a.ld_w + col) * 2;
@@ -658,9 +659,9 @@ __device__ __forceinline__ void wide_body(const Args &a, const WideTile t, uint8
       rv[j] = (uint32_t)(row * a.ld_w + rr) * 2;
     }
   }
-  int rrow[kUnits];  // weight gradient: the rows of A of the next requested step, -1: zeros (dC's rows are the same r)
+  int rrow[kUnits];  // weight gradient of groups: the rows of A of the next requested step, -1: zeros (dC's rows are the same r)
   auto fetch_rows = [&](int s) __attribute__((always_inline)) {
-    if constexpr (Mode == kWgrad) {
+    if constexpr (Mode == kWgrad && !kRows) {
 #pragma unroll
       for (int i = 0; i < kUnits; ++i) {
         const int r = at_step.first(s) + rr + 8 * i, p = t.first + min(r, t.nr - 1);
@@ -670,7 +671,7 @@ __device__ __forceinline__ void wide_body(const Args &a, const WideTile t, uint8
     }
   };
   // `s` is the step asked for, lbase and rbase stand at it; `whole`: every r of the step exists
-  const int64_t lstep = kLAcross ? kBR * a.ld_w * 2 : kBR * 2, rstep = Mode == kDgrad ? kBR * a.ld_w * 2 : Mode == kFwd ? kBR * 2 : 0;
+  const int64_t lstep = kLAcross ? kBR * a.ld_w * 2 : kBR * 2, rstep = Mode == kDgrad ? kBR * a.ld_w * 2 : Mode == kFwd ? kBR * 2 : kRows ? kBR * a.ld_rows * 2 : 0;
   auto advance = [&]() __attribute__((always_inline)) {
     int64_t l, r;
     at_step.next(a, t.nr, lstep / 2, rstep / 2, l, r);
@@ -679,13 +680,13 @@ __device__ __forceinline__ void wide_body(const Args &a, const WideTile t, uint8
   };
   auto request_l = [&](int s, int i, uint8_t *buf, auto whole) __attribute__((always_inline)) {
     const char *p = uniform(lbase + (kLAcross ? (lstep >> 3) * i : 0)) + lv[kLAcross ? 0 : i];
-    if constexpr (Mode == kWgrad) p = rrow[i] >= 0 ? p : (const char *)&g_zeros;  // a masked row's dC may hold anything
-    else if constexpr (!decltype(whole)::value) p = at_step.first(s) + lr < t.nr ? p : (const char *)&g_zeros;
+    if constexpr (Mode == kWgrad && !kRows) p = rrow[i] >= 0 ? p : (const char *)&g_zeros;  // a masked row's dC may hold anything
+    else if constexpr (!decltype(whole)::value) p = at_step.first(s) + lr + (kLAcross ? 8 * i : 0) < t.nr ? p : (const char *)&g_zeros;
     load_lds16(p, buf + row_piece<Mode>(8 * i) + row_piece<Mode>(1) * wave);
   };
   auto request_r = [&](int s, int i, uint8_t *buf, auto whole) __attribute__((always_inline)) {
     const char *p;
-    if constexpr (Mode == kWgrad) {
+    if constexpr (Mode == kWgrad && !kRows) {
       p = rbase + (uint64_t)((uint32_t)rrow[i] * (uint32_t)(a.ld_rows * 2) + rv[0]);
       p = rrow[i] >= 0 ? p : (const char *)&g_zeros;
     } else {
