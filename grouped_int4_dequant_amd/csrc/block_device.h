@@ -115,8 +115,9 @@ __device__ __forceinline__ float wave_sum(float v) {
   return (lane(0) + lane(16)) + (lane(32) + lane(48));
 }
 
-// s(v) = 1 / (1 + e^-v) and 1 - s(v). e^-|v| is 2^(-|v| log2 e) with the product rounded, which is off by |v| 2^-24 of
-// itself at most: for the small one of the two that is its relative error (and a few 2^-24 more), and nothing to the other.
+// s(v) = 1 / (1 + e^-v) and 1 - s(v). e^-|v| is 2^(-|v| log2 e) with the constant (within 0.22 2^-24 of log2 e) and the product
+// rounded, which is off by 1.25 |v| 2^-24 of itself at most, and the exponential's own 2^-23: for the small one of the two that
+// is its relative error (with three 2^-24 more for the sum and the reciprocal), and nothing to the other.
 struct Sigmoid {
   float s, rest;
 };

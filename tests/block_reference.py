@@ -3,10 +3,11 @@ product with bias, activation and residual, the norms before and after a block,
 their gradients, the layer for a few tokens), each with an element-wise bound on what
 a kernel that works in fp32 and rounds once may be off. U = 2^-24 is half a step of fp32.
 
-Activations. With e^-|v| within 4 U (v_exp_f32 1 ulp = 2 U, its argument's rounding corrected), 1 + e one
-rounding and the reciprocal 1 ulp, a sigmoid is within 8 U of its value and a curve within 10 U; where the
-sigmoid's (or erfc's) argument is itself rounded, its relative error grows by the argument's size, at most
-1 + z^2 times. So a curve is allowed 16 U (1 + z^2) |value|, its derivative, a sum of terms of size 1 + |z|
+Activations. e^-|v| is v_exp_f32 (1 ulp = 2 U) of the rounded product of |v| and a rounded log2 e, which is off by 1.25 |v| U
+more; with 1 + e one rounding and the reciprocal 1 ulp a sigmoid is within (5 + 1.25 |v|) U of its value and a curve within
+(7 + 1.25 |z|) U, which is below 8 U (1 + z^2). Where the sigmoid's (or erfc's) argument is itself formed with
+roundings, its relative error grows by as many times the argument's size, which costs as much again.
+So a curve is allowed 16 U (1 + z^2) |value|, its derivative, a sum of terms of size 1 + |z|
 that may cancel, 32 U (1 + z^2). Curves change by at most 1.2 times what their argument does.
 
 Norms. A mean of d squares is within (d + 32) U, its root within half of that and 4 U (square root, reciprocal).
