@@ -766,8 +766,8 @@ int moe_residual_norm_backward(int32_t dtype, const void *dy, int64_t lddy, cons
  *   topk_ids, topk_w   int32 and fp32 [T][k]: the picks, or NULL (not wanted)
  *   ws        moe_few_tokens_workspace_bytes(L, T) bytes, 256-byte aligned; calls that may run at
  *             the same time, in replayed graphs too, need one each
- * Each picked expert's weights are read once for all its tokens (of 16 at most). Sums and FFN's inner
- * values are held in fp32, and the inner values enter the second product so. The k experts are added in slot
+ * An expert's weights are read once for every 16 of its tokens, W_dn's rows of more than 512 once for every four. Sums
+ * and FFN's inner values are held in fp32, and the inner values enter the second product so. The k experts are added in slot
  * order, then the shared one, then `add`. A row's result does not depend on the other rows of the call, but may
  * differ in the last bits between a call of one token and a longer one (the sums are cut in other places).
  * Errors: MOE_EINVAL (null or misaligned pointer, unknown type, T < 0, a size < 1, f_sh < 0, k > E, a stride
