@@ -13,7 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Dict, Optional
+from typing import Dict, Optional, Union
 
 import torch
 
@@ -942,25 +942,30 @@ def linear_backward_workspace_bytes(T: int, N: int, K: int, act: str = "none", r
     return int(load().moe_linear_backward_workspace_bytes(T, N, K, _activation(act, N)[0] | (_ROUND_DZ if round_dz else 0)))
 
 
-def linear_backward(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, pre: Optional[torch.Tensor] = None, act: str = "none",
-                    bias_grad: bool = False, dx: Optional[torch.Tensor] = None, dW: Optional[torch.Tensor] = None,
+def linear_backward(dy: torch.Tensor, x: Optional[torch.Tensor], W: Optional[torch.Tensor], pre: Optional[torch.Tensor] = None,
+                    act: str = "none", bias_grad: bool = False, dx: Union[torch.Tensor, bool, None] = None, dW: Union[torch.Tensor, bool, None] = None,
                     db: Optional[torch.Tensor] = None, grad_dtype: Optional[torch.dtype] = None, accumulate: bool = False,
                     ws: Optional[torch.Tensor] = None, stream=None, round_dz: bool = False):
     """moe_linear_backward: (dx [T][K], dW [N][K], db [N] or None) from dy
     [T][columns of y] and pre [T][N], which linear wrote (not needed without
     activation). db is formed with bias_grad or where it is given; dW and db are of
     grad_dtype (None: x's type), and with accumulate are added to the given ones
-    (fp32). The C call takes NULL for those that are not wanted. round_dz: the
-    gradient of `pre` is rounded to x's type before the products, in about half the time
-    (MOE_ACT_ROUND_DZ)."""
+    (fp32). dx=False or dW=False: that one is not formed, and W or x may be None;
+    None stands in its place. round_dz: the gradient of `pre` is rounded to x's type
+    before the products, in about half the time (MOE_ACT_ROUND_DZ)."""
     c = _Call(dy, "dy", stream)
-    if dy.dim() != 2 or not isinstance(x, torch.Tensor) or x.dim() != 2 or not isinstance(W, torch.Tensor) or W.dim() != 2:
-        raise ValueError("dy must be [T][columns], x [T][K] and W [N][K]")
-    (T, K), N = x.shape, W.shape[0]
+    if (dy.dim() != 2 or (not isinstance(x, torch.Tensor) or x.dim() != 2) and not (x is None and dW is False and W is not None)
+            or (not isinstance(W, torch.Tensor) or W.dim() != 2) and not (W is None and dx is False and x is not None)):
+        raise ValueError("dy must be [T][columns], x [T][K] (None only with dW=False) and W [N][K] (None only with dx=False)")
+    T, K = dy.shape[0], (x if W is None else W).shape[1]
+    N = W.shape[0] if W is not None else 2 * dy.shape[1] if act in ("swiglu", "geglu") else dy.shape[1]
     _sizes(T, N, K)
     code, cols = _activation(act, N)
-    lddy, ldx = c.ld(dy, "dy", (T, cols)), c.ld(x, "x", (T, K))
-    c.need(W, "W", c.dtype, (N, K))
+    lddy, ldx = c.ld(dy, "dy", (T, cols)), K
+    if x is not None:
+        ldx = c.ld(x, "x", (T, K))
+    if W is not None:
+        c.need(W, "W", c.dtype, (N, K))
     z, ldz = None, 0
     if code:
         if pre is None:
@@ -970,14 +975,18 @@ def linear_backward(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor, pre: Opt
     bias_grad = bias_grad or db is not None
     if accumulate and (dW is None or (bias_grad and db is None)):
         raise ValueError("accumulate needs the tensors to add to in dW and db")
-    dx = c.result(dx, "dx", (T, K), None)
-    dW = c.whole(dW, "dW", (N, K), grad_dtype)
-    db = c.whole(db, "db", (N,), dW.dtype) if bias_grad else None
+    if dx is False and dW is False and not bias_grad:
+        raise ValueError("one of dx, dW and db must be wanted")
+    dx = None if dx is False else c.result(dx, "dx", (T, K), None)
+    dW = None if dW is False else c.whole(dW, "dW", (N, K), grad_dtype)
+    db = c.whole(db, "db", (N,), grad_dtype if dW is None else dW.dtype) if bias_grad else None
+    sums = dW if dW is not None else db
     if round_dz:
         code |= _ROUND_DZ
     ws = c.workspace(ws, int(load().moe_linear_backward_workspace_bytes(T, N, K, code)))
-    c("moe_linear_backward", c.code, dy.data_ptr(), lddy, x.data_ptr(), ldx, T, N, K, W.data_ptr(), z, ldz, code, dx.data_ptr(),
-      _CODES[dx.dtype], _ld(dx, K), dW.data_ptr(), None if db is None else db.data_ptr(), _CODES[dW.dtype], int(accumulate), ws.data_ptr(), ws.numel() * ws.element_size())
+    c("moe_linear_backward", c.code, dy.data_ptr(), lddy, _ptr(x), ldx, T, N, K, _ptr(W), z, ldz, code, _ptr(dx),
+      c.code if dx is None else _CODES[dx.dtype], _ld(dx, K), _ptr(dW), _ptr(db), c.code if sums is None else _CODES[sums.dtype], int(accumulate), ws.data_ptr(),
+      ws.numel() * ws.element_size())
     return dx, dW, db
 
 
@@ -1067,9 +1076,9 @@ def residual_norm_backward_workspace_bytes(T: int, d: int, gates: int = 1) -> in
 
 def residual_norm_backward(dy: Optional[torch.Tensor], dn: Optional[torch.Tensor], o: Optional[torch.Tensor], y: Optional[torch.Tensor],
                            w_o: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None, scale: float = 1.0,
-                           w_n: Optional[torch.Tensor] = None, eps: float = 1e-6, dx: Optional[torch.Tensor] = None,
-                           d_o: Optional[torch.Tensor] = None, dw_o: Optional[torch.Tensor] = None, dgate: Optional[torch.Tensor] = None,
-                           dw_n: Optional[torch.Tensor] = None, grad_dtype: Optional[torch.dtype] = None, accumulate: bool = False,
+                           w_n: Optional[torch.Tensor] = None, eps: float = 1e-6, dx: Union[torch.Tensor, bool, None] = None,
+                           d_o: Union[torch.Tensor, bool, None] = None, dw_o: Union[torch.Tensor, bool, None] = None,
+                           dgate: Union[torch.Tensor, bool, None] = None, dw_n: Union[torch.Tensor, bool, None] = None, grad_dtype: Optional[torch.dtype] = None, accumulate: bool = False,
                            ws: Optional[torch.Tensor] = None, stream=None):
     """moe_residual_norm_backward: (dx, d_o, dw_o, dgate, dw_n) from dy and dn,
     the gradients of residual_norm's y (None: zeros) and n (None: no norm behind;
@@ -1077,7 +1086,8 @@ def residual_norm_backward(dy: Optional[torch.Tensor], dn: Optional[torch.Tensor
     what it wrote (or x, where it formed n alone with scale 1). Those of what the
     forward call did not have are None. dx is of dy's type (without it y's) and may be
     dy itself; dw_o, dgate and dw_n are of grad_dtype (None: the weights' type), and with
-    accumulate are added to the given ones (fp32)."""
+    accumulate are added to the given ones (fp32). Those given as False are not formed, and
+    None stands in their places."""
     lead, name = next(((t, n) for t, n in ((o, "o"), (dn, "dn"), (dy, "dy")) if t is not None), (None, None))
     if lead is None:
         raise ValueError("dy or dn must be given")
@@ -1108,16 +1118,18 @@ def residual_norm_backward(dy: Optional[torch.Tensor], dn: Optional[torch.Tensor
     else:
         ldo, p_of = c.ld(o, "o", shape), o.data_ptr()
     wcode, gates, p_o, p_g, p_n = _norm_args(c, T, d, w_o, gate, w_n)
-    dx = c.result(dx, "dx", shape, stream_type)
-    if o is not None:
+    dx = None if dx is False else c.result(dx, "dx", shape, stream_type)
+    if d_o is False:
+        d_o = None
+    elif o is not None:
         d_o = c.new(shape, c.dtype) if d_o is None else c.rows(d_o, "d_o", shape)
         lddo, p_do = _ld(d_o, d), d_o.data_ptr()
     elif d_o is not None:
         raise ValueError("d_o has nothing that it is the gradient of")
     grads, ptrs, gcode = [], [], c.code
     for w, g, what in ((w_o, dw_o, "dw_o"), (gate, dgate, "dgate"), (w_n, dw_n, "dw_n")):
-        if w is None:
-            if g is not None:
+        if w is None or g is False:
+            if g is not None and g is not False:
                 raise ValueError(f"{what} has nothing that it is the gradient of")
             grads.append(None)
             ptrs.append(None)
@@ -1128,12 +1140,14 @@ def residual_norm_backward(dy: Optional[torch.Tensor], dn: Optional[torch.Tensor
         grads.append(g)
         ptrs.append(g.data_ptr())
         gcode = _CODES[g.dtype]
+    if dx is None and d_o is None and not any(ptrs):
+        raise ValueError("one of the gradients must be wanted")
     p_ws, ws_bytes = None, 0
-    if p_o or p_g or p_n:
+    if any(ptrs):
         ws = c.workspace(ws, int(load().moe_residual_norm_backward_workspace_bytes(T, d, gates)))
         p_ws, ws_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
     c("moe_residual_norm_backward", c.code, p_dy, lddy, p_dn, lddn, p_of, ldo, p_y, ldy, _CODES[stream_type], T, d, p_o, p_g, gates, p_n, wcode, scale,
-      eps, dx.data_ptr(), _ld(dx, d), p_do, lddo, *ptrs, gcode, int(accumulate), p_ws, ws_bytes)
+      eps, _ptr(dx), _ld(dx, d), p_do, lddo, *ptrs, gcode, int(accumulate), p_ws, ws_bytes)
     return (dx, d_o, *grads)
 
 

@@ -96,3 +96,44 @@ def test_norm(lib, codes, T, d, gates, dtype, stream_type, weights, wanted):
         else:
             assert (v == 9).all()
     assert ws is None or (ws[need:] == 255).all()
+
+
+@pytest.mark.parametrize("act,dtype,grad", [("none", BF, F4), ("swiglu", BF, BF), ("gelu", FP, F4)], ids=lambda v: v if isinstance(v, str) else str(v)[6:])
+@pytest.mark.parametrize("shape", ["few", "small", "odd", "wide", "none"])
+def test_linear_from_python(lib, shape, act, dtype, grad):
+    import grouped_int4_dequant_amd as m
+    T, N, K = SHAPES[shape]
+    g = torch.Generator().manual_seed(9)
+    cols = N // 2 if act in R.GATED else N
+    dy, x, W, pre = rnd(g, T, cols, dtype=dtype), rnd(g, T, K, dtype=dtype), rnd(g, N, K, dtype=dtype, scale=K ** -0.5), rnd(g, T, N, dtype=dtype)
+    want = [(v, R.stored(v, s, t)) for (v, s), t in zip(R.linear_grad(dy, x, W, pre, act, dtype), (dtype, grad, grad))]
+    kw = dict(pre=pre, act=act, grad_dtype=grad)
+    db = torch.full((N,), 2.0, device="cuda")
+    for got, formed in ((m.linear_backward(dy, x, W, dW=False, **kw), (0,)), (m.linear_backward(dy, None, W, dW=False, bias_grad=True, **kw), (0, 2)),
+                        (m.linear_backward(dy, x, W, dx=False, **kw), (1,)), (m.linear_backward(dy, x, None, dx=False, bias_grad=True, **kw), (1, 2)),
+                        (m.linear_backward(dy, None, W, dx=False, dW=False, bias_grad=True, **kw), (2,))):
+        for i, (v, (value, bound), name) in enumerate(zip(got, want, ("dx", "dW", "db"))):
+            if i in formed:
+                R.within(v, value, bound, name)
+            else:
+                assert v is None
+    got = m.linear_backward(dy, None, W, pre=pre, act=act, dx=False, dW=False, db=db, accumulate=True)
+    assert got[2] is db and got[:2] == (None, None)
+    value, slack = R.linear_grad(dy, x, W, pre, act, dtype)[2]
+    R.within(db, value + 2.0, R.stored(value + 2.0, slack, F4), "db added")
+
+
+@pytest.mark.parametrize("T,d,gates", [(60, 520, 1), (60, 77, 5), (30, 4104, 2)])
+def test_norm_from_python(lib, T, d, gates):
+    import grouped_int4_dequant_amd as m
+    g = torch.Generator().manual_seed(10)
+    o, dn, y, dy = rnd(g, T, d), rnd(g, T, d), rnd(g, T, d), rnd(g, T, d)
+    w_o, w_n, gate = (rnd(g, *s, scale=0.3, shift=1.0) for s in ((d,), (d,), (gates, d)))
+    expect = R.norm_grad(dy, dn, o, y, w_o, gate, 0.75, w_n, 1e-6)
+    for wanted in [(n,) for n in NORM] + [("dx", "d_o"), ("dgate", "dw_n")]:
+        got = m.residual_norm_backward(dy, dn, o, y, w_o=w_o, gate=gate, scale=0.75, w_n=w_n, grad_dtype=F4, **{n: False for n in NORM if n not in wanted})
+        for name, v in zip(NORM, got):
+            if name in wanted:
+                R.within(v, expect[name][0], R.stored(*expect[name], v.dtype), name)
+            else:
+                assert v is None
