@@ -69,13 +69,13 @@ __device__ __forceinline__ void dense_tile(int item, int ti, int tj, int &it, in
   jt = x / h;
   it = 8 * band + x - jt * h;
 }
-// Where a kernel stands in the steps of a sum, as it asks for them one after the other. Where operands come in parts, all
+// Where small tiles stand in the steps of a sum, as they ask for them one after the other. Where operands come in parts, all
 // terms of the smallest pair of parts come first and those of the first parts last: the sum of the small ones has small
 // roundings. (With a block's pairs one after the other, the larger sum is rounded once for each: fp32 gradients of 4096 rows,
 // 8192 x 2048 1.0e-6 off, this way 5.9e-7.)
 template <typename Args>
 struct Steps {
-  int r = 0;          // first term of the step (without parts the caller counts); behind the last step nr or more
+  int r = 0;          // first term of the step (without parts the caller counts)
   int c = 0, o = 0;   // the parts
   __device__ __forceinline__ explicit Steps(const Args &a) {
     if constexpr (Args::kSplit) {
@@ -102,19 +102,15 @@ struct Steps {
     if constexpr (Args::kSplit) return o * a.o_next;
     else return 0;
   }
-  // Moves on; what is added to the places of dC's and the other operand's step, where a step of terms is
-  // `c_step` and `o_step` long.
-  __device__ __forceinline__ void next(const Args &a, int nr, int64_t c_step, int64_t o_step, int64_t &c_add, int64_t &o_add) {
-    c_add = c_step;
-    o_add = o_step;
+  __device__ __forceinline__ void next(const Args &a, int nr) {
     if constexpr (Args::kSplit) {
-      const bool end = r + kBR >= nr, c_end = c == 0;
-      const int64_t back = (nr + kBR - 1) / kBR - 1;
-      c_add = end ? (c_end ? (a.c_parts - 1) * a.c_next : -a.c_next) - back * c_step : c_step;
-      o_add = end ? (c_end ? -a.o_next : 0) - back * o_step : o_step;
-      o -= end && c_end;
-      c = !end ? c : c_end ? a.c_parts - 1 : c - 1;
-      r = !end ? r + kBR : o < 0 ? nr : 0;
+      r += kBR;
+      if (r < nr) return;
+      r = 0;
+      if (--c < 0) {
+        c = a.c_parts - 1;
+        --o;
+      }
     }
   }
 };
@@ -291,8 +287,7 @@ __device__ __forceinline__ void small_body(const Args &a, const int block, Small
         rreg[i] = load_unit<Vec>(rp[i] + rpart + r0, kAll ? 8 : nr - r0 - rslot);
       }
     }
-    int64_t unused_c, unused_o;
-    at_step.next(a, nr, 0, 0, unused_c, unused_o);
+    at_step.next(a, nr);
   };
   auto keep = [&](int buf, const u4 (&lreg)[U], const u4 (&rreg)[U]) __attribute__((always_inline)) {
 #pragma unroll
@@ -606,8 +601,7 @@ __device__ __forceinline__ void wide_body(const Args &a, const WideTile t, uint8
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wi = wave >> 2, wj = wave & 3;
   const int p16 = lane & 15, q4 = lane >> 4;
-  const int steps = Steps<Args>::count(a, t.nr), whole_steps = Steps<Args>::whole(a, t.nr);
-  Steps<Args> at_step(a);
+  const int steps = (t.nr + kBR - 1) / kBR;
 
   // ---- requests. Unit i is piece 8 i + wave: a straight operand's tile rows
   // 64 i + tid / 8, an across operand's r = 8 i + wave of the step in the lower 32 lanes and 32 more in the upper. Rows and
@@ -664,7 +658,7 @@ __device__ __forceinline__ void wide_body(const Args &a, const WideTile t, uint8
     if constexpr (Mode == kWgrad && !kRows) {
 #pragma unroll
       for (int i = 0; i < kUnits; ++i) {
-        const int r = at_step.first(s) + rr + 8 * i, p = t.first + min(r, t.nr - 1);
+        const int r = s * kBR + rr + 8 * i, p = t.first + min(r, t.nr - 1);
         const int at = Gather ? a.a_row[p] : p;
         rrow[i] = ((r < t.nr) & (at < a.a_rows)) ? at : -1;
       }
@@ -672,16 +666,10 @@ __device__ __forceinline__ void wide_body(const Args &a, const WideTile t, uint8
   };
   // `s` is the step asked for, lbase and rbase stand at it; `whole`: every r of the step exists
   const int64_t lstep = kLAcross ? kBR * a.ld_w * 2 : kBR * 2, rstep = Mode == kDgrad ? kBR * a.ld_w * 2 : Mode == kFwd ? kBR * 2 : kRows ? kBR * a.ld_rows * 2 : 0;
-  auto advance = [&]() __attribute__((always_inline)) {
-    int64_t l, r;
-    at_step.next(a, t.nr, lstep / 2, rstep / 2, l, r);
-    lbase += 2 * l;
-    rbase += 2 * r;
-  };
   auto request_l = [&](int s, int i, uint8_t *buf, auto whole) __attribute__((always_inline)) {
     const char *p = uniform(lbase + (kLAcross ? (lstep >> 3) * i : 0)) + lv[kLAcross ? 0 : i];
     if constexpr (Mode == kWgrad && !kRows) p = rrow[i] >= 0 ? p : (const char *)&g_zeros;  // a masked row's dC may hold anything
-    else if constexpr (!decltype(whole)::value) p = at_step.first(s) + lr + (kLAcross ? 8 * i : 0) < t.nr ? p : (const char *)&g_zeros;
+    else if constexpr (!decltype(whole)::value) p = s * kBR + lr + (kLAcross ? 8 * i : 0) < t.nr ? p : (const char *)&g_zeros;
     load_lds16(p, buf + row_piece<Mode>(8 * i) + row_piece<Mode>(1) * wave);
   };
   auto request_r = [&](int s, int i, uint8_t *buf, auto whole) __attribute__((always_inline)) {
@@ -691,7 +679,7 @@ __device__ __forceinline__ void wide_body(const Args &a, const WideTile t, uint8
       p = rrow[i] >= 0 ? p : (const char *)&g_zeros;
     } else {
       p = uniform(rbase + (kRAcross ? (rstep >> 3) * i : 0)) + rv[kRAcross ? 0 : i];
-      if constexpr (!decltype(whole)::value) p = at_step.first(s) + rr + (kRAcross ? 8 * i : 0) < t.nr ? p : (const char *)&g_zeros;
+      if constexpr (!decltype(whole)::value) p = s * kBR + rr + (kRAcross ? 8 * i : 0) < t.nr ? p : (const char *)&g_zeros;
     }
     load_lds16(p, buf + col_piece<Mode>(8 * i) + col_wave);
   };
@@ -777,7 +765,8 @@ __device__ __forceinline__ void wide_body(const Args &a, const WideTile t, uint8
       for (int j = 0; j < kTJ; ++j) acc[i][j] = Tr::mfma(r1[j], l1[i], acc[i][j]);
       __builtin_amdgcn_sched_barrier(0);
     }
-    advance();
+    lbase += lstep;
+    rbase += rstep;
   };
   // The weight gradient's variant of a step. Both its operands come from LDS
   // in pairs of 8-byte fetches, and a half held ahead spills; here the next
@@ -802,25 +791,26 @@ __device__ __forceinline__ void wide_body(const Args &a, const WideTile t, uint8
       for (int j = 0; j < kTJ; ++j) acc[i][j] = Tr::mfma(r[ks][j], l[x & 1], acc[i][j]);
       __builtin_amdgcn_sched_barrier(0);
     }
-    advance();
+    lbase += lstep;
+    rbase += rstep;
     fetch_rows(s + 2);
     meet(none);
   };
   constexpr std::false_type partly{};
-  lbase += 2 * at_step.c_part(a);
-  rbase += 2 * at_step.o_part(a);
-  if (steps > 0) {
+  auto sum = [&]() __attribute__((always_inline)) {
+    if (steps == 0) return;
     fetch_rows(0);
 #pragma unroll
     for (int i = 0; i < UL; ++i) request_l(0, i, s_l0, partly);
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) request_r(0, i, s_r0, partly);
-    advance();
+    lbase += lstep;
+    rbase += rstep;
     fetch_rows(1);
     if constexpr (kNear) {
       meet(none);
       int s = 0;
-      for (; s + 3 <= whole_steps; s += 2) {  // steps s + 1 and s + 2 are whole
+      for (; (s + 3) * kBR <= t.nr; s += 2) {  // steps s + 1 and s + 2 are whole
         step_near(s, s_l0, s_r0, s_l1, s_r1, std::true_type{});
         step_near(s + 1, s_l1, s_r1, s_l0, s_r0, std::true_type{});
       }
@@ -835,7 +825,8 @@ __device__ __forceinline__ void wide_body(const Args &a, const WideTile t, uint8
         for (int i = 0; i < UL; ++i) request_l(x, i, x == 1 ? s_l1 : s_l2, partly);
 #pragma unroll
         for (int i = 0; i < kUnits; ++i) request_r(x, i, x == 1 ? s_r1 : s_r2, partly);
-        advance();
+        lbase += lstep;
+        rbase += rstep;
       }
       meet(std::integral_constant<int, Stages - 1>{});
 #pragma unroll
@@ -853,9 +844,21 @@ __device__ __forceinline__ void wide_body(const Args &a, const WideTile t, uint8
         }
       };
       int s = 0;
-      for (; s + 2 * Stages <= whole_steps; s += Stages) round(s, std::true_type{});  // the steps it asks for are whole
+      for (; (s + 2 * Stages) * kBR <= t.nr; s += Stages) round(s, std::true_type{});  // the steps it asks for are whole
       for (; s < steps; s += Stages) round(s, partly);  // a part of a round ends with steps of zeros
     }
+  };
+  if constexpr (Args::kSplit) {  // one pair of parts after the other
+    const char *const l = lbase, *const r = rbase;
+    for (int o = a.o_parts - 1; o >= 0; --o)
+      for (int c = a.c_parts - 1; c >= 0; --c) {
+        lbase = l + 2 * c * a.c_next;
+        rbase = r + 2 * o * a.o_next;
+        sum();
+        meet(none);
+      }
+  } else {
+    sum();
   }
   meet(none);  // the buffers are free
   if constexpr (Args::kEpilogue) {
