@@ -16,8 +16,8 @@
 //            token in slot order. The matrix instructions have no part in it: with one or two pairs a block they would be
 //            nearly empty, and laying h out for them took three times the loads of the weights (57 us at 16 tokens of 8
 //            of 256 experts, 2048 x 512).
-// One token of 8 of 256 experts and the shared one, 2048 x 512, bf16: 13.8 and 5.7 us for 38 and 19 MB; 16 tokens: 83 us for
-// 426 MB and 52 for 214 (5.1 and 4.1 TB/s).
+// One token of 8 of 256 experts and the shared one, 2048 x 512, bf16: 13.4 and 5.3 us for 38 and 19 MB; 16 tokens: 82 us for
+// 426 MB and 52 for 214 (5.2 and 4.1 TB/s).
 // Weights go straight from memory to registers. They are read once for each 16 pairs of an expert, but by down, where a row is longer
 // than the 512 terms that a wave's lanes hold, again for each four (from L2).
 

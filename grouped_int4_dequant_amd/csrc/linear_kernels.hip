@@ -161,7 +161,7 @@ __global__ __launch_bounds__(256) void halves_kernel(HalvesArgs a) {
 
 // A workgroup takes 256 columns of a chunk of rows; a thread eight of them, every eighth row. dz enters the two products
 // as an operand of the matrix instructions, in 16-bit parts; the column sums are of its values before
-// that. Bound by memory: 4096 x 8192, swiglu, 37 us for 168 MB where dz is rounded (45 with db), 62 for 235 MB in two parts.
+// that. Bound by memory: 4096 x 8192, swiglu, 37 us for 168 MB where dz is rounded (45 with db), 55 for 235 MB in two parts.
 template <typename Tr, bool Gated>
 __global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs a) {
   __shared__ float s_sum[8][Gated ? 2 : 1][256];

@@ -11,6 +11,8 @@
 // is formed from there, in fp32; results are rounded once. n comes from y before y is
 // rounded. Weights stay in registers (in the gradient in LDS) over the rows of a workgroup. bf16, 8192 rows of 2048
 // with everything: 28.6 us for 134 MB (4.7 TB/s; a copy runs at 5.1), gradients 54 for 201 MB and 18 MB of column sums.
+// The gradient has three workgroups a CU up to 2048 columns and one above; above 4096 its 1024 threads spill registers. 201 MB
+// each: 4096 rows of 4096 61 us, 2048 of 8192 120, 1024 of 16384 345.
 
 #include "block_device.h"
 
