@@ -177,3 +177,32 @@ def test_no_rows(moe):
     for act, dy in (("silu", e), ("swiglu", e[:, :4])):
         dx, dW, db = moe.linear_backward(dy, x, W, pre=e, act=act, bias_grad=True, grad_dtype=F4)
         assert dx.shape == (0, 16) and (dW == 0).all() and (db == 0).all()
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "geglu"])
+@pytest.mark.parametrize("T", [1, 70])
+def test_parts_add_up(moe, T, act):
+    """With ones for weights and inputs the three bf16 parts give dz itself, to the last bit, which db shows: of one row, and of rows of zeros beside it.
+    Values from 2^-90 to 2^90, those of few bits among them."""
+    N = 512
+    g = torch.Generator().manual_seed(6)
+    cols = N // 2 if act in R.GATED else N
+    dy = torch.zeros(T, cols, dtype=BF, device="cuda")
+    dy[T // 2] = rnd(g, cols) * (2.0 ** torch.randint(-90, 90, (cols,), generator=g)).to(BF).cuda()
+    dy[T // 2, :cols // 4] = (2.0 ** torch.randint(-90, 90, (cols // 4,), generator=g)).to(BF).cuda()
+    pre = rnd(g, T, N)
+    W, x = torch.eye(N, dtype=BF, device="cuda"), torch.ones(T, 8, dtype=BF, device="cuda")
+    dx, _, db = moe.linear_backward(dy, torch.zeros(T, N, dtype=BF, device="cuda"), W, pre=pre, act=act, bias_grad=True, dx=torch.empty(T, N, device="cuda"), grad_dtype=F4)
+    assert torch.equal(dx[T // 2], db) and (db != 0).all()
+    assert (dx[:T // 2] == 0).all() and (dx[T // 2 + 1:] == 0).all()
+    _, dW, _ = moe.linear_backward(dy, x, None, pre=pre, act=act, dx=False, grad_dtype=F4)
+    assert torch.equal(dW, db[:, None].expand(N, 8))
+    # two parts: 2^-15 of dz, and the result's own rounding
+    for dtype in (BF, FP):
+        e = torch.where(torch.arange(cols) % 2 == 0, 1.0, 2.0 ** -6).cuda()
+        d = torch.zeros(T, cols, dtype=dtype, device="cuda")
+        d[T // 2] = (rnd(g, cols, dtype=F4) * e).to(dtype)
+        dx, _, db = moe.linear_backward(d, torch.zeros(T, N, dtype=dtype, device="cuda"), W.to(dtype), pre=pre.to(dtype), act=act, bias_grad=True)
+        _, _, db = moe.linear_backward(d, None, W.to(dtype), pre=pre.to(dtype), act=act, dx=False, dW=False, bias_grad=True, grad_dtype=F4)
+        value = R.d(db)
+        R.within(dx[T // 2], value, R.stored(value, 2.0 ** -15 * value.abs() if dtype is BF else 2.0 ** -22 * value.abs() + 2.0 ** -25, dtype), "dx")
